@@ -15,6 +15,13 @@ library is missing the calls raise.
     gemm_f16_nt_splitk_static(A, B, C)       # split-K into the library's static
                                              # scratch area: allocates nothing
 
+and, from ``include/mi355fused.h`` (module ``fused``), a model's products with
+the work around them folded in:
+
+    gemm_gated / gemm_gated_bwd              # act(X@Wg.T) * (X@Wu.T), gradients
+    gemm_w4                                  # 4-bit weights with group scales
+    gemm_xent / gemm_xent_bwd                # cross entropy over X@W.T, gradients
+
 The library allocates no memory.  Where a call's kernels need scratch memory
 (split-K partial sums, gemm_ex's transposed copies and matrix-vector partial
 sums) the caller may pass a ``workspace`` tensor; if it does not, this module
@@ -423,3 +430,8 @@ def ex_path(A, B, C, op_a: str = "n", op_b: str = "t", bias=None, act: str = "no
     workspace of ``ex_workspace_bytes`` (host only)."""
     return _path_name(load_library().gemm_ex_path(*_ex_args(A, B, C, op_a, op_b, bias, act,
                                                             residual)))
+
+
+from .fused import (gated_bwd_workspace_bytes, gated_workspace_bytes, gemm_gated,  # noqa: E402,F401
+                    gemm_gated_bwd, gemm_w4, gemm_xent, gemm_xent_bwd, xent_bwd_workspace_bytes,
+                    xent_workspace_bytes)

@@ -1,8 +1,9 @@
-"""Builds ``libmi355gemm.so`` (the C-ABI library) from ``csrc/`` with hipcc for gfx950.
+"""Builds ``libmi355gemm.so`` and ``libmi355fused.so`` (the C-ABI libraries)
+from ``csrc/`` and ``csrc/fused/`` with hipcc for gfx950.
 
 Usage: ``python -m dense_gemm_sgemm_amd.build`` or ``build()`` from Python.
 Each ``.hip`` file is compiled to an object in ``_build/`` (in parallel), then
-linked in place next to this file so that the library travels with the tree.
+linked in place next to this file so that the libraries travel with the tree.
 """
 from __future__ import annotations
 
@@ -19,6 +20,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libmi355gemm.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+FUSED_CSRC = os.path.join(CSRC, "fused")
+FUSED_LIB_PATH = os.path.join(HERE, "libmi355fused.so")
 ARCH = "gfx950"
 
 # Packed fp32 VALU instructions are kept out of the generated code on purpose;
@@ -46,11 +49,14 @@ def hipcc() -> str:
 FILE_FLAGS = {
     "hgemm_mfma.hip": ["-mllvm", "--amdgpu-sched-strategy=iterative-minreg"],
     "hgemm_kmajor.hip": ["-mllvm", "--amdgpu-sched-strategy=iterative-minreg"],
+    "tiles_gated.hip": ["-mllvm", "--amdgpu-sched-strategy=iterative-minreg"],
+    "tiles_logits.hip": ["-mllvm", "--amdgpu-sched-strategy=iterative-minreg"],
+    "tiles_grad.hip": ["-mllvm", "--amdgpu-sched-strategy=iterative-minreg"],
 }
 
 
-def sources() -> list[str]:
-    return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".hip"))
+def sources(folder: str = CSRC) -> list[str]:
+    return sorted(os.path.join(folder, f) for f in os.listdir(folder) if f.endswith(".hip"))
 
 
 def _compile(src: str, extra: list[str]) -> str:
@@ -63,19 +69,24 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
-def build(extra_flags: list[str] | None = None, jobs: int | None = None) -> str:
-    """Compile every kernel source for gfx950 and link the shared library."""
-    extra = list(extra_flags or [])
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sources()
-    with ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra), srcs))
-    tmp = LIB_PATH + ".tmp%d" % os.getpid()
+def _link(objs: list[str], lib_path: str) -> None:
+    tmp = lib_path + ".tmp%d" % os.getpid()
     cmd = [hipcc(), "--offload-arch=" + ARCH, "-shared", "-fPIC", *objs, "-o", tmp]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("link failed:\n%s\n%s" % (" ".join(cmd), res.stderr))
-    os.replace(tmp, LIB_PATH)
+    os.replace(tmp, lib_path)
+
+
+def build(extra_flags: list[str] | None = None, jobs: int | None = None) -> str:
+    """Compile every kernel source for gfx950 and link the shared libraries."""
+    extra = list(extra_flags or [])
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    srcs, fused = sources(), sources(FUSED_CSRC)
+    with ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs) + len(fused))) as ex:
+        objs = list(ex.map(lambda s: _compile(s, extra), srcs + fused))
+    _link(objs[:len(srcs)], LIB_PATH)
+    _link(objs[len(srcs):], FUSED_LIB_PATH)
     return LIB_PATH
 
 

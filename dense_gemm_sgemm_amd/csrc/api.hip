@@ -14,6 +14,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "device.hpp"
 #include "internal.h"
 
 using namespace mi355gemm;
@@ -36,31 +37,6 @@ bool force_general() {
 
 // Size of the static scratch area behind gemm_f16_nt_splitk_static.
 constexpr size_t kStaticScratchBytes = GEMM_STATIC_SCRATCH_BYTES;
-
-// Per-device verdict of the gfx950 check: 0 unknown, -1 not supported, else
-// the device's compute-unit count.
-constexpr int kMaxDevices = 64;
-std::atomic<int> g_device_state[kMaxDevices];
-
-// Returns the current device's CU count, or GEMM_ERR_UNSUPPORTED_DEVICE.
-int check_device() {
-  int dev = -1;
-  if (hipGetDevice(&dev) != hipSuccess || dev < 0) return GEMM_ERR_UNSUPPORTED_DEVICE;
-  if (dev >= kMaxDevices) return GEMM_ERR_UNSUPPORTED_DEVICE;
-  int s = g_device_state[dev].load(std::memory_order_acquire);
-  if (s == 0) {
-    hipDeviceProp_t prop;
-    const bool ok = hipGetDeviceProperties(&prop, dev) == hipSuccess &&
-                    std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 &&
-                    prop.multiProcessorCount > 0;
-    s = ok ? prop.multiProcessorCount : -1;
-    g_device_state[dev].store(s, std::memory_order_release);
-  }
-  return s > 0 ? s : GEMM_ERR_UNSUPPORTED_DEVICE;
-}
-
-int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Stands for the address of a workspace copy in the path choice.
 const void* const kCopyAddress = reinterpret_cast<const void*>(uintptr_t(256));
@@ -206,15 +182,6 @@ Plan16 plan16(int type, int op_a, int op_b, int M, int N, int K, const void* A, 
   if (large_product(M, N, K) && f16_staged_fits(M, N, K, pl.lda, pl.ldb))
     return done(GEMM_PATH_F16_STAGED);
   return done(GEMM_PATH_F16_GENERAL);
-}
-
-int to_status(hipError_t e) { return e == hipSuccess ? GEMM_OK : GEMM_ERR_LAUNCH; }
-
-// A caller's workspace: 16-byte aligned and at least `need` bytes (or not
-// needed at all).
-bool workspace_ok(size_t need, const void* ws, unsigned long long bytes) {
-  return need == 0 ||
-         (ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 15u) == 0 && bytes >= need);
 }
 
 // Runs a validated 16-bit plan.  a holds the caller's operands (in their

@@ -1,0 +1,94 @@
+// Declarations shared by the fused operators (libmi355fused.so).
+#pragma once
+
+#include <algorithm>
+
+#include "device.hpp"
+#include "hgemm_tile.hpp"
+#include "internal.h"
+#include "mi355fused.h"
+
+namespace mi355gemm {
+namespace fused {
+
+using hgemm::FusedExtra;
+
+// A 16-bit matrix as a caller gave it.
+struct Mat {
+  const half_t* p = nullptr;
+  int64_t ld = 0;
+};
+
+// The tile kernels read operands of at least kMinRows rows and kMinK columns
+// in whole 16-byte pieces.  What is not so is first copied, padded with
+// zeros, into the workspace.
+constexpr int kMinRows = 128, kMinK = 128;
+inline int pad_rows(int rows) { return rows < kMinRows ? kMinRows : rows; }
+inline int pad_k(int K) { return K < kMinK ? kMinK : (int)round_up(K, 8); }
+inline bool needs_copy(const void* p, int64_t ld, int rows, int K) {
+  return rows < kMinRows || K < kMinK || K % 8 != 0 || !aligned16(p) || ld % 8 != 0 ||
+         ld >= (int64_t(1) << 28);
+}
+inline size_t copy_bytes(int rows, int K) {
+  return round256((size_t)pad_rows(rows) * pad_k(K) * 2);
+}
+
+// Up to three padded copies in one launch: dst[r][c] (ld a multiple of 8,
+// cols_p % 8 == 0) for r < rows_p, c < cols_p, zero outside the source.
+struct PadJob {
+  const half_t* src = nullptr;
+  half_t* dst = nullptr;
+  int64_t lds = 0, ldd = 0;
+  int rows = 0, cols = 0, rows_p = 0, cols_p = 0;
+};
+struct PadJobs {
+  PadJob job[3];
+  int64_t blocks[3] = {0, 0, 0};   // blocks up to and including each job's
+  int count = 0;
+  // Adds the copy of m ([rows][K]) to dst (add: if it needs one); returns the
+  // matrix the kernels read and advances dst past the copy.
+  Mat add(Mat m, int rows, int K, char*& dst);
+  Mat copy(Mat m, int rows, int K, char*& dst);
+};
+hipError_t launch_pad(const PadJobs& jobs, hipStream_t stream);
+
+// The tile-kernel launchers (tiles_*.hip); a.fmt selects the format.
+hipError_t launch_gated_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
+hipError_t launch_grad_w(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
+hipError_t launch_grad_x(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
+hipError_t launch_lse_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
+hipError_t launch_dlogit_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
+// Wave columns of the kLse tiles: partial results per row.
+int lse_chunks(int M, int N, int cus);
+
+// Cost model of hgemm_shapes.hpp for the ragged form over M x N outputs whose
+// tiles are (bm, bn, workgroups per CU, tile-time); returns the cheapest index.
+struct Shape {
+  int bm, bn, per_cu;
+  int64_t time, time_alone;   // alone: tiles do not outnumber the CUs
+};
+inline int choose_shape(const Shape* s, int n, int M, int N, int tiles_mul, int cus) {
+  int best = -1;
+  int64_t best_cost = 0;
+  for (int i = 0; i < n; ++i) {
+    if (M < s[i].bm || N < s[i].bn) continue;
+    const int64_t tiles = (int64_t)((M + s[i].bm - 1) / s[i].bm) * tiles_mul *
+                          ((N + s[i].bn - 1) / s[i].bn);
+    const int64_t slots = (int64_t)s[i].per_cu * cus;
+    const int64_t cost = (tiles + slots - 1) / slots * (tiles <= cus ? s[i].time_alone : s[i].time);
+    if (best < 0 || cost < best_cost) {
+      best = i;
+      best_cost = cost;
+    }
+  }
+  return best;
+}
+
+inline bool bad_type(int type) { return type != GEMM_TYPE_F16 && type != GEMM_TYPE_BF16; }
+inline bool bad_act(int act) {
+  return act != GEMM_ACT_NONE && act != GEMM_ACT_RELU && act != GEMM_ACT_SILU;
+}
+inline bool bad_ld(int ld, int64_t cols) { return ld < (cols > 1 ? cols : 1); }
+
+}  // namespace fused
+}  // namespace mi355gemm

@@ -1,0 +1,268 @@
+// The gated product H = act(X Wg^T) * (X Wu^T) and its gradients: C entry
+// points, and the elementwise kernel of the backward pass.
+#define MI355FUSED_BUILDING 1
+#include "fused.hpp"
+
+namespace mi355gemm {
+namespace fused {
+namespace {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+constexpr int kThreads = 256;
+
+// dG and dU as the products of the backward pass read them: rows of ld
+// elements, dG's Np columns, then dU's, zero in the columns past N and the
+// rows past M; and, for N % 64 != 0, the last 64 columns of each once more in
+// `tail` (128 to a row), zero where they lie in a slab of 64 before the last.
+struct GradArgs {
+  const half_t *G, *U, *dH;
+  half_t *d, *tail;
+  int64_t ldg, ldu, lddh, ld;
+  int M, N, Mp, Np, Nk, act;   // Nk: columns the products sum over (N, or 128 if less)
+};
+
+// Columns c .. c + 7 of a row of N at any 2-byte address, zero past it.
+__device__ __forceinline__ h8 load_cols(const half_t* row, int c, int N) {
+  h8 v = {};
+  if (c + 8 <= N) {
+    __builtin_memcpy(&v, row + c, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < N) v[e] = row[c + e];
+  }
+  return v;
+}
+
+// One thread makes 8 columns of dG and dU.  With s = 1 / (1 + e^-g): silu =
+// g s, its slope s (1 + g (1 - s)).  Bound by HBM: 6 bytes read and 4 written
+// an element.
+template <int FMT>
+__global__ __launch_bounds__(kThreads) void gated_grad_kernel(GradArgs p, int64_t base) {
+  const int main = p.Np / 8, chunks = main + (p.tail ? 8 : 0);
+  const int64_t t = (base + blockIdx.x) * kThreads + threadIdx.x;
+  if (t >= (int64_t)p.Mp * chunks) return;
+  const int64_t m = t / chunks;
+  const int q = (int)(t % chunks);
+  const bool is_tail = q >= main;
+  const int c = is_tail ? p.Nk - 64 + 8 * (q - main) : 8 * q;
+  const int first = is_tail ? (p.Nk - 1) / 64 * 64 : 0;   // first column that counts
+  h8 dg = {}, du = {};
+  if (m < p.M && c < p.N) {
+    const h8 g = load_cols(p.G + m * p.ldg, c, p.N);
+    const h8 u = load_cols(p.U + m * p.ldu, c, p.N);
+    const h8 dh = load_cols(p.dH + m * p.lddh, c, p.N);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float x = word_to_f32<FMT>(g[e]), y = word_to_f32<FMT>(dh[e]);
+      float a = x, slope = 1.f;
+      if (p.act == GEMM_ACT_SILU) {
+        const float s = __builtin_amdgcn_rcpf(1.f + __expf(-x));
+        a = x * s;
+        slope = s * (1.f + x * (1.f - s));
+      } else if (p.act == GEMM_ACT_RELU) {
+        a = epi_relu(x);
+        slope = x > 0.f ? 1.f : 0.f;
+      }
+      if (c + e >= first && c + e < p.N) {
+        dg[e] = f32_to_word<FMT>(y * word_to_f32<FMT>(u[e]) * slope);
+        du[e] = f32_to_word<FMT>(y * a);
+      }
+    }
+  }
+  if (is_tail) {
+    half_t* d = p.tail + m * 128 + 8 * (q - main);
+    *(h8*)d = dg;
+    *(h8*)(d + 64) = du;
+  } else {
+    half_t* d = p.d + m * p.ld + c;
+    *(h8*)d = dg;
+    *(h8*)(d + p.Np) = du;
+  }
+}
+
+int check(int type, int act, int M, int N, int K) {
+  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_NEGATIVE_DIM;
+  if (bad_type(type) || bad_act(act)) return GEMM_ERR_BAD_ARG;
+  return GEMM_OK;
+}
+
+const half_t* in16(const void* p) { return static_cast<const half_t*>(p); }
+half_t* out16(void* p) { return static_cast<half_t*>(p); }
+
+// The workspace of the backward pass: dG | dU, their tails, padded copies.
+struct BwdPlan {
+  int Mp, Np, Nk;
+  int64_t ld;
+  bool tail;
+  size_t bytes_d, bytes_tail, bytes_x = 0, bytes_g = 0, bytes_u = 0;
+  size_t total() const { return bytes_d + bytes_tail + bytes_x + bytes_g + bytes_u; }
+};
+BwdPlan plan_bwd(int M, int N, int K, Mat X, Mat Wg, Mat Wu, bool dx, bool dw) {
+  BwdPlan p;
+  p.Mp = pad_rows(M);
+  p.Nk = pad_rows(N);
+  p.Np = (int)round_up(p.Nk, 8);
+  p.ld = 2 * (int64_t)p.Np;
+  p.tail = dx && p.Nk % 64 != 0;
+  p.bytes_d = round256((size_t)p.Mp * p.ld * 2);
+  p.bytes_tail = p.tail ? (size_t)p.Mp * 256 : 0;
+  if (dw && needs_copy(X.p, X.ld, M, K)) p.bytes_x = copy_bytes(M, K);
+  // W as a K-major operand of dX: both at one leading dimension
+  const bool copy = needs_copy(Wg.p, Wg.ld, N, K) || needs_copy(Wu.p, Wu.ld, N, K) ||
+                    Wg.ld != Wu.ld;
+  if (dx && copy) p.bytes_g = p.bytes_u = copy_bytes(N, K);
+  return p;
+}
+
+}  // namespace
+}  // namespace fused
+}  // namespace mi355gemm
+
+using namespace mi355gemm;
+using namespace mi355gemm::fused;
+
+extern "C" {
+
+MI355FUSED_API unsigned long long gemm_gated_workspace(int type, int M, int N, int K,
+                                                       const void* X, int ldx, const void* Wg,
+                                                       int ldwg, const void* Wu, int ldwu) {
+  if (check(type, 0, M, N, K) != GEMM_OK || M == 0 || N == 0 || bad_ld(ldx, K) ||
+      bad_ld(ldwg, K) || bad_ld(ldwu, K))
+    return 0;
+  return (needs_copy(X, ldx, M, K) ? copy_bytes(M, K) : 0) +
+         (needs_copy(Wg, ldwg, N, K) ? copy_bytes(N, K) : 0) +
+         (needs_copy(Wu, ldwu, N, K) ? copy_bytes(N, K) : 0);
+}
+
+MI355FUSED_API int gemm_gated(int type, int act, int M, int N, int K, const void* X, int ldx,
+                              const void* Wg, int ldwg, const void* Wu, int ldwu, void* H, int ldh,
+                              void* G, int ldg, void* U, int ldu, void* workspace,
+                              unsigned long long workspace_bytes, void* stream) {
+  const int status = check(type, act, M, N, K);
+  if (status != GEMM_OK) return status;
+  if (M == 0 || N == 0) return GEMM_OK;
+  if (bad_ld(ldx, K) || bad_ld(ldwg, K) || bad_ld(ldwu, K) || bad_ld(ldh, N) ||
+      (G && bad_ld(ldg, N)) || (U && bad_ld(ldu, N)))
+    return GEMM_ERR_BAD_LD;
+  if (H == nullptr || (K > 0 && (X == nullptr || Wg == nullptr || Wu == nullptr)))
+    return GEMM_ERR_NULL_POINTER;
+  const size_t need = gemm_gated_workspace(type, M, N, K, X, ldx, Wg, ldwg, Wu, ldwu);
+  if (!workspace_ok(need, workspace, workspace_bytes)) return GEMM_ERR_WORKSPACE;
+  const int cus = check_device();
+  if (cus < 0) return cus;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  PadJobs jobs;
+  char* ws = static_cast<char*>(workspace);
+  const Mat x = jobs.add(Mat{in16(X), ldx}, M, K, ws);
+  const Mat g = jobs.add(Mat{in16(Wg), ldwg}, N, K, ws);
+  const Mat u = jobs.add(Mat{in16(Wu), ldwu}, N, K, ws);
+  const hipError_t e = launch_pad(jobs, s);
+  if (e != hipSuccess) return to_status(e);
+  Args16 a{x.p, g.p, out16(H), x.ld, g.ld, ldh, pad_rows(M), pad_rows(N), pad_k(K)};
+  a.act = act;
+  a.fmt = type == GEMM_TYPE_BF16 ? kFmtBF16 : kFmtF16;
+  FusedExtra f;
+  f.m_end = M;
+  f.n_end = N;
+  f.B2 = u.p;
+  f.ldb2 = u.ld;
+  f.C2 = out16(G);
+  f.ldc2 = ldg;
+  f.C3 = out16(U);
+  f.ldc3 = ldu;
+  return to_status(launch_gated_tiles(a, f, cus, s));
+}
+
+MI355FUSED_API unsigned long long gemm_gated_bwd_workspace(int type, int M, int N, int K,
+                                                           const void* X, int ldx, const void* Wg,
+                                                           int ldwg, const void* Wu, int ldwu,
+                                                           int want_dx, int want_dw) {
+  if (check(type, 0, M, N, K) != GEMM_OK || K == 0) return 0;
+  const bool dx = want_dx && M > 0, dw = want_dw && N > 0;
+  if (!dx && !dw) return 0;
+  if ((dw && bad_ld(ldx, K)) || (dx && (bad_ld(ldwg, K) || bad_ld(ldwu, K)))) return 0;
+  return plan_bwd(M, N, K, Mat{in16(X), ldx}, Mat{in16(Wg), ldwg}, Mat{in16(Wu), ldwu}, dx, dw)
+      .total();
+}
+
+MI355FUSED_API int gemm_gated_bwd(int type, int act, int M, int N, int K, const void* X, int ldx,
+                                  const void* Wg, int ldwg, const void* Wu, int ldwu,
+                                  const void* G, int ldg, const void* U, int ldu, const void* dH,
+                                  int lddh, void* dX, int lddx, void* dWg, int lddwg, void* dWu,
+                                  int lddwu, void* workspace, unsigned long long workspace_bytes,
+                                  void* stream) {
+  const int status = check(type, act, M, N, K);
+  if (status != GEMM_OK) return status;
+  const bool dx = dX != nullptr && M > 0 && K > 0;
+  const bool dw = (dWg != nullptr || dWu != nullptr) && N > 0 && K > 0;
+  if (!dx && !dw) return GEMM_OK;
+  if ((dw && bad_ld(ldx, K)) || (dx && (bad_ld(ldwg, K) || bad_ld(ldwu, K) || bad_ld(lddx, K))) ||
+      bad_ld(ldg, N) || bad_ld(ldu, N) || bad_ld(lddh, N) || (dw && dWg && bad_ld(lddwg, K)) ||
+      (dw && dWu && bad_ld(lddwu, K)))
+    return GEMM_ERR_BAD_LD;
+  if (M > 0 && N > 0 &&
+      (G == nullptr || U == nullptr || dH == nullptr || (dw && X == nullptr) ||
+       (dx && (Wg == nullptr || Wu == nullptr))))
+    return GEMM_ERR_NULL_POINTER;
+  const BwdPlan p =
+      plan_bwd(M, N, K, Mat{in16(X), ldx}, Mat{in16(Wg), ldwg}, Mat{in16(Wu), ldwu}, dx, dw);
+  if (!workspace_ok(p.total(), workspace, workspace_bytes)) return GEMM_ERR_WORKSPACE;
+  const int cus = check_device();
+  if (cus < 0) return cus;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int fmt = type == GEMM_TYPE_BF16 ? kFmtBF16 : kFmtF16;
+  char* ws = static_cast<char*>(workspace);
+  half_t* d = reinterpret_cast<half_t*>(ws);
+  half_t* tail = p.tail ? reinterpret_cast<half_t*>(ws + p.bytes_d) : nullptr;
+  ws += p.bytes_d + p.bytes_tail;
+
+  const GradArgs ga{in16(G), in16(U), in16(dH), d,    tail, ldg,  ldu, lddh,
+                    p.ld,    M,       N,        p.Mp, p.Np, p.Nk, act};
+  const int64_t pieces = (int64_t)p.Mp * (p.Np / 8 + (p.tail ? 8 : 0));
+  hipError_t e = launch_tiles(fmt == kFmtBF16 ? (const void*)gated_grad_kernel<kFmtBF16>
+                                              : (const void*)gated_grad_kernel<kFmtF16>,
+                              ga, (pieces + kThreads - 1) / kThreads, kThreads, 0, s);
+  if (e != hipSuccess) return to_status(e);
+  PadJobs jobs;
+  Mat x{in16(X), ldx}, wg{in16(Wg), ldwg}, wu{in16(Wu), ldwu};
+  if (p.bytes_x) x = jobs.add(x, M, K, ws);
+  if (p.bytes_g) {
+    wg = jobs.copy(wg, N, K, ws);
+    wu = jobs.copy(wu, N, K, ws);
+  }
+  e = launch_pad(jobs, s);
+  if (e != hipSuccess) return to_status(e);
+  if (dx) {
+    Args16 a{d, wg.p, out16(dX), p.ld, wg.ld, lddx, p.Mp, pad_k(K), p.Nk};
+    a.fmt = fmt;
+    FusedExtra f;
+    f.m_end = M;
+    f.n_end = K;
+    f.parts = 2;
+    f.partA = p.Np;
+    f.B2 = wu.p;
+    f.tail = tail;
+    f.ldt = 128;
+    e = launch_grad_x(a, f, cus, s);
+    if (e != hipSuccess) return to_status(e);
+  }
+  if (dw) {
+    // both gradients as two parts of one product's rows, or the one asked for
+    const bool both = dWg != nullptr && dWu != nullptr;
+    Args16 a{dWg ? d : d + p.Np, x.p, out16(dWg ? dWg : dWu), p.ld, x.ld, dWg ? lddwg : lddwu,
+             p.Np, pad_k(K), p.Mp};
+    a.fmt = fmt;
+    FusedExtra f;
+    f.m_end = N;
+    f.n_end = K;
+    f.parts = both ? 2 : 1;
+    f.partA = p.Np;
+    f.C2 = out16(dWu);
+    f.ldc2 = lddwu;
+    e = launch_grad_w(a, f, cus, s);
+  }
+  return to_status(e);
+}
+
+}  // extern "C"

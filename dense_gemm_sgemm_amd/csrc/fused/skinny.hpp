@@ -1,0 +1,57 @@
+// What the kernels for few rows of X share (decode steps: M <= 64 rows a
+// workgroup, the weights streamed from HBM once).
+//
+// A workgroup owns 16 weight rows (outputs n) and all of K, which its waves
+// share out; no LDS and no barrier until the sums of the waves are added at
+// the end.  A wave multiplies with v_mfma_f32_16x16x32: X rows are the first
+// operand (lane l: row l % 16, k = 8 (l / 16) .. + 7 of a step's 32), weight
+// rows the second (lane l: row n0 + l % 16, the same k), so a lane's four
+// accumulators are rows 4 (l / 16) .. + 3 of X against its one weight row.
+// Any one-to-one choice of the 32 k of a step does, as long as both operands
+// make the same.  MT = 1, 2 or 4 blocks of 16 X rows.
+#pragma once
+
+#include "fused.hpp"
+
+namespace mi355gemm {
+namespace fused {
+namespace skinny {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef float f4 __attribute__((ext_vector_type(4)));
+using hgemm::mfma16;
+
+// k .. k + 7 of an X row (TAIL: zeros past K).  Rows start at any 2-byte
+// address.
+template <bool TAIL>
+__device__ __forceinline__ h8 load_x(const half_t* row, int k, int K) {
+  h8 v = {};
+  if (!TAIL || k <= K - 8) {
+    __builtin_memcpy(&v, row + k, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k < K - e) v[e] = row[k + e];
+  }
+  return v;
+}
+
+// Adds the waves' sums (Q f4 of each lane) in the order of the waves; the
+// result is complete in wave 0.
+template <int Q>
+__device__ __forceinline__ void add_waves(f4 (&acc)[Q], float* lds, int wave, int lane, int waves) {
+  f4* part = reinterpret_cast<f4*>(lds);
+  if (wave > 0) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) part[((wave - 1) * Q + q) * 64 + lane] = acc[q];
+  }
+  __syncthreads();
+  if (wave > 0) return;
+  for (int w = 0; w + 1 < waves; ++w)
+#pragma unroll
+    for (int q = 0; q < Q; ++q) acc[q] += part[(w * Q + q) * 64 + lane];
+}
+
+}  // namespace skinny
+}  // namespace fused
+}  // namespace mi355gemm

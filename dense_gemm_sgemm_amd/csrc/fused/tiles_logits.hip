@@ -1,0 +1,45 @@
+// Tile-kernel instances that turn logits X * W^T into softmax statistics
+// (TileMode kLse) or their gradients (kDlogit) while they are in registers.
+#include "fused.hpp"
+#include "hgemm_shapes.hpp"
+
+namespace mi355gemm {
+namespace fused {
+
+using namespace hshape;
+
+static constexpr Shape kShapes[] = {
+    {256, 256, 1, 256 * 256, 256 * 256},
+    {128, 128, 2, 2 * 128 * 128 * 6 / 5, 128 * 128 * 8 / 5},
+};
+
+template <int FMT, int MODE>
+static hipError_t launch_fmt(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream) {
+  switch (choose_shape(kShapes, 2, a.M, a.N, 1, cus)) {
+    case 0:
+      return hgemm::launch_fused<256, 256, BK, 4, 2, GM, 1, 2, FMT, 0, MODE>(a, x, cus, stream);
+    case 1:
+      return hgemm::launch_fused<128, 128, BK, 2, 2, GM, 0, 0, FMT, 0, MODE>(a, x, 2 * cus, stream);
+    default:
+      return hipErrorInvalidValue;
+  }
+}
+
+hipError_t launch_lse_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream) {
+  return a.fmt == kFmtBF16 ? launch_fmt<kFmtBF16, hgemm::kLse>(a, x, cus, stream)
+                           : launch_fmt<kFmtF16, hgemm::kLse>(a, x, cus, stream);
+}
+
+// Both shapes have two wave columns.
+int lse_chunks(int M, int N, int cus) {
+  const int i = choose_shape(kShapes, 2, M, N, 1, cus);
+  return i < 0 ? 0 : (N + kShapes[i].bn - 1) / kShapes[i].bn * 2;
+}
+
+hipError_t launch_dlogit_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream) {
+  return a.fmt == kFmtBF16 ? launch_fmt<kFmtBF16, hgemm::kDlogit>(a, x, cus, stream)
+                           : launch_fmt<kFmtF16, hgemm::kDlogit>(a, x, cus, stream);
+}
+
+}  // namespace fused
+}  // namespace mi355gemm

@@ -1,0 +1,331 @@
+// Softmax cross entropy of X * W^T without storing the logits, and its
+// gradients: C entry points, the join of the tiles' softmax statistics, and
+// the common factor of fp16 gradients.
+#define MI355FUSED_BUILDING 1
+#include "fused.hpp"
+
+namespace mi355gemm {
+namespace fused {
+namespace {
+
+// ---- The join.  The kLse tiles leave, for each row, a maximum t_c and a sum
+// of exp(z - t_c) for each chunk c of the columns.  With t = max t_c:
+// lse = t + log(sum_c s_c exp(t_c - t)).  A workgroup of 16 waves takes 64
+// rows (a lane a row, coalesced over the rows), the waves sharing the chunks.
+constexpr int kJoinWaves = 16;
+
+struct JoinArgs {
+  const float2* partial;
+  const float* target_logit;
+  const long long* targets;
+  long long ignore, vocab;
+  float *loss, *lse;
+  int64_t ld;
+  int M, chunks;
+};
+
+__device__ __forceinline__ void join(float& t, float& s, float t2, float s2) {
+  const float top = fmaxf(t, t2);
+  const float base = top == -__builtin_inff() ? 0.f : top;
+  s = s * __expf(t - base) + s2 * __expf(t2 - base);
+  t = top;
+}
+
+__global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(JoinArgs p, int64_t base) {
+  __shared__ float2 part[kJoinWaves][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t m = (base + blockIdx.x) * 64 + lane;
+  float t = -__builtin_inff(), s = 0.f;
+  if (m < p.M) {
+    constexpr int U = 8;   // chunks in flight
+    for (int c = wave; c < p.chunks; c += U * kJoinWaves) {
+      float2 v[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int cu = c + u * kJoinWaves;
+        v[u] = cu < p.chunks ? p.partial[cu * p.ld + m] : make_float2(-__builtin_inff(), 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) join(t, s, v[u].x, v[u].y);
+    }
+  }
+  part[wave][lane] = make_float2(t, s);
+  __syncthreads();
+  if (wave != 0 || m >= p.M) return;
+  for (int w = 1; w < kJoinWaves; ++w) join(t, s, part[w][lane].x, part[w][lane].y);
+  const float lse = t + __logf(s);
+  const long long y = p.targets[m];
+  float loss = 0.f;
+  if (y != p.ignore)
+    loss = y >= 0 && y < p.vocab ? lse - p.target_logit[m] : __builtin_nanf("");
+  p.lse[m] = lse;
+  p.loss[m] = loss;
+}
+
+// ---- fp16 gradients: {f, 1 / f} with f the power of two that brings the
+// largest |dloss| of the rows that count into [2^13, 2^14), so that
+// d = (p - [target]) dloss f keeps probabilities down to 2^-37 (binary16's
+// smallest step is 2^-24) and never overflows (|p - 1| <= 1).  1 where that
+// maximum is 0 or not finite.
+struct ScaleArgs {
+  const float* dloss;
+  const long long* targets;
+  long long ignore;
+  float* scale;
+  int M;
+};
+
+__global__ __launch_bounds__(1024) void scale_kernel(ScaleArgs p, int64_t) {
+  __shared__ float part[16];
+  float top = 0.f;
+  for (int m = threadIdx.x; m < p.M; m += 1024) {
+    const float v = fabsf(p.dloss[m]);
+    if (p.targets[m] != p.ignore) top = fmaxf(top, v);
+  }
+#pragma unroll
+  for (int k = 32; k >= 1; k /= 2) top = fmaxf(top, __shfl_xor(top, k));
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 16; ++w) top = fmaxf(top, part[w]);
+  float f = 1.f, r = 1.f;
+  if (top > 0.f && top < __builtin_inff()) {
+    int e;
+    (void)frexpf(top, &e);   // top in [2^(e-1), 2^e)
+    e = 14 - e;
+    e = e > 100 ? 100 : e < -100 ? -100 : e;
+    f = ldexpf(1.f, e);
+    r = ldexpf(1.f, -e);
+  }
+  p.scale[0] = f;
+  p.scale[1] = r;
+}
+
+int check(int type, int M, int N, int K) {
+  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_NEGATIVE_DIM;
+  if (bad_type(type) || (N == 0 && M > 0)) return GEMM_ERR_BAD_ARG;
+  return GEMM_OK;
+}
+
+const half_t* in16(const void* p) { return static_cast<const half_t*>(p); }
+half_t* out16(void* p) { return static_cast<half_t*>(p); }
+
+// The partial statistics of the forward pass are sized for the narrowest
+// tiles (64 columns a wave).
+size_t chunk_bound(int N) { return (size_t)((pad_rows(N) + 127) / 128) * 2; }
+
+// ---- Pieces of the columns.  A piece's d ([rows][width], 16-bit) takes about
+// kPieceBytes at most, so that it is written and read twice mostly out of the
+// last-level cache; pieces are at least 2048 wide, which keeps the products'
+// K deep, and a multiple of 256.  The last one starts early enough to be 128
+// wide; its columns that the one before has had are zero in d.
+constexpr size_t kPieceBytes = size_t(256) << 20;
+constexpr int kMinPiece = 2048;
+
+struct BwdPlan {
+  int Mp, Np, Kp;
+  int width, pieces;      // every piece but the last is `width` columns
+  int64_t ldd;            // leading dimension of a piece's d
+  size_t bytes_d, bytes_tail, bytes_sum, bytes_scale, bytes_x = 0, bytes_w = 0;
+  size_t total() const {
+    return bytes_d + bytes_tail + bytes_sum + bytes_scale + bytes_x + bytes_w;
+  }
+};
+BwdPlan plan_bwd(int M, int N, int K, Mat X, Mat W, bool dx) {
+  BwdPlan p;
+  p.Mp = pad_rows(M);
+  p.Np = pad_rows(N);
+  p.Kp = pad_k(K);
+  const int64_t most = std::max<int64_t>(kMinPiece, kPieceBytes / ((size_t)p.Mp * 2) / 256 * 256);
+  const int64_t n = (p.Np + most - 1) / most;
+  p.width = (int)std::min<int64_t>(round_up((p.Np + n - 1) / n, 256), p.Np);
+  p.pieces = (p.Np + p.width - 1) / p.width;
+  p.ldd = round_up(std::max(p.width, 128), 64);
+  p.bytes_d = round256((size_t)p.Mp * p.ldd * 2);
+  p.bytes_tail = dx ? (size_t)p.Mp * 128 : 0;
+  p.bytes_sum = dx && p.pieces > 1 ? round256((size_t)p.Mp * p.Kp * 4) : 0;
+  p.bytes_scale = 256;
+  if (needs_copy(X.p, X.ld, M, K)) p.bytes_x = copy_bytes(M, K);
+  if (needs_copy(W.p, W.ld, N, K)) p.bytes_w = copy_bytes(N, K);
+  return p;
+}
+
+}  // namespace
+}  // namespace fused
+}  // namespace mi355gemm
+
+using namespace mi355gemm;
+using namespace mi355gemm::fused;
+
+extern "C" {
+
+MI355FUSED_API unsigned long long gemm_xent_workspace(int type, int M, int N, int K, const void* X,
+                                                      int ldx, const void* W, int ldw) {
+  if (check(type, M, N, K) != GEMM_OK || M == 0 || bad_ld(ldx, K) || bad_ld(ldw, K)) return 0;
+  return round256(chunk_bound(N) * M * sizeof(float2)) + round256((size_t)M * sizeof(float)) +
+         (needs_copy(X, ldx, M, K) ? copy_bytes(M, K) : 0) +
+         (needs_copy(W, ldw, N, K) ? copy_bytes(N, K) : 0);
+}
+
+MI355FUSED_API int gemm_xent(int type, int M, int N, int K, const void* X, int ldx, const void* W,
+                             int ldw, const long long* targets, long long ignore, float* loss,
+                             float* lse, void* workspace, unsigned long long workspace_bytes,
+                             void* stream) {
+  const int status = check(type, M, N, K);
+  if (status != GEMM_OK) return status;
+  if (M == 0) return GEMM_OK;
+  if (bad_ld(ldx, K) || bad_ld(ldw, K)) return GEMM_ERR_BAD_LD;
+  if (targets == nullptr || loss == nullptr || lse == nullptr ||
+      (K > 0 && (X == nullptr || W == nullptr)))
+    return GEMM_ERR_NULL_POINTER;
+  const size_t need = gemm_xent_workspace(type, M, N, K, X, ldx, W, ldw);
+  if (!workspace_ok(need, workspace, workspace_bytes)) return GEMM_ERR_WORKSPACE;
+  const int cus = check_device();
+  if (cus < 0) return cus;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  float2* partial = reinterpret_cast<float2*>(ws);
+  ws += round256(chunk_bound(N) * M * sizeof(float2));
+  float* target_logit = reinterpret_cast<float*>(ws);
+  ws += round256((size_t)M * sizeof(float));
+  PadJobs jobs;
+  const Mat x = jobs.add(Mat{in16(X), ldx}, M, K, ws);
+  const Mat w = jobs.add(Mat{in16(W), ldw}, N, K, ws);
+  hipError_t e = launch_pad(jobs, s);
+  if (e != hipSuccess) return to_status(e);
+  Args16 a{x.p, w.p, nullptr, x.ld, w.ld, 0, pad_rows(M), pad_rows(N), pad_k(K)};
+  a.fmt = type == GEMM_TYPE_BF16 ? kFmtBF16 : kFmtF16;
+  FusedExtra f;
+  f.m_end = M;
+  f.n_end = N;
+  f.targets = targets;
+  f.ignore = ignore;
+  f.target_logit = target_logit;
+  f.partial = partial;
+  f.ld_partial = M;
+  e = launch_lse_tiles(a, f, cus, s);
+  if (e != hipSuccess) return to_status(e);
+  const JoinArgs j{partial, target_logit, targets, ignore, N, loss, lse, M, M,
+                   lse_chunks(a.M, a.N, cus)};
+  return to_status(launch_tiles((const void*)join_kernel, j, ((int64_t)M + 63) / 64,
+                                64 * kJoinWaves, 0, s));
+}
+
+MI355FUSED_API unsigned long long gemm_xent_bwd_workspace(int type, int M, int N, int K,
+                                                          const void* X, int ldx, const void* W,
+                                                          int ldw, int want_dx, int want_dw) {
+  if (check(type, M, N, K) != GEMM_OK || K == 0 || N == 0 || bad_ld(ldx, K) || bad_ld(ldw, K))
+    return 0;
+  const bool dx = want_dx && M > 0;
+  if (!dx && !want_dw) return 0;
+  return plan_bwd(M, N, K, Mat{in16(X), ldx}, Mat{in16(W), ldw}, dx).total();
+}
+
+MI355FUSED_API int gemm_xent_bwd(int type, int M, int N, int K, const void* X, int ldx,
+                                 const void* W, int ldw, const long long* targets,
+                                 long long ignore, const float* lse, const float* dloss, void* dX,
+                                 int lddx, void* dW, int lddw, void* workspace,
+                                 unsigned long long workspace_bytes, void* stream) {
+  const int status = check(type, M, N, K);
+  if (status != GEMM_OK) return status;
+  const bool dx = dX != nullptr && M > 0 && K > 0;
+  const bool dw = dW != nullptr && N > 0 && K > 0;
+  if (!dx && !dw) return GEMM_OK;
+  if (bad_ld(ldx, K) || bad_ld(ldw, K) || (dx && bad_ld(lddx, K)) || (dw && bad_ld(lddw, K)))
+    return GEMM_ERR_BAD_LD;
+  if (M > 0 && (X == nullptr || W == nullptr || targets == nullptr || lse == nullptr ||
+                dloss == nullptr))
+    return GEMM_ERR_NULL_POINTER;
+  const BwdPlan p = plan_bwd(M, N, K, Mat{in16(X), ldx}, Mat{in16(W), ldw}, dx);
+  if (!workspace_ok(p.total(), workspace, workspace_bytes)) return GEMM_ERR_WORKSPACE;
+  const int cus = check_device();
+  if (cus < 0) return cus;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int fmt = type == GEMM_TYPE_BF16 ? kFmtBF16 : kFmtF16;
+  char* ws = static_cast<char*>(workspace);
+  half_t* d = reinterpret_cast<half_t*>(ws);
+  ws += p.bytes_d;
+  half_t* tail = reinterpret_cast<half_t*>(ws);
+  ws += p.bytes_tail;
+  float* sum = reinterpret_cast<float*>(ws);
+  ws += p.bytes_sum;
+  float* scale = reinterpret_cast<float*>(ws);
+  ws += p.bytes_scale;
+  PadJobs jobs;
+  Mat x{in16(X), ldx}, w{in16(W), ldw};
+  if (p.bytes_x) x = jobs.copy(x, M, K, ws);
+  if (p.bytes_w) w = jobs.copy(w, N, K, ws);
+  hipError_t e = launch_pad(jobs, s);
+  if (e != hipSuccess) return to_status(e);
+  if (fmt == kFmtF16) {
+    const ScaleArgs sa{dloss, targets, ignore, scale, M};
+    e = launch_tiles((const void*)scale_kernel, sa, 1, 1024, 0, s);
+    if (e != hipSuccess) return to_status(e);
+  } else {
+    scale = nullptr;   // bf16 has fp32's range
+  }
+  if (M == 0) {   // no rows: d is zero (Mp = 128 rows)
+    PadJobs zero;
+    char* at = reinterpret_cast<char*>(d);
+    zero.copy(Mat{}, 0, (int)p.ldd, at);
+    e = launch_pad(zero, s);
+    if (e != hipSuccess) return to_status(e);
+  }
+  for (int i = 0; i < p.pieces; ++i) {
+    const bool last = i + 1 == p.pieces;
+    const int owned = i * p.width;   // first column that this piece stores
+    const int end = last ? p.Np : owned + p.width;
+    const int begin = std::min(owned, end - 128);
+    const int width = end - begin;
+    const half_t* wp = w.p + (int64_t)begin * w.ld;
+    // d of the piece
+    Args16 a{x.p, wp, d, x.ld, w.ld, p.ldd, p.Mp, width, p.Kp};
+    a.fmt = fmt;
+    FusedExtra f;
+    f.m_end = M;
+    f.n_begin = owned - begin;
+    f.n_end = N - begin;
+    f.targets = targets;
+    f.ignore = ignore;
+    f.vocab = N;
+    f.col0 = begin;
+    f.lse = lse;
+    f.row_scale = dloss;
+    f.scale = scale;
+    f.tail = dx && width % 64 != 0 ? tail : nullptr;
+    f.ldt = 64;
+    if (M > 0) e = launch_dlogit_tiles(a, f, cus, s);
+    if (e != hipSuccess) return to_status(e);
+    if (dw) {
+      Args16 b{d, x.p, out16(dW) + (int64_t)begin * lddw, p.ldd, x.ld, lddw,
+               (int)round_up(width, 8), p.Kp, p.Mp};
+      b.fmt = fmt;
+      FusedExtra g;
+      g.m_begin = owned - begin;
+      g.m_end = N - begin < width ? N - begin : width;
+      g.n_end = K;
+      g.scale = scale;
+      e = launch_grad_w(b, g, cus, s);
+      if (e != hipSuccess) return to_status(e);
+    }
+    if (dx) {
+      Args16 b{d, wp, out16(dX), p.ldd, w.ld, lddx, p.Mp, p.Kp, width};
+      b.fmt = fmt;
+      FusedExtra g;
+      g.m_end = M;
+      g.n_end = K;
+      g.tail = f.tail;
+      g.ldt = 64;
+      g.scale = scale;
+      g.sum = sum;
+      g.ld_sum = p.Kp;
+      g.sum_read = i > 0;
+      g.sum_write = !last;
+      e = launch_grad_x(b, g, cus, s);
+      if (e != hipSuccess) return to_status(e);
+    }
+  }
+  return GEMM_OK;
+}
+
+}  // extern "C"

@@ -165,6 +165,64 @@ struct TileArgs {
   int64_t tiles;
 };
 
+// What a tile's accumulators become (the kernel's MODE).  kProduct stores C;
+// the others are the operators built on the product (fused/), always on the
+// ragged form (RAG):
+//   kGated    B's tile rows come in blocks of 16 from two matrices in turn,
+//             p.B and x.B2 (the same rows of each), so that a wave holds both
+//             products of an output in neighbouring accumulators; stores
+//             act(first) * second (and, if asked, both products).
+//   kLse      no C: each wave's row maxima and sums of exponentials over its
+//             columns, and the logit of each row's target column.
+//   kDlogit   C = (exp(acc - lse) - [column is the target]) * scale of the row.
+//   kGradW    (both operands K-major) C = acc * factor; the tile rows may come
+//             in two parts of p.M rows each: A's columns m and x.partA + m,
+//             outputs p.C and x.C2.
+//   kGradX    (B K-major) C = acc * factor, or, over several launches, sums in
+//             fp32 in x.sum first; K may come in two parts of p.K each: A's
+//             columns k and x.partA + k against the rows of p.B and x.B2.
+enum TileMode { kProduct = 0, kGated, kLse, kDlogit, kGradW, kGradX };
+
+// What these modes need beside the product's arguments.  Operands may be
+// padded past the operator's own sizes: results count for rows m < m_end and
+// columns n < n_end, and the part before m_begin (kGradW) or n_begin
+// (kDlogit) belongs to another launch.
+struct FusedExtra {
+  int m_begin = 0, m_end = 0, n_begin = 0, n_end = 0;
+  int parts = 1;                   // kGradW: parts of the tile rows; kGradX: parts of K
+  int64_t partA = 0;               // columns of A between the two parts
+  const half_t* B2 = nullptr;      // kGated, kGradX: the second matrix
+  int64_t ldb2 = 0;                //   (kGradX: rows as far apart as B's)
+  half_t* C2 = nullptr;            // kGated: first product (or null); kGradW: second part
+  half_t* C3 = nullptr;            // kGated: second product (or null)
+  int64_t ldc2 = 0, ldc3 = 0;
+  // The last 64 values of K where p.K % 64 != 0, [rows][ldt], 64 columns a
+  // part, zero where they repeat the slab before: A's last slab of kGradX,
+  // written by kDlogit (its columns are that K).
+  half_t* tail = nullptr;
+  int64_t ldt = 0;
+  const long long* targets = nullptr;   // [rows]
+  long long ignore = 0, vocab = 0;      // rows to leave out; targets lie in [0, vocab)
+  long long col0 = 0;                   // column n stands for target col0 + n
+  float* target_logit = nullptr;        // kLse, [rows]
+  float2* partial = nullptr;            // kLse, [tile column, wave column][ld_partial]
+  int64_t ld_partial = 0;
+  const float* lse = nullptr;           // kDlogit, [rows]
+  const float* row_scale = nullptr;     // kDlogit, [rows]
+  const float* scale = nullptr;         // {factor, 1 / factor}, or null for 1: kDlogit
+                                        //   multiplies by the first, gradients by the second
+  float* sum = nullptr;                 // kGradX: fp32 sums over launches, [rows][ld_sum]
+  int64_t ld_sum = 0;
+  int sum_read = 0, sum_write = 0;      // add what x.sum holds; store to x.sum instead of C
+};
+struct FusedTileArgs {
+  Args16 p;
+  int64_t tiles;
+  FusedExtra x;
+};
+template <int MODE>
+using TileArgsOf = std::conditional_t<MODE == kProduct, TileArgs, FusedTileArgs>;
+
 // Waves of the kernel that share each SIMD: 8-wave workgroups put two on
 // each; 4-wave 128 x 128 tiles run two workgroups per CU (the launcher's
 // slot count), so their register budget must leave room for the second.
@@ -211,10 +269,17 @@ __device__ __forceinline__ void static_for(F&& f) {
 // from K - 64 when K % 64 != 0 (K > 64; K % 8 == 0 if an operand is
 // K-contiguous) and has its repeated positions zeroed.
 template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int GM, int COPY_SEL, int OPT, bool EPI,
-          int FMT, bool SPLIT = false, bool RAG = false, int LAY = 0>
+          int FMT, bool SPLIT = false, bool RAG = false, int LAY = 0, int MODE = kProduct>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, waves_per_simd(BM, BN, WAVES_M * WAVES_N))
-void hgemm_nt_kernel(TileArgs ta) {
+void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   static_assert(!(RAG && SPLIT), "ragged tiles store C");
+  static_assert(MODE == kProduct || (RAG && !EPI), "operators on the ragged form");
+  static_assert(MODE != kGated || (LAY == 0 && (BN / WAVES_N) % 32 == 0),
+                "pairs of B blocks inside a wave");
+  static_assert((MODE != kLse && MODE != kDlogit) || LAY == 0, "logits from A * B^T");
+  static_assert((MODE != kGradW || LAY == 3) && (MODE != kGradX || LAY == 1),
+                "gradients from K-major operands");
+  constexpr int kTileN = MODE == kGated ? BN / 2 : BN;   // output columns of a tile
   typedef Config<BM, BN, BK, WAVES_M, WAVES_N, COPY_SEL> C;
   constexpr bool kAT = LAY == 2 || LAY == 3, kBT = LAY == 1 || LAY == 3;   // stored K-major
   static_assert(LAY == 0 || (!SPLIT && C::kCopyWaves == 4),
@@ -246,8 +311,10 @@ void hgemm_nt_kernel(TileArgs ta) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);   // wave-uniform
   const int wm = (wave / WAVES_N) * C::WM, wn = (wave % WAVES_N) * C::WN;
-  const int tiles_m = RAG ? (p.M + BM - 1) / BM : p.M / BM;
-  const int tiles_n = RAG ? (p.N + BN - 1) / BN : p.N / BN;
+  const int part_tiles = RAG ? (p.M + BM - 1) / BM : p.M / BM;
+  int tiles_m = part_tiles;
+  if constexpr (MODE == kGradW) tiles_m *= ta.x.parts;
+  const int tiles_n = RAG ? (p.N + kTileN - 1) / kTileN : p.N / BN;
   // K values in the last slab of a tile (RAG: 8 .. 64)
   const int kv = RAG ? p.K - ((p.K + BK - 1) / BK - 1) * BK : BK;
   const int64_t stride = gridDim.x;
@@ -268,10 +335,14 @@ void hgemm_nt_kernel(TileArgs ta) {
     kb = sp * (SPLIT ? p.sk.per : 0);
     int tm, tn;
     map_tile<GM>(item, tiles_m, tiles_n, tm, tn);
+    if constexpr (MODE == kGradW) {
+      sp = tm >= part_tiles;   // the part
+      if (sp) tm -= part_tiles;
+    }
     mlo = tm * BM;
-    nlo = tn * BN;
+    nlo = tn * kTileN;
     m0 = RAG && mlo > p.M - BM ? p.M - BM : mlo;
-    n0 = RAG && nlo > p.N - BN ? p.N - BN : nlo;
+    n0 = RAG && nlo > p.N - kTileN ? p.N - kTileN : nlo;
   };
 
   // Copy assignment: copy instruction c of a slab fills rows [8 c, 8 c + 8);
@@ -290,17 +361,30 @@ void hgemm_nt_kernel(TileArgs ta) {
   const int lane_row = lane / kChunks;
   const int lane_chunk = (lane % kChunks) ^ ((4 * (cwp & 1) + (lane >> 4)) & 7);
   const uint32_t offA = (uint32_t)(lane_row * p.lda + 8 * lane_chunk) * 2;   // bytes
-  const uint32_t offB = (uint32_t)(lane_row * p.ldb + 8 * lane_chunk) * 2;
+  // kGated: copy c fills tile rows 8 c .. 8 c + 7, half of block c / 2 = 2 i + cw / 2
+  // (four copying waves): waves 0 and 1 copy from p.B, 2 and 3 from x.B2, and
+  // copy i holds rows 16 i + 8 (cw & 1) .. + 7 of either.
+  static_assert(MODE != kGated || C::kCopyWaves == 4, "copy assignment of the two B matrices");
+  int64_t ldb = p.ldb;
+  const half_t* pB = p.B;
+  if constexpr (MODE == kGated) {
+    if (cwp >= 2) {
+      ldb = ta.x.ldb2;
+      pB = ta.x.B2;
+    }
+  }
+  const uint32_t offB = (uint32_t)(lane_row * ldb + 8 * lane_chunk) * 2;
   // RAG, the last slab of K: a lane whose chunk lies past K loads the last
   // chunk inside K instead (zeroed once it has landed).
   const bool chunk_past = RAG && 8 * lane_chunk >= kv;
   const int tail_chunk = chunk_past ? kv / 8 - 1 : lane_chunk;
   const uint32_t offA_tail = (uint32_t)(lane_row * p.lda + 8 * tail_chunk) * 2;
-  const uint32_t offB_tail = (uint32_t)(lane_row * p.ldb + 8 * tail_chunk) * 2;
+  const uint32_t offB_tail = (uint32_t)(lane_row * ldb + 8 * tail_chunk) * 2;
   const int64_t copy_strideA = (int64_t)C::kCopyWaves * C::kRowsPerCopy * p.lda * 2;
-  const int64_t copy_strideB = (int64_t)C::kCopyWaves * C::kRowsPerCopy * p.ldb * 2;
+  const int64_t copy_strideB =
+      (int64_t)(MODE == kGated ? 16 : C::kCopyWaves * C::kRowsPerCopy) * ldb * 2;
   const int64_t firstA = (int64_t)cwp * C::kRowsPerCopy * p.lda * 2;
-  const int64_t firstB = (int64_t)cwp * C::kRowsPerCopy * p.ldb * 2;
+  const int64_t firstB = (int64_t)(MODE == kGated ? cwp & 1 : cwp) * C::kRowsPerCopy * ldb * 2;
   // A K-major operand (LAY) with R = 1024 / kTP k-rows per copy: copy c
   // fills k-rows R c .. R c + R - 1, lane l writing k-row R c + l / (kTP / 16)
   // at position l % (kTP / 16), so it loads logical chunk
@@ -336,18 +420,39 @@ void hgemm_nt_kernel(TileArgs ta) {
     const char* b;
     unsigned char* l;
     uint32_t oa, ob;   // this lane's offsets (RAG: the clamped ones in a tile's last slab)
+    int64_t sa;        // kGradX: bytes between A's copies
   };
+  // kGradX: slabs of each part of K
+  const int nk_part = (p.K + BK - 1) / BK;
   // LAY with a K tail (RAG): the last slab is copied from K - 64 .. K - 1,
   // every row and chunk inside the matrix; its first 64 - kv positions repeat
   // the slab before and are zeroed in LDS (wait_zero_sync), so they add 0 x 0.
-  auto slab_base = [&](int stage, int m0, int n0, int t, bool tail) __attribute__((always_inline)) {
+  auto slab_base = [&](int stage, int m0, int n0, int t, bool tail, int part)
+                       __attribute__((always_inline)) {
     CopyBase cb;
     cb.l = lds + stage * kStage;
+    if constexpr (MODE == kGradX) {
+      // slab t of part t / (slabs of a part); the last one of a part with a
+      // K tail holds k = p.K - 64 .. p.K - 1, A's side of it in x.tail
+      const int h = t >= nk_part;
+      const int64_t k0 = tail ? (int64_t)p.K - BK : (int64_t)(t - (h ? nk_part : 0)) * BK;
+      const half_t* a = tail ? ta.x.tail + (int64_t)m0 * ta.x.ldt + h * BK
+                             : p.A + (int64_t)m0 * p.lda + h * ta.x.partA + k0;
+      const int64_t lda = tail ? ta.x.ldt : p.lda;
+      cb.a = (const char*)(a + (int64_t)cwp * C::kRowsPerCopy * lda);
+      cb.sa = (int64_t)C::kCopyWaves * C::kRowsPerCopy * lda * 2;
+      cb.b = (const char*)((h ? ta.x.B2 : p.B) + k0 * p.ldb + n0) + firstTB;
+      cb.oa = (uint32_t)(lane_row * lda + 8 * lane_chunk) * 2;
+      cb.ob = offB;
+      return cb;
+    }
     const int64_t k0 = LAY != 0 && RAG && tail ? (int64_t)p.K - BK : (int64_t)t * BK;
     cb.a = kAT ? (const char*)(p.A + k0 * p.lda + m0) + firstTA
                : (const char*)(p.A + (int64_t)m0 * p.lda) + firstA + 2 * k0;
+    if constexpr (MODE == kGradW && kAT) cb.a += part * ta.x.partA * 2;
     cb.b = kBT ? (const char*)(p.B + k0 * p.ldb + n0) + firstTB
-               : (const char*)(p.B + (int64_t)n0 * p.ldb) + firstB + 2 * k0;
+               : (const char*)(pB + (int64_t)n0 * ldb) + firstB + 2 * k0;
+    (void)part;
     cb.oa = LAY == 0 && RAG && tail ? offA_tail : offA;
     cb.ob = LAY == 0 && RAG && tail ? offB_tail : offB;
     return cb;
@@ -367,7 +472,8 @@ void hgemm_nt_kernel(TileArgs ta) {
           issue(cb.a + c * copy_strideTA, t_hi(kTPA, c) ? offTA1 : offTA0,
                 cb.l + (c * C::kCopyWaves + cw) * 1024);
         else
-          issue(cb.a + c * copy_strideA, cb.oa, cb.l + (c * C::kCopyWaves + cw) * 1024);
+          issue(cb.a + c * (MODE == kGradX ? cb.sa : copy_strideA), cb.oa,
+                cb.l + (c * C::kCopyWaves + cw) * 1024);
       }
     } else {
       const int i = c - kPerWaveA;
@@ -407,7 +513,8 @@ void hgemm_nt_kernel(TileArgs ta) {
         };
 #pragma unroll
         for (int c = 0; c < kPerWaveA; ++c)
-          if ((kCopiesA % C::kCopyWaves == 0 || c * C::kCopyWaves + cw < kCopiesA) &&
+          if (MODE != kGradX &&   // A's tail slab has its zeros in memory
+              (kCopiesA % C::kCopyWaves == 0 || c * C::kCopyWaves + cw < kCopiesA) &&
               (kAT ? trow(kTPA, c) < ks : 8 * lane_chunk < ks))
             *(h8*)(l + (c * C::kCopyWaves + cw) * 1024 + 16 * lane) = h8{};
 #pragma unroll
@@ -613,6 +720,203 @@ void hgemm_nt_kernel(TileArgs ta) {
     }
   };
 
+  // The operators' epilogues (MODE).  flush stores the 16 staged rows of row
+  // block i, `cols` columns from n_first, to dst: rows [mlo, mhi) and columns
+  // [nlo, nhi) only, at any 2-byte address.
+  auto put = [&](int j, h4 o) __attribute__((always_inline)) {
+    const int c = 2 * j + (g >> 1);
+    *(h4*)(stage_out + r * C::kOutRowBytes + 16 * (c ^ r) + 8 * (g & 1)) = o;
+  };
+  auto flush = [&](half_t* dst, int64_t ld, int m_first, int n_first, int cols, int mlo, int mhi,
+                   int nlo, int nhi) __attribute__((always_inline)) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    const int cc = lane & 15;
+#pragma unroll
+    for (int q = 0; q < kOutRows / 4; ++q) {
+      const int R = 4 * q + (lane >> 4);
+      const h8 v = *(const h8*)(stage_out + R * C::kOutRowBytes + 16 * (cc ^ R));
+      const int m = m_first + R, n = n_first + 8 * cc;
+      if (cc < cols / 8 && m >= mlo && m < mhi && n + 8 > nlo && n < nhi) {
+        half_t* d = dst + (int64_t)m * ld + n;
+        if (n >= nlo && n + 8 <= nhi) {
+          __builtin_memcpy(d, &v, 16);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (n + e >= nlo && n + e < nhi) d[e] = v[e];
+        }
+      }
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  };
+  auto round4 = [&](f4 x) __attribute__((always_inline)) {
+    h4 o;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) o[v] = f32_to_word<FMT>(x[v]);
+    return o;
+  };
+  auto epilogue_fused = [&](int m0, int n0, int mlo, int nlo, int part)
+                            __attribute__((always_inline)) {
+    if constexpr (MODE == kGated) {
+      const FusedExtra& x = ta.x;
+      const int nw = n0 + wn / 2;
+#pragma unroll
+      for (int i = 0; i < C::kBlocksM; ++i) {
+        const int m = m0 + wm + 16 * i;
+#pragma unroll
+        for (int j = 0; j < C::kBlocksN / 2; ++j) {
+          f4 y = acc[i][2 * j];
+          if (p.act == GEMM_ACT_SILU) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) y[v] = epi_silu(y[v]);
+          } else if (p.act == GEMM_ACT_RELU) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) y[v] = epi_relu(y[v]);
+          }
+          put(j, round4(y * acc[i][2 * j + 1]));
+        }
+        flush(p.C, p.ldc, m, nw, C::WN / 2, mlo, x.m_end, nlo, x.n_end);
+        if (x.C2) {
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN / 2; ++j) put(j, round4(acc[i][2 * j]));
+          flush(x.C2, x.ldc2, m, nw, C::WN / 2, mlo, x.m_end, nlo, x.n_end);
+        }
+        if (x.C3) {
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN / 2; ++j) put(j, round4(acc[i][2 * j + 1]));
+          flush(x.C3, x.ldc3, m, nw, C::WN / 2, mlo, x.m_end, nlo, x.n_end);
+        }
+      }
+    } else if constexpr (MODE == kLse) {
+      // Row m of block i is held by the four lanes of equal r: 4 kBlocksN
+      // columns each.  Columns of an earlier tile or past n_end count as
+      // -inf; a wave without any leaves (-inf, 0).
+      const FusedExtra& x = ta.x;
+      const int nf = n0 + wn + 4 * g;
+      const bool inside = n0 + wn >= nlo && n0 + wn + C::WN <= x.n_end;
+      const int64_t chunk = (int64_t)((nlo / BN) * WAVES_N + wave % WAVES_N) * x.ld_partial;
+#pragma unroll
+      for (int i = 0; i < C::kBlocksM; ++i) {
+        const int m = m0 + wm + 16 * i + r;
+        const bool mine = m >= mlo && m < x.m_end;
+        // the target's logit, stored by the one lane of the one tile that has it
+        const long long y = mine ? x.targets[m] : -1;
+        const long long rel = y - x.col0 - nf;
+        const bool has = mine && y != x.ignore && rel >= 0 && rel < C::WN && (rel & 15) < 4 &&
+                         nf + rel >= nlo && nf + rel < x.n_end;
+        if (has) {
+          float t = 0.f;
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) t = (int)rel == 16 * j + v ? acc[i][j][v] : t;
+          x.target_logit[m] = t;
+        }
+        if (!inside) {
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int n = nf + 16 * j + v;
+              if (n < nlo || n >= x.n_end) acc[i][j][v] = -__builtin_inff();
+            }
+        }
+        float top = -__builtin_inff();
+#pragma unroll
+        for (int j = 0; j < C::kBlocksN; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) top = fmaxf(top, acc[i][j][v]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float base = top == -__builtin_inff() ? 0.f : top;
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < C::kBlocksN; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v) s += __expf(acc[i][j][v] - base);
+        s += __shfl_xor(s, 16);
+        s += __shfl_xor(s, 32);
+        if (g == 0 && mine) x.partial[chunk + m] = make_float2(top, s);
+      }
+    } else if constexpr (MODE == kDlogit) {
+      // Rows past m_end and rows to ignore are zero, and so are columns
+      // before n_begin (which an earlier piece of the columns has).
+      const FusedExtra& x = ta.x;
+      const int nf = n0 + wn + 4 * g;
+      const float f = x.scale ? x.scale[0] : 1.f;
+      const int last = (p.N - 1) / BK * BK;   // first column of the last slab of K there
+      const bool tail = x.tail != nullptr && n0 + wn + C::WN > p.N - BK;
+#pragma unroll
+      for (int i = 0; i < C::kBlocksM; ++i) {
+        const int m = m0 + wm + 16 * i + r;
+        const bool row = m < x.m_end;
+        const long long y = row ? x.targets[m] : x.ignore;
+        const bool live = row && y != x.ignore;
+        const bool known = y >= 0 && y < x.vocab;
+        const float lse = live ? x.lse[m] : 0.f;
+        float w = live ? x.row_scale[m] * f : 0.f;
+        if (live && !known) w = __builtin_nanf("");
+        const long long at = y - x.col0 - nf;
+        const int rel = at >= 0 && at < C::WN ? (int)at : -1;
+#pragma unroll
+        for (int j = 0; j < C::kBlocksN; ++j) {
+          f4 d;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const float e = __expf(acc[i][j][v] - lse) - (rel == 16 * j + v ? 1.f : 0.f);
+            const int n = nf + 16 * j + v;
+            d[v] = live && n >= x.n_begin && n < x.n_end ? e * w : 0.f;
+          }
+          const h4 o = round4(d);
+          put(j, o);
+          if (tail) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int n = nf + 16 * j + v;
+              if (m >= mlo && n >= nlo && n >= p.N - BK)
+                x.tail[m * x.ldt + n - (p.N - BK)] = n >= last ? o[v] : (half_t)0;
+            }
+          }
+        }
+        flush(p.C, p.ldc, m0 + wm + 16 * i, n0 + wn, C::WN, mlo, p.M, nlo, p.N);
+      }
+    } else if constexpr (MODE == kGradW) {
+      const FusedExtra& x = ta.x;
+      const float f = x.scale ? x.scale[1] : 1.f;
+#pragma unroll
+      for (int i = 0; i < C::kBlocksM; ++i) {
+#pragma unroll
+        for (int j = 0; j < C::kBlocksN; ++j) put(j, round4(acc[i][j] * f));
+        flush(part ? x.C2 : p.C, part ? x.ldc2 : p.ldc, m0 + wm + 16 * i, n0 + wn, C::WN,
+              mlo > x.m_begin ? mlo : x.m_begin, x.m_end, nlo, x.n_end);
+      }
+    } else if constexpr (MODE == kGradX) {
+      const FusedExtra& x = ta.x;
+      const float f = x.scale ? x.scale[1] : 1.f;
+#pragma unroll
+      for (int i = 0; i < C::kBlocksM; ++i) {
+        const int m = m0 + wm + 16 * i + r;
+        const bool mine = m >= mlo;
+        float* sum = x.sum + (int64_t)m * x.ld_sum + n0 + wn + 4 * g;
+        if (x.sum_read) {
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j)
+            if (mine && n0 + wn + 16 * j + 4 * g >= nlo) acc[i][j] += *(const f4*)(sum + 16 * j);
+        }
+        if (x.sum_write) {
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j)
+            if (mine && n0 + wn + 16 * j + 4 * g >= nlo) *(f4*)(sum + 16 * j) = acc[i][j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j) put(j, round4(acc[i][j] * f));
+          flush(p.C, p.ldc, m0 + wm + 16 * i, n0 + wn, C::WN, mlo, x.m_end, nlo, x.n_end);
+        }
+      }
+    }
+    (void)part;
+  };
+
   // Split-K partial tile: acc[i][j] is row m0 + wm + 16 i + r, columns
   // n0 + wn + 16 j + 4 g .. + 3; one 16-byte store per block into the
   // workspace (padded to whole tiles, no bounds).
@@ -650,7 +954,8 @@ void hgemm_nt_kernel(TileArgs ta) {
   constexpr int kReadInstr = kReads + (kAT ? C::kBlocksM : 0) + (kBT ? C::kBlocksN : 0);
   constexpr int kCopies = kPerWaveA + kPerWaveB;
   static_assert(kReadInstr <= kMfma && kCopies <= kMfma, "interleave pattern");
-  const int nk = SPLIT ? p.sk.per : RAG ? (p.K + BK - 1) / BK : p.K / BK;   // slabs per work item
+  const int nk = (MODE == kGradX ? ta.x.parts : 1) *
+                 (SPLIT ? p.sk.per : RAG ? (p.K + BK - 1) / BK : p.K / BK);   // slabs per work item
   // The copy target runs two slabs ahead of the compute: slab tc of the tile
   // `ahead` tiles after the current one (origins o[0..2] are refreshed once
   // per tile, outside the MFMA loop).  Past the end of the stream it stays on
@@ -685,7 +990,9 @@ void hgemm_nt_kernel(TileArgs ta) {
     const int n0 = d == 0 ? on[0] : d == 1 ? on[1] : on[2];
     const int kb = d == 0 ? ok[0] : d == 1 ? ok[1] : ok[2];
     const int t = past ? nk - 1 : tc;
-    return slab_base(stage, m0, n0, kb + t, RAG && kv < BK && t == nk - 1);
+    const int part = MODE == kGradW ? (d == 0 ? os[0] : d == 1 ? os[1] : os[2]) : 0;
+    const bool last = t == nk - 1 || (MODE == kGradX && t == nk_part - 1);
+    return slab_base(stage, m0, n0, kb + t, RAG && kv < BK && last, part);
   };
   auto copy_next = [&](int stage) __attribute__((always_inline)) {
     const CopyBase cb = next_base(stage);
@@ -822,16 +1129,21 @@ void hgemm_nt_kernel(TileArgs ta) {
     // RAG: slab nk - 1 reaches past K when kv < BK; it is the next slab of
     // slab nk - 2 (nk >= 2: K > BK).  The next tile's first slab never is.
     const int zt = RAG && kv < BK ? nk - 2 : -1;
+    const int zt0 = MODE == kGradX && kv < BK ? nk_part - 2 : -1;   // the first part's
     if (copies) {
-      for (int t = 0; t + 1 < nk; ++t, ++gs) slab(gs, yes(), yes(), t == zt);
+      for (int t = 0; t + 1 < nk; ++t, ++gs)
+        slab(gs, yes(), yes(), t == zt || (MODE == kGradX && t == zt0));
       slab(gs, no(), yes(), false);
     } else {
-      for (int t = 0; t + 1 < nk; ++t, ++gs) slab(gs, yes(), no(), t == zt);
+      for (int t = 0; t + 1 < nk; ++t, ++gs)
+        slab(gs, yes(), no(), t == zt || (MODE == kGradX && t == zt0));
       slab(gs, no(), no(), false);
     }
     ++gs;
     if constexpr (SPLIT) {
       epilogue_partial(m0, n0, sp);
+    } else if constexpr (MODE != kProduct) {
+      epilogue_fused(m0, n0, mlo0, nlo0, sp);
     } else {
       (void)sp;
       epilogue(m0, n0, mlo0, nlo0);
@@ -863,6 +1175,24 @@ hipError_t launch(const Args16& a, int slots, hipStream_t stream) {
           hgemm_nt_kernel<BM, BN, BK, WAVES_M, WAVES_N, GM, COPY_SEL, OPT, EPI, FMT, SPLIT, RAG,
                           LAY>,
       dim3((unsigned)grid), dim3(C::kThreads), args, 0, stream);
+}
+
+// An operator's mode over the tiles of its output: ceil(M / BM) (times the
+// parts of kGradW) by ceil(N / BN) (kGated: BN / 2) of them, persistent.
+template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int GM, int COPY_SEL, int OPT, int FMT,
+          int LAY, int MODE>
+hipError_t launch_fused(const Args16& a, const FusedExtra& x, int slots, hipStream_t stream) {
+  typedef Config<BM, BN, BK, WAVES_M, WAVES_N, COPY_SEL> C;
+  constexpr int kTileN = MODE == kGated ? BN / 2 : BN;
+  const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * (MODE == kGradW ? x.parts : 1) *
+                        ((a.N + kTileN - 1) / kTileN);
+  int64_t grid = tiles < slots ? tiles : slots;
+  if (grid < 1) grid = 1;
+  FusedTileArgs ta{a, tiles, x};
+  void* args[] = {&ta};
+  return hipLaunchKernel((const void*)hgemm_nt_kernel<BM, BN, BK, WAVES_M, WAVES_N, GM, COPY_SEL,
+                                                      OPT, false, FMT, false, true, LAY, MODE>,
+                         dim3((unsigned)grid), dim3(C::kThreads), args, 0, stream);
 }
 
 // Leading dimensions must also keep a lane's 32-bit copy offset (up to 8 rows
