@@ -58,6 +58,9 @@ hipError_t launch_grad_w(const Args16& a, const FusedExtra& x, int cus, hipStrea
 hipError_t launch_grad_x(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
 hipError_t launch_lse_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
 hipError_t launch_dlogit_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
+// The gated product for a.M <= kFewRows, operands as they are (no copies).
+constexpr int kFewRows = 64;
+hipError_t launch_gated_rows(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
 // Wave columns of the kLse tiles: partial results per row.
 int lse_chunks(int M, int N, int cus);
 

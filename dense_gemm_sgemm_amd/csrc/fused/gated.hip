@@ -127,7 +127,7 @@ extern "C" {
 MI355FUSED_API unsigned long long gemm_gated_workspace(int type, int M, int N, int K,
                                                        const void* X, int ldx, const void* Wg,
                                                        int ldwg, const void* Wu, int ldwu) {
-  if (check(type, 0, M, N, K) != GEMM_OK || M == 0 || N == 0 || bad_ld(ldx, K) ||
+  if (check(type, 0, M, N, K) != GEMM_OK || M <= kFewRows || N == 0 || bad_ld(ldx, K) ||
       bad_ld(ldwg, K) || bad_ld(ldwu, K))
     return 0;
   return (needs_copy(X, ldx, M, K) ? copy_bytes(M, K) : 0) +
@@ -152,25 +152,35 @@ MI355FUSED_API int gemm_gated(int type, int act, int M, int N, int K, const void
   const int cus = check_device();
   if (cus < 0) return cus;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  PadJobs jobs;
-  char* ws = static_cast<char*>(workspace);
-  const Mat x = jobs.add(Mat{in16(X), ldx}, M, K, ws);
-  const Mat g = jobs.add(Mat{in16(Wg), ldwg}, N, K, ws);
-  const Mat u = jobs.add(Mat{in16(Wu), ldwu}, N, K, ws);
-  const hipError_t e = launch_pad(jobs, s);
-  if (e != hipSuccess) return to_status(e);
-  Args16 a{x.p, g.p, out16(H), x.ld, g.ld, ldh, pad_rows(M), pad_rows(N), pad_k(K)};
+  Args16 a{in16(X), in16(Wg), out16(H), ldx, ldwg, ldh, M, N, K};
   a.act = act;
   a.fmt = type == GEMM_TYPE_BF16 ? kFmtBF16 : kFmtF16;
   FusedExtra f;
   f.m_end = M;
   f.n_end = N;
-  f.B2 = u.p;
-  f.ldb2 = u.ld;
+  f.B2 = in16(Wu);
+  f.ldb2 = ldwu;
   f.C2 = out16(G);
   f.ldc2 = ldg;
   f.C3 = out16(U);
   f.ldc3 = ldu;
+  if (M <= kFewRows) return to_status(launch_gated_rows(a, f, cus, s));
+  PadJobs jobs;
+  char* ws = static_cast<char*>(workspace);
+  const Mat x = jobs.add(Mat{a.A, ldx}, M, K, ws);
+  const Mat g = jobs.add(Mat{a.B, ldwg}, N, K, ws);
+  const Mat u = jobs.add(Mat{f.B2, ldwu}, N, K, ws);
+  const hipError_t e = launch_pad(jobs, s);
+  if (e != hipSuccess) return to_status(e);
+  a.A = x.p;
+  a.lda = x.ld;
+  a.B = g.p;
+  a.ldb = g.ld;
+  f.B2 = u.p;
+  f.ldb2 = u.ld;
+  a.M = pad_rows(M);
+  a.N = pad_rows(N);
+  a.K = pad_k(K);
   return to_status(launch_gated_tiles(a, f, cus, s));
 }
 

@@ -279,11 +279,7 @@ extern "C" MI355FUSED_API int gemm_w4(int type, int M, int N, int K, int group, 
            static_cast<half_t*>(C), ldx, ldq, lds, ldz, ldr, ldc, M, N, K, group, act, 0};
   const int mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
   const int64_t wgs = ((int64_t)N + 15) / 16 * (((int64_t)M + 63) / 64);
-  // as many waves as have a chunk, to about 16 a CU
-  const int chunks = std::max(1, K / (kBlock * kUnroll));
-  int waves = 4;
-  while (waves < kMaxWaves && waves < chunks && wgs * waves < 16 * (int64_t)cus) waves *= 2;
-  while (waves > 1 && waves > (K + kBlock - 1) / kBlock) waves /= 2;
+  const int waves = skinny::waves_for(wgs, std::max(1, K / kBlock), kMaxWaves, cus);
   a.waves = waves;
   const unsigned lds_bytes = (unsigned)((waves - 1) * mt * 64 * sizeof(f4));
   const void* k = type == GEMM_TYPE_BF16 ? (const void*)pick<kFmtBF16>(M, group)
