@@ -29,6 +29,8 @@ inline bool needs_copy(const void* p, int64_t ld, int rows, int K) {
   return rows < kMinRows || K < kMinK || K % 8 != 0 || !aligned16(p) || ld % 8 != 0 ||
          ld >= (int64_t(1) << 28);
 }
+// Rows of the reduction of dW = d^T X: whole slabs.
+inline int pad_slabs(int M) { return (int)round_up(pad_rows(M), 64); }
 inline size_t copy_bytes(int rows, int K) {
   return round256((size_t)pad_rows(rows) * pad_k(K) * 2);
 }
@@ -49,13 +51,28 @@ struct PadJobs {
   // matrix the kernels read and advances dst past the copy.
   Mat add(Mat m, int rows, int K, char*& dst);
   Mat copy(Mat m, int rows, int K, char*& dst);
+  // Adds zeros for `rows` packed rows of `cols` (a multiple of 8) at dst.
+  void zeros(half_t* dst, int rows, int cols);
 };
 hipError_t launch_pad(const PadJobs& jobs, hipStream_t stream);
 
 // The tile-kernel launchers (tiles_*.hip); a.fmt selects the format.
 hipError_t launch_gated_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
 hipError_t launch_grad_w(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
-hipError_t launch_grad_x(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
+// kGradX: the tile shape and the ranges of K (splits == 1: none) for an M x N
+// result over `slabs` slabs of 64, made for the chip's 256 CUs since the
+// workspace is sized before a device is asked.  sums: fp32 sums are kept
+// anyway (K comes in pieces).
+constexpr int kPlanCus = 256;
+struct GradXPlan {
+  int shape = 0, splits = 0, per = 0;
+};
+GradXPlan plan_grad_x(int M, int N, int slabs, bool sums);
+hipError_t launch_grad_x(const Args16& a, const FusedExtra& x, const GradXPlan& plan, int cus,
+                         hipStream_t stream);
+// out = the sums of x.sum's ranges, scaled and rounded.
+hipError_t launch_sums(int fmt, const FusedExtra& x, int splits, half_t* out, int64_t ldo, int M,
+                       int N, hipStream_t stream);
 hipError_t launch_lse_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
 hipError_t launch_dlogit_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
 // The gated product for a.M <= kFewRows, operands as they are (no copies).

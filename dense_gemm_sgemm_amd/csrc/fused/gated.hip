@@ -90,28 +90,35 @@ int check(int type, int act, int M, int N, int K) {
 const half_t* in16(const void* p) { return static_cast<const half_t*>(p); }
 half_t* out16(void* p) { return static_cast<half_t*>(p); }
 
-// The workspace of the backward pass: dG | dU, their tails, padded copies.
+// The workspace of the backward pass: dG | dU, their tails, X^T, padded copies
+// of the weights, fp32 sums of dX.
 struct BwdPlan {
-  int Mp, Np, Nk;
+  int Mp, Np, Nk;         // Mp: whole slabs of rows (they are summed over for dW)
   int64_t ld;
   bool tail;
-  size_t bytes_d, bytes_tail, bytes_x = 0, bytes_g = 0, bytes_u = 0;
-  size_t total() const { return bytes_d + bytes_tail + bytes_x + bytes_g + bytes_u; }
+  GradXPlan gx;
+  size_t bytes_d, bytes_tail, bytes_x = 0, bytes_g = 0, bytes_u = 0, bytes_sum = 0;
+  size_t total() const { return bytes_d + bytes_tail + bytes_x + bytes_g + bytes_u + bytes_sum; }
 };
-BwdPlan plan_bwd(int M, int N, int K, Mat X, Mat Wg, Mat Wu, bool dx, bool dw) {
+BwdPlan plan_bwd(int M, int N, int K, Mat Wg, Mat Wu, bool dx, bool dw) {
   BwdPlan p;
-  p.Mp = pad_rows(M);
+  p.Mp = pad_slabs(M);
   p.Nk = pad_rows(N);
   p.Np = (int)round_up(p.Nk, 8);
   p.ld = 2 * (int64_t)p.Np;
   p.tail = dx && p.Nk % 64 != 0;
   p.bytes_d = round256((size_t)p.Mp * p.ld * 2);
   p.bytes_tail = p.tail ? (size_t)p.Mp * 256 : 0;
-  if (dw && needs_copy(X.p, X.ld, M, K)) p.bytes_x = copy_bytes(M, K);
+  if (dw) p.bytes_x = round256((size_t)pad_k(K) * p.Mp * 2);
   // W as a K-major operand of dX: both at one leading dimension
   const bool copy = needs_copy(Wg.p, Wg.ld, N, K) || needs_copy(Wu.p, Wu.ld, N, K) ||
                     Wg.ld != Wu.ld;
   if (dx && copy) p.bytes_g = p.bytes_u = copy_bytes(N, K);
+  if (dx) {
+    p.gx = plan_grad_x(pad_rows(M), pad_k(K), 2 * ((p.Nk + 63) / 64), false);
+    if (p.gx.splits > 1)
+      p.bytes_sum = round256((size_t)p.gx.splits * pad_rows(M) * pad_k(K) * sizeof(float));
+  }
   return p;
 }
 
@@ -192,8 +199,7 @@ MI355FUSED_API unsigned long long gemm_gated_bwd_workspace(int type, int M, int 
   const bool dx = want_dx && M > 0, dw = want_dw && N > 0;
   if (!dx && !dw) return 0;
   if ((dw && bad_ld(ldx, K)) || (dx && (bad_ld(ldwg, K) || bad_ld(ldwu, K)))) return 0;
-  return plan_bwd(M, N, K, Mat{in16(X), ldx}, Mat{in16(Wg), ldwg}, Mat{in16(Wu), ldwu}, dx, dw)
-      .total();
+  return plan_bwd(M, N, K, Mat{in16(Wg), ldwg}, Mat{in16(Wu), ldwu}, dx, dw).total();
 }
 
 MI355FUSED_API int gemm_gated_bwd(int type, int act, int M, int N, int K, const void* X, int ldx,
@@ -215,8 +221,7 @@ MI355FUSED_API int gemm_gated_bwd(int type, int act, int M, int N, int K, const 
       (G == nullptr || U == nullptr || dH == nullptr || (dw && X == nullptr) ||
        (dx && (Wg == nullptr || Wu == nullptr))))
     return GEMM_ERR_NULL_POINTER;
-  const BwdPlan p =
-      plan_bwd(M, N, K, Mat{in16(X), ldx}, Mat{in16(Wg), ldwg}, Mat{in16(Wu), ldwu}, dx, dw);
+  const BwdPlan p = plan_bwd(M, N, K, Mat{in16(Wg), ldwg}, Mat{in16(Wu), ldwu}, dx, dw);
   if (!workspace_ok(p.total(), workspace, workspace_bytes)) return GEMM_ERR_WORKSPACE;
   const int cus = check_device();
   if (cus < 0) return cus;
@@ -234,9 +239,10 @@ MI355FUSED_API int gemm_gated_bwd(int type, int act, int M, int N, int K, const 
                                               : (const void*)gated_grad_kernel<kFmtF16>,
                               ga, (pieces + kThreads - 1) / kThreads, kThreads, 0, s);
   if (e != hipSuccess) return to_status(e);
+  half_t* xt = reinterpret_cast<half_t*>(ws);
+  ws += p.bytes_x;
   PadJobs jobs;
-  Mat x{in16(X), ldx}, wg{in16(Wg), ldwg}, wu{in16(Wu), ldwu};
-  if (p.bytes_x) x = jobs.add(x, M, K, ws);
+  Mat wg{in16(Wg), ldwg}, wu{in16(Wu), ldwu};
   if (p.bytes_g) {
     wg = jobs.copy(wg, N, K, ws);
     wu = jobs.copy(wu, N, K, ws);
@@ -244,7 +250,7 @@ MI355FUSED_API int gemm_gated_bwd(int type, int act, int M, int N, int K, const 
   e = launch_pad(jobs, s);
   if (e != hipSuccess) return to_status(e);
   if (dx) {
-    Args16 a{d, wg.p, out16(dX), p.ld, wg.ld, lddx, p.Mp, pad_k(K), p.Nk};
+    Args16 a{d, wg.p, out16(dX), p.ld, wg.ld, lddx, pad_rows(M), pad_k(K), p.Nk};
     a.fmt = fmt;
     FusedExtra f;
     f.m_end = M;
@@ -254,13 +260,23 @@ MI355FUSED_API int gemm_gated_bwd(int type, int act, int M, int N, int K, const 
     f.B2 = wu.p;
     f.tail = tail;
     f.ldt = 128;
-    e = launch_grad_x(a, f, cus, s);
+    if (p.bytes_sum) {
+      f.sum = reinterpret_cast<float*>(ws);
+      f.ld_sum = a.N;
+      f.split_stride = (int64_t)a.M * a.N;
+    }
+    e = launch_grad_x(a, f, p.gx, cus, s);
+    if (e == hipSuccess && f.sum)
+      e = launch_sums(fmt, f, p.gx.splits, out16(dX), lddx, M, K, s);
     if (e != hipSuccess) return to_status(e);
   }
   if (dw) {
+    const PadCopy tr{in16(X), xt, ldx, p.Mp, M, K, p.Mp, pad_k(K)};
+    e = launch_transpose16(tr, nullptr, s);
+    if (e != hipSuccess) return to_status(e);
     // both gradients as two parts of one product's rows, or the one asked for
     const bool both = dWg != nullptr && dWu != nullptr;
-    Args16 a{dWg ? d : d + p.Np, x.p, out16(dWg ? dWg : dWu), p.ld, x.ld, dWg ? lddwg : lddwu,
+    Args16 a{dWg ? d : d + p.Np, xt, out16(dWg ? dWg : dWu), p.ld, p.Mp, dWg ? lddwg : lddwu,
              p.Np, pad_k(K), p.Mp};
     a.fmt = fmt;
     FusedExtra f;

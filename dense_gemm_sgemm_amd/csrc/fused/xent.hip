@@ -123,17 +123,19 @@ constexpr size_t kPieceBytes = size_t(256) << 20;
 constexpr int kMinPiece = 2048;
 
 struct BwdPlan {
-  int Mp, Np, Kp;
+  int Mp, Ms, Np, Kp;     // Ms: whole slabs of rows (they are summed over for dW)
   int width, pieces;      // every piece but the last is `width` columns
   int64_t ldd;            // leading dimension of a piece's d
-  size_t bytes_d, bytes_tail, bytes_sum, bytes_scale, bytes_x = 0, bytes_w = 0;
+  GradXPlan gx;           // for `width` columns
+  size_t bytes_d, bytes_tail, bytes_sum = 0, bytes_scale, bytes_xt, bytes_x = 0, bytes_w = 0;
   size_t total() const {
-    return bytes_d + bytes_tail + bytes_sum + bytes_scale + bytes_x + bytes_w;
+    return bytes_d + bytes_tail + bytes_sum + bytes_scale + bytes_xt + bytes_x + bytes_w;
   }
 };
-BwdPlan plan_bwd(int M, int N, int K, Mat X, Mat W, bool dx) {
+BwdPlan plan_bwd(int M, int N, int K, Mat X, Mat W, bool dx, bool dw) {
   BwdPlan p;
   p.Mp = pad_rows(M);
+  p.Ms = pad_slabs(M);
   p.Np = pad_rows(N);
   p.Kp = pad_k(K);
   const int64_t most = std::max<int64_t>(kMinPiece, kPieceBytes / ((size_t)p.Mp * 2) / 256 * 256);
@@ -141,10 +143,15 @@ BwdPlan plan_bwd(int M, int N, int K, Mat X, Mat W, bool dx) {
   p.width = (int)std::min<int64_t>(round_up((p.Np + n - 1) / n, 256), p.Np);
   p.pieces = (p.Np + p.width - 1) / p.width;
   p.ldd = round_up(std::max(p.width, 128), 64);
-  p.bytes_d = round256((size_t)p.Mp * p.ldd * 2);
+  p.bytes_d = round256((size_t)p.Ms * p.ldd * 2);
   p.bytes_tail = dx ? (size_t)p.Mp * 128 : 0;
-  p.bytes_sum = dx && p.pieces > 1 ? round256((size_t)p.Mp * p.Kp * 4) : 0;
+  if (dx) {
+    p.gx = plan_grad_x(p.Mp, p.Kp, (p.width + 63) / 64, p.pieces > 1);
+    if (p.pieces > 1 || p.gx.splits > 1)
+      p.bytes_sum = round256((size_t)p.gx.splits * p.Mp * p.Kp * sizeof(float));
+  }
   p.bytes_scale = 256;
+  p.bytes_xt = dw ? round256((size_t)p.Kp * p.Ms * 2) : 0;
   if (needs_copy(X.p, X.ld, M, K)) p.bytes_x = copy_bytes(M, K);
   if (needs_copy(W.p, W.ld, N, K)) p.bytes_w = copy_bytes(N, K);
   return p;
@@ -218,7 +225,7 @@ MI355FUSED_API unsigned long long gemm_xent_bwd_workspace(int type, int M, int N
     return 0;
   const bool dx = want_dx && M > 0;
   if (!dx && !want_dw) return 0;
-  return plan_bwd(M, N, K, Mat{in16(X), ldx}, Mat{in16(W), ldw}, dx).total();
+  return plan_bwd(M, N, K, Mat{in16(X), ldx}, Mat{in16(W), ldw}, dx, want_dw != 0).total();
 }
 
 MI355FUSED_API int gemm_xent_bwd(int type, int M, int N, int K, const void* X, int ldx,
@@ -236,7 +243,7 @@ MI355FUSED_API int gemm_xent_bwd(int type, int M, int N, int K, const void* X, i
   if (M > 0 && (X == nullptr || W == nullptr || targets == nullptr || lse == nullptr ||
                 dloss == nullptr))
     return GEMM_ERR_NULL_POINTER;
-  const BwdPlan p = plan_bwd(M, N, K, Mat{in16(X), ldx}, Mat{in16(W), ldw}, dx);
+  const BwdPlan p = plan_bwd(M, N, K, Mat{in16(X), ldx}, Mat{in16(W), ldw}, dx, dw);
   if (!workspace_ok(p.total(), workspace, workspace_bytes)) return GEMM_ERR_WORKSPACE;
   const int cus = check_device();
   if (cus < 0) return cus;
@@ -251,6 +258,8 @@ MI355FUSED_API int gemm_xent_bwd(int type, int M, int N, int K, const void* X, i
   ws += p.bytes_sum;
   float* scale = reinterpret_cast<float*>(ws);
   ws += p.bytes_scale;
+  half_t* xt = reinterpret_cast<half_t*>(ws);
+  ws += p.bytes_xt;
   PadJobs jobs;
   Mat x{in16(X), ldx}, w{in16(W), ldw};
   if (p.bytes_x) x = jobs.copy(x, M, K, ws);
@@ -264,12 +273,18 @@ MI355FUSED_API int gemm_xent_bwd(int type, int M, int N, int K, const void* X, i
   } else {
     scale = nullptr;   // bf16 has fp32's range
   }
-  if (M == 0) {   // no rows: d is zero (Mp = 128 rows)
-    PadJobs zero;
-    char* at = reinterpret_cast<char*>(d);
-    zero.copy(Mat{}, 0, (int)p.ldd, at);
-    e = launch_pad(zero, s);
+  if (dw) {
+    const PadCopy tr{in16(X), xt, ldx, p.Ms, M, K, p.Ms, p.Kp};
+    e = launch_transpose16(tr, nullptr, s);
     if (e != hipSuccess) return to_status(e);
+    // the rows of d that no piece writes (all of them for M == 0) are zero
+    const int written = M > 0 ? p.Mp : 0;
+    if (p.Ms > written) {
+      PadJobs zero;
+      zero.zeros(d + written * p.ldd, p.Ms - written, (int)p.ldd);
+      e = launch_pad(zero, s);
+      if (e != hipSuccess) return to_status(e);
+    }
   }
   for (int i = 0; i < p.pieces; ++i) {
     const bool last = i + 1 == p.pieces;
@@ -297,8 +312,8 @@ MI355FUSED_API int gemm_xent_bwd(int type, int M, int N, int K, const void* X, i
     if (M > 0) e = launch_dlogit_tiles(a, f, cus, s);
     if (e != hipSuccess) return to_status(e);
     if (dw) {
-      Args16 b{d, x.p, out16(dW) + (int64_t)begin * lddw, p.ldd, x.ld, lddw,
-               (int)round_up(width, 8), p.Kp, p.Mp};
+      Args16 b{d, xt, out16(dW) + (int64_t)begin * lddw, p.ldd, p.Ms, lddw,
+               (int)round_up(width, 8), p.Kp, p.Ms};
       b.fmt = fmt;
       FusedExtra g;
       g.m_begin = owned - begin;
@@ -317,11 +332,22 @@ MI355FUSED_API int gemm_xent_bwd(int type, int M, int N, int K, const void* X, i
       g.tail = f.tail;
       g.ldt = 64;
       g.scale = scale;
-      g.sum = sum;
-      g.ld_sum = p.Kp;
-      g.sum_read = i > 0;
-      g.sum_write = !last;
-      e = launch_grad_x(b, g, cus, s);
+      // (the last piece has fewer columns: fewer slabs a range, not fewer ranges)
+      GradXPlan plan = p.gx;
+      const int slabs = (width + 63) / 64;
+      if (last && p.pieces > 1) {
+        plan.per = (slabs + plan.splits - 1) / plan.splits;
+        plan.splits = (slabs + plan.per - 1) / plan.per;
+      }
+      if (p.bytes_sum) {
+        g.sum = sum;
+        g.ld_sum = p.Kp;
+        g.split_stride = (int64_t)p.Mp * p.Kp;
+        g.sum_add = i > 0;
+      }
+      e = launch_grad_x(b, g, plan, cus, s);
+      if (e == hipSuccess && last && g.sum)
+        e = launch_sums(fmt, g, p.gx.splits, out16(dX), lddx, M, K, s);
       if (e != hipSuccess) return to_status(e);
     }
   }

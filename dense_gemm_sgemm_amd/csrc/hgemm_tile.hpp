@@ -175,12 +175,15 @@ struct TileArgs {
 //   kLse      no C: each wave's row maxima and sums of exponentials over its
 //             columns, and the logit of each row's target column.
 //   kDlogit   C = (exp(acc - lse) - [column is the target]) * scale of the row.
-//   kGradW    (both operands K-major) C = acc * factor; the tile rows may come
-//             in two parts of p.M rows each: A's columns m and x.partA + m,
-//             outputs p.C and x.C2.
-//   kGradX    (B K-major) C = acc * factor, or, over several launches, sums in
-//             fp32 in x.sum first; K may come in two parts of p.K each: A's
-//             columns k and x.partA + k against the rows of p.B and x.B2.
+//   kGradW    (A K-major) C = acc * factor; the tile rows may come in two parts
+//             of p.M rows each: A's columns m and x.partA + m, outputs p.C and
+//             x.C2.
+//   kGradX    (B K-major) C = acc * factor.  K may come in two parts of p.K
+//             each: A's columns k and x.partA + k against the rows of p.B and
+//             x.B2.  The slabs of all of K may be cut into x.splits ranges of
+//             x.per (the last may be shorter), each a work item of its own
+//             that leaves fp32 sums in x.sum, or adds to those of an earlier
+//             launch.
 enum TileMode { kProduct = 0, kGated, kLse, kDlogit, kGradW, kGradX };
 
 // What these modes need beside the product's arguments.  Operands may be
@@ -211,9 +214,10 @@ struct FusedExtra {
   const float* row_scale = nullptr;     // kDlogit, [rows]
   const float* scale = nullptr;         // {factor, 1 / factor}, or null for 1: kDlogit
                                         //   multiplies by the first, gradients by the second
-  float* sum = nullptr;                 // kGradX: fp32 sums over launches, [rows][ld_sum]
-  int64_t ld_sum = 0;
-  int sum_read = 0, sum_write = 0;      // add what x.sum holds; store to x.sum instead of C
+  int splits = 1, per = 0;              // kGradX: ranges of K (per: slabs of each)
+  float* sum = nullptr;                 // kGradX: store fp32 sums here, [splits][rows][ld_sum],
+  int64_t ld_sum = 0, split_stride = 0; //   instead of C
+  int sum_add = 0;                      //   added to what is there
 };
 struct FusedTileArgs {
   Args16 p;
@@ -277,7 +281,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   static_assert(MODE != kGated || (LAY == 0 && (BN / WAVES_N) % 32 == 0),
                 "pairs of B blocks inside a wave");
   static_assert((MODE != kLse && MODE != kDlogit) || LAY == 0, "logits from A * B^T");
-  static_assert((MODE != kGradW || LAY == 3) && (MODE != kGradX || LAY == 1),
+  static_assert((MODE != kGradW || LAY == 2) && (MODE != kGradX || LAY == 1),
                 "gradients from K-major operands");
   constexpr int kTileN = MODE == kGated ? BN / 2 : BN;   // output columns of a tile
   typedef Config<BM, BN, BK, WAVES_M, WAVES_N, COPY_SEL> C;
@@ -332,7 +336,12 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       sp = (int)(item / tiles);
       item -= sp * tiles;
     }
-    kb = sp * (SPLIT ? p.sk.per : 0);
+    if constexpr (MODE == kGradX) {
+      const int64_t tiles = (int64_t)tiles_m * tiles_n;
+      sp = (int)(item / tiles);
+      item -= sp * tiles;
+    }
+    kb = sp * (SPLIT ? p.sk.per : MODE == kGradX ? ta.x.per : 0);
     int tm, tn;
     map_tile<GM>(item, tiles_m, tiles_n, tm, tn);
     if constexpr (MODE == kGradW) {
@@ -422,7 +431,9 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     uint32_t oa, ob;   // this lane's offsets (RAG: the clamped ones in a tile's last slab)
     int64_t sa;        // kGradX: bytes between A's copies
   };
-  // kGradX: slabs of each part of K
+  // kGradX: this lane's offset in x.tail; slabs of each part of K
+  uint32_t offA_x = 0;
+  if constexpr (MODE == kGradX) offA_x = (uint32_t)(lane_row * ta.x.ldt + 8 * lane_chunk) * 2;
   const int nk_part = (p.K + BK - 1) / BK;
   // LAY with a K tail (RAG): the last slab is copied from K - 64 .. K - 1,
   // every row and chunk inside the matrix; its first 64 - kv positions repeat
@@ -442,7 +453,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       cb.a = (const char*)(a + (int64_t)cwp * C::kRowsPerCopy * lda);
       cb.sa = (int64_t)C::kCopyWaves * C::kRowsPerCopy * lda * 2;
       cb.b = (const char*)((h ? ta.x.B2 : p.B) + k0 * p.ldb + n0) + firstTB;
-      cb.oa = (uint32_t)(lane_row * lda + 8 * lane_chunk) * 2;
+      cb.oa = tail ? offA_x : offA;
       cb.ob = offB;
       return cb;
     }
@@ -513,8 +524,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         };
 #pragma unroll
         for (int c = 0; c < kPerWaveA; ++c)
-          if (MODE != kGradX &&   // A's tail slab has its zeros in memory
-              (kCopiesA % C::kCopyWaves == 0 || c * C::kCopyWaves + cw < kCopiesA) &&
+          if ((kCopiesA % C::kCopyWaves == 0 || c * C::kCopyWaves + cw < kCopiesA) &&
               (kAT ? trow(kTPA, c) < ks : 8 * lane_chunk < ks))
             *(h8*)(l + (c * C::kCopyWaves + cw) * 1024 + 16 * lane) = h8{};
 #pragma unroll
@@ -546,6 +556,14 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   // K-major operand fragments (LAY): per-lane byte offsets of block x's
   // first transposing read within the operand's stage area (block x covers
   // values x0 = w0 + 16 x .. + 15 of the wave's w0 = wm for A, wn for B).
+  // Where a wave's values are 4 or 8 whole blocks from a multiple of their
+  // width, x only enters as an XOR of 32 x (32 x and the row and wave parts
+  // share no bits): the operators' instances keep block 0's offset alone, and
+  // the registers that saves are what keeps their slab loop free of spills.
+  constexpr bool kXorA = MODE != kProduct && (C::kBlocksM == 4 || C::kBlocksM == 8);
+  constexpr bool kXorB = MODE != kProduct && (C::kBlocksN == 4 || C::kBlocksN == 8);
+  const std::integral_constant<bool, kXorA> xor_a{};
+  const std::integral_constant<bool, kXorB> xor_b{};
   uint32_t toffA[kAT ? C::kBlocksM : 1], toffB[kBT ? C::kBlocksN : 1];
   {
     const int ti = lane & 15;
@@ -562,12 +580,16 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   // Block x of k-step s from the operand area `area` (A's or B's part of a
   // stage, offsets toff, k-rows of `pitch` bytes): two transposing reads,
   // k-rows 4 apart.
-  auto tread = [&](const unsigned char* area, const uint32_t* toff, int x, int s, int pitch)
-                   __attribute__((always_inline)) {
+  auto tread = [&](const unsigned char* area, const uint32_t* toff, int x, int s, int pitch,
+                   auto by_xor) __attribute__((always_inline)) {
     typedef short s4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) s4 lds_s4;
     typedef __attribute__((address_space(3))) const unsigned char lds_u8;
     lds_u8* base = (lds_u8*)area + toff[x] + s * 32 * pitch;
+    if constexpr (decltype(by_xor)::value) {
+      const uint32_t block0 = (uint32_t)(uintptr_t)(lds_u8*)area + toff[0];
+      base = (lds_u8*)(uintptr_t)(block0 ^ (32u * x)) + s * 32 * pitch;
+    }
     const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)base);
     const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(base + 4 * pitch));
     return __builtin_bit_cast(h8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
@@ -592,12 +614,12 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     const int pc = (4 * s + g) ^ fr;
 #pragma unroll
     for (int i = 0; i < C::kBlocksM; ++i) {
-      if constexpr (kAT) fa[set][i] = tread(sa, toffA, i, s, kTPA);
+      if constexpr (kAT) fa[set][i] = tread(sa, toffA, i, s, kTPA, xor_a);
       else fa[set][i] = st[a_off + 16 * kChunks * i + pc];
     }
 #pragma unroll
     for (int j = 0; j < C::kBlocksN; ++j) {
-      if constexpr (kBT) fb[kOneB ? 0 : set][j] = tread(sa + kAreaA, toffB, j, s, kTPB);
+      if constexpr (kBT) fb[kOneB ? 0 : set][j] = tread(sa + kAreaA, toffB, j, s, kTPB, xor_b);
       else fb[kOneB ? 0 : set][j] = st[b_off + 16 * kChunks * j + pc];
     }
   };
@@ -615,11 +637,11 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     const unsigned char* sa = lds + stage * kStage;
     const int pc = (4 * step + g) ^ fr;
     if (q < C::kBlocksM) {
-      if constexpr (kAT) fa[set][q] = tread(sa, toffA, q, step, kTPA);
+      if constexpr (kAT) fa[set][q] = tread(sa, toffA, q, step, kTPA, xor_a);
       else fa[set][q] = st[a_off + 16 * kChunks * q + pc];
     } else {
       if constexpr (kBT)
-        fb[set][q - C::kBlocksM] = tread(sa + kAreaA, toffB, q - C::kBlocksM, step, kTPB);
+        fb[set][q - C::kBlocksM] = tread(sa + kAreaA, toffB, q - C::kBlocksM, step, kTPB, xor_b);
       else fb[set][q - C::kBlocksM] = st[b_off + 16 * kChunks * (q - C::kBlocksM) + pc];
     }
   };
@@ -749,6 +771,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   };
+  constexpr float kLog2e = 1.44269504088896340736f;
   auto round4 = [&](f4 x) __attribute__((always_inline)) {
     h4 o;
 #pragma unroll
@@ -828,12 +851,14 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
           for (int v = 0; v < 4; ++v) top = fmaxf(top, acc[i][j][v]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float base = top == -__builtin_inff() ? 0.f : top;
+        // exp(z - top) = 2^(z log2(e) - top log2(e)): the rounding of the second
+        // term is 2^-24 of it, which is what lse = top + log(s) keeps anyway
+        const float base = top == -__builtin_inff() ? 0.f : -top * kLog2e;
         float s = 0.f;
 #pragma unroll
         for (int j = 0; j < C::kBlocksN; ++j)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) s += __expf(acc[i][j][v] - base);
+          for (int v = 0; v < 4; ++v) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, base));
         s += __shfl_xor(s, 16);
         s += __shfl_xor(s, 32);
         if (g == 0 && mine) x.partial[chunk + m] = make_float2(top, s);
@@ -846,6 +871,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       const float f = x.scale ? x.scale[0] : 1.f;
       const int last = (p.N - 1) / BK * BK;   // first column of the last slab of K there
       const bool tail = x.tail != nullptr && n0 + wn + C::WN > p.N - BK;
+      const bool inside = n0 + wn >= x.n_begin && n0 + wn + C::WN <= x.n_end;
 #pragma unroll
       for (int i = 0; i < C::kBlocksM; ++i) {
         const int m = m0 + wm + 16 * i + r;
@@ -853,19 +879,32 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         const long long y = row ? x.targets[m] : x.ignore;
         const bool live = row && y != x.ignore;
         const bool known = y >= 0 && y < x.vocab;
-        const float lse = live ? x.lse[m] : 0.f;
         float w = live ? x.row_scale[m] * f : 0.f;
         if (live && !known) w = __builtin_nanf("");
+        const float base = live ? -x.lse[m] * kLog2e : 0.f;
         const long long at = y - x.col0 - nf;
-        const int rel = at >= 0 && at < C::WN ? (int)at : -1;
+        const int rel = live && at >= 0 && at < C::WN ? (int)at : -1;
 #pragma unroll
         for (int j = 0; j < C::kBlocksN; ++j) {
           f4 d;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const float e = __expf(acc[i][j][v] - lse) - (rel == 16 * j + v ? 1.f : 0.f);
-            const int n = nf + 16 * j + v;
-            d[v] = live && n >= x.n_begin && n < x.n_end ? e * w : 0.f;
+          for (int v = 0; v < 4; ++v)
+            d[v] = live ? __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, base)) * w : 0.f;
+          // the block of the row's target, in the one lane that has it
+          if (rel >> 4 == j && (rel & 15) < 4) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if ((rel & 15) == v) {
+                const float e = __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, base));
+                d[v] = (e - 1.f) * w;
+              }
+          }
+          if (!inside) {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const int n = nf + 16 * j + v;
+              if (n < x.n_begin || n >= x.n_end) d[v] = 0.f;
+            }
           }
           const h4 o = round4(d);
           put(j, o);
@@ -896,14 +935,16 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
 #pragma unroll
       for (int i = 0; i < C::kBlocksM; ++i) {
         const int m = m0 + wm + 16 * i + r;
-        const bool mine = m >= mlo;
-        float* sum = x.sum + (int64_t)m * x.ld_sum + n0 + wn + 4 * g;
-        if (x.sum_read) {
+        if (x.sum) {
+          // rows and columns of an earlier tile are left to it (columns come
+          // in whole quads: N and the tiles' widths are multiples of 8)
+          float* sum = x.sum + part * x.split_stride + (int64_t)m * x.ld_sum + n0 + wn + 4 * g;
+          const bool mine = m >= mlo;
+          if (x.sum_add) {
 #pragma unroll
-          for (int j = 0; j < C::kBlocksN; ++j)
-            if (mine && n0 + wn + 16 * j + 4 * g >= nlo) acc[i][j] += *(const f4*)(sum + 16 * j);
-        }
-        if (x.sum_write) {
+            for (int j = 0; j < C::kBlocksN; ++j)
+              if (mine && n0 + wn + 16 * j + 4 * g >= nlo) acc[i][j] += *(const f4*)(sum + 16 * j);
+          }
 #pragma unroll
           for (int j = 0; j < C::kBlocksN; ++j)
             if (mine && n0 + wn + 16 * j + 4 * g >= nlo) *(f4*)(sum + 16 * j) = acc[i][j];
@@ -954,8 +995,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   constexpr int kReadInstr = kReads + (kAT ? C::kBlocksM : 0) + (kBT ? C::kBlocksN : 0);
   constexpr int kCopies = kPerWaveA + kPerWaveB;
   static_assert(kReadInstr <= kMfma && kCopies <= kMfma, "interleave pattern");
-  const int nk = (MODE == kGradX ? ta.x.parts : 1) *
-                 (SPLIT ? p.sk.per : RAG ? (p.K + BK - 1) / BK : p.K / BK);   // slabs per work item
+  const int nk = SPLIT ? p.sk.per : RAG ? (p.K + BK - 1) / BK : p.K / BK;   // slabs per work item
   // The copy target runs two slabs ahead of the compute: slab tc of the tile
   // `ahead` tiles after the current one (origins o[0..2] are refreshed once
   // per tile, outside the MFMA loop).  Past the end of the stream it stays on
@@ -963,6 +1003,18 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   int tc = 0, ahead = 0, cur = 0;
   int om[3], on[3], ok[3], os[3];
   int mlo0 = 0, nlo0 = 0;   // the current tile's first stored row and column
+  // slabs of the work item `ahead` items after the current one (kGradX: the
+  // last range of K may be shorter)
+  const int nk_all = MODE == kGradX ? ta.x.parts * nk_part : nk;
+  auto slabs_of = [&](int d) __attribute__((always_inline)) {
+    if constexpr (MODE == kGradX) {
+      const int left = nk_all - (d == 0 ? ok[0] : d == 1 ? ok[1] : ok[2]);
+      return left < ta.x.per ? left : ta.x.per;
+    } else {
+      (void)d;
+      return nk;
+    }
+  };
   auto refresh_origins = [&](int j) __attribute__((always_inline)) {
     cur = j;
 #pragma unroll
@@ -973,11 +1025,18 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         mlo0 = mlo;
         nlo0 = nlo;
       }
+      if constexpr (MODE != kProduct) {
+        // wave-uniform, but a 64-bit division leaves them in vector registers
+        om[d] = __builtin_amdgcn_readfirstlane(om[d]);
+        on[d] = __builtin_amdgcn_readfirstlane(on[d]);
+        ok[d] = __builtin_amdgcn_readfirstlane(ok[d]);
+        os[d] = __builtin_amdgcn_readfirstlane(os[d]);
+      }
     }
   };
   refresh_origins(0);
   auto advance_copy = [&]() __attribute__((always_inline)) {
-    if (++tc == nk) {
+    if (++tc == slabs_of(ahead < 2 ? ahead : 2)) {
       tc = 0;
       ++ahead;
     }
@@ -989,10 +1048,10 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     const int m0 = d == 0 ? om[0] : d == 1 ? om[1] : om[2];
     const int n0 = d == 0 ? on[0] : d == 1 ? on[1] : on[2];
     const int kb = d == 0 ? ok[0] : d == 1 ? ok[1] : ok[2];
-    const int t = past ? nk - 1 : tc;
+    const int t = kb + (past ? slabs_of(d) - 1 : tc);
     const int part = MODE == kGradW ? (d == 0 ? os[0] : d == 1 ? os[1] : os[2]) : 0;
-    const bool last = t == nk - 1 || (MODE == kGradX && t == nk_part - 1);
-    return slab_base(stage, m0, n0, kb + t, RAG && kv < BK && last, part);
+    const bool last = MODE == kGradX ? t == nk_part - 1 || t == nk_all - 1 : t == nk - 1;
+    return slab_base(stage, m0, n0, t, RAG && kv < BK && last, part);
   };
   auto copy_next = [&](int stage) __attribute__((always_inline)) {
     const CopyBase cb = next_base(stage);
@@ -1002,7 +1061,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   // zero_next (RAG): the next slab is the last of its tile and reaches past K.
   auto slab = [&](int gs, auto next, auto is_copier, bool zero_next) __attribute__((always_inline)) {
     auto sync = [&]() __attribute__((always_inline)) {
-      if constexpr (RAG) wait_zero_sync(zero_next, (gs + 1) & 1);
+      // kGradX needs no zeros in LDS: its A side of a tail slab has them in memory
+      if constexpr (RAG && MODE != kGradX) wait_zero_sync(zero_next, (gs + 1) & 1);
       else wait_and_sync();
     };
     constexpr bool kCp = decltype(is_copier)::value;
@@ -1037,11 +1097,11 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         if constexpr (step == 0) {
           // step 1 of this slab: A fragment qq, B fragment j after its last use
           if constexpr (qq < MB) {
-            if constexpr (kAT) fa[1][qq] = tread(cur_sa, toffA, qq, 1, kTPA);
+            if constexpr (kAT) fa[1][qq] = tread(cur_sa, toffA, qq, 1, kTPA, xor_a);
             else fa[1][qq] = cur_st[a_off + 16 * kChunks * qq + pc1];
           }
           if constexpr (i == MB - 1) {
-            if constexpr (kBT) fb[0][j] = tread(cur_sa + kAreaA, toffB, j, 1, kTPB);
+            if constexpr (kBT) fb[0][j] = tread(cur_sa + kAreaA, toffB, j, 1, kTPB, xor_b);
             else fb[0][j] = cur_st[b_off + 16 * kChunks * j + pc1];
           }
         }
@@ -1050,7 +1110,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
           static_for<MB>([&](auto ic) __attribute__((always_inline)) {
             constexpr int i2 = decltype(ic)::value;
             if constexpr (q == (kB > kMfma + i2 ? kB : kMfma + i2)) {
-              if constexpr (kAT) fa[0][i2] = tread(nxt_sa, toffA, i2, 0, kTPA);
+              if constexpr (kAT) fa[0][i2] = tread(nxt_sa, toffA, i2, 0, kTPA, xor_a);
               else fa[0][i2] = nxt_st[a_off + 16 * kChunks * i2 + pc0];
             }
           });
@@ -1058,7 +1118,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
             constexpr int j2 = decltype(jc)::value;
             constexpr int last = kMfma + MB * j2 + MB - 1;
             if constexpr (q == (kB > last ? kB : last)) {
-              if constexpr (kBT) fb[0][j2] = tread(nxt_sa + kAreaA, toffB, j2, 0, kTPB);
+              if constexpr (kBT) fb[0][j2] = tread(nxt_sa + kAreaA, toffB, j2, 0, kTPB, xor_b);
               else fb[0][j2] = nxt_st[b_off + 16 * kChunks * j2 + pc0];
             }
           });
@@ -1129,14 +1189,12 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     // RAG: slab nk - 1 reaches past K when kv < BK; it is the next slab of
     // slab nk - 2 (nk >= 2: K > BK).  The next tile's first slab never is.
     const int zt = RAG && kv < BK ? nk - 2 : -1;
-    const int zt0 = MODE == kGradX && kv < BK ? nk_part - 2 : -1;   // the first part's
+    const int nk_item = slabs_of(0);
     if (copies) {
-      for (int t = 0; t + 1 < nk; ++t, ++gs)
-        slab(gs, yes(), yes(), t == zt || (MODE == kGradX && t == zt0));
+      for (int t = 0; t + 1 < nk_item; ++t, ++gs) slab(gs, yes(), yes(), t == zt);
       slab(gs, no(), yes(), false);
     } else {
-      for (int t = 0; t + 1 < nk; ++t, ++gs)
-        slab(gs, yes(), no(), t == zt || (MODE == kGradX && t == zt0));
+      for (int t = 0; t + 1 < nk_item; ++t, ++gs) slab(gs, yes(), no(), t == zt);
       slab(gs, no(), no(), false);
     }
     ++gs;
@@ -1177,15 +1235,16 @@ hipError_t launch(const Args16& a, int slots, hipStream_t stream) {
       dim3((unsigned)grid), dim3(C::kThreads), args, 0, stream);
 }
 
-// An operator's mode over the tiles of its output: ceil(M / BM) (times the
-// parts of kGradW) by ceil(N / BN) (kGated: BN / 2) of them, persistent.
+// An operator's mode over the tiles of its output: ceil(M / BM) by ceil(N / BN)
+// (kGated: BN / 2) of them, times kGradW's parts or kGradX's ranges of K;
+// persistent.
 template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int GM, int COPY_SEL, int OPT, int FMT,
           int LAY, int MODE>
 hipError_t launch_fused(const Args16& a, const FusedExtra& x, int slots, hipStream_t stream) {
   typedef Config<BM, BN, BK, WAVES_M, WAVES_N, COPY_SEL> C;
   constexpr int kTileN = MODE == kGated ? BN / 2 : BN;
-  const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * (MODE == kGradW ? x.parts : 1) *
-                        ((a.N + kTileN - 1) / kTileN);
+  const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * ((a.N + kTileN - 1) / kTileN) *
+                        (MODE == kGradW ? x.parts : MODE == kGradX ? x.splits : 1);
   int64_t grid = tiles < slots ? tiles : slots;
   if (grid < 1) grid = 1;
   FusedTileArgs ta{a, tiles, x};
