@@ -10,7 +10,7 @@
 // adds); bf16 has no packed add, so a second product of X with ones makes the
 // group's sum of x and (128 + z) times it is taken off in fp32 (the matrix
 // cores idle here: the bound is HBM).  s multiplies the group's fp32 sum.  X
-// is put in the nibbles' order (0 4 1 5 2 6 3 7) in registers.
+// is put in the nibbles' order (0 4 1 5 2 6 3 7), once where it is kept in LDS.
 //
 // Where a block holds several groups (a group is a multiple of 32) each step
 // of 32 k must lie in one: the four lanes of a row exchange words (a 4 x 4
@@ -29,8 +29,10 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBlock = 128;   // K values of a block
-constexpr int kUnroll = 4;    // blocks in flight a wave
+constexpr int kUnroll = 4;    // blocks of a chunk; a wave has two chunks in flight
 constexpr int kMaxWaves = 8;
+constexpr int kStaged = 4;    // 16-byte pieces of X a thread loads ahead of its weights
+constexpr int kXBytes = 32 << 10;   // X up to this size is kept in LDS
 
 struct W4Args {
   const half_t* X;
@@ -41,61 +43,67 @@ struct W4Args {
   const half_t* res;
   half_t* C;
   int64_t ldx, ldq, lds, ldz, ldr, ldc;
-  int M, N, K, group, act, waves;
+  int M, N, K, group, act, waves, chunks;
 };
 
-// How the groups lie in a block: one a block (group % 128 == 0), two of 64,
-// four of 32, or any other multiple of 32 (a lookup for each step).
-enum Groups { kOne = 0, kTwo, kFour, kAny };
+// How the groups lie in blocks: one a block (128), two (64), four (32), one
+// for several blocks (a larger multiple of 128: looked up for each block), or
+// any other multiple of 32 (looked up for each step of 32 k).
+enum Groups { kOne = 0, kTwo, kFour, kWide, kAny };
+constexpr int groups_per_block(int gr) { return gr == kTwo ? 2 : gr >= kFour && gr != kWide ? 4 : 1; }
 
-// A block as loaded: weights, and the raw scales and zero points of its
-// groups (up to four of each).
-struct Block {
-  u4 w;
-  uint16_t s[4];
-  uint8_t z[4];
+// U blocks as loaded: weights, and the raw scales and zero points of their groups.
+template <int GR, int U>
+struct Blocks {
+  static constexpr int kG = groups_per_block(GR);
+  u4 w[U];
+  uint16_t s[U * kG];
+  uint8_t z[U * kG];
 };
 
-template <int GR, bool TAIL>
-__device__ __forceinline__ Block load_block(const W4Args& p, const uint8_t* row,
-                                            const half_t* scales, const uint8_t* zeros, int block,
-                                            int quarter) {
-  Block b;
+// Zero points of a call without any.
+__device__ const uint8_t kEights[16] = {8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8};
+
+// A lane's weight row.  No zero points: kEights, whose groups all have index 0.
+struct Row {
+  const uint8_t* w;
+  const half_t* s;
+  const uint8_t* z;
+  int z_mask;
+};
+
+template <int GR, int U, bool TAIL>
+__device__ __forceinline__ void load_blocks(const W4Args& p, const Row& row, int block, int quarter,
+                                            Blocks<GR, U>& b) {
+  constexpr int kG = Blocks<GR, U>::kG;
   const int k0 = block * kBlock;
-  const uint8_t* src = row + (int64_t)block * (kBlock / 2) + 16 * quarter;
+  const uint8_t* src = row.w + (int64_t)block * (kBlock / 2) + 16 * quarter;
   if constexpr (!TAIL) {
-    __builtin_memcpy(&b.w, src, 16);
+#pragma unroll
+    for (int u = 0; u < U; ++u) __builtin_memcpy(&b.w[u], src + u * (kBlock / 2), 16);
   } else {
-    // the bytes inside the row only; past it the weights meet zeros of X
+    // one block: the bytes inside the row only; past it the weights meet zeros of X
     const int have = p.K / 2 + (p.K & 1) - (k0 / 2 + 16 * quarter);
-    b.w = u4{0, 0, 0, 0};
+    u4 w = {0, 0, 0, 0};
 #pragma unroll
     for (int e = 0; e < 16; ++e)
-      if (e < have) b.w[e / 4] |= (uint32_t)src[e] << (8 * (e % 4));
+      if (e < have) w[e / 4] |= (uint32_t)src[e] << (8 * (e % 4));
+    b.w[0] = w;
   }
-  constexpr int kN = GR == kOne ? 1 : GR == kTwo ? 2 : 4;
-  uint16_t s[kN];
-  uint8_t z[kN];
-  if constexpr (!TAIL && GR != kAny) {
-    const int g0 = GR == kOne ? k0 / p.group : block * kN;
-    __builtin_memcpy(s, scales + g0, 2 * kN);
-    if (zeros) __builtin_memcpy(z, zeros + g0, kN);
+  if constexpr (!TAIL && GR <= kFour) {
+    const int g0 = block * kG;
+    __builtin_memcpy(b.s, row.s + g0, 2 * U * kG);
+    __builtin_memcpy(b.z, row.z + (g0 & row.z_mask), U * kG);
   } else {
-    // group of each step, the last one past the row's end
+    // the group of each block or step, the last one past the row's end
     const int last = (p.K - 1) / p.group;
 #pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      const int g = min((k0 + j * (kBlock / kN)) / p.group, last);
-      s[j] = __builtin_bit_cast(uint16_t, scales[g]);
-      if (zeros) z[j] = zeros[g];
+    for (int j = 0; j < U * kG; ++j) {
+      const int g = min((k0 + j * (kBlock / kG)) / p.group, last);
+      b.s[j] = __builtin_bit_cast(uint16_t, row.s[g]);
+      b.z[j] = row.z[g & row.z_mask];
     }
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    b.s[j] = s[j * kN / 4];
-    b.z[j] = zeros ? z[j * kN / 4] : (uint8_t)8;
-  }
-  return b;
 }
 
 // Word j of lane row c becomes word c of lane row j.
@@ -121,106 +129,177 @@ __device__ __forceinline__ h8 reorder(h8 v) {
   return __builtin_shufflevector(v, v, 0, 4, 1, 5, 2, 6, 3, 7);
 }
 
-template <int FMT, int GR, int MT, bool TAIL>
-__device__ __forceinline__ void multiply(const W4Args& p, const Block& b,
-                                         const half_t* const (&xrow)[MT], int block, int quarter,
-                                         f4 (&tot)[MT]) {
-  const u4 w = GR == kOne ? b.w : transpose4(b.w);
-  f4 acc[MT], sum[MT];
+// First k of step j of a block for a lane.
+template <int GR>
+__device__ __forceinline__ int step_k(int j, int quarter) {
+  return groups_per_block(GR) == 1 ? 32 * quarter + 8 * j : 32 * j + 8 * quarter;
+}
+
+// One block's products.  x[t][j]: the X fragments of its four steps, reordered.
+template <int FMT, int GR, int MT>
+__device__ __forceinline__ void multiply(u4 raw, const uint16_t* scales, const uint8_t* zeros,
+                                         const h8 (&x)[MT][4], f4 (&tot)[MT]) {
+  constexpr int kG = groups_per_block(GR), kSteps = 4 / kG;   // steps of a group
+  const u4 w = kG == 1 ? raw : transpose4(raw);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    constexpr int kSteps = GR == kOne ? 4 : GR == kTwo ? 2 : 1;   // steps of a group
-    if (j % kSteps == 0) {
+  for (int g = 0; g < kG; ++g) {
+    f4 acc[MT], sum[MT];
 #pragma unroll
-      for (int t = 0; t < MT; ++t) acc[t] = sum[t] = f4{0.f, 0.f, 0.f, 0.f};
-    }
-    const int k = block * kBlock + (GR == kOne ? 32 * quarter + 8 * j : 32 * j + 8 * quarter);
-    u4 q = spread<FMT>(w[j]);
-    if constexpr (FMT == kFmtF16) {
-      const half_t off = (half_t)(-1024.f - (float)b.z[j]);
+    for (int t = 0; t < MT; ++t) acc[t] = sum[t] = f4{0.f, 0.f, 0.f, 0.f};
+    const float z = (float)zeros[g];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t pair = q[i];
-        q[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, pair) + h2{off, off});
+    for (int j = g * kSteps; j < (g + 1) * kSteps; ++j) {
+      u4 q = spread<FMT>(w[j]);
+      if constexpr (FMT == kFmtF16) {
+        const half_t off = (half_t)(-1024.f - z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t pair = q[i];
+          q[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, pair) + h2{off, off});
+        }
+      }
+      const h8 wf = __builtin_bit_cast(h8, q);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        acc[t] = mfma16<FMT>(x[t][j], wf, acc[t]);
+        if constexpr (FMT == kFmtBF16) {
+          const u4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+          sum[t] = mfma16<FMT>(x[t][j], __builtin_bit_cast(h8, ones), sum[t]);
+        }
       }
     }
-    const h8 wf = __builtin_bit_cast(h8, q);
+    const uint16_t bits = scales[g];
+    const float s = word_to_f32<FMT>(__builtin_bit_cast(half_t, bits));
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      const h8 x = reorder(load_x<TAIL>(xrow[t], k, p.K));
-      acc[t] = mfma16<FMT>(x, wf, acc[t]);
-      if constexpr (FMT == kFmtBF16) {
-        const u4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-        sum[t] = mfma16<FMT>(x, __builtin_bit_cast(h8, ones), sum[t]);
-      }
-    }
-    if (j % kSteps == kSteps - 1) {
-      const float s = word_to_f32<FMT>(__builtin_bit_cast(half_t, b.s[j]));
-      const float off = 128.f + (float)b.z[j];
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          tot[t][v] += s * (FMT == kFmtBF16 ? acc[t][v] - off * sum[t][v] : acc[t][v]);
-    }
+      for (int v = 0; v < 4; ++v)
+        tot[t][v] += s * (FMT == kFmtBF16 ? acc[t][v] - (128.f + z) * sum[t][v] : acc[t][v]);
   }
 }
 
-template <int FMT, int GR, int MT>
+// XL: the rows of X (M <= 16 of them) lie in LDS, reordered, zero past K, in
+// rows of K rounded up to blocks plus 16 bytes (rows then start in different
+// banks).  Otherwise they are read from global memory (L2) one block ahead.
+template <int FMT, int GR, int MT, bool XL>
 __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t base) {
-  extern __shared__ __attribute__((aligned(16))) float lds[];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, quarter = lane >> 4;
   const int64_t groups_n = (p.N + 15) / 16;
   const int64_t id = base + blockIdx.x;
   const int m0 = (int)(id / groups_n) * 64;
   const int n = (int)(id % groups_n) * 16 + r;
-  const int row = n < p.N ? n : p.N - 1;   // rows past N repeat the last one, unstored
-  const uint8_t* wrow = p.Wq + row * p.ldq;
-  const half_t* scales = p.scales + row * p.lds;
-  const uint8_t* zeros = p.zeros ? p.zeros + row * p.ldz : nullptr;
-  const half_t* xrow[MT];
+  const int nr = n < p.N ? n : p.N - 1;   // rows past N repeat the last one, unstored
+  const Row row{p.Wq + nr * p.ldq, p.scales + nr * p.lds,
+                p.zeros ? p.zeros + nr * p.ldz : kEights, p.zeros ? -1 : 0};
+  const int blocks = (int)(((int64_t)p.K + kBlock - 1) / kBlock), full = p.K / kBlock;
+  const int64_t x_pitch = (int64_t)blocks * (kBlock * 2) + 16;
+
+  // X's first pieces, then the wave's first two chunks of weights, then the
+  // pieces go to LDS: loads return in order, so X does not wait for them.
+  h8 staged[kStaged];
+  const int row_pieces = blocks * (kBlock / 8);
+  const int pieces = p.M * row_pieces;
+  auto load_piece = [&](int i) __attribute__((always_inline)) {
+    return reorder(load_x<true>(p.X + (int64_t)(i / row_pieces) * p.ldx, i % row_pieces * 8, p.K));
+  };
+  auto store_piece = [&](int i, h8 v) __attribute__((always_inline)) {
+    *(h8*)(lds + i / row_pieces * x_pitch + i % row_pieces * 16) = v;
+  };
+  if constexpr (XL) {
+#pragma unroll
+    for (int q = 0; q < kStaged; ++q)
+      if (tid + q * (int)blockDim.x < pieces) staged[q] = load_piece(tid + q * blockDim.x);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  Blocks<GR, kUnroll> cur, nxt;
+  int c = wave;
+  if (c < p.chunks) {
+    load_blocks<GR, kUnroll, false>(p, row, c * kUnroll, quarter, cur);
+    const int cn = c + p.waves < p.chunks ? c + p.waves : c;
+    load_blocks<GR, kUnroll, false>(p, row, cn * kUnroll, quarter, nxt);
+  }
+  if constexpr (XL) {
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < kStaged; ++q)
+      if (tid + q * (int)blockDim.x < pieces) store_piece(tid + q * blockDim.x, staged[q]);
+    for (int i = tid + kStaged * blockDim.x; i < pieces; i += blockDim.x)
+      store_piece(i, load_piece(i));
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
+
+  // Fragments of X: rows past M repeat the last one, unstored.
+  const half_t* xg[MT];
+  const unsigned char* xl = lds + (r < p.M ? r : p.M - 1) * x_pitch;
 #pragma unroll
   for (int t = 0; t < MT; ++t) {
     const int m = m0 + 16 * t + r;
-    xrow[t] = p.X + (m < p.M ? m : p.M - 1) * p.ldx;   // rows past M repeat the last, unstored
+    xg[t] = p.X + (m < p.M ? m : p.M - 1) * p.ldx;
   }
+  auto read_x = [&](h8 (&x)[MT][4], int block, auto tail) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = block * kBlock + step_k<GR>(j, quarter);
+        if constexpr (XL) x[t][j] = *(const h8*)(xl + 2 * k);
+        else x[t][j] = load_x<decltype(tail)::value>(xg[t], k, p.K);
+      }
+  };
+  auto ordered = [&](h8 (&x)[MT][4]) __attribute__((always_inline)) {
+    if constexpr (!XL) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[t][j] = reorder(x[t][j]);
+    }
+  };
+  constexpr int kG = groups_per_block(GR);
   f4 tot[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) tot[t] = f4{0.f, 0.f, 0.f, 0.f};
 
-  // chunks of kUnroll blocks, in turn to the waves; then the blocks left over
-  const int full = p.K / kBlock, chunks = full / kUnroll;
-  Block cur[kUnroll], nxt[kUnroll];
-  int c = wave;
-  if (c < chunks) {
+  const std::integral_constant<bool, false> inside{};
+  const std::integral_constant<bool, true> at_end{};
+  // (64 rows: one set of fragments, two and their weights do not fit the registers)
+  constexpr int kSets = MT < 4 ? 2 : 1;
+  h8 x[kSets][MT][4];
+  if (kSets == 2 && c < p.chunks) read_x(x[0], c * kUnroll, inside);
+  for (; c < p.chunks; c += p.waves) {
+    const int cn = c + p.waves < p.chunks ? c + p.waves : c;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      cur[u] = load_block<GR, false>(p, wrow, scales, zeros, c * kUnroll + u, quarter);
+    for (int u = 0; u < kUnroll; ++u) {
+      if constexpr (kSets == 2)
+        read_x(x[(u + 1) & 1], u + 1 < kUnroll ? c * kUnroll + u + 1 : cn * kUnroll, inside);
+      else
+        read_x(x[0], c * kUnroll + u, inside);
+      ordered(x[u & (kSets - 1)]);
+      multiply<FMT, GR, MT>(cur.w[u], cur.s + u * kG, cur.z + u * kG, x[u & (kSets - 1)], tot);
+    }
+    cur = nxt;
+    const int cnn = cn + p.waves < p.chunks ? cn + p.waves : cn;
+    load_blocks<GR, kUnroll, false>(p, row, cnn * kUnroll, quarter, nxt);
   }
-  for (; c < chunks; c += p.waves) {
-    const int cn = c + p.waves < chunks ? c + p.waves : c;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      nxt[u] = load_block<GR, false>(p, wrow, scales, zeros, cn * kUnroll + u, quarter);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      multiply<FMT, GR, MT, false>(p, cur[u], xrow, c * kUnroll + u, quarter, tot);
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) cur[u] = nxt[u];
-  }
-  const int left = chunks * kUnroll;
+  // blocks left over, one at a time in turn to the waves
+  const int left = p.chunks * kUnroll;
+  Blocks<GR, 1> one;
   for (int b = left + wave; b < full; b += p.waves) {
-    const Block k = load_block<GR, false>(p, wrow, scales, zeros, b, quarter);
-    multiply<FMT, GR, MT, false>(p, k, xrow, b, quarter, tot);
+    load_blocks<GR, 1, false>(p, row, b, quarter, one);
+    read_x(x[0], b, inside);
+    ordered(x[0]);
+    multiply<FMT, GR, MT>(one.w[0], one.s, one.z, x[0], tot);
   }
-  if (full * kBlock < p.K && wave == (full - left) % p.waves) {
-    const Block k = load_block<GR, true>(p, wrow, scales, zeros, full, quarter);
-    multiply<FMT, GR, MT, true>(p, k, xrow, full, quarter, tot);
+  if (full < blocks && wave == (full - left) % p.waves) {
+    load_blocks<GR, 1, true>(p, row, full, quarter, one);
+    read_x(x[0], full, at_end);
+    ordered(x[0]);
+    multiply<FMT, GR, MT>(one.w[0], one.s, one.z, x[0], tot);
   }
 
-  add_waves<MT>(tot, lds, wave, lane, p.waves);
+  add_waves<MT>(tot, reinterpret_cast<float*>(lds + (XL ? p.M * x_pitch : 0)), wave, lane, p.waves);
   if (wave > 0 || n >= p.N) return;
   const float bias = p.bias ? word_to_f32<FMT>(p.bias[n]) : 0.f;
 #pragma unroll
@@ -235,19 +314,21 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t ba
     }
 }
 
-typedef void (*W4Kernel)(W4Args, int64_t);
-
 template <int FMT, int GR>
-W4Kernel pick_rows(int M) {
-  return M <= 16 ? w4_kernel<FMT, GR, 1> : M <= 32 ? w4_kernel<FMT, GR, 2> : w4_kernel<FMT, GR, 4>;
+const void* pick_rows(int M, bool x_in_lds) {
+  if (x_in_lds) return (const void*)w4_kernel<FMT, GR, 1, true>;
+  return M <= 16   ? (const void*)w4_kernel<FMT, GR, 1, false>
+         : M <= 32 ? (const void*)w4_kernel<FMT, GR, 2, false>
+                   : (const void*)w4_kernel<FMT, GR, 4, false>;
 }
 
 template <int FMT>
-W4Kernel pick(int M, int group) {
-  if (group % kBlock == 0) return pick_rows<FMT, kOne>(M);
-  if (group == 64) return pick_rows<FMT, kTwo>(M);
-  if (group == 32) return pick_rows<FMT, kFour>(M);
-  return pick_rows<FMT, kAny>(M);
+const void* pick(int M, int group, bool x_in_lds) {
+  if (group == kBlock) return pick_rows<FMT, kOne>(M, x_in_lds);
+  if (group == 64) return pick_rows<FMT, kTwo>(M, x_in_lds);
+  if (group == 32) return pick_rows<FMT, kFour>(M, x_in_lds);
+  if (group % kBlock == 0) return pick_rows<FMT, kWide>(M, x_in_lds);
+  return pick_rows<FMT, kAny>(M, x_in_lds);
 }
 
 }  // namespace
@@ -276,13 +357,19 @@ extern "C" MI355FUSED_API int gemm_w4(int type, int M, int N, int K, int group, 
   W4Args a{static_cast<const half_t*>(X), static_cast<const uint8_t*>(Wq),
            static_cast<const half_t*>(scales), static_cast<const uint8_t*>(zeros),
            static_cast<const half_t*>(bias), static_cast<const half_t*>(residual),
-           static_cast<half_t*>(C), ldx, ldq, lds, ldz, ldr, ldc, M, N, K, group, act, 0};
+           static_cast<half_t*>(C), ldx, ldq, lds, ldz, ldr, ldc, M, N, K, group, act, 0, 0};
   const int mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
   const int64_t wgs = ((int64_t)N + 15) / 16 * (((int64_t)M + 63) / 64);
-  const int waves = skinny::waves_for(wgs, std::max(1, K / kBlock), kMaxWaves, cus);
-  a.waves = waves;
-  const unsigned lds_bytes = (unsigned)((waves - 1) * mt * 64 * sizeof(f4));
-  const void* k = type == GEMM_TYPE_BF16 ? (const void*)pick<kFmtBF16>(M, group)
-                                         : (const void*)pick<kFmtF16>(M, group);
-  return to_status(launch_tiles(k, a, wgs, 64 * waves, lds_bytes, static_cast<hipStream_t>(stream)));
+  const int64_t blocks = ((int64_t)K + kBlock - 1) / kBlock;
+  a.waves = skinny::waves_for(wgs, std::max<int>(1, (int)blocks), kMaxWaves, cus);
+  // whole chunks only where every wave has one
+  a.chunks = K / kBlock >= kUnroll * a.waves ? K / (kBlock * kUnroll) : 0;
+  const int64_t x_bytes = M * (blocks * kBlock * 2 + 16);
+  const bool x_in_lds = M <= 16 && K > 0 && x_bytes <= kXBytes;
+  const unsigned lds_bytes =
+      (unsigned)((x_in_lds ? x_bytes : 0) + (a.waves - 1) * mt * 64 * sizeof(f4));
+  const void* k = type == GEMM_TYPE_BF16 ? pick<kFmtBF16>(M, group, x_in_lds)
+                                         : pick<kFmtF16>(M, group, x_in_lds);
+  return to_status(
+      launch_tiles(k, a, wgs, 64 * a.waves, lds_bytes, static_cast<hipStream_t>(stream)));
 }
