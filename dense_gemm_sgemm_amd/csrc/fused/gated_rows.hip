@@ -74,8 +74,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_rows_kernel(RowsArgs p, 
   int c = wave;
   if (c < chunks) load_chunk<false>(wg, wu, c * kChunk, K, cur);
   for (; c < chunks; c += p.waves) {
-    const int cn = c + p.waves < chunks ? c + p.waves : c;
-    load_chunk<false>(wg, wu, cn * kChunk, K, nxt);
+    if (c + p.waves < chunks) load_chunk<false>(wg, wu, (c + p.waves) * kChunk, K, nxt);
     multiply<FMT, MT, false>(xrow, c * kChunk, K, cur, acc);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {

@@ -52,11 +52,12 @@ __device__ __forceinline__ void add_waves(f4 (&acc)[Q], float* lds, int wave, in
     for (int q = 0; q < Q; ++q) acc[q] += part[(w * Q + q) * 64 + lane];
 }
 
-// Waves of a workgroup that share `pieces` of K: four, or more while they have
-// a piece each and the launch has less than 16 waves a CU.
+// Waves of a workgroup that share `pieces` of K: four, or eight while they have
+// two pieces each (one to multiply, one in flight) and the launch has less than
+// 32 waves a CU; fewer where there are fewer pieces.
 inline int waves_for(int64_t workgroups, int pieces, int most, int cus) {
   int waves = 4;
-  while (waves < most && 2 * waves <= pieces && workgroups * waves < 16 * (int64_t)cus) waves *= 2;
+  while (waves < most && 4 * waves <= pieces && workgroups * waves < 32 * (int64_t)cus) waves *= 2;
   while (waves > 1 && waves > pieces) waves /= 2;
   return waves;
 }

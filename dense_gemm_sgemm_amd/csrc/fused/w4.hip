@@ -4,13 +4,13 @@
 // W[n][k] = (q - z) s with one s and z for each group of a row.  A lane takes
 // 16 bytes = 32 weights of its row in one load, so a wave takes 16 rows x 128
 // k ("a block") at a time.  The nibbles become 16-bit floats without a
-// conversion: (word >> 4 i) & 0x000f000f picks k = i and i + 4 of the word's
-// eight, and or-ing in an exponent makes 1024 + q (fp16, 0x6400) or 128 + q
-// (bf16, 0x4300), both exact.  fp16 then subtracts 1024 + z exactly (packed
-// adds); bf16 has no packed add, so a second product of X with ones makes the
-// group's sum of x and (128 + z) times it is taken off in fp32 (the matrix
-// cores idle here: the bound is HBM).  s multiplies the group's fp32 sum.  X
-// is put in the nibbles' order (0 4 1 5 2 6 3 7), once where it is kept in LDS.
+// conversion: a mask picks k = i and i + 4 of a word's eight, and or-ing in an
+// exponent makes 1024 + q or 64 + q (fp16) or 128 + q (bf16), all exact.  fp16
+// then subtracts the offset and z exactly (packed adds); bf16 has no packed
+// add, so a second product of X with ones makes the group's sum of x and
+// (128 + z) times it is taken off in fp32 (the matrix cores idle here: the
+// bound is HBM).  s multiplies the group's fp32 sum.  X is put in the nibbles'
+// order (0 4 1 5 2 6 3 7), once where it is kept in LDS.
 //
 // Where a block holds several groups (a group is a multiple of 32) each step
 // of 32 k must lie in one: the four lanes of a row exchange words (a 4 x 4
@@ -61,14 +61,19 @@ struct Blocks {
   uint8_t z[U * kG];
 };
 
+// A pointer to global memory: loads through it are no flat loads, which would
+// wait for LDS reads too.
+template <typename T>
+using Global = __attribute__((address_space(1))) const T*;
+
 // Zero points of a call without any.
 __device__ const uint8_t kEights[16] = {8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8, 8};
 
 // A lane's weight row.  No zero points: kEights, whose groups all have index 0.
 struct Row {
-  const uint8_t* w;
-  const half_t* s;
-  const uint8_t* z;
+  Global<uint8_t> w;
+  Global<uint16_t> s;
+  Global<uint8_t> z;
   int z_mask;
 };
 
@@ -77,7 +82,7 @@ __device__ __forceinline__ void load_blocks(const W4Args& p, const Row& row, int
                                             Blocks<GR, U>& b) {
   constexpr int kG = Blocks<GR, U>::kG;
   const int k0 = block * kBlock;
-  const uint8_t* src = row.w + (int64_t)block * (kBlock / 2) + 16 * quarter;
+  Global<uint8_t> src = row.w + (int64_t)block * (kBlock / 2) + 16 * quarter;
   if constexpr (!TAIL) {
 #pragma unroll
     for (int u = 0; u < U; ++u) __builtin_memcpy(&b.w[u], src + u * (kBlock / 2), 16);
@@ -100,7 +105,7 @@ __device__ __forceinline__ void load_blocks(const W4Args& p, const Row& row, int
 #pragma unroll
     for (int j = 0; j < U * kG; ++j) {
       const int g = min((k0 + j * (kBlock / kG)) / p.group, last);
-      b.s[j] = __builtin_bit_cast(uint16_t, row.s[g]);
+      b.s[j] = row.s[g];
       b.z[j] = row.z[g & row.z_mask];
     }
   }
@@ -115,13 +120,42 @@ __device__ __forceinline__ u4 transpose4(u4 w) {
   return u4{c[0], c[1], d[0], d[1]};
 }
 
-// Eight nibbles as 16-bit floats 1024 + q (fp16) or 128 + q (bf16), k in the
-// order 0 4 1 5 2 6 3 7.
+// a & mask | bits in one instruction: the two constants would not both fit it
+// as literals, so `bits` is kept in a register the compiler cannot see through.
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t bits) {
+  return (a & mask) | bits;
+}
 template <int FMT>
-__device__ __forceinline__ u4 spread(uint32_t w) {
-  constexpr uint32_t kOr = FMT == kFmtF16 ? 0x64006400u : 0x43004300u;
-  return u4{(w & 0x000f000fu) | kOr, ((w >> 4) & 0x000f000fu) | kOr,
-            ((w >> 8) & 0x000f000fu) | kOr, ((w >> 12) & 0x000f000fu) | kOr};
+struct Magic {
+  uint32_t low, high;
+  __device__ __forceinline__ Magic() {
+    low = FMT == kFmtF16 ? 0x64006400u : 0x43004300u;
+    high = 0x54005400u;
+    asm("" : "+v"(low));
+    if constexpr (FMT == kFmtF16) asm("" : "+v"(high));
+  }
+};
+
+// Eight nibbles as 16-bit floats, k in the order 0 4 1 5 2 6 3 7: bf16 128 + q;
+// fp16 q - z, from 1024 + q where the nibble lies in the low four bits of a
+// half word and 64 + q where it lies in the next four (no shift).
+template <int FMT>
+__device__ __forceinline__ u4 spread(uint32_t w, const Magic<FMT>& magic, float z) {
+  if constexpr (FMT == kFmtF16) {
+    const half_t a = (half_t)(-1024.f - z), b = (half_t)(-64.f - z);
+    const h2 offa = {a, a}, offb = {b, b};
+    const uint32_t v = w >> 8;
+    const uint32_t q[4] = {and_or(w, 0x000f000fu, magic.low), and_or(w, 0x00f000f0u, magic.high),
+                           and_or(v, 0x000f000fu, magic.low), and_or(v, 0x00f000f0u, magic.high)};
+    u4 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, q[i]) + (i & 1 ? offb : offa));
+    return r;
+  } else {
+    return u4{and_or(w, 0x000f000fu, magic.low), and_or(w >> 4, 0x000f000fu, magic.low),
+              and_or(w >> 8, 0x000f000fu, magic.low), and_or(w >> 12, 0x000f000fu, magic.low)};
+  }
 }
 
 // The same order for eight X values.
@@ -138,7 +172,8 @@ __device__ __forceinline__ int step_k(int j, int quarter) {
 // One block's products.  x[t][j]: the X fragments of its four steps, reordered.
 template <int FMT, int GR, int MT>
 __device__ __forceinline__ void multiply(u4 raw, const uint16_t* scales, const uint8_t* zeros,
-                                         const h8 (&x)[MT][4], f4 (&tot)[MT]) {
+                                         const h8 (&x)[MT][4], const Magic<FMT>& magic,
+                                         f4 (&tot)[MT]) {
   constexpr int kG = groups_per_block(GR), kSteps = 4 / kG;   // steps of a group
   const u4 w = kG == 1 ? raw : transpose4(raw);
 #pragma unroll
@@ -149,16 +184,7 @@ __device__ __forceinline__ void multiply(u4 raw, const uint16_t* scales, const u
     const float z = (float)zeros[g];
 #pragma unroll
     for (int j = g * kSteps; j < (g + 1) * kSteps; ++j) {
-      u4 q = spread<FMT>(w[j]);
-      if constexpr (FMT == kFmtF16) {
-        const half_t off = (half_t)(-1024.f - z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t pair = q[i];
-          q[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, pair) + h2{off, off});
-        }
-      }
-      const h8 wf = __builtin_bit_cast(h8, q);
+      const h8 wf = __builtin_bit_cast(h8, spread<FMT>(w[j], magic, z));
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         acc[t] = mfma16<FMT>(x[t][j], wf, acc[t]);
@@ -192,8 +218,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t ba
   const int m0 = (int)(id / groups_n) * 64;
   const int n = (int)(id % groups_n) * 16 + r;
   const int nr = n < p.N ? n : p.N - 1;   // rows past N repeat the last one, unstored
-  const Row row{p.Wq + nr * p.ldq, p.scales + nr * p.lds,
-                p.zeros ? p.zeros + nr * p.ldz : kEights, p.zeros ? -1 : 0};
+  const Row row{(Global<uint8_t>)(p.Wq + nr * p.ldq), (Global<uint16_t>)(p.scales + nr * p.lds),
+                p.zeros ? (Global<uint8_t>)(p.zeros + nr * p.ldz) : (Global<uint8_t>)kEights,
+                p.zeros ? -1 : 0};
   const int blocks = (int)(((int64_t)p.K + kBlock - 1) / kBlock), full = p.K / kBlock;
   const int64_t x_pitch = (int64_t)blocks * (kBlock * 2) + 16;
 
@@ -218,8 +245,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t ba
   int c = wave;
   if (c < p.chunks) {
     load_blocks<GR, kUnroll, false>(p, row, c * kUnroll, quarter, cur);
-    const int cn = c + p.waves < p.chunks ? c + p.waves : c;
-    load_blocks<GR, kUnroll, false>(p, row, cn * kUnroll, quarter, nxt);
+    if (c + p.waves < p.chunks)
+      load_blocks<GR, kUnroll, false>(p, row, (c + p.waves) * kUnroll, quarter, nxt);
   }
   if constexpr (XL) {
     __builtin_amdgcn_sched_barrier(0);
@@ -258,6 +285,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t ba
     }
   };
   constexpr int kG = groups_per_block(GR);
+  const Magic<FMT> magic;
   f4 tot[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) tot[t] = f4{0.f, 0.f, 0.f, 0.f};
@@ -277,11 +305,12 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t ba
       else
         read_x(x[0], c * kUnroll + u, inside);
       ordered(x[u & (kSets - 1)]);
-      multiply<FMT, GR, MT>(cur.w[u], cur.s + u * kG, cur.z + u * kG, x[u & (kSets - 1)], tot);
+      multiply<FMT, GR, MT>(cur.w[u], cur.s + u * kG, cur.z + u * kG, x[u & (kSets - 1)],
+                            magic, tot);
     }
     cur = nxt;
-    const int cnn = cn + p.waves < p.chunks ? cn + p.waves : cn;
-    load_blocks<GR, kUnroll, false>(p, row, cnn * kUnroll, quarter, nxt);
+    if (c + 2 * p.waves < p.chunks)
+      load_blocks<GR, kUnroll, false>(p, row, (c + 2 * p.waves) * kUnroll, quarter, nxt);
   }
   // blocks left over, one at a time in turn to the waves
   const int left = p.chunks * kUnroll;
@@ -290,13 +319,13 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t ba
     load_blocks<GR, 1, false>(p, row, b, quarter, one);
     read_x(x[0], b, inside);
     ordered(x[0]);
-    multiply<FMT, GR, MT>(one.w[0], one.s, one.z, x[0], tot);
+    multiply<FMT, GR, MT>(one.w[0], one.s, one.z, x[0], magic, tot);
   }
   if (full < blocks && wave == (full - left) % p.waves) {
     load_blocks<GR, 1, true>(p, row, full, quarter, one);
     read_x(x[0], full, at_end);
     ordered(x[0]);
-    multiply<FMT, GR, MT>(one.w[0], one.s, one.z, x[0], tot);
+    multiply<FMT, GR, MT>(one.w[0], one.s, one.z, x[0], magic, tot);
   }
 
   add_waves<MT>(tot, reinterpret_cast<float*>(lds + (XL ? p.M * x_pitch : 0)), wave, lane, p.waves);
@@ -361,9 +390,10 @@ extern "C" MI355FUSED_API int gemm_w4(int type, int M, int N, int K, int group, 
   const int mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
   const int64_t wgs = ((int64_t)N + 15) / 16 * (((int64_t)M + 63) / 64);
   const int64_t blocks = ((int64_t)K + kBlock - 1) / kBlock;
-  a.waves = skinny::waves_for(wgs, std::max<int>(1, (int)blocks), kMaxWaves, cus);
-  // whole chunks only where every wave has one
-  a.chunks = K / kBlock >= kUnroll * a.waves ? K / (kBlock * kUnroll) : 0;
+  // whole chunks where four waves have one each, else single blocks
+  a.chunks = K / kBlock >= 4 * kUnroll ? K / (kBlock * kUnroll) : 0;
+  a.waves = skinny::waves_for(wgs, a.chunks ? a.chunks : std::max<int>(1, (int)blocks), kMaxWaves,
+                              cus);
   const int64_t x_bytes = M * (blocks * kBlock * 2 + 16);
   const bool x_in_lds = M <= 16 && K > 0 && x_bytes <= kXBytes;
   const unsigned lds_bytes =
