@@ -36,6 +36,46 @@ __device__ __forceinline__ h8 load_x(const half_t* row, int k, int K) {
   return v;
 }
 
+// A wave's own copy in LDS of KB values of its X rows.  Read straight into the
+// fragments' layout, X costs 16 rows x 64 bytes an instruction, and a CU took
+// such loads at one per 50-80 cycles: with 16 rows of X and 4-bit weights they
+// were half the time.  Here a load instruction covers whole lines (KB = 64: 8
+// rows x 128 bytes), one stage ahead in registers, and the fragments come from
+// LDS.  Rows are 16 bytes longer than their data, so that 16 of them start in
+// different banks.  Only the one wave uses the copy: LDS serves a wave's
+// accesses in order, so no barrier is needed.
+template <int MT, int KB>
+struct XStage {
+  static constexpr int kPitch = 2 * KB + 16, kPieces = KB / 8, kRows = 64 / kPieces;
+  static constexpr int kLoads = 16 * MT / kRows;
+  static constexpr int kBytes = 16 * MT * kPitch;
+  h8 v[kLoads];
+
+  // Rows from m0 (past M the last one again, unstored), columns from k.
+  template <bool TAIL>
+  __device__ __forceinline__ void load(const half_t* X, int64_t ldx, int m0, int M, int k, int K,
+                                       int lane) {
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int m = m0 + i * kRows + lane / kPieces;
+      v[i] = load_x<TAIL>(X + (m < M ? m : M - 1) * ldx, k + lane % kPieces * 8, K);
+    }
+  }
+  template <typename F>
+  __device__ __forceinline__ void store(unsigned char* buf, int lane, F order) const {
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+      *(h8*)(buf + (i * kRows + lane / kPieces) * kPitch + lane % kPieces * 16) = order(v[i]);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+  }
+  // Row 16 t + r, values k .. k + 7 of the stage.
+  __device__ __forceinline__ static h8 read(const unsigned char* buf, int t, int r, int k) {
+    return *(const h8*)(buf + (16 * t + r) * kPitch + 2 * k);
+  }
+};
+
 // Adds the waves' sums (Q f4 of each lane) in the order of the waves; the
 // result is complete in wave 0.
 template <int Q>

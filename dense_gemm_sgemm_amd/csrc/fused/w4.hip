@@ -31,6 +31,7 @@ typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 constexpr int kBlock = 128;   // K values of a block
 constexpr int kUnroll = 4;    // blocks of a chunk; a wave has two chunks in flight
 constexpr int kMaxWaves = 8;
+constexpr int most_waves(int mt) { return mt == 4 ? 4 : kMaxWaves; }   // two workgroups' LDS a CU
 constexpr int kStaged = 4;    // 16-byte pieces of X a thread loads ahead of its weights
 constexpr int kXBytes = 32 << 10;   // X up to this size is kept in LDS
 
@@ -206,10 +207,14 @@ __device__ __forceinline__ void multiply(u4 raw, const uint16_t* scales, const u
 
 // XL: the rows of X (M <= 16 of them) lie in LDS, reordered, zero past K, in
 // rows of K rounded up to blocks plus 16 bytes (rows then start in different
-// banks).  Otherwise they are read from global memory (L2) one block ahead.
+// banks).  Otherwise each wave stages the rows of a block in turn (XStage).
 template <int FMT, int GR, int MT, bool XL>
 __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t base) {
-  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  typedef XStage<MT, kBlock> Stage;
+  extern __shared__ __attribute__((aligned(16))) unsigned char dynamic_lds[];
+  __shared__ __attribute__((aligned(16))) unsigned char
+      stage_lds[XL ? 16 : most_waves(MT) * Stage::kBytes];
+  unsigned char* lds = XL ? dynamic_lds : stage_lds;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, quarter = lane >> 4;
@@ -258,31 +263,23 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t ba
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
 
-  // Fragments of X: rows past M repeat the last one, unstored.
-  const half_t* xg[MT];
+  // Fragments of X (rows past M repeat the last one, unstored).
   const unsigned char* xl = lds + (r < p.M ? r : p.M - 1) * x_pitch;
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int m = m0 + 16 * t + r;
-    xg[t] = p.X + (m < p.M ? m : p.M - 1) * p.ldx;
-  }
-  auto read_x = [&](h8 (&x)[MT][4], int block, auto tail) __attribute__((always_inline)) {
+  unsigned char* buf = lds + wave * Stage::kBytes;
+  Stage stage;
+  auto read_x = [&](h8 (&x)[MT][4], int block) __attribute__((always_inline)) {
+    if constexpr (!XL) stage.store(buf, lane, [](h8 v) { return reorder(v); });
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int k = block * kBlock + step_k<GR>(j, quarter);
-        if constexpr (XL) x[t][j] = *(const h8*)(xl + 2 * k);
-        else x[t][j] = load_x<decltype(tail)::value>(xg[t], k, p.K);
+        const int k = step_k<GR>(j, quarter);
+        x[t][j] = XL ? *(const h8*)(xl + 2 * (block * kBlock + k)) : Stage::read(buf, t, r, k);
       }
   };
-  auto ordered = [&](h8 (&x)[MT][4]) __attribute__((always_inline)) {
-    if constexpr (!XL) {
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[t][j] = reorder(x[t][j]);
-    }
+  auto load_rows = [&](int block, auto tail) __attribute__((always_inline)) {
+    if constexpr (!XL)
+      stage.template load<decltype(tail)::value>(p.X, p.ldx, m0, p.M, block * kBlock, p.K, lane);
   };
   constexpr int kG = groups_per_block(GR);
   const Magic<FMT> magic;
@@ -292,21 +289,15 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t ba
 
   const std::integral_constant<bool, false> inside{};
   const std::integral_constant<bool, true> at_end{};
-  // (64 rows: one set of fragments, two and their weights do not fit the registers)
-  constexpr int kSets = MT < 4 ? 2 : 1;
-  h8 x[kSets][MT][4];
-  if (kSets == 2 && c < p.chunks) read_x(x[0], c * kUnroll, inside);
+  h8 x[MT][4];
+  if (c < p.chunks) load_rows(c * kUnroll, inside);
   for (; c < p.chunks; c += p.waves) {
     const int cn = c + p.waves < p.chunks ? c + p.waves : c;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if constexpr (kSets == 2)
-        read_x(x[(u + 1) & 1], u + 1 < kUnroll ? c * kUnroll + u + 1 : cn * kUnroll, inside);
-      else
-        read_x(x[0], c * kUnroll + u, inside);
-      ordered(x[u & (kSets - 1)]);
-      multiply<FMT, GR, MT>(cur.w[u], cur.s + u * kG, cur.z + u * kG, x[u & (kSets - 1)],
-                            magic, tot);
+      read_x(x, c * kUnroll + u);
+      load_rows(u + 1 < kUnroll ? c * kUnroll + u + 1 : cn * kUnroll, inside);
+      multiply<FMT, GR, MT>(cur.w[u], cur.s + u * kG, cur.z + u * kG, x, magic, tot);
     }
     cur = nxt;
     if (c + 2 * p.waves < p.chunks)
@@ -317,17 +308,19 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t ba
   Blocks<GR, 1> one;
   for (int b = left + wave; b < full; b += p.waves) {
     load_blocks<GR, 1, false>(p, row, b, quarter, one);
-    read_x(x[0], b, inside);
-    ordered(x[0]);
-    multiply<FMT, GR, MT>(one.w[0], one.s, one.z, x[0], magic, tot);
+    load_rows(b, inside);
+    read_x(x, b);
+    multiply<FMT, GR, MT>(one.w[0], one.s, one.z, x, magic, tot);
   }
   if (full < blocks && wave == (full - left) % p.waves) {
     load_blocks<GR, 1, true>(p, row, full, quarter, one);
-    read_x(x[0], full, at_end);
-    ordered(x[0]);
-    multiply<FMT, GR, MT>(one.w[0], one.s, one.z, x[0], magic, tot);
+    load_rows(full, at_end);
+    read_x(x, full);
+    multiply<FMT, GR, MT>(one.w[0], one.s, one.z, x, magic, tot);
   }
 
+  // (the sums take the place of X)
+  if (!XL) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   add_waves<MT>(tot, reinterpret_cast<float*>(lds + (XL ? p.M * x_pitch : 0)), wave, lane, p.waves);
   if (wave > 0 || n >= p.N) return;
   const float bias = p.bias ? word_to_f32<FMT>(p.bias[n]) : 0.f;
@@ -392,12 +385,12 @@ extern "C" MI355FUSED_API int gemm_w4(int type, int M, int N, int K, int group, 
   const int64_t blocks = ((int64_t)K + kBlock - 1) / kBlock;
   // whole chunks where four waves have one each, else single blocks
   a.chunks = K / kBlock >= 4 * kUnroll ? K / (kBlock * kUnroll) : 0;
-  a.waves = skinny::waves_for(wgs, a.chunks ? a.chunks : std::max<int>(1, (int)blocks), kMaxWaves,
-                              cus);
+  a.waves = skinny::waves_for(wgs, a.chunks ? a.chunks : std::max<int>(1, (int)blocks),
+                              most_waves(mt), cus);
   const int64_t x_bytes = M * (blocks * kBlock * 2 + 16);
   const bool x_in_lds = M <= 16 && K > 0 && x_bytes <= kXBytes;
   const unsigned lds_bytes =
-      (unsigned)((x_in_lds ? x_bytes : 0) + (a.waves - 1) * mt * 64 * sizeof(f4));
+      x_in_lds ? (unsigned)(x_bytes + (a.waves - 1) * mt * 64 * sizeof(f4)) : 0;
   const void* k = type == GEMM_TYPE_BF16 ? pick<kFmtBF16>(M, group, x_in_lds)
                                          : pick<kFmtF16>(M, group, x_in_lds);
   return to_status(
