@@ -86,9 +86,7 @@ def build(extra_flags: list[str] | None = None, jobs: int | None = None) -> str:
     with ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs) + len(fused))) as ex:
         objs = list(ex.map(lambda s: _compile(s, extra), srcs + fused))
     _link(objs[:len(srcs)], LIB_PATH)
-    # the fused operators transpose with the first library's kernel
-    shared = [o for o in objs[:len(srcs)] if os.path.basename(o) == "transpose.hip.o"]
-    _link(objs[len(srcs):] + shared, FUSED_LIB_PATH)
+    _link(objs[len(srcs):], FUSED_LIB_PATH)
     return LIB_PATH
 
 

@@ -51,10 +51,55 @@ struct PadJobs {
   // matrix the kernels read and advances dst past the copy.
   Mat add(Mat m, int rows, int K, char*& dst);
   Mat copy(Mat m, int rows, int K, char*& dst);
-  // Adds zeros for `rows` packed rows of `cols` (a multiple of 8) at dst.
-  void zeros(half_t* dst, int rows, int cols);
 };
 hipError_t launch_pad(const PadJobs& jobs, hipStream_t stream);
+
+// A transposition for the gradients of weights: dst[c][r] = src[r][c], rows of
+// dst `ldd` (a multiple of 8) apart; its rows_p x cols_p extent (in the
+// source's orientation, rows_p a multiple of 64) is written, zero outside the
+// source.  A wave takes 64 x 64: lane (i, j) = (l / 8, l % 8) the 8 x 8 block
+// at rows 8 i, columns 8 j, eight row pieces of 16 bytes turned in registers.
+struct Transpose {
+  const half_t* src;
+  half_t* dst;
+  int64_t lds, ldd;
+  int rows, cols, rows_p, cols_p;
+  int64_t tiles() const { return (int64_t)(rows_p / 64) * ((cols_p + 63) / 64); }
+};
+
+__device__ __forceinline__ void transpose_tile(const Transpose& p, int64_t tile, int lane) {
+  typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const int tiles_c = (p.cols_p + 63) / 64;
+  if (tile >= (int64_t)(p.rows_p / 64) * tiles_c) return;
+  const int r0 = (int)(tile / tiles_c) * 64 + 8 * (lane >> 3);
+  const int c0 = (int)(tile % tiles_c) * 64 + 8 * (lane & 7);
+  u32x4 x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    h8 v = {};
+    if (r0 + e < p.rows && c0 < p.cols) {
+      const half_t* s = p.src + (int64_t)(r0 + e) * p.lds + c0;
+      if (c0 + 8 <= p.cols) {
+        __builtin_memcpy(&v, s, 16);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (c0 + k < p.cols) v[k] = s[k];
+      }
+    }
+    x[e] = __builtin_bit_cast(u32x4, v);
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int sh = 16 * (k & 1);
+    u32x4 w;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = ((x[2 * q][k >> 1] >> sh) & 0xFFFFu) | (((x[2 * q + 1][k >> 1] >> sh) & 0xFFFFu) << 16);
+    if (c0 + k < p.cols_p) *(u32x4*)(p.dst + (int64_t)(c0 + k) * p.ldd + r0) = w;
+  }
+}
 
 // The tile-kernel launchers (tiles_*.hip); a.fmt selects the format.
 hipError_t launch_gated_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);

@@ -19,6 +19,8 @@ struct GradArgs {
   half_t *d, *tail;
   int64_t ldg, ldu, lddh, ld;
   int M, N, Mp, Np, Nk, act;   // Nk: columns the products sum over (N, or 128 if less)
+  int64_t blocks;              // of dG and dU; the ones after them transpose X
+  Transpose x;
 };
 
 // Columns c .. c + 7 of a row of N at any 2-byte address, zero past it.
@@ -39,6 +41,11 @@ __device__ __forceinline__ h8 load_cols(const half_t* row, int c, int N) {
 // an element.
 template <int FMT>
 __global__ __launch_bounds__(kThreads) void gated_grad_kernel(GradArgs p, int64_t base) {
+  if (base + blockIdx.x >= p.blocks) {
+    transpose_tile(p.x, (base + blockIdx.x - p.blocks) * (kThreads / 64) + (threadIdx.x >> 6),
+                   threadIdx.x & 63);
+    return;
+  }
   const int main = p.Np / 8, chunks = main + (p.tail ? 8 : 0);
   const int64_t t = (base + blockIdx.x) * kThreads + threadIdx.x;
   if (t >= (int64_t)p.Mp * chunks) return;
@@ -232,15 +239,17 @@ MI355FUSED_API int gemm_gated_bwd(int type, int act, int M, int N, int K, const 
   half_t* tail = p.tail ? reinterpret_cast<half_t*>(ws + p.bytes_d) : nullptr;
   ws += p.bytes_d + p.bytes_tail;
 
-  const GradArgs ga{in16(G), in16(U), in16(dH), d,    tail, ldg,  ldu, lddh,
-                    p.ld,    M,       N,        p.Mp, p.Np, p.Nk, act};
-  const int64_t pieces = (int64_t)p.Mp * (p.Np / 8 + (p.tail ? 8 : 0));
-  hipError_t e = launch_tiles(fmt == kFmtBF16 ? (const void*)gated_grad_kernel<kFmtBF16>
-                                              : (const void*)gated_grad_kernel<kFmtF16>,
-                              ga, (pieces + kThreads - 1) / kThreads, kThreads, 0, s);
-  if (e != hipSuccess) return to_status(e);
   half_t* xt = reinterpret_cast<half_t*>(ws);
   ws += p.bytes_x;
+  const int64_t pieces = (int64_t)p.Mp * (p.Np / 8 + (p.tail ? 8 : 0));
+  GradArgs ga{in16(G), in16(U), in16(dH), d,    tail, ldg,  ldu, lddh,
+              p.ld,    M,       N,        p.Mp, p.Np, p.Nk, act, (pieces + kThreads - 1) / kThreads,
+              Transpose{in16(X), xt, ldx, p.Mp, M, K, p.Mp, pad_k(K)}};
+  const int64_t blocks_x = dw ? (ga.x.tiles() + kThreads / 64 - 1) / (kThreads / 64) : 0;
+  hipError_t e = launch_tiles(fmt == kFmtBF16 ? (const void*)gated_grad_kernel<kFmtBF16>
+                                              : (const void*)gated_grad_kernel<kFmtF16>,
+                              ga, ga.blocks + blocks_x, kThreads, 0, s);
+  if (e != hipSuccess) return to_status(e);
   PadJobs jobs;
   Mat wg{in16(Wg), ldwg}, wu{in16(Wu), ldwu};
   if (p.bytes_g) {
@@ -271,9 +280,6 @@ MI355FUSED_API int gemm_gated_bwd(int type, int act, int M, int N, int K, const 
     if (e != hipSuccess) return to_status(e);
   }
   if (dw) {
-    const PadCopy tr{in16(X), xt, ldx, p.Mp, M, K, p.Mp, pad_k(K)};
-    e = launch_transpose16(tr, nullptr, s);
-    if (e != hipSuccess) return to_status(e);
     // both gradients as two parts of one product's rows, or the one asked for
     const bool both = dWg != nullptr && dWu != nullptr;
     Args16 a{dWg ? d : d + p.Np, xt, out16(dWg ? dWg : dWu), p.ld, p.Mp, dWg ? lddwg : lddwu,

@@ -59,17 +59,6 @@ Mat PadJobs::copy(Mat m, int rows, int K, char*& dst) {
   return Mat{j.dst, j.ldd};
 }
 
-void PadJobs::zeros(half_t* dst, int rows, int cols) {
-  char* at = reinterpret_cast<char*>(dst);
-  PadJob& j = job[count];
-  copy(Mat{}, 0, cols, at);
-  j.ldd = cols;
-  j.rows_p = rows;
-  j.cols_p = cols;
-  blocks[count - 1] = (count > 1 ? blocks[count - 2] : 0) +
-                      ((int64_t)rows * (cols / 8) + kThreads - 1) / kThreads;
-}
-
 hipError_t launch_pad(const PadJobs& jobs, hipStream_t stream) {
   if (jobs.count == 0) return hipSuccess;
   return launch_tiles((const void*)pad_kernel, jobs, jobs.blocks[jobs.count - 1], kThreads, 0,

@@ -29,7 +29,15 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(SumArgs p, int64_t base) 
   const int n = (int)(t % quads) * 4;
   const float* src = p.sum + m * p.ld_sum + n;
   f4 s = *(const f4*)src;
-  for (int k = 1; k < p.splits; ++k) s += *(const f4*)(src + k * p.split_stride);
+  int k = 1;
+  for (; k + 4 <= p.splits; k += 4) {   // four loads in flight
+    f4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = *(const f4*)(src + (k + u) * p.split_stride);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) s += v[u];
+  }
+  for (; k < p.splits; ++k) s += *(const f4*)(src + k * p.split_stride);
   if (p.scale) s *= p.scale[1];
   h4 o;
 #pragma unroll

@@ -8,11 +8,15 @@ namespace mi355gemm {
 namespace fused {
 namespace {
 
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+constexpr int kPrepareThreads = 256;
+
 // ---- The join.  The kLse tiles leave, for each row, a maximum t_c and a sum
 // of exp(z - t_c) for each chunk c of the columns.  With t = max t_c:
-// lse = t + log(sum_c s_c exp(t_c - t)).  A workgroup of 16 waves takes 64
-// rows (a lane a row, coalesced over the rows), the waves sharing the chunks.
-constexpr int kJoinWaves = 16;
+// lse = t + log(sum_c s_c exp(t_c - t)).  A workgroup of 16 waves takes 16
+// rows; the four groups of 16 lanes of its waves share the chunks 64 ways,
+// eight loads in flight each.
+constexpr int kJoinWaves = 16, kJoinRows = 16, kJoinParts = 4 * kJoinWaves;
 
 struct JoinArgs {
   const float2* partial;
@@ -32,27 +36,35 @@ __device__ __forceinline__ void join(float& t, float& s, float t2, float s2) {
 }
 
 __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(JoinArgs p, int64_t base) {
-  __shared__ float2 part[kJoinWaves][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m = (base + blockIdx.x) * 64 + lane;
+  __shared__ float2 part[kJoinParts][kJoinRows];
+  const int row = threadIdx.x & 15, mine = threadIdx.x >> 4;
+  const int64_t m = (base + blockIdx.x) * kJoinRows + row;
   float t = -__builtin_inff(), s = 0.f;
   if (m < p.M) {
     constexpr int U = 8;   // chunks in flight
-    for (int c = wave; c < p.chunks; c += U * kJoinWaves) {
+    for (int c = mine; c < p.chunks; c += U * kJoinParts) {
       float2 v[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int cu = c + u * kJoinWaves;
+        const int cu = c + u * kJoinParts;
         v[u] = cu < p.chunks ? p.partial[cu * p.ld + m] : make_float2(-__builtin_inff(), 0.f);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) join(t, s, v[u].x, v[u].y);
     }
   }
-  part[wave][lane] = make_float2(t, s);
+  part[mine][row] = make_float2(t, s);
   __syncthreads();
-  if (wave != 0 || m >= p.M) return;
-  for (int w = 1; w < kJoinWaves; ++w) join(t, s, part[w][lane].x, part[w][lane].y);
+  // halving over the parts, in a fixed order
+  for (int half = kJoinParts / 2; half >= 1; half /= 2) {
+    if (mine < half) {
+      const float2 o = part[mine + half][row];
+      join(t, s, o.x, o.y);
+      part[mine][row] = make_float2(t, s);
+    }
+    __syncthreads();
+  }
+  if (mine != 0 || m >= p.M) return;
   const float lse = t + __logf(s);
   const long long y = p.targets[m];
   float loss = 0.f;
@@ -75,10 +87,10 @@ struct ScaleArgs {
   int M;
 };
 
-__global__ __launch_bounds__(1024) void scale_kernel(ScaleArgs p, int64_t) {
-  __shared__ float part[16];
+__device__ __forceinline__ void find_scale(const ScaleArgs& p) {
+  __shared__ float part[kPrepareThreads / 64];
   float top = 0.f;
-  for (int m = threadIdx.x; m < p.M; m += 1024) {
+  for (int m = threadIdx.x; m < p.M; m += kPrepareThreads) {
     const float v = fabsf(p.dloss[m]);
     if (p.targets[m] != p.ignore) top = fmaxf(top, v);
   }
@@ -87,7 +99,7 @@ __global__ __launch_bounds__(1024) void scale_kernel(ScaleArgs p, int64_t) {
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
   __syncthreads();
   if (threadIdx.x != 0) return;
-  for (int w = 1; w < 16; ++w) top = fmaxf(top, part[w]);
+  for (int w = 1; w < kPrepareThreads / 64; ++w) top = fmaxf(top, part[w]);
   float f = 1.f, r = 1.f;
   if (top > 0.f && top < __builtin_inff()) {
     int e;
@@ -99,6 +111,29 @@ __global__ __launch_bounds__(1024) void scale_kernel(ScaleArgs p, int64_t) {
   }
   p.scale[0] = f;
   p.scale[1] = r;
+}
+
+// What the backward pass needs first, in one launch: the last workgroup finds
+// the factor (fp16), the others transpose X and clear the rows of d that no
+// tile writes.
+struct PrepareArgs {
+  Transpose x;
+  half_t* zero;
+  int64_t zero_pieces;      // of 16 bytes
+  int64_t blocks_x, blocks_zero;
+  ScaleArgs scale;
+};
+
+__global__ __launch_bounds__(kPrepareThreads) void prepare_kernel(PrepareArgs p, int64_t base) {
+  const int64_t b = base + blockIdx.x;
+  if (b < p.blocks_x) {
+    transpose_tile(p.x, b * (kPrepareThreads / 64) + (threadIdx.x >> 6), threadIdx.x & 63);
+  } else if (b < p.blocks_x + p.blocks_zero) {
+    const int64_t t = (b - p.blocks_x) * kPrepareThreads + threadIdx.x;
+    if (t < p.zero_pieces) *((h8*)p.zero + t) = h8{};
+  } else {
+    find_scale(p.scale);
+  }
 }
 
 int check(int type, int M, int N, int K) {
@@ -214,8 +249,8 @@ MI355FUSED_API int gemm_xent(int type, int M, int N, int K, const void* X, int l
   if (e != hipSuccess) return to_status(e);
   const JoinArgs j{partial, target_logit, targets, ignore, N, loss, lse, M, M,
                    lse_chunks(a.M, a.N, cus)};
-  return to_status(launch_tiles((const void*)join_kernel, j, ((int64_t)M + 63) / 64,
-                                64 * kJoinWaves, 0, s));
+  return to_status(launch_tiles((const void*)join_kernel, j,
+                                ((int64_t)M + kJoinRows - 1) / kJoinRows, 64 * kJoinWaves, 0, s));
 }
 
 MI355FUSED_API unsigned long long gemm_xent_bwd_workspace(int type, int M, int N, int K,
@@ -266,25 +301,22 @@ MI355FUSED_API int gemm_xent_bwd(int type, int M, int N, int K, const void* X, i
   if (p.bytes_w) w = jobs.copy(w, N, K, ws);
   hipError_t e = launch_pad(jobs, s);
   if (e != hipSuccess) return to_status(e);
-  if (fmt == kFmtF16) {
-    const ScaleArgs sa{dloss, targets, ignore, scale, M};
-    e = launch_tiles((const void*)scale_kernel, sa, 1, 1024, 0, s);
-    if (e != hipSuccess) return to_status(e);
-  } else {
-    scale = nullptr;   // bf16 has fp32's range
-  }
+  PrepareArgs prep{};
   if (dw) {
-    const PadCopy tr{in16(X), xt, ldx, p.Ms, M, K, p.Ms, p.Kp};
-    e = launch_transpose16(tr, nullptr, s);
-    if (e != hipSuccess) return to_status(e);
+    prep.x = Transpose{in16(X), xt, ldx, p.Ms, M, K, p.Ms, p.Kp};
+    prep.blocks_x = (prep.x.tiles() + kPrepareThreads / 64 - 1) / (kPrepareThreads / 64);
     // the rows of d that no piece writes (all of them for M == 0) are zero
-    const int written = M > 0 ? p.Mp : 0;
-    if (p.Ms > written) {
-      PadJobs zero;
-      zero.zeros(d + written * p.ldd, p.Ms - written, (int)p.ldd);
-      e = launch_pad(zero, s);
-      if (e != hipSuccess) return to_status(e);
-    }
+    const int64_t written = M > 0 ? p.Mp : 0;
+    prep.zero = d + written * p.ldd;
+    prep.zero_pieces = (p.Ms - written) * p.ldd / 8;
+    prep.blocks_zero = (prep.zero_pieces + kPrepareThreads - 1) / kPrepareThreads;
+  }
+  prep.scale = ScaleArgs{dloss, targets, ignore, scale, M};
+  if (fmt == kFmtBF16) scale = nullptr;   // bf16 has fp32's range
+  const int64_t blocks = prep.blocks_x + prep.blocks_zero + (scale ? 1 : 0);
+  if (blocks > 0) {
+    e = launch_tiles((const void*)prepare_kernel, prep, blocks, kPrepareThreads, 0, s);
+    if (e != hipSuccess) return to_status(e);
   }
   for (int i = 0; i < p.pieces; ++i) {
     const bool last = i + 1 == p.pieces;

@@ -127,6 +127,22 @@ __device__ __forceinline__ void map_tile(int64_t b, int tiles_m, int tiles_n, in
   tn = (int)(w / rows);
 }
 
+// The same in 32 bits, for fewer than 2^31 tiles (a 64-bit division by a
+// variable is some 70 instructions, and every tile needs several).
+template <int GM>
+__device__ __forceinline__ void map_tile32(uint32_t b, uint32_t tiles_m, uint32_t tiles_n, int& tm,
+                                           int& tn) {
+  const uint32_t T = tiles_m * tiles_n;
+  const uint32_t x = b % 8, q = T / 8, rem = T % 8;
+  const uint32_t L = x * q + (x < rem ? x : rem) + b / 8;
+  const uint32_t per_group = GM * tiles_n;
+  const uint32_t g = L / per_group, w = L - g * per_group;
+  const uint32_t left = tiles_m - g * GM;
+  const uint32_t rows = left < GM ? left : GM;
+  tn = (int)(w / rows);
+  tm = (int)(g * GM + w - tn * rows);
+}
+
 template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int COPY_SEL = 0>
 struct Config {
   static constexpr int kWaves = WAVES_M * WAVES_N;
@@ -337,13 +353,16 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       item -= sp * tiles;
     }
     if constexpr (MODE == kGradX) {
-      const int64_t tiles = (int64_t)tiles_m * tiles_n;
-      sp = (int)(item / tiles);
-      item -= sp * tiles;
+      const uint32_t tiles = (uint32_t)tiles_m * tiles_n;
+      sp = (int)((uint32_t)item / tiles);
+      item -= (uint32_t)sp * tiles;
     }
     kb = sp * (SPLIT ? p.sk.per : MODE == kGradX ? ta.x.per : 0);
     int tm, tn;
-    map_tile<GM>(item, tiles_m, tiles_n, tm, tn);
+    if constexpr (MODE == kProduct)
+      map_tile<GM>(item, tiles_m, tiles_n, tm, tn);
+    else
+      map_tile32<GM>((uint32_t)item, tiles_m, tiles_n, tm, tn);
     if constexpr (MODE == kGradW) {
       sp = tm >= part_tiles;   // the part
       if (sp) tm -= part_tiles;
@@ -771,6 +790,14 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   };
+  // op over the four lanes of equal l % 16 (row swaps in registers, no LDS)
+  auto across4 = [&](float v, auto op) __attribute__((always_inline)) {
+    const uint32_t a = __float_as_uint(v);
+    const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    const uint32_t b = __float_as_uint(op(__uint_as_float(x[0]), __uint_as_float(x[1])));
+    const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return op(__uint_as_float(y[0]), __uint_as_float(y[1]));
+  };
   constexpr float kLog2e = 1.44269504088896340736f;
   auto round4 = [&](f4 x) __attribute__((always_inline)) {
     h4 o;
@@ -818,15 +845,21 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       const int nf = n0 + wn + 4 * g;
       const bool inside = n0 + wn >= nlo && n0 + wn + C::WN <= x.n_end;
       const int64_t chunk = (int64_t)((nlo / BN) * WAVES_N + wave % WAVES_N) * x.ld_partial;
+      // all rows' targets first: one memory latency
+      long long target[C::kBlocksM];
+#pragma unroll
+      for (int i = 0; i < C::kBlocksM; ++i) {
+        const int m = m0 + wm + 16 * i + r;
+        target[i] = x.targets[m < x.m_end ? m : x.m_end - 1];
+      }
 #pragma unroll
       for (int i = 0; i < C::kBlocksM; ++i) {
         const int m = m0 + wm + 16 * i + r;
         const bool mine = m >= mlo && m < x.m_end;
         // the target's logit, stored by the one lane of the one tile that has it
-        const long long y = mine ? x.targets[m] : -1;
-        const long long rel = y - x.col0 - nf;
-        const bool has = mine && y != x.ignore && rel >= 0 && rel < C::WN && (rel & 15) < 4 &&
-                         nf + rel >= nlo && nf + rel < x.n_end;
+        const long long rel = target[i] - x.col0 - nf;
+        const bool has = mine && target[i] != x.ignore && rel >= 0 && rel < C::WN &&
+                         (rel & 15) < 4 && nf + rel >= nlo && nf + rel < x.n_end;
         if (has) {
           float t = 0.f;
 #pragma unroll
@@ -849,8 +882,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         for (int j = 0; j < C::kBlocksN; ++j)
 #pragma unroll
           for (int v = 0; v < 4; ++v) top = fmaxf(top, acc[i][j][v]);
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
+        top = across4(top, [](float a, float b) { return fmaxf(a, b); });
         // exp(z - top) = 2^(z log2(e) - top log2(e)): the rounding of the second
         // term is 2^-24 of it, which is what lse = top + log(s) keeps anyway
         const float base = top == -__builtin_inff() ? 0.f : -top * kLog2e;
@@ -859,8 +891,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         for (int j = 0; j < C::kBlocksN; ++j)
 #pragma unroll
           for (int v = 0; v < 4; ++v) s += __builtin_amdgcn_exp2f(fmaf(acc[i][j][v], kLog2e, base));
-        s += __shfl_xor(s, 16);
-        s += __shfl_xor(s, 32);
+        s = across4(s, [](float a, float b) { return a + b; });
         if (g == 0 && mine) x.partial[chunk + m] = make_float2(top, s);
       }
     } else if constexpr (MODE == kDlogit) {
@@ -872,16 +903,24 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       const int last = (p.N - 1) / BK * BK;   // first column of the last slab of K there
       const bool tail = x.tail != nullptr && n0 + wn + C::WN > p.N - BK;
       const bool inside = n0 + wn >= x.n_begin && n0 + wn + C::WN <= x.n_end;
+      // all rows' data first: one memory latency
+      long long target[C::kBlocksM];
+      float lse[C::kBlocksM], weight[C::kBlocksM];
+#pragma unroll
+      for (int i = 0; i < C::kBlocksM; ++i) {
+        const int m = m0 + wm + 16 * i + r, mc = m < x.m_end ? m : x.m_end - 1;
+        target[i] = x.targets[mc];
+        lse[i] = x.lse[mc];
+        weight[i] = x.row_scale[mc];
+      }
 #pragma unroll
       for (int i = 0; i < C::kBlocksM; ++i) {
         const int m = m0 + wm + 16 * i + r;
-        const bool row = m < x.m_end;
-        const long long y = row ? x.targets[m] : x.ignore;
-        const bool live = row && y != x.ignore;
+        const long long y = target[i];
+        const bool live = m < x.m_end && y != x.ignore;
         const bool known = y >= 0 && y < x.vocab;
-        float w = live ? x.row_scale[m] * f : 0.f;
-        if (live && !known) w = __builtin_nanf("");
-        const float base = live ? -x.lse[m] * kLog2e : 0.f;
+        const float w = known ? weight[i] * f : __builtin_nanf("");
+        const float base = -lse[i] * kLog2e;
         const long long at = y - x.col0 - nf;
         const int rel = live && at >= 0 && at < C::WN ? (int)at : -1;
 #pragma unroll
@@ -1015,22 +1054,37 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       return nk;
     }
   };
+  // (the operators compute one new origin a tile and move the others up)
+  int fm[3], fn[3];   // first stored rows and columns
   auto refresh_origins = [&](int j) __attribute__((always_inline)) {
     cur = j;
 #pragma unroll
     for (int d = 0; d < 3; ++d) {
-      int mlo, nlo;
-      tile_origin(j + d < ntiles ? j + d : ntiles - 1, om[d], on[d], ok[d], os[d], mlo, nlo);
-      if (d == 0) {
-        mlo0 = mlo;
-        nlo0 = nlo;
+      if (MODE != kProduct && j > 0 && d < 2) {
+        om[d] = om[d + 1];
+        on[d] = on[d + 1];
+        ok[d] = ok[d + 1];
+        os[d] = os[d + 1];
+        fm[d] = fm[d + 1];
+        fn[d] = fn[d + 1];
+      } else {
+        int mlo, nlo;
+        tile_origin(j + d < ntiles ? j + d : ntiles - 1, om[d], on[d], ok[d], os[d], mlo, nlo);
+        fm[d] = mlo;
+        fn[d] = nlo;
+        if constexpr (MODE != kProduct) {
+          // wave-uniform, but a division leaves them in vector registers
+          om[d] = __builtin_amdgcn_readfirstlane(om[d]);
+          on[d] = __builtin_amdgcn_readfirstlane(on[d]);
+          ok[d] = __builtin_amdgcn_readfirstlane(ok[d]);
+          os[d] = __builtin_amdgcn_readfirstlane(os[d]);
+          fm[d] = __builtin_amdgcn_readfirstlane(fm[d]);
+          fn[d] = __builtin_amdgcn_readfirstlane(fn[d]);
+        }
       }
-      if constexpr (MODE != kProduct) {
-        // wave-uniform, but a 64-bit division leaves them in vector registers
-        om[d] = __builtin_amdgcn_readfirstlane(om[d]);
-        on[d] = __builtin_amdgcn_readfirstlane(on[d]);
-        ok[d] = __builtin_amdgcn_readfirstlane(ok[d]);
-        os[d] = __builtin_amdgcn_readfirstlane(os[d]);
+      if (d == 0) {
+        mlo0 = fm[0];
+        nlo0 = fn[0];
       }
     }
   };
@@ -1245,6 +1299,7 @@ hipError_t launch_fused(const Args16& a, const FusedExtra& x, int slots, hipStre
   constexpr int kTileN = MODE == kGated ? BN / 2 : BN;
   const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * ((a.N + kTileN - 1) / kTileN) *
                         (MODE == kGradW ? x.parts : MODE == kGradX ? x.splits : 1);
+  if (tiles >= (int64_t(1) << 31)) return hipErrorInvalidValue;   // map_tile32
   int64_t grid = tiles < slots ? tiles : slots;
   if (grid < 1) grid = 1;
   FusedTileArgs ta{a, tiles, x};

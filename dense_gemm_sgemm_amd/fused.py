@@ -22,7 +22,8 @@ import ctypes
 import os
 import threading
 
-from . import (ACTS, HERE, _check, _epilogue_args, _matrix, _torch_module, _workspace)
+from . import (ACTS, HERE, _check, _current_stream_handle, _epilogue_args, _matrix, _torch_module,
+               _workspace)
 
 LIB_PATH = os.path.join(HERE, "libmi355fused.so")
 _lock = threading.Lock()
@@ -61,14 +62,19 @@ def load_library() -> ctypes.CDLL:
         return lib
 
 
-def _dtype(t):
+def _first(t):
+    """(dtype, GEMM_TYPE_*, GPU index, rows, columns, pointer, leading dimension)
+    of the call's X; the other operands are held to its type and GPU."""
     torch = _torch_module()
     dtype = t.dtype if isinstance(t, torch.Tensor) else None
     if dtype is torch.bfloat16:
-        return dtype, 1
-    if dtype is torch.float16:
-        return dtype, 0
-    raise TypeError("X must be a float16 or bfloat16 tensor")
+        typ = 1
+    elif dtype is torch.float16:
+        typ = 0
+    else:
+        raise TypeError("X must be a float16 or bfloat16 tensor")
+    rows, cols, ld, ptr = _matrix(t, "X", dtype)
+    return dtype, typ, t.get_device(), rows, cols, ptr, ld
 
 
 def _rows(t, name) -> int:
@@ -78,62 +84,61 @@ def _rows(t, name) -> int:
     return t.shape[0]
 
 
-def _shaped(t, name, dtype, rows, cols):
-    """(device pointer or None, leading dimension) of a rows x cols matrix."""
+def _shaped(t, name, dtype, index, rows, cols):
+    """(device pointer or None, leading dimension) of a rows x cols matrix on GPU
+    ``index``.  Runs for every operand of every call: the usual case is told by
+    the cheapest queries, and anything else by _matrix, which says what is wrong."""
+    torch = _torch_module()
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (rows, cols) and \
+            t.get_device() == index:
+        s0, s1 = t.stride()
+        if s1 == 1 and rows > 1 and cols > 1:
+            return t.data_ptr(), s0
     r, c, ld, ptr = _matrix(t, name, dtype)
     if r != rows or c != cols:
         raise ValueError("%s must be %d x %d, got %s" % (name, rows, cols, tuple(t.shape)))
+    if t.get_device() != index:
+        raise ValueError("all tensors of a call must live on one GPU")
     return ptr, ld
 
 
-def _optional(t, name, dtype, rows, cols):
-    return (None, 0) if t is None else _shaped(t, name, dtype, rows, cols)
+def _optional(t, name, dtype, index, rows, cols):
+    return (None, 0) if t is None else _shaped(t, name, dtype, index, rows, cols)
 
 
-def _vector(t, name, dtype, n):
+def _vector(t, name, dtype, index, n):
     torch = _torch_module()
     if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or t.dim() != 1 or \
             t.shape[0] != n or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s GPU vector of length %d" % (name, dtype, n))
+    if t.get_device() != index:
+        raise ValueError("all tensors of a call must live on one GPU")
     return t.data_ptr() if n else None
 
 
-class _Place:
-    """The one GPU a call's tensors live on, and the stream it runs on."""
-
-    __slots__ = ("index", "stream", "guard")
-
-    def __init__(self, stream, first, *others):
-        torch = _torch_module()
-        index = first.get_device()
-        for t in others:
-            if t is not None and t.get_device() != index:
-                raise ValueError("all tensors of a call must live on one GPU")
-        if stream is not None and stream.device.index != index:
-            raise ValueError("stream belongs to another GPU than the tensors")
-        self.index, self.stream = index, stream
-        self.guard = None if index == torch.cuda.current_device() else torch.cuda.device(index)
-
-    def run(self, fn, args, need=None, workspace=None, like=None):
-        """``fn(*args[, workspace, bytes], stream)`` with the GPU current;
-        ``need()`` gives the workspace's size."""
-        if self.guard is not None:
-            with self.guard:
-                return self._run(fn, args, need, workspace, like)
-        return self._run(fn, args, need, workspace, like)
-
-    def _run(self, fn, args, need, workspace, like):
-        torch = _torch_module()
-        handle = self.stream.cuda_stream if self.stream is not None else \
-            torch._C._cuda_getCurrentRawStream(self.index)
-        if need is None:
-            _check(fn(*args, handle))
-            return
-        if workspace is not None and workspace.get_device() != self.index:
+def _run(index, stream, fn, args, need=None, workspace=None):
+    """``fn(*args[, workspace, bytes], stream)`` with GPU ``index`` current;
+    ``need()`` gives the size of the workspace the call takes."""
+    torch = _torch_module()
+    if stream is not None and stream.device.index != index:
+        raise ValueError("stream belongs to another GPU than the tensors")
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
+            return _run(index, stream, fn, args, need, workspace)
+    handle = stream.cuda_stream if stream is not None else _current_stream_handle()
+    if need is None:
+        status = fn(*args, handle)
+    else:
+        if workspace is not None and workspace.get_device() != index:
             raise ValueError("workspace must live on the GPU of the tensors")
-        pw, nw, _ws = _workspace(workspace, need() if workspace is None else 0, like.device,
-                                 self.stream)
-        _check(fn(*args, pw, nw, handle))
+        bytes_ = need() if workspace is None else 0
+        if workspace is None and bytes_ == 0:
+            status = fn(*args, None, 0, handle)
+        else:
+            pw, nw, _ws = _workspace(workspace, bytes_, "cuda:%d" % index, stream)
+            status = fn(*args, pw, nw, handle)
+    if status:
+        _check(status)
 
 
 def _act(act):
@@ -148,28 +153,27 @@ def gemm_gated(X, Wg, Wu, H, act: str = "silu", G=None, U=None, workspace=None, 
     ([M,N], or None) receive the two products, which ``gemm_gated_bwd`` takes.
     ``workspace``: a contiguous GPU tensor of ``gated_workspace_bytes`` bytes, or
     None (taken from torch's allocator if the call needs one).  Returns H."""
-    dtype, typ = _dtype(X)
-    M, K, ldx, px = _matrix(X, "X", dtype)
+    dtype, typ, at, M, K, px, ldx = _first(X)
     N = _rows(Wg, "Wg")
-    pg, ldg = _shaped(Wg, "Wg", dtype, N, K)
-    pu, ldu = _shaped(Wu, "Wu", dtype, N, K)
-    ph, ldh = _shaped(H, "H", dtype, M, N)
-    outs = _optional(G, "G", dtype, M, N) + _optional(U, "U", dtype, M, N)
-    lib = load_library()
-    sizes = (M, N, K, px, ldx, pg, ldg, pu, ldu)
-    _Place(stream, X, Wg, Wu, H, G, U).run(
-        lib.gemm_gated, (typ, _act(act)) + sizes + (ph, ldh) + outs,
-        lambda: int(lib.gemm_gated_workspace(typ, *sizes)), workspace, H)
+    pg, ldg = _shaped(Wg, "Wg", dtype, at, N, K)
+    pu, ldu = _shaped(Wu, "Wu", dtype, at, N, K)
+    ph, ldh = _shaped(H, "H", dtype, at, M, N)
+    pG, ldG = _optional(G, "G", dtype, at, M, N)
+    pU, ldU = _optional(U, "U", dtype, at, M, N)
+    lib = _lib or load_library()
+    _run(at, stream, lib.gemm_gated,
+         (typ, _act(act), M, N, K, px, ldx, pg, ldg, pu, ldu, ph, ldh, pG, ldG, pU, ldU),
+         lambda: lib.gemm_gated_workspace(typ, M, N, K, px, ldx, pg, ldg, pu, ldu), workspace)
     return H
 
 
 def gated_workspace_bytes(X, Wg, Wu) -> int:
     """Workspace bytes ``gemm_gated`` needs for these tensors (0 when none)."""
-    dtype, typ = _dtype(X)
-    M, K, ldx, px = _matrix(X, "X", dtype)
+    dtype, typ, at, M, K, px, ldx = _first(X)
     N = _rows(Wg, "Wg")
-    return int(load_library().gemm_gated_workspace(
-        typ, M, N, K, px, ldx, *_shaped(Wg, "Wg", dtype, N, K), *_shaped(Wu, "Wu", dtype, N, K)))
+    return load_library().gemm_gated_workspace(typ, M, N, K, px, ldx,
+                                               *_shaped(Wg, "Wg", dtype, at, N, K),
+                                               *_shaped(Wu, "Wu", dtype, at, N, K))
 
 
 def gemm_gated_bwd(X, Wg, Wu, G, U, dH, dX=None, dWg=None, dWu=None, act: str = "silu",
@@ -178,32 +182,28 @@ def gemm_gated_bwd(X, Wg, Wu, G, U, dH, dX=None, dWg=None, dWu=None, act: str = 
     the products G, U it stored: ``dX`` [M,K], ``dWg`` and ``dWu`` [N,K], each
     computed if given.  ``workspace``: ``gated_bwd_workspace_bytes`` bytes, or
     None.  Returns (dX, dWg, dWu)."""
-    dtype, typ = _dtype(X)
-    M, K, ldx, px = _matrix(X, "X", dtype)
+    dtype, typ, at, M, K, px, ldx = _first(X)
     N = _rows(Wg, "Wg")
-    pg, ldg = _shaped(Wg, "Wg", dtype, N, K)
-    pu, ldu = _shaped(Wu, "Wu", dtype, N, K)
-    ins = _shaped(G, "G", dtype, M, N) + _shaped(U, "U", dtype, M, N) + \
-        _shaped(dH, "dH", dtype, M, N)
-    outs = _optional(dX, "dX", dtype, M, K) + _optional(dWg, "dWg", dtype, N, K) + \
-        _optional(dWu, "dWu", dtype, N, K)
-    lib = load_library()
-    sizes = (M, N, K, px, ldx, pg, ldg, pu, ldu)
-    want = (dX is not None, dWg is not None or dWu is not None)
-    _Place(stream, X, Wg, Wu, G, U, dH, dX, dWg, dWu).run(
-        lib.gemm_gated_bwd, (typ, _act(act)) + sizes + ins + outs,
-        lambda: int(lib.gemm_gated_bwd_workspace(typ, *sizes, *want)), workspace, X)
+    sizes = (M, N, K, px, ldx, *_shaped(Wg, "Wg", dtype, at, N, K),
+             *_shaped(Wu, "Wu", dtype, at, N, K))
+    ins = (*_shaped(G, "G", dtype, at, M, N), *_shaped(U, "U", dtype, at, M, N),
+           *_shaped(dH, "dH", dtype, at, M, N))
+    outs = (*_optional(dX, "dX", dtype, at, M, K), *_optional(dWg, "dWg", dtype, at, N, K),
+            *_optional(dWu, "dWu", dtype, at, N, K))
+    lib = _lib or load_library()
+    _run(at, stream, lib.gemm_gated_bwd, (typ, _act(act)) + sizes + ins + outs,
+         lambda: lib.gemm_gated_bwd_workspace(typ, *sizes, dX is not None,
+                                              dWg is not None or dWu is not None), workspace)
     return dX, dWg, dWu
 
 
 def gated_bwd_workspace_bytes(X, Wg, Wu, want_dx: bool = True, want_dw: bool = True) -> int:
     """Workspace bytes ``gemm_gated_bwd`` needs for these tensors and gradients."""
-    dtype, typ = _dtype(X)
-    M, K, ldx, px = _matrix(X, "X", dtype)
+    dtype, typ, at, M, K, px, ldx = _first(X)
     N = _rows(Wg, "Wg")
-    return int(load_library().gemm_gated_bwd_workspace(
-        typ, M, N, K, px, ldx, *_shaped(Wg, "Wg", dtype, N, K), *_shaped(Wu, "Wu", dtype, N, K),
-        bool(want_dx), bool(want_dw)))
+    return load_library().gemm_gated_bwd_workspace(
+        typ, M, N, K, px, ldx, *_shaped(Wg, "Wg", dtype, at, N, K),
+        *_shaped(Wu, "Wu", dtype, at, N, K), bool(want_dx), bool(want_dw))
 
 
 def gemm_w4(X, Wq, scales, C, group: int = 128, zeros=None, bias=None, act: str = "none",
@@ -216,32 +216,31 @@ def gemm_w4(X, Wq, scales, C, group: int = 128, zeros=None, bias=None, act: str 
     or None for 8.  Meant for the few rows of decode steps (the weights are
     streamed once for every 64 rows).  Returns C."""
     torch = _torch_module()
-    dtype, typ = _dtype(X)
-    M, K, ldx, px = _matrix(X, "X", dtype)
+    dtype, typ, at, M, K, px, ldx = _first(X)
     if group <= 0:
         raise ValueError("group must be a positive multiple of 32")
     N = _rows(Wq, "Wq")
     groups = -(-K // group)
-    pq, ldq = _shaped(Wq, "Wq", torch.uint8, N, (K + 1) // 2)
-    ps, lds = _shaped(scales, "scales", dtype, N, groups)
-    pz, ldz = _optional(zeros, "zeros", torch.uint8, N, groups)
-    pc, ldc = _shaped(C, "C", dtype, M, N)
+    pq, ldq = _shaped(Wq, "Wq", torch.uint8, at, N, (K + 1) // 2)
+    ps, lds = _shaped(scales, "scales", dtype, at, N, groups)
+    pz, ldz = _optional(zeros, "zeros", torch.uint8, at, N, groups)
+    pc, ldc = _shaped(C, "C", dtype, at, M, N)
     if bias is None and residual is None:
         pbias, code, pres, ldr = None, _act(act), None, 0
     else:
+        for t in (bias, residual):
+            if t is not None and t.get_device() != at:
+                raise ValueError("all tensors of a call must live on one GPU")
         pbias, code, pres, ldr = _epilogue_args(bias, act, residual, M, N, dtype)
-    _Place(stream, X, Wq, scales, C, zeros, bias, residual).run(
-        load_library().gemm_w4, (typ, M, N, K, group, px, ldx, pq, ldq, ps, lds, pz, ldz, pbias,
-                                 code, pres, ldr, pc, ldc))
+    _run(at, stream, (_lib or load_library()).gemm_w4,
+         (typ, M, N, K, group, px, ldx, pq, ldq, ps, lds, pz, ldz, pbias, code, pres, ldr, pc, ldc))
     return C
 
 
 def _xent_args(X, W):
-    dtype, typ = _dtype(X)
-    M, K, ldx, px = _matrix(X, "X", dtype)
+    dtype, typ, at, M, K, px, ldx = _first(X)
     N = _rows(W, "W")
-    pw, ldw = _shaped(W, "W", dtype, N, K)
-    return dtype, (typ, M, N, K, px, ldx, pw, ldw)
+    return dtype, at, (typ, M, N, K, px, ldx, *_shaped(W, "W", dtype, at, N, K))
 
 
 def gemm_xent(X, W, targets, loss, lse, ignore_index: int = -100, workspace=None, stream=None):
@@ -252,21 +251,20 @@ def gemm_xent(X, W, targets, loss, lse, ignore_index: int = -100, workspace=None
     0; a target outside [0, N) otherwise gives NaN.  ``workspace``:
     ``xent_workspace_bytes`` bytes, or None.  Returns loss."""
     torch = _torch_module()
-    _, sizes = _xent_args(X, W)
+    _, at, sizes = _xent_args(X, W)
     M = sizes[1]
-    pt = _vector(targets, "targets", torch.int64, M)
-    pl = _vector(loss, "loss", torch.float32, M)
-    pe = _vector(lse, "lse", torch.float32, M)
-    lib = load_library()
-    _Place(stream, X, W, targets, loss, lse).run(
-        lib.gemm_xent, sizes + (pt, int(ignore_index), pl, pe),
-        lambda: int(lib.gemm_xent_workspace(*sizes)), workspace, X)
+    pt = _vector(targets, "targets", torch.int64, at, M)
+    pl = _vector(loss, "loss", torch.float32, at, M)
+    pe = _vector(lse, "lse", torch.float32, at, M)
+    lib = _lib or load_library()
+    _run(at, stream, lib.gemm_xent, sizes + (pt, int(ignore_index), pl, pe),
+         lambda: lib.gemm_xent_workspace(*sizes), workspace)
     return loss
 
 
 def xent_workspace_bytes(X, W) -> int:
     """Workspace bytes ``gemm_xent`` needs for these tensors."""
-    return int(load_library().gemm_xent_workspace(*_xent_args(X, W)[1]))
+    return load_library().gemm_xent_workspace(*_xent_args(X, W)[2])
 
 
 def gemm_xent_bwd(X, W, targets, lse, dloss, dX=None, dW=None, ignore_index: int = -100,
@@ -276,21 +274,19 @@ def gemm_xent_bwd(X, W, targets, lse, dloss, dX=None, dW=None, ignore_index: int
     computed if given.  ``workspace``: ``xent_bwd_workspace_bytes`` bytes, or None.
     Returns (dX, dW)."""
     torch = _torch_module()
-    dtype, sizes = _xent_args(X, W)
+    dtype, at, sizes = _xent_args(X, W)
     M, N, K = sizes[1:4]
-    pt = _vector(targets, "targets", torch.int64, M)
-    pe = _vector(lse, "lse", torch.float32, M)
-    pd = _vector(dloss, "dloss", torch.float32, M)
-    outs = _optional(dX, "dX", dtype, M, K) + _optional(dW, "dW", dtype, N, K)
-    lib = load_library()
-    _Place(stream, X, W, targets, lse, dloss, dX, dW).run(
-        lib.gemm_xent_bwd, sizes + (pt, int(ignore_index), pe, pd) + outs,
-        lambda: int(lib.gemm_xent_bwd_workspace(*sizes, dX is not None, dW is not None)),
-        workspace, X)
+    pt = _vector(targets, "targets", torch.int64, at, M)
+    pe = _vector(lse, "lse", torch.float32, at, M)
+    pd = _vector(dloss, "dloss", torch.float32, at, M)
+    outs = (*_optional(dX, "dX", dtype, at, M, K), *_optional(dW, "dW", dtype, at, N, K))
+    lib = _lib or load_library()
+    _run(at, stream, lib.gemm_xent_bwd, sizes + (pt, int(ignore_index), pe, pd) + outs,
+         lambda: lib.gemm_xent_bwd_workspace(*sizes, dX is not None, dW is not None), workspace)
     return dX, dW
 
 
 def xent_bwd_workspace_bytes(X, W, want_dx: bool = True, want_dw: bool = True) -> int:
     """Workspace bytes ``gemm_xent_bwd`` needs for these tensors and gradients."""
-    return int(load_library().gemm_xent_bwd_workspace(*_xent_args(X, W)[1], bool(want_dx),
-                                                      bool(want_dw)))
+    return load_library().gemm_xent_bwd_workspace(*_xent_args(X, W)[2], bool(want_dx),
+                                                  bool(want_dw))

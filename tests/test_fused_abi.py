@@ -73,25 +73,35 @@ def test_workspace_sizes(lib):
     assert ws(F16, 0, 512, 127, A, 127, A, 127, A, 127) == 0
     assert ws(7, 256, 512, 127, A, 127, A, 127, A, 127) == 0
     bwd = lib.gemm_gated_bwd_workspace
-    # dG and dU, and the last 64 columns again where N is no multiple of 64
-    assert bwd(F16, 256, 512, 128, A, 128, A, 128, A, 128, 1, 1) == 256 * 1024 * 2
-    assert bwd(F16, 256, 520, 128, A, 128, A, 128, A, 128, 1, 0) == 256 * 1040 * 2 + 256 * 256
-    assert bwd(F16, 256, 520, 128, A, 128, A, 128, A, 128, 0, 1) == 256 * 1040 * 2
-    assert bwd(F16, 256, 512, 128, A, 128, A, 128, A, 136, 0, 1) == 256 * 1024 * 2
-    assert bwd(F16, 256, 512, 128, A, 128, A, 128, A, 136, 1, 0) == 256 * 1024 * 2 + 2 * copy
+    # dW: dG and dU, and X transposed
+    assert bwd(F16, 256, 512, 128, A, 128, A, 128, A, 128, 0, 1) == 256 * 1024 * 2 + 128 * 256 * 2
+    assert bwd(F16, 256, 520, 128, A, 128, A, 128, A, 128, 0, 1) == 256 * 1040 * 2 + 128 * 256 * 2
+    # dX: the last 64 columns of dG and dU again where N is no multiple of 64,
+    # copies of weights whose rows are not equally far apart, fp32 sums where K
+    # (here N of both weights) is cut into ranges: one of 256 x 128 for each
+    d, sums = 256 * 1040 * 2 + 256 * 256, 256 * 128 * 4
+    dx = bwd(F16, 256, 520, 128, A, 128, A, 128, A, 128, 1, 0)
+    assert dx > d and (dx - d) % sums == 0 and (dx - d) // sums <= 64
+    apart = bwd(F16, 256, 520, 128, A, 128, A, 128, A, 136, 1, 0)
+    assert apart == dx + 2 * (520 * 128 * 2)
+    assert bwd(F16, 256, 512, 128, A, 128, A, 128, A, 136, 0, 1) == 256 * 1024 * 2 + 128 * 256 * 2
     assert bwd(F16, 256, 512, 128, A, 128, A, 128, A, 128, 0, 0) == 0
+    # enough tiles: no ranges
+    assert bwd(BF16, 4096, 16384, 4096, A, 4096, A, 4096, A, 4096, 1, 0) == 4096 * 32768 * 2
     x = lib.gemm_xent_workspace
     assert x(BF16, 0, 1000, 128, A, 128, A, 128) == 0
     assert x(BF16, 200, 0, 128, A, 128, A, 128) == 0
     assert x(BF16, 200, 1000, 128, A, 128, A, 128) == 200 * 16 * 8 + 1024
     xb = lib.gemm_xent_bwd_workspace
-    small, large = (xb(BF16, 4096, n, 128, A, 128, A, 128, 1, 1) for n in (1024, 131072))
-    assert small == 4096 * (1024 * 2 + 128) + 256
+    # dW alone: d and X transposed (and 256 bytes for the factor)
+    assert xb(BF16, 4096, 1024, 128, A, 128, A, 128, 0, 1) == 4096 * (1024 + 128) * 2 + 256
     # pieces: far less than the logits' 2^30 bytes
-    assert large < 400 << 20
+    large = xb(BF16, 4096, 131072, 128, A, 128, A, 128, 1, 1)
+    assert 256 << 20 < large < 512 << 20
     assert xb(BF16, 4096, 1024, 128, A, 128, A, 128, 0, 0) == 0
     # sizes past 32 bits
-    assert bwd(BF16, 1 << 20, 1 << 14, 4096, A, 4096, A, 4096, A, 4096, 1, 1) == 1 << 36
+    assert bwd(BF16, 1 << 20, 1 << 14, 4096, A, 4096, A, 4096, A, 4096, 1, 1) == \
+        (1 << 36) + (1 << 33)
 
 
 def bwd(lib, type=F16, act=2, M=4, N=8, K=16, X=A, ldx=16, Wg=A, ldg=16, Wu=A, ldu=16, G=A, ldG=8,
