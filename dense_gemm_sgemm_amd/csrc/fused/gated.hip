@@ -111,7 +111,7 @@ BwdPlan plan_bwd(int M, int N, int K, Mat Wg, Mat Wu, bool dx, bool dw) {
   BwdPlan p;
   p.Mp = pad_slabs(M);
   p.Nk = pad_rows(N);
-  p.Np = (int)round_up(p.Nk, 8);
+  p.Np = (int)line_ld(p.Nk);
   p.ld = 2 * (int64_t)p.Np;
   p.tail = dx && p.Nk % 64 != 0;
   p.bytes_d = round256((size_t)p.Mp * p.ld * 2);
@@ -283,7 +283,7 @@ MI355FUSED_API int gemm_gated_bwd(int type, int act, int M, int N, int K, const 
     // both gradients as two parts of one product's rows, or the one asked for
     const bool both = dWg != nullptr && dWu != nullptr;
     Args16 a{dWg ? d : d + p.Np, xt, out16(dWg ? dWg : dWu), p.ld, p.Mp, dWg ? lddwg : lddwu,
-             p.Np, pad_k(K), p.Mp};
+             (int)round_up(p.Nk, 8), pad_k(K), p.Mp};
     a.fmt = fmt;
     FusedExtra f;
     f.m_end = N;

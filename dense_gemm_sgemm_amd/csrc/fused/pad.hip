@@ -47,7 +47,7 @@ Mat PadJobs::copy(Mat m, int rows, int K, char*& dst) {
   j.src = m.p;
   j.dst = reinterpret_cast<half_t*>(dst);
   j.lds = m.ld;
-  j.ldd = pad_k(K);
+  j.ldd = line_ld(pad_k(K));
   j.rows = rows;
   j.cols = K;
   j.rows_p = pad_rows(rows);

@@ -9,7 +9,8 @@
 namespace mi355gemm {
 namespace fused {
 
-using namespace hshape;
+using hshape::BK;
+constexpr int GM = 4;   // tile rows of a group: 4 against 8 measured 2 % faster here
 
 static constexpr Shape kShapes[] = {
     {256, 256, 1, 256 * 256, 256 * 256},

@@ -70,16 +70,17 @@ def test_workspace_sizes(lib):
     assert ws(F16, 256, 512, 128, A, 128, ODD, 128, A, 128) == copy      # address
     assert ws(F16, 256, 512, 128, A, 128, A, 132, A, 128) == copy        # rows apart
     assert ws(F16, 256, 512, 127, A, 127, A, 127, A, 127) == 256 * 256 + 2 * copy
+    assert ws(F16, 256, 512, 130, A, 130, A, 130, A, 130) == (256 + 2 * 512) * 192 * 2
     assert ws(F16, 0, 512, 127, A, 127, A, 127, A, 127) == 0
     assert ws(7, 256, 512, 127, A, 127, A, 127, A, 127) == 0
     bwd = lib.gemm_gated_bwd_workspace
     # dW: dG and dU, and X transposed
     assert bwd(F16, 256, 512, 128, A, 128, A, 128, A, 128, 0, 1) == 256 * 1024 * 2 + 128 * 256 * 2
-    assert bwd(F16, 256, 520, 128, A, 128, A, 128, A, 128, 0, 1) == 256 * 1040 * 2 + 128 * 256 * 2
+    assert bwd(F16, 256, 520, 128, A, 128, A, 128, A, 128, 0, 1) == 256 * 1152 * 2 + 128 * 256 * 2
     # dX: the last 64 columns of dG and dU again where N is no multiple of 64,
     # copies of weights whose rows are not equally far apart, fp32 sums where K
     # (here N of both weights) is cut into ranges: one of 256 x 128 for each
-    d, sums = 256 * 1040 * 2 + 256 * 256, 256 * 128 * 4
+    d, sums = 256 * 1152 * 2 + 256 * 256, 256 * 128 * 4
     dx = bwd(F16, 256, 520, 128, A, 128, A, 128, A, 128, 1, 0)
     assert dx > d and (dx - d) % sums == 0 and (dx - d) // sums <= 64
     apart = bwd(F16, 256, 520, 128, A, 128, A, 128, A, 136, 1, 0)
