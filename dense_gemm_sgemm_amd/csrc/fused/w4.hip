@@ -29,11 +29,20 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBlock = 128;   // K values of a block
-constexpr int kUnroll = 4;    // blocks of a chunk; a wave has two chunks in flight
+// Blocks of a chunk (a wave has two chunks in flight): four, two where each
+// block brings four groups' scales or four blocks of X rows, one where both:
+// more registers would spill (64 x 4096 x 16384: 64.9 against 35.5 us).
+constexpr int unroll_of(bool four_groups, bool four_tiles) {
+  return four_groups && four_tiles ? 1 : four_groups || four_tiles ? 2 : 4;
+}
 constexpr int kMaxWaves = 8;
 constexpr int most_waves(int mt) { return mt == 4 ? 4 : kMaxWaves; }   // two workgroups' LDS a CU
 constexpr int kStaged = 4;    // 16-byte pieces of X a thread loads ahead of its weights
-constexpr int kXBytes = 32 << 10;   // X up to this size is kept in LDS
+// X of up to three rows is kept in LDS where it takes no more than kXBytes, or,
+// with a workgroup a CU at most, kXBytesAlone; with more rows each wave's own
+// copy is no slower, and smaller (1 x 4096 x 16384: 12.1 against 16.4 us in
+// LDS; 3 x 16384 x 4096: 12.7 against 14.3; 5 x 16384 x 4096: 17.0 against 14.5).
+constexpr int kXRows = 3, kXBytes = 32 << 10, kXBytesAlone = 56 << 10;
 
 struct W4Args {
   const half_t* X;
@@ -205,11 +214,12 @@ __device__ __forceinline__ void multiply(u4 raw, const uint16_t* scales, const u
   }
 }
 
-// XL: the rows of X (M <= 16 of them) lie in LDS, reordered, zero past K, in
+// XL: the rows of X (M <= 16) lie in LDS, reordered, zero past K, in
 // rows of K rounded up to blocks plus 16 bytes (rows then start in different
 // banks).  Otherwise each wave stages the rows of a block in turn (XStage).
 template <int FMT, int GR, int MT, bool XL>
 __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t base) {
+  constexpr int kUnroll = unroll_of(groups_per_block(GR) == 4, MT == 4);
   typedef XStage<MT, kBlock> Stage;
   extern __shared__ __attribute__((aligned(16))) unsigned char dynamic_lds[];
   __shared__ __attribute__((aligned(16))) unsigned char
@@ -384,11 +394,13 @@ extern "C" MI355FUSED_API int gemm_w4(int type, int M, int N, int K, int group, 
   const int64_t wgs = ((int64_t)N + 15) / 16 * (((int64_t)M + 63) / 64);
   const int64_t blocks = ((int64_t)K + kBlock - 1) / kBlock;
   // whole chunks where four waves have one each, else single blocks
-  a.chunks = K / kBlock >= 4 * kUnroll ? K / (kBlock * kUnroll) : 0;
+  const int unroll = unroll_of(group % kBlock != 0 && group != 64, mt == 4);
+  a.chunks = K / kBlock >= 4 * unroll ? K / (kBlock * unroll) : 0;
   a.waves = skinny::waves_for(wgs, a.chunks ? a.chunks : std::max<int>(1, (int)blocks),
                               most_waves(mt), cus);
   const int64_t x_bytes = M * (blocks * kBlock * 2 + 16);
-  const bool x_in_lds = M <= 16 && K > 0 && x_bytes <= kXBytes;
+  const bool x_in_lds =
+      M <= kXRows && K > 0 && x_bytes <= (wgs <= cus ? kXBytesAlone : kXBytes);
   const unsigned lds_bytes =
       x_in_lds ? (unsigned)(x_bytes + (a.waves - 1) * mt * 64 * sizeof(f4)) : 0;
   const void* k = type == GEMM_TYPE_BF16 ? pick<kFmtBF16>(M, group, x_in_lds)

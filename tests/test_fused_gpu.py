@@ -241,7 +241,10 @@ def w4_check(C, X, Wq, s, z, group, bias=None, name="none", res=None):
     (16, 64, 640, 64, False), (17, 70, 2048, 128, True), (7, 31, 333, 96, True),
     (31, 40, 1536, 256, True), (33, 50, 257, 128, True), (64, 96, 1024, 64, True),
     (65, 40, 520, 32, True), (130, 17, 300, 160, False), (1, 300, 16384, 128, True),
-    (4, 20, 31, 128, True), (9, 65, 130, 1024, True)])
+    (4, 20, 31, 128, True), (9, 65, 130, 1024, True), (3, 40, 8192, 64, True),
+    (1, 33, 28000, 128, True), (20, 129, 2048, 64, True), (32, 300, 4100, 128, False),
+    (40, 128, 16384, 128, True), (48, 257, 9000, 32, True), (100, 250, 3333, 96, True),
+    (17, 16, 100, 32, False)])
 def test_w4(M, N, K, group, zeros, typ):
     dt = DT[typ]
     X, Wq, s, z = w4_inputs(M, N, K, group, dt, zeros, M + N + K)
@@ -266,8 +269,9 @@ def test_w4_strides(group, pad, shift):
 
 @pytest.mark.parametrize("typ", TYPES)
 @pytest.mark.parametrize("name", ["none", "relu", "silu"])
-def test_w4_write_back(name, typ):
-    M, N, K, dt = 9, 50, 384, DT[typ]
+@pytest.mark.parametrize("M,K", [(2, 384), (9, 384), (33, 4096)])
+def test_w4_write_back(M, K, name, typ):
+    N, dt = 50, DT[typ]
     X, Wq, s, z = w4_inputs(M, N, K, 128, dt, True, 6)
     r = gen(7)
     bias, res = randn((N,), 5.0, dt, r).to(DEV), randn((M, N), 5.0, dt, r).to(DEV)
