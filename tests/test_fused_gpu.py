@@ -502,6 +502,29 @@ def test_xent_extreme_logits():
         xent_bwd_check(X, W, t, lse, dloss, dX, None)
 
 
+@pytest.mark.parametrize("typ", TYPES)
+def test_xent_bwd_one_dloss_for_all(typ):
+    """A mean's dloss, just below halfway between two 16-bit values: its own
+    rounding (up to half a step, the same way in every row) must not reach the
+    gradients.  Their outputs' rounding is at most half a step each, evenly
+    spread: 1 / sqrt(3) of it in the norm; the rounding of d adds as much of the
+    probabilities' share, here a tenth (300 rows, 1000 columns)."""
+    M, N, K, dt = 300, 1000, 128, DT[typ]
+    X, W, t = xent_inputs(M, N, K, dt, 17, sd=1.0)
+    loss, lse = torch.empty((M,), device=DEV), torch.empty((M,), device=DEV)
+    dg.gemm_xent(X, W, t, loss, lse)
+    half = torch.finfo(dt).eps / 2
+    dloss = torch.full((M,), 1.0 + 0.99 * half, device=DEV)
+    dX, dW = torch.empty_like(X), torch.empty_like(W)
+    dg.gemm_xent_bwd(X, W, t, lse, dloss, dX=dX, dW=dW)
+    d = torch.softmax(X.double() @ W.double().T, 1)
+    live = t != IGN
+    d[torch.arange(M, device=DEV)[live], t[live]] -= 1
+    d *= live[:, None] * dloss.double()[:, None]
+    for got, ref in ((dX, d @ W.double()), (dW, d.T @ X.double())):
+        norm_close(got, ref, 1.2 * half / 3 ** 0.5, "one dloss")
+
+
 # ---------------------------------------------------------------- how they are called
 
 def test_run_together():
