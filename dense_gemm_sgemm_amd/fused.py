@@ -62,11 +62,16 @@ def load_library() -> ctypes.CDLL:
         return lib
 
 
+_Tensor = None   # torch.Tensor, once a call has needed it
+
+
 def _first(t):
     """(dtype, GEMM_TYPE_*, GPU index, rows, columns, pointer, leading dimension)
     of the call's X; the other operands are held to its type and GPU."""
+    global _Tensor
     torch = _torch_module()
-    dtype = t.dtype if isinstance(t, torch.Tensor) else None
+    _Tensor = torch.Tensor
+    dtype = t.dtype if isinstance(t, _Tensor) else None
     if dtype is torch.bfloat16:
         typ = 1
     elif dtype is torch.float16:
@@ -78,8 +83,7 @@ def _first(t):
 
 
 def _rows(t, name) -> int:
-    torch = _torch_module()
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+    if not isinstance(t, _Tensor) or t.dim() != 2:
         raise TypeError("%s must be a 2-D torch tensor" % name)
     return t.shape[0]
 
@@ -88,11 +92,10 @@ def _shaped(t, name, dtype, index, rows, cols):
     """(device pointer or None, leading dimension) of a rows x cols matrix on GPU
     ``index``.  Runs for every operand of every call: the usual case is told by
     the cheapest queries, and anything else by _matrix, which says what is wrong."""
-    torch = _torch_module()
-    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (rows, cols) and \
-            t.get_device() == index:
+    if isinstance(t, _Tensor) and t.dtype is dtype and t.shape == (rows, cols) and \
+            t.get_device() == index and rows > 1 and cols > 1:
         s0, s1 = t.stride()
-        if s1 == 1 and rows > 1 and cols > 1:
+        if s1 == 1:
             return t.data_ptr(), s0
     r, c, ld, ptr = _matrix(t, name, dtype)
     if r != rows or c != cols:
@@ -116,13 +119,19 @@ def _vector(t, name, dtype, index, n):
     return t.data_ptr() if n else None
 
 
+def _current_gpu() -> int:
+    torch = _torch_module()
+    get = getattr(torch._C, "_cuda_getDevice", None)   # as torch.cuda.current_device, less set-up
+    return get() if get is not None else torch.cuda.current_device()
+
+
 def _run(index, stream, fn, args, need=None, workspace=None):
     """``fn(*args[, workspace, bytes], stream)`` with GPU ``index`` current;
     ``need()`` gives the size of the workspace the call takes."""
     torch = _torch_module()
     if stream is not None and stream.device.index != index:
         raise ValueError("stream belongs to another GPU than the tensors")
-    if index != torch.cuda.current_device():
+    if index != _current_gpu():
         with torch.cuda.device(index):
             return _run(index, stream, fn, args, need, workspace)
     handle = stream.cuda_stream if stream is not None else _current_stream_handle()
