@@ -357,7 +357,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       sp = (int)((uint32_t)item / tiles);
       item -= (uint32_t)sp * tiles;
     }
-    kb = sp * (SPLIT ? p.sk.per : MODE == kGradX ? ta.x.per : 0);
+    kb = sp * (SPLIT ? p.sk.per : 0);
+    if constexpr (MODE == kGradX) kb = sp * ta.x.per;
     int tm, tn;
     if constexpr (MODE == kProduct)
       map_tile<GM>(item, tiles_m, tiles_n, tm, tn);
@@ -393,26 +394,27 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   // (four copying waves): waves 0 and 1 copy from p.B, 2 and 3 from x.B2, and
   // copy i holds rows 16 i + 8 (cw & 1) .. + 7 of either.
   static_assert(MODE != kGated || C::kCopyWaves == 4, "copy assignment of the two B matrices");
-  int64_t ldb = p.ldb;
-  const half_t* pB = p.B;
-  if constexpr (MODE == kGated) {
-    if (cwp >= 2) {
-      ldb = ta.x.ldb2;
-      pB = ta.x.B2;
-    }
-  }
-  const uint32_t offB = (uint32_t)(lane_row * ldb + 8 * lane_chunk) * 2;
+  auto ldb_of_wave = [&]() __attribute__((always_inline)) {
+    if constexpr (MODE == kGated) return cwp >= 2 ? ta.x.ldb2 : p.ldb;
+    else return p.ldb;
+  };
+  auto b_of_wave = [&]() __attribute__((always_inline)) {
+    if constexpr (MODE == kGated) return cwp >= 2 ? ta.x.B2 : p.B;
+    else return p.B;
+  };
+  const uint32_t offB = (uint32_t)(lane_row * ldb_of_wave() + 8 * lane_chunk) * 2;
   // RAG, the last slab of K: a lane whose chunk lies past K loads the last
   // chunk inside K instead (zeroed once it has landed).
   const bool chunk_past = RAG && 8 * lane_chunk >= kv;
   const int tail_chunk = chunk_past ? kv / 8 - 1 : lane_chunk;
   const uint32_t offA_tail = (uint32_t)(lane_row * p.lda + 8 * tail_chunk) * 2;
-  const uint32_t offB_tail = (uint32_t)(lane_row * ldb + 8 * tail_chunk) * 2;
+  const uint32_t offB_tail = (uint32_t)(lane_row * ldb_of_wave() + 8 * tail_chunk) * 2;
   const int64_t copy_strideA = (int64_t)C::kCopyWaves * C::kRowsPerCopy * p.lda * 2;
   const int64_t copy_strideB =
-      (int64_t)(MODE == kGated ? 16 : C::kCopyWaves * C::kRowsPerCopy) * ldb * 2;
+      (int64_t)(MODE == kGated ? 16 : C::kCopyWaves * C::kRowsPerCopy) * ldb_of_wave() * 2;
   const int64_t firstA = (int64_t)cwp * C::kRowsPerCopy * p.lda * 2;
-  const int64_t firstB = (int64_t)(MODE == kGated ? cwp & 1 : cwp) * C::kRowsPerCopy * ldb * 2;
+  const int64_t firstB =
+      (int64_t)(MODE == kGated ? cwp & 1 : cwp) * C::kRowsPerCopy * ldb_of_wave() * 2;
   // A K-major operand (LAY) with R = 1024 / kTP k-rows per copy: copy c
   // fills k-rows R c .. R c + R - 1, lane l writing k-row R c + l / (kTP / 16)
   // at position l % (kTP / 16), so it loads logical chunk
@@ -448,18 +450,24 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     const char* b;
     unsigned char* l;
     uint32_t oa, ob;   // this lane's offsets (RAG: the clamped ones in a tile's last slab)
-    int64_t sa;        // kGradX: bytes between A's copies
   };
+  struct CopyBaseX : CopyBase {   // kGradX
+    int64_t sa;        // bytes between A's copies
+  };
+  typedef std::conditional_t<MODE == kGradX, CopyBaseX, CopyBase> CopyBaseT;
   // kGradX: this lane's offset in x.tail; slabs of each part of K
   uint32_t offA_x = 0;
-  if constexpr (MODE == kGradX) offA_x = (uint32_t)(lane_row * ta.x.ldt + 8 * lane_chunk) * 2;
-  const int nk_part = (p.K + BK - 1) / BK;
+  int nk_part = 0;
+  if constexpr (MODE == kGradX) {
+    offA_x = (uint32_t)(lane_row * ta.x.ldt + 8 * lane_chunk) * 2;
+    nk_part = (p.K + BK - 1) / BK;
+  }
   // LAY with a K tail (RAG): the last slab is copied from K - 64 .. K - 1,
   // every row and chunk inside the matrix; its first 64 - kv positions repeat
   // the slab before and are zeroed in LDS (wait_zero_sync), so they add 0 x 0.
   auto slab_base = [&](int stage, int m0, int n0, int t, bool tail, int part)
                        __attribute__((always_inline)) {
-    CopyBase cb;
+    CopyBaseT cb;
     cb.l = lds + stage * kStage;
     if constexpr (MODE == kGradX) {
       // slab t of part t / (slabs of a part); the last one of a part with a
@@ -481,7 +489,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
                : (const char*)(p.A + (int64_t)m0 * p.lda) + firstA + 2 * k0;
     if constexpr (MODE == kGradW && kAT) cb.a += part * ta.x.partA * 2;
     cb.b = kBT ? (const char*)(p.B + k0 * p.ldb + n0) + firstTB
-               : (const char*)(pB + (int64_t)n0 * ldb) + firstB + 2 * k0;
+               : (const char*)(b_of_wave() + (int64_t)n0 * ldb_of_wave()) + firstB + 2 * k0;
     (void)part;
     cb.oa = LAY == 0 && RAG && tail ? offA_tail : offA;
     cb.ob = LAY == 0 && RAG && tail ? offB_tail : offB;
@@ -495,15 +503,16 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     else
       __builtin_amdgcn_global_load_lds((gbl_void_t*)(base + off), (lds_void_t*)dst, 16, 0, 0);
   };
-  auto copy_one = [&](const CopyBase& cb, int c) __attribute__((always_inline)) {
+  auto copy_one = [&](const CopyBaseT& cb, int c) __attribute__((always_inline)) {
     if (c < kPerWaveA) {
       if (kCopiesA % C::kCopyWaves == 0 || c * C::kCopyWaves + cw < kCopiesA) {
         if constexpr (kAT)
           issue(cb.a + c * copy_strideTA, t_hi(kTPA, c) ? offTA1 : offTA0,
                 cb.l + (c * C::kCopyWaves + cw) * 1024);
+        else if constexpr (MODE == kGradX)
+          issue(cb.a + c * cb.sa, cb.oa, cb.l + (c * C::kCopyWaves + cw) * 1024);
         else
-          issue(cb.a + c * (MODE == kGradX ? cb.sa : copy_strideA), cb.oa,
-                cb.l + (c * C::kCopyWaves + cw) * 1024);
+          issue(cb.a + c * copy_strideA, cb.oa, cb.l + (c * C::kCopyWaves + cw) * 1024);
       }
     } else {
       const int i = c - kPerWaveA;
@@ -1044,7 +1053,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   int mlo0 = 0, nlo0 = 0;   // the current tile's first stored row and column
   // slabs of the work item `ahead` items after the current one (kGradX: the
   // last range of K may be shorter)
-  const int nk_all = MODE == kGradX ? ta.x.parts * nk_part : nk;
+  int nk_all = nk;
+  if constexpr (MODE == kGradX) nk_all = ta.x.parts * nk_part;
   auto slabs_of = [&](int d) __attribute__((always_inline)) {
     if constexpr (MODE == kGradX) {
       const int left = nk_all - (d == 0 ? ok[0] : d == 1 ? ok[1] : ok[2]);
@@ -1055,24 +1065,32 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     }
   };
   // (the operators compute one new origin a tile and move the others up)
-  int fm[3], fn[3];   // first stored rows and columns
+  int fm[3], fn[3];   // their first stored rows and columns
   auto refresh_origins = [&](int j) __attribute__((always_inline)) {
     cur = j;
+    if constexpr (MODE == kProduct) {
 #pragma unroll
-    for (int d = 0; d < 3; ++d) {
-      if (MODE != kProduct && j > 0 && d < 2) {
-        om[d] = om[d + 1];
-        on[d] = on[d + 1];
-        ok[d] = ok[d + 1];
-        os[d] = os[d + 1];
-        fm[d] = fm[d + 1];
-        fn[d] = fn[d + 1];
-      } else {
+      for (int d = 0; d < 3; ++d) {
         int mlo, nlo;
         tile_origin(j + d < ntiles ? j + d : ntiles - 1, om[d], on[d], ok[d], os[d], mlo, nlo);
-        fm[d] = mlo;
-        fn[d] = nlo;
-        if constexpr (MODE != kProduct) {
+        if (d == 0) {
+          mlo0 = mlo;
+          nlo0 = nlo;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int d = 0; d < 3; ++d) {
+        if (j > 0 && d < 2) {
+          om[d] = om[d + 1];
+          on[d] = on[d + 1];
+          ok[d] = ok[d + 1];
+          os[d] = os[d + 1];
+          fm[d] = fm[d + 1];
+          fn[d] = fn[d + 1];
+        } else {
+          tile_origin(j + d < ntiles ? j + d : ntiles - 1, om[d], on[d], ok[d], os[d], fm[d],
+                      fn[d]);
           // wave-uniform, but a division leaves them in vector registers
           om[d] = __builtin_amdgcn_readfirstlane(om[d]);
           on[d] = __builtin_amdgcn_readfirstlane(on[d]);
@@ -1082,10 +1100,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
           fn[d] = __builtin_amdgcn_readfirstlane(fn[d]);
         }
       }
-      if (d == 0) {
-        mlo0 = fm[0];
-        nlo0 = fn[0];
-      }
+      mlo0 = fm[0];
+      nlo0 = fn[0];
     }
   };
   refresh_origins(0);
@@ -1102,13 +1118,17 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     const int m0 = d == 0 ? om[0] : d == 1 ? om[1] : om[2];
     const int n0 = d == 0 ? on[0] : d == 1 ? on[1] : on[2];
     const int kb = d == 0 ? ok[0] : d == 1 ? ok[1] : ok[2];
-    const int t = kb + (past ? slabs_of(d) - 1 : tc);
-    const int part = MODE == kGradW ? (d == 0 ? os[0] : d == 1 ? os[1] : os[2]) : 0;
-    const bool last = MODE == kGradX ? t == nk_part - 1 || t == nk_all - 1 : t == nk - 1;
-    return slab_base(stage, m0, n0, t, RAG && kv < BK && last, part);
+    if constexpr (MODE == kGradX) {
+      const int t = kb + (past ? slabs_of(d) - 1 : tc);
+      return slab_base(stage, m0, n0, t, kv < BK && (t == nk_part - 1 || t == nk_all - 1), 0);
+    } else {
+      const int part = MODE == kGradW ? (d == 0 ? os[0] : d == 1 ? os[1] : os[2]) : 0;
+      const int t = past ? nk - 1 : tc;
+      return slab_base(stage, m0, n0, kb + t, RAG && kv < BK && t == nk - 1, part);
+    }
   };
   auto copy_next = [&](int stage) __attribute__((always_inline)) {
-    const CopyBase cb = next_base(stage);
+    const CopyBaseT cb = next_base(stage);
 #pragma unroll
     for (int c = 0; c < kCopies; ++c) copy_one(cb, c);
   };
@@ -1121,7 +1141,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     };
     constexpr bool kCp = decltype(is_copier)::value;
     constexpr bool kNext = decltype(next)::value;
-    CopyBase cb{};
+    CopyBaseT cb{};
     if constexpr (kCp) cb = next_base(gs & 1);
     if constexpr (kOneB) {
       // One set of B fragments: each k-step runs its MFMAs column block by
