@@ -155,6 +155,14 @@ inline int choose_shape(const Shape* s, int n, int M, int N, int tiles_mul, int 
   return best;
 }
 
+// Sizes are limited so that rows made here (d of two parts, transposed X) keep
+// the tiles' 32-bit lane offsets (rows below 2^28 elements) and padded sizes
+// stay ints.
+constexpr int kMaxSize = 1 << 27;
+inline int check_sizes(int M, int N, int K) {
+  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_NEGATIVE_DIM;
+  return M > kMaxSize || N > kMaxSize || K > kMaxSize ? GEMM_ERR_BAD_ARG : GEMM_OK;
+}
 inline bool bad_type(int type) { return type != GEMM_TYPE_F16 && type != GEMM_TYPE_BF16; }
 inline bool bad_act(int act) {
   return act != GEMM_ACT_NONE && act != GEMM_ACT_RELU && act != GEMM_ACT_SILU;

@@ -89,9 +89,9 @@ __global__ __launch_bounds__(kThreads) void gated_grad_kernel(GradArgs p, int64_
 }
 
 int check(int type, int act, int M, int N, int K) {
-  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_NEGATIVE_DIM;
-  if (bad_type(type) || bad_act(act)) return GEMM_ERR_BAD_ARG;
-  return GEMM_OK;
+  const int status = check_sizes(M, N, K);
+  if (status != GEMM_OK) return status;
+  return bad_type(type) || bad_act(act) ? GEMM_ERR_BAD_ARG : GEMM_OK;
 }
 
 const half_t* in16(const void* p) { return static_cast<const half_t*>(p); }

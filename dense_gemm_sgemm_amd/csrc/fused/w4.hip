@@ -375,7 +375,8 @@ extern "C" MI355FUSED_API int gemm_w4(int type, int M, int N, int K, int group, 
                                       const void* zeros, int ldz, const void* bias, int act,
                                       const void* residual, int ldr, void* C, int ldc,
                                       void* stream) {
-  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_NEGATIVE_DIM;
+  const int status = check_sizes(M, N, K);
+  if (status != GEMM_OK) return status;
   if (bad_type(type) || bad_act(act) || group <= 0 || group % 32 != 0) return GEMM_ERR_BAD_ARG;
   if (M == 0 || N == 0) return GEMM_OK;
   const int64_t groups = ((int64_t)K + group - 1) / group;

@@ -138,9 +138,9 @@ __global__ __launch_bounds__(kPrepareThreads) void prepare_kernel(PrepareArgs p,
 }
 
 int check(int type, int M, int N, int K) {
-  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_NEGATIVE_DIM;
-  if (bad_type(type) || (N == 0 && M > 0)) return GEMM_ERR_BAD_ARG;
-  return GEMM_OK;
+  const int status = check_sizes(M, N, K);
+  if (status != GEMM_OK) return status;
+  return bad_type(type) || (N == 0 && M > 0) ? GEMM_ERR_BAD_ARG : GEMM_OK;
 }
 
 const half_t* in16(const void* p) { return static_cast<const half_t*>(p); }

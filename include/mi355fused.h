@@ -15,6 +15,8 @@
  * output is rounded once (nearest, ties to even).  Results repeat bit for bit:
  * there are no atomics.  No output may overlap an input or another output.
  *
+ * Sizes M, N and K go up to 2^27; larger ones are GEMM_ERR_BAD_ARG.
+ *
  * Workspaces: a call that takes one needs at least the bytes its size query
  * reports for the same arguments (the query looks at the pointers' alignment
  * only), at a 16-byte aligned device address, or NULL when that is 0.  Its

@@ -49,6 +49,8 @@ def gated(lib, type=F16, act=2, M=4, N=8, K=16, X=A, ldx=16, Wg=A, ldg=16, Wu=A,
 
 def test_gated_refusals(lib):
     assert gated(lib, M=-1) == -1 and gated(lib, N=-1) == -1 and gated(lib, K=-1) == -1
+    big = (1 << 27) + 1
+    assert gated(lib, K=big, ldx=big, ldg=big, ldu=big) == -6 and gated(lib, M=big) == -6
     assert gated(lib, type=2) == -6 and gated(lib, act=3) == -6 and gated(lib, act=-1) == -6
     assert gated(lib, ldx=15) == -2 and gated(lib, ldg=15) == -2 and gated(lib, ldu=15) == -2
     assert gated(lib, ldh=7) == -2 and gated(lib, G=A, ldG=7) == -2 and gated(lib, U=A) == -2
