@@ -70,6 +70,9 @@ struct Transpose {
   half_t* dst;
   int64_t lds, ldd;
   int rows, cols, rows_p, cols_p;
+  // rows to leave out (zeros, whatever they hold): those with this target
+  const long long* targets = nullptr;
+  long long ignore = 0;
   int64_t tiles() const { return (int64_t)(rows_p / 64) * ((cols_p + 63) / 64); }
 };
 
@@ -84,7 +87,8 @@ __device__ __forceinline__ void transpose_tile(const Transpose& p, int64_t tile,
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     h8 v = {};
-    if (r0 + e < p.rows && c0 < p.cols) {
+    if (r0 + e < p.rows && c0 < p.cols &&
+        (p.targets == nullptr || p.targets[r0 + e] != p.ignore)) {
       const half_t* s = p.src + (int64_t)(r0 + e) * p.lds + c0;
       if (c0 + 8 <= p.cols) {
         __builtin_memcpy(&v, s, 16);

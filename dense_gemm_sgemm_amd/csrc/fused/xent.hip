@@ -304,7 +304,7 @@ MI355FUSED_API int gemm_xent_bwd(int type, int M, int N, int K, const void* X, i
   if (e != hipSuccess) return to_status(e);
   PrepareArgs prep{};
   if (dw) {
-    prep.x = Transpose{in16(X), xt, ldx, p.Ms, M, K, p.Ms, p.Kp};
+    prep.x = Transpose{in16(X), xt, ldx, p.Ms, M, K, p.Ms, p.Kp, targets, ignore};
     prep.blocks_x = (prep.x.tiles() + kPrepareThreads / 64 - 1) / (kPrepareThreads / 64);
     // the rows of d that no piece writes (all of them for M == 0) are zero
     const int64_t written = M > 0 ? p.Mp : 0;

@@ -184,9 +184,9 @@ MI355FUSED_API unsigned long long gemm_xent_workspace(int type, int M, int N, in
  *   dX      : [M][lddx], lddx >= max(1, K), or NULL  (written)
  *   dW      : [N][lddw], lddw >= max(1, K), or NULL  (written)
  *
- * Rows with target `ignore` contribute nothing as long as their X is finite,
- * whatever their lse and dloss; a target outside [0, N) that is not `ignore`
- * makes the row's d NaN.  M == 0 gives dW = 0.
+ * Rows with target `ignore` contribute nothing, whatever their X, lse and
+ * dloss; a target outside [0, N) that is not `ignore` makes the row's d NaN.
+ * M == 0 gives dW = 0.
  */
 MI355FUSED_API int gemm_xent_bwd(int type, int M, int N, int K,
                                  const void* X, int ldx, const void* W, int ldw,
