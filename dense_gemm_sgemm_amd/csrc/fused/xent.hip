@@ -30,7 +30,7 @@ struct JoinArgs {
 
 __device__ __forceinline__ void join(float& t, float& s, float t2, float s2) {
   const float top = fmaxf(t, t2);
-  const float base = top == -__builtin_inff() ? 0.f : top;
+  const float base = fabsf(top) == __builtin_inff() ? 0.f : top;   // (0 * exp(-inf), inf)
   s = s * __expf(t - base) + s2 * __expf(t2 - base);
   t = top;
 }

@@ -894,7 +894,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         top = across4(top, [](float a, float b) { return fmaxf(a, b); });
         // exp(z - top) = 2^(z log2(e) - top log2(e)): the rounding of the second
         // term is 2^-24 of it, which is what lse = top + log(s) keeps anyway
-        const float base = top == -__builtin_inff() ? 0.f : -top * kLog2e;
+        // (an infinite maximum: exp(z) as it is)
+        const float base = fabsf(top) == __builtin_inff() ? 0.f : -top * kLog2e;
         float s = 0.f;
 #pragma unroll
         for (int j = 0; j < C::kBlocksN; ++j)

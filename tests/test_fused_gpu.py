@@ -481,6 +481,37 @@ def test_xent_no_rows():
     assert bool((dW == 0).all())
 
 
+def test_xent_no_columns_of_x():
+    """K == 0: all logits are 0."""
+    X, W = (torch.empty((n, 0), dtype=torch.bfloat16, device=DEV) for n in (5, 300))
+    t = torch.tensor([0, 299, IGN, 7, 300], device=DEV)
+    loss, lse = torch.empty((5,), device=DEV), torch.empty((5,), device=DEV)
+    dg.gemm_xent(X, W, t, loss, lse)
+    log300 = torch.full((5,), 300.0, dtype=torch.float64, device=DEV).log()
+    close(lse, log300, 64 * 2.0 ** -24 + 2.0 ** -22 * log300, "lse")
+    want = log300.clone()
+    want[2], want[4] = 0.0, float("nan")
+    close(loss, want, 64 * 2.0 ** -24 + 2.0 ** -22 * log300, "loss")
+
+
+def test_xent_infinite_logits():
+    """A logit of +inf gives lse = +inf, one of -inf counts for nothing, NaN
+    stays NaN, each in its row only."""
+    M, N, K, dt = 130, 400, 128, torch.bfloat16
+    X, W, t = xent_inputs(M, N, K, dt, 14)
+    W[:, 0], X[:, 0] = 0.0, 0.0
+    W[5, 0], t[:] = 1.0, 9
+    X[0, 0], X[1, 0], X[2, 0] = float("inf"), float("-inf"), float("nan")
+    W[:5, 0], W[6:, 0] = 2.0 ** -60, 2.0 ** -60
+    loss, lse = torch.empty((M,), device=DEV), torch.empty((M,), device=DEV)
+    dg.gemm_xent(X, W, t, loss, lse)
+    assert float(lse[0]) == float("inf") and float(lse[1]) == float("-inf")
+    assert bool(torch.isnan(lse[2])) and bool(torch.isfinite(lse[3:]).all())
+    X[1, 0], W[7, 0] = float("-inf"), -1.0     # one column of +inf beside columns of -inf
+    dg.gemm_xent(X, W, t, loss, lse)
+    assert float(lse[1]) == float("inf")
+
+
 def test_xent_extreme_logits():
     """A row whose largest logit leaves nothing beside it, one with equal
     logits, and tiny fp16 gradients of a large mean."""
