@@ -13,9 +13,13 @@ static constexpr Shape kShapes[] = {
     {128, 128, 2, 2 * 128 * 128 * 6 / 5, 128 * 128 * 8 / 5},
 };
 
+// The shape is chosen for the chip's 256 CUs: the statistics' workspace is
+// sized by it before a device is asked.
+static int shape_of(int M, int N) { return choose_shape(kShapes, 2, M, N, 1, kPlanCus); }
+
 template <int FMT, int MODE>
 static hipError_t launch_fmt(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream) {
-  switch (choose_shape(kShapes, 2, a.M, a.N, 1, cus)) {
+  switch (shape_of(a.M, a.N)) {
     case 0:
       return hgemm::launch_fused<256, 256, BK, 4, 2, GM, 1, 2, FMT, 0, MODE>(a, x, cus, stream);
     case 1:
@@ -31,9 +35,9 @@ hipError_t launch_lse_tiles(const Args16& a, const FusedExtra& x, int cus, hipSt
 }
 
 // Both shapes have two wave columns.
-int lse_chunks(int M, int N, int cus) {
-  const int i = choose_shape(kShapes, 2, M, N, 1, cus);
-  return i < 0 ? 0 : (N + kShapes[i].bn - 1) / kShapes[i].bn * 2;
+int lse_chunks(int M, int N) {
+  const int i = shape_of(pad_rows(M), pad_rows(N));
+  return (pad_rows(N) + kShapes[i].bn - 1) / kShapes[i].bn * 2;
 }
 
 hipError_t launch_dlogit_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream) {

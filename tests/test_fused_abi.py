@@ -95,6 +95,7 @@ def test_workspace_sizes(lib):
     assert x(BF16, 0, 1000, 128, A, 128, A, 128) == 0
     assert x(BF16, 200, 0, 128, A, 128, A, 128) == 0
     assert x(BF16, 200, 1000, 128, A, 128, A, 128) == 200 * 16 * 8 + 1024
+    assert x(BF16, 8192, 131072, 128, A, 128, A, 128) == 8192 * 1024 * 8 + 8192 * 4
     xb = lib.gemm_xent_bwd_workspace
     # dW alone: d and X transposed (and 256 bytes for the factor)
     assert xb(BF16, 4096, 1024, 128, A, 128, A, 128, 0, 1) == 4096 * (1024 + 128) * 2 + 256

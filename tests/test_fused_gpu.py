@@ -706,6 +706,19 @@ def test_streams_and_repeats():
     call, outs, _ = everything(seed=70)
     call()
     torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(ws=None)      # workspaces from the graph's own pool
+    first = [o.clone() for o in outs]
+    for _ in range(3):
+        for o in outs:
+            o.fill_(5)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(first, outs):
+            assert torch.equal(a, b)
+    call()
+    torch.cuda.synchronize()
     want = [o.clone() for o in outs]
     s = torch.cuda.Stream()
     for how in range(3):
