@@ -957,13 +957,10 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
           }
           const h4 o = round4(d);
           put(j, o);
-          if (tail) {
-#pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const int n = nf + 16 * j + v;
-              if (m >= mlo && n >= nlo && n >= p.N - BK)
-                x.tail[m * x.ldt + n - (p.N - BK)] = n >= last ? o[v] : (half_t)0;
-            }
+          if (tail) {   // in whole quads: N, BK and the tiles' widths are multiples of 4
+            const int n = nf + 16 * j;
+            if (m >= mlo && n >= nlo && n >= p.N - BK)
+              *(h4*)(x.tail + m * x.ldt + n - (p.N - BK)) = n >= last ? o : h4{};
           }
         }
         flush(p.C, p.ldc, m0 + wm + 16 * i, n0 + wn, C::WN, mlo, p.M, nlo, p.N);
