@@ -128,13 +128,15 @@ __device__ __forceinline__ void map_tile(int64_t b, int tiles_m, int tiles_n, in
 }
 
 // The same in 32 bits, for fewer than 2^31 tiles (a 64-bit division by a
-// variable is some 70 instructions, and every tile needs several).
-template <int GM>
-__device__ __forceinline__ void map_tile32(uint32_t b, uint32_t tiles_m, uint32_t tiles_n, int& tm,
-                                           int& tn) {
-  const uint32_t T = tiles_m * tiles_n;
+// variable is some 70 instructions, and every tile needs several), and in two
+// steps: b's place in the order, and the tile at place L.
+__device__ __forceinline__ uint32_t xcd_order32(uint32_t b, uint32_t T) {
   const uint32_t x = b % 8, q = T / 8, rem = T % 8;
-  const uint32_t L = x * q + (x < rem ? x : rem) + b / 8;
+  return x * q + (x < rem ? x : rem) + b / 8;
+}
+template <int GM>
+__device__ __forceinline__ void tile_at32(uint32_t L, uint32_t tiles_m, uint32_t tiles_n, int& tm,
+                                          int& tn) {
   const uint32_t per_group = GM * tiles_n;
   const uint32_t g = L / per_group, w = L - g * per_group;
   const uint32_t left = tiles_m - g * GM;
@@ -352,7 +354,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       sp = (int)(item / tiles);
       item -= sp * tiles;
     }
-    if constexpr (MODE == kGradX) {
+    if constexpr (MODE != kProduct) item = xcd_order32((uint32_t)item, (uint32_t)ta.tiles);
+    if constexpr (MODE == kGradX) {   // an XCD's tiles of a range share its slabs of d and W
       const uint32_t tiles = (uint32_t)tiles_m * tiles_n;
       sp = (int)((uint32_t)item / tiles);
       item -= (uint32_t)sp * tiles;
@@ -363,7 +366,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     if constexpr (MODE == kProduct)
       map_tile<GM>(item, tiles_m, tiles_n, tm, tn);
     else
-      map_tile32<GM>((uint32_t)item, tiles_m, tiles_n, tm, tn);
+      tile_at32<GM>((uint32_t)item, tiles_m, tiles_n, tm, tn);
     if constexpr (MODE == kGradW) {
       sp = tm >= part_tiles;   // the part
       if (sp) tm -= part_tiles;
@@ -1317,7 +1320,7 @@ hipError_t launch_fused(const Args16& a, const FusedExtra& x, int slots, hipStre
   constexpr int kTileN = MODE == kGated ? BN / 2 : BN;
   const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * ((a.N + kTileN - 1) / kTileN) *
                         (MODE == kGradW ? x.parts : MODE == kGradX ? x.splits : 1);
-  if (tiles >= (int64_t(1) << 31)) return hipErrorInvalidValue;   // map_tile32
+  if (tiles >= (int64_t(1) << 31)) return hipErrorInvalidValue;   // xcd_order32
   int64_t grid = tiles < slots ? tiles : slots;
   if (grid < 1) grid = 1;
   FusedTileArgs ta{a, tiles, x};
