@@ -960,10 +960,21 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
           }
           const h4 o = round4(d);
           put(j, o);
-          if (tail) {   // in whole quads: N, BK and the tiles' widths are multiples of 4
-            const int n = nf + 16 * j;
-            if (m >= mlo && n >= nlo && n >= p.N - BK)
-              *(h4*)(x.tail + m * x.ldt + n - (p.N - BK)) = n >= last ? o : h4{};
+          if (tail && m >= mlo) {
+            // a store for the quad, or for each value where the tail or this
+            // tile's own columns begin inside it (N need not be a multiple of 4)
+            const int n = nf + 16 * j, at = n - (p.N - BK);
+            half_t* dst = x.tail + m * x.ldt + at;
+            h4 t;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) t[v] = n + v >= last ? o[v] : (half_t)0;
+            if (at >= 0 && n >= nlo) {
+              __builtin_memcpy(dst, &t, 8);
+            } else {
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                if (at + v >= 0 && n + v >= nlo) dst[v] = t[v];
+            }
           }
         }
         flush(p.C, p.ldc, m0 + wm + 16 * i, n0 + wn, C::WN, mlo, p.M, nlo, p.N);

@@ -764,3 +764,38 @@ def test_two_threads_at_once():
     for want, (_, outs, _) in zip(wants, sides):
         for a, b in zip(want, outs):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("M,N,K", [(200, 333, 136), (430, 2751, 1024), (926, 2749, 128),
+                                   (65, 4098, 200), (300, 5004, 72), (129, 255, 65),
+                                   (40000, 3715, 128)])
+def test_what_a_workspace_holds(M, N, K, typ):
+    """Nothing of a workspace is read before it is written: NaN everywhere in
+    it (all bits set, in 16 and in 32 bits) gives the bits that zeros give."""
+    dt = DT[typ]
+    X, Wg, Wu = gated_inputs(M, N, K, dt, M)
+    H, G, U = (torch.empty((M, N), dtype=dt, device=DEV) for _ in range(3))
+    dH = randn((M, N), 1.0, dt, gen(1)).to(DEV)
+    dX, dWg, dWu = torch.empty_like(X), torch.empty_like(Wg), torch.empty_like(Wu)
+    t = torch.randint(0, N, (M,), generator=gen(2)).to(DEV)
+    loss, lse = torch.empty((M,), device=DEV), torch.empty((M,), device=DEV)
+    dloss = torch.rand((M,), generator=gen(3)).to(DEV)
+    ops = [
+        (lambda ws: dg.gemm_gated(X, Wg, Wu, H, G=G, U=U, workspace=ws),
+         dg.gated_workspace_bytes(X, Wg, Wu), (H, G, U)),
+        (lambda ws: dg.gemm_gated_bwd(X, Wg, Wu, G, U, dH, dX, dWg, dWu, workspace=ws),
+         dg.gated_bwd_workspace_bytes(X, Wg, Wu), (dX, dWg, dWu)),
+        (lambda ws: dg.gemm_xent(X, Wg, t, loss, lse, workspace=ws),
+         dg.xent_workspace_bytes(X, Wg), (loss, lse)),
+        (lambda ws: dg.gemm_xent_bwd(X, Wg, t, lse, dloss, dX, dWg, workspace=ws),
+         dg.xent_bwd_workspace_bytes(X, Wg), (dX, dWg)),
+    ]
+    for i, (op, size, outs) in enumerate(ops):
+        results = []
+        for fill in (0, 255):
+            ws = torch.full((size,), fill, dtype=torch.uint8, device=DEV)
+            op(ws)
+            results.append([o.clone() for o in outs])
+        for a, b in zip(*results):
+            assert bool(torch.isfinite(a).all()) and torch.equal(a, b), (i, M, N, K)
