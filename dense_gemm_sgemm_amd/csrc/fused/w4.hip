@@ -29,20 +29,56 @@ typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h2 __attribute__((ext_vector_type(2)));
 
 constexpr int kBlock = 128;   // K values of a block
-// Blocks of a chunk (a wave has two chunks in flight): four, two where each
-// block brings four groups' scales or four blocks of X rows, one where both:
-// more registers would spill (64 x 4096 x 16384: 64.9 against 35.5 us).
-constexpr int unroll_of(bool four_groups, bool four_tiles) {
-  return four_groups && four_tiles ? 1 : four_groups || four_tiles ? 2 : 4;
+// How the groups lie in blocks: one a block (128), two (64), four (32), one
+// for several blocks (a larger multiple of 128: looked up for each block), or
+// any other multiple of 32 (looked up for each step of 32 k).
+enum Groups { kOne = 0, kTwo, kFour, kWide, kAny };
+constexpr int groups_per_block(int gr) { return gr == kTwo ? 2 : gr >= kFour && gr != kWide ? 4 : 1; }
+inline int groups_of(int group) {
+  return group == kBlock ? kOne : group == 64 ? kTwo : group == 32 ? kFour
+         : group % kBlock == 0 ? kWide : kAny;
 }
-constexpr int kMaxWaves = 8;
-constexpr int most_waves(int mt) { return mt == 4 ? 4 : kMaxWaves; }   // two workgroups' LDS a CU
+
+// Blocks of a chunk (a wave has two chunks in flight): four; two where each
+// block brings four groups' scales or four blocks of X rows, one where both:
+// more registers would spill (64 x 4096 x 16384: 64.9 against 35.5 us); two
+// for up to 16 rows in bf16 with two groups a block, whose 170 registers leave
+// a SIMD too few waves (16 x 10000 x 2432: 10.6 against 8.7 us; not fp16's 130:
+// 8.4 against 8.9); two with sixteen waves.
+constexpr int unroll_of(int fmt, int gr, int mt, int most) {
+  const bool four = groups_per_block(gr) == 4;
+  if (four && mt == 4) return 1;
+  if (four || mt == 4 || most == 16) return 2;
+  return mt == 1 && gr == kTwo && fmt == kFmtBF16 ? 2 : 4;
+}
+// The most waves of a workgroup: four with four blocks of X rows (two
+// workgroups' LDS a CU), eight, or sixteen: with X in LDS where chunks are two
+// blocks and the registers of sixteen waves do (1 x 4096 x 16384, groups of 32:
+// 15.0 against 13.0 us); with X staged and up to 16 rows where a CU has one
+// workgroup and each wave four chunks (16 x 4096 x 16384, groups of 128, 64 and
+// 32 in fp16: 15.7, 16.1 and 17.1 against 15.1, 15.3 and 16.5 us; bf16 with
+// groups of 32 would spill: 19.1 against 27.7).
+constexpr int x_waves(int fmt, int gr) {
+  return gr == kFour || (gr == kTwo && fmt == kFmtBF16) ? 16 : 8;
+}
+constexpr bool sixteen_staged(int fmt, int gr) {
+  return gr == kOne || gr == kTwo || (gr == kFour && fmt == kFmtF16);
+}
+// The threads that registers are allotted for.  Four waves may have 512 each:
+// bf16 with four blocks of X rows and several groups a block spills in 256 (64
+// x 4096 x 16384, groups of 64: 65.4 against 41.0 us); the others do not, and a
+// CU holds two workgroups of them (64 x 16384 x 4096 fp16, groups of 32: 40.8
+// against 57.8 us in more than 256).
+constexpr int bound_of(int fmt, int gr, int mt, int most) {
+  return 64 * (mt == 4 && (fmt == kFmtF16 || groups_per_block(gr) == 1) ? 8 : most);
+}
 constexpr int kStaged = 4;    // 16-byte pieces of X a thread loads ahead of its weights
 // X of up to three rows is kept in LDS where it takes no more than kXBytes, or,
 // with a workgroup a CU at most, kXBytesAlone; with more rows each wave's own
 // copy is no slower, and smaller (1 x 4096 x 16384: 12.1 against 16.4 us in
 // LDS; 3 x 16384 x 4096: 12.7 against 14.3; 5 x 16384 x 4096: 17.0 against 14.5).
 constexpr int kXRows = 3, kXBytes = 32 << 10, kXBytesAlone = 56 << 10;
+constexpr int kXBytesSixteen = 48 << 10;   // beside sixteen waves' sums
 
 struct W4Args {
   const half_t* X;
@@ -55,12 +91,6 @@ struct W4Args {
   int64_t ldx, ldq, lds, ldz, ldr, ldc;
   int M, N, K, group, act, waves, chunks;
 };
-
-// How the groups lie in blocks: one a block (128), two (64), four (32), one
-// for several blocks (a larger multiple of 128: looked up for each block), or
-// any other multiple of 32 (looked up for each step of 32 k).
-enum Groups { kOne = 0, kTwo, kFour, kWide, kAny };
-constexpr int groups_per_block(int gr) { return gr == kTwo ? 2 : gr >= kFour && gr != kWide ? 4 : 1; }
 
 // U blocks as loaded: weights, and the raw scales and zero points of their groups.
 template <int GR, int U>
@@ -217,13 +247,13 @@ __device__ __forceinline__ void multiply(u4 raw, const uint16_t* scales, const u
 // XL: the rows of X (M <= 16) lie in LDS, reordered, zero past K, in
 // rows of K rounded up to blocks plus 16 bytes (rows then start in different
 // banks).  Otherwise each wave stages the rows of a block in turn (XStage).
-template <int FMT, int GR, int MT, bool XL>
-__global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t base) {
-  constexpr int kUnroll = unroll_of(groups_per_block(GR) == 4, MT == 4);
+template <int FMT, int GR, int MT, bool XL, int MOST>
+__global__ __launch_bounds__(bound_of(FMT, GR, MT, MOST)) void w4_kernel(W4Args p, int64_t base) {
+  constexpr int kUnroll = unroll_of(FMT, GR, MT, XL ? 8 : MOST);
   typedef XStage<MT, kBlock> Stage;
   extern __shared__ __attribute__((aligned(16))) unsigned char dynamic_lds[];
   __shared__ __attribute__((aligned(16))) unsigned char
-      stage_lds[XL ? 16 : most_waves(MT) * Stage::kBytes];
+      stage_lds[XL ? 16 : MOST * Stage::kBytes];
   unsigned char* lds = XL ? dynamic_lds : stage_lds;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -347,20 +377,24 @@ __global__ __launch_bounds__(64 * kMaxWaves) void w4_kernel(W4Args p, int64_t ba
 }
 
 template <int FMT, int GR>
-const void* pick_rows(int M, bool x_in_lds) {
-  if (x_in_lds) return (const void*)w4_kernel<FMT, GR, 1, true>;
-  return M <= 16   ? (const void*)w4_kernel<FMT, GR, 1, false>
-         : M <= 32 ? (const void*)w4_kernel<FMT, GR, 2, false>
-                   : (const void*)w4_kernel<FMT, GR, 4, false>;
+const void* pick_rows(int M, bool x_in_lds, int most) {
+  if (x_in_lds) return (const void*)w4_kernel<FMT, GR, 1, true, x_waves(FMT, GR)>;
+  if constexpr (sixteen_staged(FMT, GR))
+    if (most == 16) return (const void*)w4_kernel<FMT, GR, 1, false, 16>;
+  return M <= 16   ? (const void*)w4_kernel<FMT, GR, 1, false, 8>
+         : M <= 32 ? (const void*)w4_kernel<FMT, GR, 2, false, 8>
+                   : (const void*)w4_kernel<FMT, GR, 4, false, 4>;
 }
 
 template <int FMT>
-const void* pick(int M, int group, bool x_in_lds) {
-  if (group == kBlock) return pick_rows<FMT, kOne>(M, x_in_lds);
-  if (group == 64) return pick_rows<FMT, kTwo>(M, x_in_lds);
-  if (group == 32) return pick_rows<FMT, kFour>(M, x_in_lds);
-  if (group % kBlock == 0) return pick_rows<FMT, kWide>(M, x_in_lds);
-  return pick_rows<FMT, kAny>(M, x_in_lds);
+const void* pick(int M, int gr, bool x_in_lds, int most) {
+  switch (gr) {
+    case kOne: return pick_rows<FMT, kOne>(M, x_in_lds, most);
+    case kTwo: return pick_rows<FMT, kTwo>(M, x_in_lds, most);
+    case kFour: return pick_rows<FMT, kFour>(M, x_in_lds, most);
+    case kWide: return pick_rows<FMT, kWide>(M, x_in_lds, most);
+    default: return pick_rows<FMT, kAny>(M, x_in_lds, most);
+  }
 }
 
 }  // namespace
@@ -394,18 +428,23 @@ extern "C" MI355FUSED_API int gemm_w4(int type, int M, int N, int K, int group, 
   const int mt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
   const int64_t wgs = ((int64_t)N + 15) / 16 * (((int64_t)M + 63) / 64);
   const int64_t blocks = ((int64_t)K + kBlock - 1) / kBlock;
-  // whole chunks where four waves have one each, else single blocks
-  const int unroll = unroll_of(group % kBlock != 0 && group != 64, mt == 4);
-  a.chunks = K / kBlock >= 4 * unroll ? K / (kBlock * unroll) : 0;
-  a.waves = skinny::waves_for(wgs, a.chunks ? a.chunks : std::max<int>(1, (int)blocks),
-                              most_waves(mt), cus);
   const int64_t x_bytes = M * (blocks * kBlock * 2 + 16);
   const bool x_in_lds =
       M <= kXRows && K > 0 && x_bytes <= (wgs <= cus ? kXBytesAlone : kXBytes);
+  const int fmt = type == GEMM_TYPE_BF16 ? kFmtBF16 : kFmtF16, gr = groups_of(group);
+  int most = mt == 4 ? 4 : 8;
+  if (x_in_lds)
+    most = x_bytes <= kXBytesSixteen ? x_waves(fmt, gr) : 8;
+  else if (mt == 1 && sixteen_staged(fmt, gr) && wgs <= cus && blocks >= 4 * 16 * 2)
+    most = 16;
+  // whole chunks where four waves have one each, else single blocks
+  const int unroll = unroll_of(fmt, gr, mt, x_in_lds ? 8 : most);
+  a.chunks = K / kBlock >= 4 * unroll ? K / (kBlock * unroll) : 0;
+  a.waves = skinny::waves_for(wgs, a.chunks ? a.chunks : std::max<int>(1, (int)blocks), most, cus);
   const unsigned lds_bytes =
       x_in_lds ? (unsigned)(x_bytes + (a.waves - 1) * mt * 64 * sizeof(f4)) : 0;
-  const void* k = type == GEMM_TYPE_BF16 ? pick<kFmtBF16>(M, group, x_in_lds)
-                                         : pick<kFmtF16>(M, group, x_in_lds);
+  const void* k = fmt == kFmtBF16 ? pick<kFmtBF16>(M, gr, x_in_lds, most)
+                                  : pick<kFmtF16>(M, gr, x_in_lds, most);
   return to_status(
       launch_tiles(k, a, wgs, 64 * a.waves, lds_bytes, static_cast<hipStream_t>(stream)));
 }

@@ -255,6 +255,21 @@ def test_w4(M, N, K, group, zeros, typ):
     C.check_frame("w4")
 
 
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("group", [32, 64, 128, 256, 96])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 16384), (2, 30, 9000), (5, 40, 16384), (16, 33, 17000),
+                                   (64, 20, 16500)])
+def test_w4_long(M, N, K, group, typ):
+    """Few weight rows and a long K: the most waves a workgroup has."""
+    dt = DT[typ]
+    X, Wq, s, z = w4_inputs(M, N, K, group, dt, True, M + group)
+    C = Out(M, N, dt)
+    show("w4 long", M, N, K, group, typ)
+    dg.gemm_w4(X, Wq, s, C.t, group=group, zeros=z)
+    w4_check(C.t, X, Wq, s, z, group)
+    C.check_frame("w4")
+
+
 @pytest.mark.parametrize("pad,shift", [(1, 1), (3, 0), (16, 16)])
 @pytest.mark.parametrize("group", [32, 64, 128, 96])
 def test_w4_strides(group, pad, shift):
