@@ -36,7 +36,8 @@ def gated_inputs(M, N, K, dt, seed=0, pad=0, shift=0):
 # one row to several tiles; N and K off every multiple; K below, at and past a slab
 GATED = [(1, 16, 32), (1, 1, 1), (1, 200, 100), (3, 1000, 8), (16, 130, 65), (17, 96, 128),
          (33, 64, 264), (64, 513, 72), (65, 129, 127), (100, 64, 130), (128, 64, 128),
-         (129, 257, 320), (300, 500, 264), (257, 1000, 72), (513, 640, 192), (700, 333, 1537)]
+         (129, 257, 320), (300, 500, 264), (257, 1000, 72), (513, 640, 192), (700, 333, 1537),
+         (370, 11009, 200)]
 
 
 @pytest.mark.parametrize("typ", TYPES)
@@ -337,7 +338,8 @@ def xent_inputs(M, N, K, dt, seed=0, pad=0, shift=0, sd=3.0):
 
 
 XENT = [(1, 1, 1), (1, 2, 8), (2, 127, 64), (5, 128, 128), (129, 129, 130), (200, 1000, 136),
-        (128, 191, 65), (64, 300, 72), (333, 5001, 96), (300, 256, 1537), (513, 2050, 264)]
+        (128, 191, 65), (64, 300, 72), (333, 5001, 96), (300, 256, 1537), (513, 2050, 264),
+        (370, 22001, 136)]
 
 
 @pytest.mark.parametrize("typ", TYPES)
