@@ -133,8 +133,8 @@ hipError_t launch_dlogit_tiles(const Args16& a, const FusedExtra& x, int cus, hi
 // The gated product for a.M <= kFewRows, operands as they are (no copies).
 constexpr int kFewRows = 64;
 hipError_t launch_gated_rows(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
-// Wave columns of the kLse tiles for M rows and N columns: partial results of a row.
-int lse_chunks(int M, int N);
+// Wave columns of the kLse tiles for X [M][K] and W [N][K]: partial results of a row.
+int lse_chunks(int M, int N, int K);
 
 // Cost model of hgemm_shapes.hpp for the ragged form over M x N outputs whose
 // tiles are (bm, bn, workgroups per CU, tile-time); returns the cheapest index.

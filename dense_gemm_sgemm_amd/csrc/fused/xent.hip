@@ -201,7 +201,7 @@ extern "C" {
 MI355FUSED_API unsigned long long gemm_xent_workspace(int type, int M, int N, int K, const void* X,
                                                       int ldx, const void* W, int ldw) {
   if (check(type, M, N, K) != GEMM_OK || M == 0 || bad_ld(ldx, K) || bad_ld(ldw, K)) return 0;
-  return round256((size_t)lse_chunks(M, N) * M * sizeof(float2)) + round256((size_t)M * sizeof(float)) +
+  return round256((size_t)lse_chunks(M, N, K) * M * sizeof(float2)) + round256((size_t)M * sizeof(float)) +
          (needs_copy(X, ldx, M, K) ? copy_bytes(M, K) : 0) +
          (needs_copy(W, ldw, N, K) ? copy_bytes(N, K) : 0);
 }
@@ -224,7 +224,7 @@ MI355FUSED_API int gemm_xent(int type, int M, int N, int K, const void* X, int l
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   float2* partial = reinterpret_cast<float2*>(ws);
-  ws += round256((size_t)lse_chunks(M, N) * M * sizeof(float2));
+  ws += round256((size_t)lse_chunks(M, N, K) * M * sizeof(float2));
   float* target_logit = reinterpret_cast<float*>(ws);
   ws += round256((size_t)M * sizeof(float));
   PadJobs jobs;
@@ -245,7 +245,7 @@ MI355FUSED_API int gemm_xent(int type, int M, int N, int K, const void* X, int l
   e = launch_lse_tiles(a, f, cus, s);
   if (e != hipSuccess) return to_status(e);
   const JoinArgs j{partial, target_logit, targets, ignore, N, loss, lse, M, M,
-                   lse_chunks(M, N)};
+                   lse_chunks(M, N, K)};
   return to_status(launch_tiles((const void*)join_kernel, j,
                                 ((int64_t)M + kJoinRows - 1) / kJoinRows, 64 * kJoinWaves, 0, s));
 }

@@ -339,7 +339,7 @@ def xent_inputs(M, N, K, dt, seed=0, pad=0, shift=0, sd=3.0):
 
 XENT = [(1, 1, 1), (1, 2, 8), (2, 127, 64), (5, 128, 128), (129, 129, 130), (200, 1000, 136),
         (128, 191, 65), (64, 300, 72), (333, 5001, 96), (300, 256, 1537), (513, 2050, 264),
-        (370, 22001, 136)]
+        (370, 22001, 136), (370, 22001, 1032)]
 
 
 @pytest.mark.parametrize("typ", TYPES)
