@@ -37,7 +37,7 @@ def gated_inputs(M, N, K, dt, seed=0, pad=0, shift=0):
 GATED = [(1, 16, 32), (1, 1, 1), (1, 200, 100), (3, 1000, 8), (16, 130, 65), (17, 96, 128),
          (33, 64, 264), (64, 513, 72), (65, 129, 127), (100, 64, 130), (128, 64, 128),
          (129, 257, 320), (300, 500, 264), (257, 1000, 72), (513, 640, 192), (700, 333, 1537),
-         (370, 11009, 200)]
+         (370, 11009, 200), (570, 5001, 4090)]
 
 
 @pytest.mark.parametrize("typ", TYPES)
