@@ -130,8 +130,7 @@ hipError_t launch_sums(int fmt, const FusedExtra& x, int splits, half_t* out, in
                        int N, hipStream_t stream);
 hipError_t launch_lse_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
 hipError_t launch_dlogit_tiles(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
-// The gated product for a.M <= kFewRows, operands as they are (no copies).
-constexpr int kFewRows = 64;
+// The gated product where by_rows says so, operands as they are (no copies).
 hipError_t launch_gated_rows(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream);
 // Wave columns of the kLse tiles for X [M][K] and W [N][K]: partial results of a row.
 int lse_chunks(int M, int N, int K);

@@ -129,6 +129,20 @@ BwdPlan plan_bwd(int M, int N, int K, Mat Wg, Mat Wu, bool dx, bool dw) {
   return p;
 }
 
+// The kernel for few rows (gated_rows.hip) streams the weights once for 64 rows
+// of X: at most as many rows, or tiles would be too few for the chip, each with
+// all of K to walk, in 0.65 us a slab of 64.  With ceil(M / 64) passes over 4 N K
+// bytes at 4.2 TB/s both take the same near ceil(M / 64) N = 10000 (tiles and
+// rows, bf16: 128 x 4096 x 4096 45.9 and 31.6 us, 80 x 2048 x 8192 88 and 28,
+// 500 x 1024 x 1024 15.7 and 13.1; 128 x 8192 x 2048 26.9 and 35.2, 111 x 7756 x
+// 2608 47 and 52).  Rows at odd addresses are read at a third of the rate (102 x
+// 3667 x 1591: 36.6 and 40.4; 100 x 1000 x 2047: 33.8 and 29.9).
+bool by_rows(int M, int N, Mat x, Mat g, Mat u) {
+  const int64_t work = ((int64_t)M + 63) / 64 * N;
+  auto even = [](Mat m) { return m.ld % 2 == 0 && (reinterpret_cast<uintptr_t>(m.p) & 3) == 0; };
+  return M <= 64 || work <= (even(x) && even(g) && even(u) ? 10000 : 4000);
+}
+
 }  // namespace
 }  // namespace fused
 }  // namespace mi355gemm
@@ -141,8 +155,8 @@ extern "C" {
 MI355FUSED_API unsigned long long gemm_gated_workspace(int type, int M, int N, int K,
                                                        const void* X, int ldx, const void* Wg,
                                                        int ldwg, const void* Wu, int ldwu) {
-  if (check(type, 0, M, N, K) != GEMM_OK || M <= kFewRows || N == 0 || bad_ld(ldx, K) ||
-      bad_ld(ldwg, K) || bad_ld(ldwu, K))
+  if (check(type, 0, M, N, K) != GEMM_OK || N == 0 || bad_ld(ldx, K) || bad_ld(ldwg, K) ||
+      bad_ld(ldwu, K) || by_rows(M, N, Mat{in16(X), ldx}, Mat{in16(Wg), ldwg}, Mat{in16(Wu), ldwu}))
     return 0;
   return (needs_copy(X, ldx, M, K) ? copy_bytes(M, K) : 0) +
          (needs_copy(Wg, ldwg, N, K) ? copy_bytes(N, K) : 0) +
@@ -178,7 +192,8 @@ MI355FUSED_API int gemm_gated(int type, int act, int M, int N, int K, const void
   f.ldc2 = ldg;
   f.C3 = out16(U);
   f.ldc3 = ldu;
-  if (M <= kFewRows) return to_status(launch_gated_rows(a, f, cus, s));
+  if (by_rows(M, N, Mat{a.A, ldx}, Mat{a.B, ldwg}, Mat{f.B2, ldwu}))
+    return to_status(launch_gated_rows(a, f, cus, s));
   PadJobs jobs;
   char* ws = static_cast<char*>(workspace);
   const Mat x = jobs.add(Mat{a.A, ldx}, M, K, ws);

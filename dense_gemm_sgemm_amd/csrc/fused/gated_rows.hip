@@ -1,5 +1,5 @@
 // The gated product for few rows of X (decode steps): both weights streamed
-// from HBM once, bound by that.  A wave loads 16 rows x 128 or 64 k of Wg and of Wu
+// from HBM once for 64 rows, bound by that.  A wave loads 16 rows x 128 or 64 k of Wg and of Wu
 // (16 bytes a lane and step of 32 k) one chunk ahead of the products; see
 // skinny.hpp for the layout.
 #include "skinny.hpp"
@@ -54,7 +54,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_rows_kernel(RowsArgs p, 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, quarter = lane >> 4;
-  const int n = (int)(base + blockIdx.x) * 16 + r;
+  const int64_t id = base + blockIdx.x, groups_n = (p.N + 15) / 16;
+  const int m0 = (int)(id / groups_n) * 64;
+  const int n = (int)(id % groups_n) * 16 + r;
   const int row = n < p.N ? n : p.N - 1;   // rows past N repeat the last one, unstored
   const half_t* wg = p.Wg + row * p.ldwg + 8 * quarter;
   const half_t* wu = p.Wu + row * p.ldwu + 8 * quarter;
@@ -76,13 +78,13 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_rows_kernel(RowsArgs p, 
   };
   int c = wave;
   if (c < chunks) {
-    stage.template load<false>(p.X, p.ldx, 0, p.M, c * kChunk, p.K, lane);
+    stage.template load<false>(p.X, p.ldx, m0, p.M, c * kChunk, p.K, lane);
     load_chunk<false, kSteps>(wg, wu, c * kChunk, K, cur);
   }
   for (; c < chunks; c += p.waves) {
     read_x();
     if (c + p.waves < chunks) {
-      stage.template load<false>(p.X, p.ldx, 0, p.M, (c + p.waves) * kChunk, p.K, lane);
+      stage.template load<false>(p.X, p.ldx, m0, p.M, (c + p.waves) * kChunk, p.K, lane);
       load_chunk<false, kSteps>(wg, wu, (c + p.waves) * kChunk, K, nxt);
     }
     multiply<FMT, MT, kSteps>(x, cur, acc);
@@ -93,7 +95,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_rows_kernel(RowsArgs p, 
     }
   }
   if (chunks * kChunk < p.K && wave == chunks % p.waves) {
-    stage.template load<true>(p.X, p.ldx, 0, p.M, chunks * kChunk, p.K, lane);
+    stage.template load<true>(p.X, p.ldx, m0, p.M, chunks * kChunk, p.K, lane);
     load_chunk<true, kSteps>(wg, wu, chunks * kChunk, K, cur);
     read_x();
     multiply<FMT, MT, kSteps>(x, cur, acc);
@@ -107,7 +109,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_rows_kernel(RowsArgs p, 
   for (int t = 0; t < MT; ++t)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int64_t m = 16 * t + 4 * quarter + v;
+      const int64_t m = m0 + 16 * t + 4 * quarter + v;
       if (m >= p.M) continue;
       const float g = acc[t][v], u = acc[MT + t][v];
       p.H[m * p.ldh + n] = f32_to_word<FMT>(epi_act(g, p.act) * u);
@@ -128,7 +130,7 @@ const void* pick(int M) {
 hipError_t launch_gated_rows(const Args16& a, const FusedExtra& x, int cus, hipStream_t stream) {
   RowsArgs p{a.A,   a.B,    x.B2,  a.C,   x.C2,  x.C3, a.lda, a.ldb, x.ldb2,
              a.ldc, x.ldc2, x.ldc3, a.M, a.N, a.K, a.act, 1};
-  const int64_t wgs = ((int64_t)a.N + 15) / 16;
+  const int64_t wgs = ((int64_t)a.N + 15) / 16 * (((int64_t)a.M + 63) / 64);
   const int chunk = 32 * steps_of(a.M <= 16 ? 1 : 2);
   const int chunks = std::max(1, (int)(((int64_t)a.K + chunk - 1) / chunk));
   p.waves = waves_for(wgs, chunks, kMaxWaves, cus);

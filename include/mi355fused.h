@@ -63,10 +63,12 @@ MI355FUSED_API int gemm_gated(int type, int act, int M, int N, int K,
                               void* workspace, unsigned long long workspace_bytes,
                               void* stream);
 
-/* Workspace bytes of gemm_gated: 0 for M <= 64 and for operands of at least
- * 128 rows with K >= 128, K % 8 == 0, 16-byte aligned pointers and leading
- * dimensions that are multiples of 8 (below 2^28); otherwise a padded copy of
- * each operand that is not so.  0 also for arguments the call rejects. */
+/* Workspace bytes of gemm_gated: 0 for M <= 64, for few outputs (ceil(M / 64) N
+ * up to 10000, or 4000 if a pointer or leading dimension is odd) and for
+ * operands of at least 128 rows with K >= 128, K % 8 == 0, 16-byte aligned
+ * pointers and leading dimensions that are multiples of 8 (below 2^28);
+ * otherwise a padded copy of each operand that is not so.  0 also for arguments
+ * the call rejects. */
 MI355FUSED_API unsigned long long gemm_gated_workspace(int type, int M, int N, int K,
                                                        const void* X, int ldx,
                                                        const void* Wg, int ldwg,

@@ -57,9 +57,9 @@ def test_gated_refusals(lib):
     assert gated(lib, X=None) == -3 and gated(lib, Wu=None) == -3 and gated(lib, H=None) == -3
     assert gated(lib, M=0, X=None, H=None) == 0 and gated(lib, N=0, Wg=None, ldh=1) == 0
     # a padded copy is needed: no workspace, one too small, one misaligned
-    big = dict(M=200, N=130, K=20, ldx=20, ldg=20, ldu=20, ldh=130)
-    need = lib.gemm_gated_workspace(F16, 200, 130, 20, A, 20, A, 20, A, 20)
-    assert need == (200 + 130 + 130) * 128 * 2
+    big = dict(M=200, N=2600, K=20, ldx=20, ldg=20, ldu=20, ldh=2600)
+    need = lib.gemm_gated_workspace(F16, 200, 2600, 20, A, 20, A, 20, A, 20)
+    assert need == (200 + 2600 + 2600) * 128 * 2
     assert gated(lib, **big) == -7 and gated(lib, **big, ws=A, bytes=need - 1) == -7
     assert gated(lib, **big, ws=p(0x100008), bytes=need) == -7
     assert gated(lib, **big, ws=A, bytes=need) == -4      # no device here
@@ -67,14 +67,18 @@ def test_gated_refusals(lib):
 
 def test_workspace_sizes(lib):
     ws = lib.gemm_gated_workspace
-    assert ws(F16, 256, 512, 128, A, 128, A, 128, A, 128) == 0
-    copy = 512 * 128 * 2
-    assert ws(F16, 256, 512, 128, A, 128, ODD, 128, A, 128) == copy      # address
-    assert ws(F16, 256, 512, 128, A, 128, A, 132, A, 128) == copy        # rows apart
-    assert ws(F16, 256, 512, 127, A, 127, A, 127, A, 127) == 256 * 256 + 2 * copy
-    assert ws(F16, 256, 512, 130, A, 130, A, 130, A, 130) == (256 + 2 * 512) * 192 * 2
+    assert ws(F16, 256, 2560, 128, A, 128, A, 128, A, 128) == 0
+    copy = 2560 * 128 * 2
+    assert ws(F16, 256, 2560, 128, A, 128, ODD, 128, A, 128) == copy     # address
+    assert ws(F16, 256, 2560, 128, A, 128, A, 132, A, 128) == copy       # rows apart
+    assert ws(F16, 256, 2560, 127, A, 127, A, 127, A, 127) == 256 * 256 + 2 * copy
+    assert ws(F16, 256, 2560, 130, A, 130, A, 130, A, 130) == (256 + 2 * 2560) * 192 * 2
+    # few outputs: none, fewer with odd rows
+    assert ws(F16, 256, 2500, 130, A, 130, A, 130, A, 130) == 0
+    assert ws(F16, 256, 1000, 127, A, 127, A, 127, A, 127) == 0
+    assert ws(F16, 256, 1001, 127, A, 127, A, 127, A, 127) == (256 + 2 * 1001) * 256
     assert ws(F16, 0, 512, 127, A, 127, A, 127, A, 127) == 0
-    assert ws(7, 256, 512, 127, A, 127, A, 127, A, 127) == 0
+    assert ws(7, 256, 2560, 127, A, 127, A, 127, A, 127) == 0
     bwd = lib.gemm_gated_bwd_workspace
     # dW: dG and dU, and X transposed
     assert bwd(F16, 256, 512, 128, A, 128, A, 128, A, 128, 0, 1) == 256 * 1024 * 2 + 128 * 256 * 2

@@ -37,7 +37,9 @@ def gated_inputs(M, N, K, dt, seed=0, pad=0, shift=0):
 GATED = [(1, 16, 32), (1, 1, 1), (1, 200, 100), (3, 1000, 8), (16, 130, 65), (17, 96, 128),
          (33, 64, 264), (64, 513, 72), (65, 129, 127), (100, 64, 130), (128, 64, 128),
          (129, 257, 320), (300, 500, 264), (257, 1000, 72), (513, 640, 192), (700, 333, 1537),
-         (370, 11009, 200), (570, 5001, 4090)]
+         (370, 11009, 200), (570, 5001, 4090),
+         (65, 5200, 127), (100, 6001, 130), (129, 5001, 320), (300, 2500, 264), (257, 3001, 72),
+         (513, 1700, 192), (700, 1333, 1537), (2000, 400, 136), (5000, 100, 70)]
 
 
 @pytest.mark.parametrize("typ", TYPES)
@@ -658,7 +660,7 @@ def test_gradients_against_differences():
     assert abs(slope - along) <= 4 * torch.finfo(dt).eps * along
 
 
-def everything(M=200, N=333, K=136, dt=torch.bfloat16, seed=0):
+def everything(M=200, N=2777, K=136, dt=torch.bfloat16, seed=0):
     """One call of each operator; returns (function, outputs)."""
     X, Wg, Wu = gated_inputs(M, N, K, dt, seed)
     r = gen(seed + 1)
