@@ -355,7 +355,9 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       item -= sp * tiles;
     }
     if constexpr (MODE != kProduct) item = xcd_order32((uint32_t)item, (uint32_t)ta.tiles);
-    if constexpr (MODE == kGradX) {   // an XCD's tiles of a range share its slabs of d and W
+    // (an XCD's tiles of a range share its slabs of d and W: 333 x 50001 x 768
+    // fp16, a step: 213 against 223 us dealt out tile by tile)
+    if constexpr (MODE == kGradX) {
       const uint32_t tiles = (uint32_t)tiles_m * tiles_n;
       sp = (int)((uint32_t)item / tiles);
       item -= (uint32_t)sp * tiles;
