@@ -184,8 +184,9 @@ BwdPlan plan_bwd(int M, int N, int K, Mat X, Mat W, bool dx, bool dw) {
   }
   p.bytes_scale = 256;
   p.bytes_xt = dw ? round256((size_t)p.Kp * p.Ms * 2) : 0;
-  if (needs_copy(X.p, X.ld, M, K)) p.bytes_x = copy_bytes(M, K);
-  if (needs_copy(W.p, W.ld, N, K)) p.bytes_w = copy_bytes(N, K);
+  // (M == 0: dW = 0, X and W are not read and may be null)
+  if (M > 0 && needs_copy(X.p, X.ld, M, K)) p.bytes_x = copy_bytes(M, K);
+  if (M > 0 && needs_copy(W.p, W.ld, N, K)) p.bytes_w = copy_bytes(N, K);
   return p;
 }
 

@@ -188,7 +188,8 @@ MI355FUSED_API unsigned long long gemm_xent_workspace(int type, int M, int N, in
  *
  * Rows with target `ignore` contribute nothing, whatever their X, lse and
  * dloss; a target outside [0, N) that is not `ignore` makes the row's d NaN.
- * M == 0 gives dW = 0.
+ * M == 0 gives dW = 0; X, W, targets, lse and dloss are then not read and may
+ * be NULL.
  */
 MI355FUSED_API int gemm_xent_bwd(int type, int M, int N, int K,
                                  const void* X, int ldx, const void* W, int ldw,

@@ -197,3 +197,16 @@ def test_binding_refuses(lib):
         dg.gemm_xent(h, h, i, f, f)
     with pytest.raises((TypeError, ValueError)):
         dg.gemm_xent_bwd(h, h, i, f, f)
+
+
+def test_xent_bwd_without_rows_reads_no_operand(lib):
+    """M == 0: dW = 0 takes neither X nor W (either may be null), so nothing is
+    copied, whatever their alignment and sizes: the workspace is d, the factor
+    and the transposed X (zeros), 128 rows of each."""
+    ws = lib.gemm_xent_bwd_workspace
+    assert ws(BF16, 0, 200, 100, None, 100, None, 100, 0, 1) == 128 * 256 * 2 + 256 + 128 * 128 * 2
+    for N, K in ((1, 1), (100, 256), (200, 100), (131072, 4095), (1000, 4096)):
+        size = ws(BF16, 0, N, K, A, K, A, K, 1, 1)
+        assert size == ws(BF16, 0, N, K, ODD, K + 1, ODD, K + 3, 1, 1)
+        Np, Kp = max(N, 128), max((K + 63) // 64 * 64, 128)
+        assert size == 128 * ((Np + 63) // 64 * 64) * 2 + 256 + Kp * 128 * 2, (N, K)

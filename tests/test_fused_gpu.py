@@ -500,6 +500,26 @@ def test_xent_no_rows():
     assert bool((dW == 0).all())
 
 
+@pytest.mark.parametrize("N,K", [(200, 100), (1000, 4095), (70, 128)])
+def test_xent_bwd_no_rows_null_operands(N, K):
+    """No rows, through the C entry point: dW = 0 with null operands, at sizes
+    that would have padded copies."""
+    from dense_gemm_sgemm_amd import fused
+
+    dW = Out(N, K, torch.bfloat16, 3, 1)
+    lib = fused.load_library()
+    need = lib.gemm_xent_bwd_workspace(1, 0, N, K, None, K, None, K, 0, 1)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    show("xent_bwd without rows", N, K)
+    status = lib.gemm_xent_bwd(1, 0, N, K, None, K, None, K, None, IGN, None, None, None, 0,
+                               dW.t.data_ptr(), dW.t.stride(0), ws.data_ptr(), need,
+                               torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    torch.cuda.synchronize()
+    assert bool((dW.t == 0).all())
+    dW.check_frame("dW")
+
+
 def test_xent_no_columns_of_x():
     """K == 0: all logits are 0."""
     X, W = (torch.empty((n, 0), dtype=torch.bfloat16, device=DEV) for n in (5, 300))
