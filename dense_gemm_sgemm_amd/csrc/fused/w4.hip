@@ -10,7 +10,11 @@
 // add, so a second product of X with ones makes the group's sum of x and
 // (128 + z) times it is taken off in fp32 (the matrix cores idle here: the
 // bound is HBM).  s multiplies the group's fp32 sum.  X is put in the nibbles'
-// order (0 4 1 5 2 6 3 7), once where it is kept in LDS.
+// order (0 4 1 5 2 6 3 7), once where it is kept in LDS.  Where an x of bf16 is
+// infinite, or so large (from 2^120) that the two sums overflow, their
+// difference is NaN or infinite: such outputs, and no others, are computed
+// again from the weights q - z themselves (multiply_exact), so that they are
+// what the definition gives.
 //
 // Where a block holds several groups (a group is a multiple of 32) each step
 // of 32 k must lie in one: the four lanes of a row exchange words (a 4 x 4
@@ -244,6 +248,41 @@ __device__ __forceinline__ void multiply(u4 raw, const uint16_t* scales, const u
   }
 }
 
+// One block's products in bf16 with the weights q - z themselves, times 2^-12: a
+// group's sum of 128 products of up to 15 x 2^128 stays finite, and so the
+// result, 2^-12 of tot, is infinite or NaN only where the definition's is (or
+// where it is infinite within a factor of 2^12 and cancels later).
+template <int GR, int MT>
+__device__ __forceinline__ void multiply_exact(u4 raw, const uint16_t* scales, const uint8_t* zeros,
+                                               const h8 (&x)[MT][4], f4 (&tot)[MT]) {
+  constexpr int kG = groups_per_block(GR), kSteps = 4 / kG;
+  const u4 w = kG == 1 ? raw : transpose4(raw);
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    f4 acc[MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = g * kSteps; j < (g + 1) * kSteps; ++j) {
+      // the nibbles' order of spread; differences of at most 15 are exact
+      auto word = [&](int nibble) __attribute__((always_inline)) {
+        const int q = (w[j] >> (4 * nibble)) & 15;
+        return __float_as_uint((float)(q - (int)zeros[g]) * 0x1p-12f) >> 16;
+      };
+      u4 r;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[i] = word(i) | (word(i + 4) << 16);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        acc[t] = mfma16<kFmtBF16>(x[t][j], __builtin_bit_cast(h8, r), acc[t]);
+    }
+    const uint16_t bits = scales[g];
+    const float s = word_to_f32<kFmtBF16>(__builtin_bit_cast(half_t, bits));
+#pragma unroll
+    for (int t = 0; t < MT; ++t) tot[t] += s * acc[t];
+  }
+}
+
 // XL: the rows of X (M <= 16) lie in LDS, reordered, zero past K, in
 // rows of K rounded up to blocks plus 16 bytes (rows then start in different
 // banks).  Otherwise each wave stages the rows of a block in turn (XStage).
@@ -357,6 +396,42 @@ __global__ __launch_bounds__(bound_of(FMT, GR, MT, MOST)) void w4_kernel(W4Args 
     load_rows(full, at_end);
     read_x(x, full);
     multiply<FMT, GR, MT>(one.w[0], one.s, one.z, x, magic, tot);
+  }
+
+  if constexpr (FMT == kFmtBF16) {
+    // Sums that are no numbers, again and exactly.  Once infinite or NaN a sum
+    // stays so, and each of them is mended by itself: a row's outputs do not
+    // depend on the other rows.
+    auto lost = [](float v) { return !(fabsf(v) < __builtin_inff()); };
+    bool any = false;
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) any |= lost(tot[t][v]);
+    if (__ballot(any) != 0) {
+      f4 again[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) again[t] = f4{0.f, 0.f, 0.f, 0.f};
+      auto block = [&](int b, auto tail) __attribute__((always_inline)) {
+        load_blocks<GR, 1, decltype(tail)::value>(p, row, b, quarter, one);
+        load_rows(b, tail);
+        read_x(x, b);
+        multiply_exact<GR, MT>(one.w[0], one.s, one.z, x, again);
+      };
+      // the wave's blocks: its chunks and what was left over
+      const int mine = p.chunks > wave ? (p.chunks - wave + p.waves - 1) / p.waves * kUnroll : 0;
+#pragma unroll 1
+      for (int i = 0; i < mine; ++i)
+        block((wave + i / kUnroll * p.waves) * kUnroll + i % kUnroll, inside);
+#pragma unroll 1
+      for (int b = left + wave; b < full; b += p.waves) block(b, inside);
+      if (full < blocks && wave == (full - left) % p.waves) block(full, at_end);
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (lost(tot[t][v])) tot[t][v] = again[t][v] * 0x1p12f;
+    }
   }
 
   // (the sums take the place of X)

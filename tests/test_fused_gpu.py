@@ -315,6 +315,37 @@ def test_w4_offset_sums_cancel():
     w4_check(C, X, Wq, s, z, 128)
 
 
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("group", [32, 64, 96, 128, 256])
+@pytest.mark.parametrize("M,N,K", [(1, 33, 700), (2, 30, 9000), (6, 40, 300), (16, 33, 17000),
+                                   (20, 49, 2100), (64, 20, 4500), (70, 17, 513)])
+def test_w4_infinite_and_huge(M, N, K, group, typ):
+    """An infinite or NaN x gives its row what the definition gives (NaN only
+    where the weight is zero, or where infinities meet), and bf16 values whose
+    128-fold no fp32 holds are multiplied as any others; the other rows keep
+    their bits."""
+    dt = DT[typ]
+    X, Wq, s, z = w4_inputs(M, N, K, group, dt, True, M + group)
+    base = torch.empty((M, N), dtype=dt, device=DEV)
+    dg.gemm_w4(X, Wq, s, base, group=group, zeros=z)
+    m, inf = M // 2, float("inf")
+    kinds = [{0: inf}, {K - 1: -inf}, {K // 2: inf, K // 3: inf}, {5: inf, K - 2: -inf},
+             {K // 2: float("nan")}]
+    if typ == "bf16":   # 15 x 1.5 x 3 x 2^121 < 2^128
+        kinds += [{K // 3: 2.0 ** 121}, {0: -2.0 ** 121, K // 2: 2.0 ** 121, K - 1: 2.0 ** 121}]
+    for kind in kinds:
+        X2 = X.clone()
+        for k, v in kind.items():
+            X2[m, k] = v
+        C = Out(M, N, dt)
+        show("w4 infinite", M, N, K, group, typ, kind)
+        dg.gemm_w4(X2, Wq, s, C.t, group=group, zeros=z)
+        w4_check(C.t, X2, Wq, s, z, group)
+        others = torch.arange(M, device=DEV) != m
+        assert torch.equal(C.t[others], base[others]), kind
+        C.check_frame("w4")
+
+
 def test_w4_empty_k():
     C = torch.full((3, 20), 5.0, dtype=torch.float16, device=DEV)
     e = lambda r, dt: torch.empty((r, 0), dtype=dt, device=DEV)  # noqa: E731
