@@ -68,8 +68,8 @@ __global__ __launch_bounds__(kThreads) void gated_grad_kernel(GradArgs p, int64_
         a = x * s;
         slope = s * (1.f + x * (1.f - s));
       } else if (p.act == GEMM_ACT_RELU) {
-        a = epi_relu(x);
-        slope = x > 0.f ? 1.f : 0.f;
+        a = gate_relu(x);
+        slope = x > 0.f ? 1.f : a;   // 0, or NaN for NaN
       }
       if (c + e >= first && c + e < p.N) {
         dg[e] = f32_to_word<FMT>(y * word_to_f32<FMT>(u[e]) * slope);

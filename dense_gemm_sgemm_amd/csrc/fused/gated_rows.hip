@@ -112,7 +112,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void gated_rows_kernel(RowsArgs p, 
       const int64_t m = m0 + 16 * t + 4 * quarter + v;
       if (m >= p.M) continue;
       const float g = acc[t][v], u = acc[MT + t][v];
-      p.H[m * p.ldh + n] = f32_to_word<FMT>(epi_act(g, p.act) * u);
+      p.H[m * p.ldh + n] = f32_to_word<FMT>(gate_act(g, p.act) * u);
       if (p.G) p.G[m * p.ldg + n] = f32_to_word<FMT>(g);
       if (p.U) p.U[m * p.ldu + n] = f32_to_word<FMT>(u);
     }

@@ -835,7 +835,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
             for (int v = 0; v < 4; ++v) y[v] = epi_silu(y[v]);
           } else if (p.act == GEMM_ACT_RELU) {
 #pragma unroll
-            for (int v = 0; v < 4; ++v) y[v] = epi_relu(y[v]);
+            for (int v = 0; v < 4; ++v) y[v] = gate_relu(y[v]);
           }
           put(j, round4(y * acc[i][2 * j + 1]));
         }

@@ -87,6 +87,15 @@ __device__ __forceinline__ float epi_act(float x, int act) {
   return x;
 }
 
+// The gated product's activations: as above, but ReLU keeps NaN, so that a gate
+// that has overflowed to inf - inf shows in the result and in the gradients.
+__device__ __forceinline__ float gate_relu(float x) { return x <= 0.f ? 0.f : x; }
+__device__ __forceinline__ float gate_act(float x, int act) {
+  if (act == GEMM_ACT_RELU) return gate_relu(x);
+  if (act == GEMM_ACT_SILU) return epi_silu(x);
+  return x;
+}
+
 // A split-K decision: `splits` K ranges of `per` slabs each and the workspace
 // bytes they need; splits == 1 means no split.
 struct SplitPlan {

@@ -81,7 +81,7 @@ MI355FUSED_API unsigned long long gemm_gated_workspace(int type, int M, int N, i
  *     dG = dH * U * act'(G)      dU = dH * act(G)
  *     dX = dG * Wg + dU * Wu     dWg = dG^T * X     dWu = dU^T * X
  *
- * ReLU's slope at 0 is 0.  dG and dU are computed in fp32 and rounded to the
+ * ReLU's slope at 0 is 0, and NaN where the gate is NaN.  dG and dU are computed in fp32 and rounded to the
  * type for the matrix cores (half a step, 2^-9 relative in bf16 and 2^-12 in
  * fp16, beside the outputs' own rounding); the sums over N and M are fp32.
  *
@@ -126,7 +126,8 @@ MI355FUSED_API unsigned long long gemm_gated_bwd_workspace(int type, int M, int 
  *   scales   : 16-bit [N][lds], lds >= max(1, ceil(K / group))  (read)
  *   zeros    : bytes [N][ldz], ldz >= max(1, ceil(K / group)), values 0 .. 15,
  *              or NULL for 8 everywhere                  (read)
- *   bias, act, residual, ldr, C, ldc : as for gemm_ex (residual may be C)
+ *   bias, act, residual, ldr, C, ldc : as for gemm_ex (residual may be C; ReLU
+ *              of NaN is 0)
  *
  * The weights are streamed once for every 64 rows of X, so the time grows in
  * steps of 64 rows: many more rows are faster on weights unpacked to 16 bits.

@@ -205,6 +205,61 @@ def test_gated_extreme_gates():
     close(dX, ref, tol + 1e-30, "dX")
 
 
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("name", ["silu", "relu", "none"])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 72), (5, 70, 130), (40, 33, 65), (200, 2700, 136),
+                                   (129, 5001, 70)])
+def test_gated_not_a_number(M, N, K, name, typ):
+    """NaN gates give NaN (ReLU's too), an infinite x what the definition gives;
+    outputs they do not enter keep their bits.  Few rows, tiles, padded copies."""
+    dt = DT[typ]
+    X, Wg, Wu = gated_inputs(M, N, K, dt, 23)
+    base = [torch.empty((M, N), dtype=dt, device=DEV) for _ in range(3)]
+    show("gated NaN", M, N, K, name, typ)
+    dg.gemm_gated(X, Wg, Wu, base[0], act=name, G=base[1], U=base[2])
+    nan_w = Wg.clone()
+    nan_w[N // 2, K // 2] = float("nan")
+    H, G, U = (Out(M, N, dt) for _ in range(3))
+    dg.gemm_gated(X, nan_w, Wu, H.t, act=name, G=G.t, U=U.t)
+    column = torch.arange(N, device=DEV) == N // 2
+    assert bool(torch.isnan(H.t[:, column]).all()) and bool(torch.isnan(G.t[:, column]).all())
+    for o, b in zip((H, G, U), base):
+        assert torch.equal(o.t[:, ~column], b[:, ~column])
+    assert torch.equal(U.t, base[2])
+    inf_x = X.clone()
+    inf_x[M // 2, K - 1] = float("inf")
+    dg.gemm_gated(inf_x, Wg, Wu, H.t, act=name, G=G.t, U=U.t)
+    g, u, h, sg, su = gated_ref(inf_x, Wg, Wu, name)
+    tols = gated_tols(g, u, h, sg, su, name, K, dt)
+    for o, ref, tol in zip((G, U, H), (g, u, h), tols):
+        close(o.t, ref, tol, "beside an infinite row")
+        o.check_frame("gated")
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("name", ["silu", "relu", "none"])
+@pytest.mark.parametrize("M,N,K", [(1, 40, 72), (70, 130, 65), (200, 700, 136)])
+def test_gated_bwd_not_a_number(M, N, K, name, typ):
+    """A NaN gate reaches its row of dX and its rows of dWg (through the slope)
+    and dWu, and nothing else."""
+    dt = DT[typ]
+    X, Wg, Wu = gated_inputs(M, N, K, dt, 24)
+    r = gen(25)
+    G, U, dH = (randn((M, N), 1.0, dt, r).to(DEV) for _ in range(3))
+    base = [torch.empty_like(q) for q in (X, Wg, Wu)]
+    show("gated_bwd NaN", M, N, K, name, typ)
+    dg.gemm_gated_bwd(X, Wg, Wu, G, U, dH, *base, act=name)
+    m, n = M // 2, N // 3
+    G[m, n] = float("nan")
+    got = [torch.empty_like(q) for q in base]
+    dg.gemm_gated_bwd(X, Wg, Wu, G, U, dH, *got, act=name)
+    for o, b, row in zip(got, base, (m, None if name == "none" else n, n)):
+        hit = torch.zeros(len(o), dtype=torch.bool, device=DEV)
+        if row is not None:
+            hit[row] = True
+        assert bool(torch.isnan(o[hit]).all()) and torch.equal(o[~hit], b[~hit])
+
+
 # ---------------------------------------------------------------- 4-bit weights
 
 def w4_inputs(M, N, K, group, dt, zeros, seed=0, pad=0, shift=0):
