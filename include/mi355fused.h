@@ -83,7 +83,10 @@ MI355FUSED_API unsigned long long gemm_gated_workspace(int type, int M, int N, i
  *
  * ReLU's slope at 0 is 0, and NaN where the gate is NaN.  dG and dU are computed in fp32 and rounded to the
  * type for the matrix cores (half a step, 2^-9 relative in bf16 and 2^-12 in
- * fp16, beside the outputs' own rounding); the sums over N and M are fp32.
+ * fp16, beside the outputs' own rounding); the sums over N and M are fp32.  In
+ * fp16 they are rounded times a power of two that brings the largest finite
+ * one to 2^14 .. 2^15, by which the sums are divided: none overflows, and only
+ * those below 2^-28 of the largest lose bits (2^-39 of it at most).
  *
  *   G, U, dH : [M][ld], ld >= max(1, N)      (read)
  *   dX       : [M][lddx], lddx >= max(1, K), or NULL  (written)
@@ -103,8 +106,9 @@ MI355FUSED_API int gemm_gated_bwd(int type, int act, int M, int N, int K,
                                   void* workspace, unsigned long long workspace_bytes,
                                   void* stream);
 
-/* Workspace bytes of gemm_gated_bwd: dG and dU (4 bytes a row and column of H)
- * and padded copies as for gemm_gated.  want_dx: dX is asked for; want_dw:
+/* Workspace bytes of gemm_gated_bwd: dG and dU (4 bytes a row and column of H),
+ * X transposed, fp32 sums of dX where it has few outputs, and padded copies as
+ * for gemm_gated.  want_dx: dX is asked for; want_dw:
  * dWg or dWu is. */
 MI355FUSED_API unsigned long long gemm_gated_bwd_workspace(int type, int M, int N, int K,
                                                            const void* X, int ldx,

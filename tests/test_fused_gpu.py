@@ -260,6 +260,63 @@ def test_gated_bwd_not_a_number(M, N, K, name, typ):
         assert bool(torch.isnan(o[hit]).all()) and torch.equal(o[~hit], b[~hit])
 
 
+@pytest.mark.parametrize("size", ["small", "large"])
+@pytest.mark.parametrize("want", ["dX", "dWg", "dWu", "dWg dWu", "dX dWg dWu"])
+@pytest.mark.parametrize("M,N,K", [(300, 200, 136), (256, 512, 128), (1000, 130, 300),
+                                   (70, 1000, 2100)])
+def test_gated_bwd_fp16_range(M, N, K, want, size):
+    """dG and dU outside binary16's range beside gradients inside it.  Small:
+    dG = dU of 2e-6, the same in all rows of a column, as a rounding in
+    binary16's subnormal range (up to 2^-25) would be.  Large: dG and dU of
+    4e5.  A rounding of the factored values is eps / 2 at most and the outputs'
+    own as much: eps in the norm."""
+    dt = torch.float16
+    r = gen(M + N)
+    names = want.split()
+    if size == "small":
+        X = 30 + randn((M, K), 1.0, torch.float32, r)
+        G = (0.04 * (1 + 0.3 * torch.rand((N,), generator=r))).expand(M, N)
+        U = 0.5 * G
+        dH = torch.full((M, N), 1e-4)
+        W = [1000 * (1 + torch.rand((N, K), generator=r)) for _ in range(2)]
+    else:
+        X = randn((M, K), 1e-3, torch.float32, r)
+        G = 100 * (1 + 0.1 * torch.rand((M, N), generator=r))
+        U = 100 + randn((M, N), 1.0, torch.float32, r)
+        dH = randn((M, N), 4000.0, torch.float32, r)
+        W = [randn((N, K), 1e-4, torch.float32, r) for _ in range(2)]
+    X, Wg, Wu, G, U, dH = (q.to(dt).to(DEV).contiguous() for q in (X, *W, G, U, dH))
+    outs = {"dX": torch.empty_like(X), "dWg": torch.empty_like(Wg), "dWu": torch.empty_like(Wu)}
+    show("gated_bwd range", M, N, K, want, size)
+    dg.gemm_gated_bwd(X, Wg, Wu, G, U, dH, **{k: outs[k] for k in names})
+    refs = dict(zip(outs, gated_bwd_ref(X, Wg, Wu, G, U, dH, "silu", dt)))
+    for k in names:
+        ref = refs[k][0]
+        assert 2.0 ** -10 < float(ref.abs().max()) < 6e4   # representable
+        assert bool(torch.isfinite(outs[k]).all()), k
+        norm_close(outs[k], ref, torch.finfo(dt).eps, k)
+
+
+def test_gated_bwd_fp16_infinite():
+    """An infinite dH takes its row of dX and its rows of dWg and dWu with it and
+    leaves the others their bits; all of dH zero gives zeros."""
+    M, N, K, dt = 150, 200, 136, torch.float16
+    X, Wg, Wu = gated_inputs(M, N, K, dt, 26)
+    r = gen(27)
+    G, U = (1 + randn((M, N), 0.1, dt, r).to(DEV).abs() for _ in range(2))
+    dH = 1 + randn((M, N), 0.1, dt, r).to(DEV).abs()
+    base = [torch.empty_like(q) for q in (X, Wg, Wu)]
+    dg.gemm_gated_bwd(X, Wg, Wu, G, U, dH, *base)
+    dH[40, 60] = float("inf")
+    got = [torch.empty_like(q) for q in base]
+    dg.gemm_gated_bwd(X, Wg, Wu, G, U, dH, *got)
+    for o, b, row in zip(got, base, (40, 60, 60)):
+        rest = torch.arange(len(o), device=DEV) != row
+        assert not bool(torch.isfinite(o[row]).any()) and torch.equal(o[rest], b[rest])
+    dg.gemm_gated_bwd(X, Wg, Wu, G, U, torch.zeros_like(dH), *got)
+    assert all(bool((o == 0).all()) for o in got)
+
+
 # ---------------------------------------------------------------- 4-bit weights
 
 def w4_inputs(M, N, K, group, dt, zeros, seed=0, pad=0, shift=0):
