@@ -120,6 +120,22 @@ def w4_weights(Wq, scales, zeros, group, K):
     return q - z, scales.double()[:, at]
 
 
+def w4_norm_close(got, x, q, s, what):
+    """X W^T in the 2-norm, W = q s (w4_weights), for x of random signs: an
+    output's rounding, at most eps / 2 of each value, and the fp32 sums, whose
+    additions are off by 2^-24 of partial sums of random signs: those stay within
+    a few times the root of the sum of the squared products (4 of it are
+    allowed), and their errors are independent, so that K / 32 + 8 additions are
+    off by the root of that many.  The bf16 form has products of up to 143 |s x|
+    in each of two sums, fp16's up to 15."""
+    K, dt = x.shape[1], got.dtype
+    x = x.double()
+    ref = x @ (q * s).T
+    root = ((x * x) @ (s * s).T).sum() ** 0.5 * (286.0 if dt == torch.bfloat16 else 15.0)
+    off = 4 * (K / 32 + 8) ** 0.5 * 2.0 ** -24 * float(root)
+    norm_close(got, ref, torch.finfo(dt).eps / 2 + off / float(ref.norm()), what)
+
+
 def xent_ref(X, W, targets, ignore):
     """(z, lse, loss) in 64 bits; NaN loss for a target out of range."""
     z = X.double() @ W.double().T

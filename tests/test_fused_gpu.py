@@ -8,7 +8,8 @@ torch = pytest.importorskip("torch")
 
 import dense_gemm_sgemm_amd as dg  # noqa: E402
 from fused_ref import (DT, Out, act, act_slope, close, gated_ref, gated_tols, half_step,  # noqa: E402
-                       norm_close, place, randn, sum_error, w4_weights, xent_ref, xent_tol)
+                       norm_close, place, randn, sum_error, w4_norm_close, w4_weights, xent_ref,
+                       xent_tol)
 
 pytestmark = pytest.mark.gpu
 
@@ -383,6 +384,24 @@ def test_w4_long(M, N, K, group, typ):
     dg.gemm_w4(X, Wq, s, C.t, group=group, zeros=z)
     w4_check(C.t, X, Wq, s, z, group)
     C.check_frame("w4")
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("zeros", [True, False])
+@pytest.mark.parametrize("group", [32, 64, 128, 256, 96])
+@pytest.mark.parametrize("M,N,K", [(1, 100, 16384), (3, 100, 9001), (5, 64, 16384), (16, 65, 17000),
+                                   (16, 200, 300), (24, 64, 9000), (40, 50, 16400), (64, 64, 4100),
+                                   (70, 40, 2050)])
+def test_w4_in_norm(M, N, K, group, zeros, typ):
+    """A bound that one wrong K value in a thousand exceeds (see
+    test_fused_checks.py), at a long K too, where the elementwise one of bf16's
+    two large sums is wide."""
+    dt = DT[typ]
+    X, Wq, s, z = w4_inputs(M, N, K, group, dt, zeros, M + K + group)
+    C = torch.empty((M, N), dtype=dt, device=DEV)
+    show("w4 in norm", M, N, K, group, zeros, typ)
+    dg.gemm_w4(X, Wq, s, C, group=group, zeros=z)
+    w4_norm_close(C, X, *w4_weights(Wq, s, z, group, K), "C")
 
 
 @pytest.mark.parametrize("pad,shift", [(1, 1), (3, 0), (16, 16)])
