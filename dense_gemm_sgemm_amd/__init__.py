@@ -135,6 +135,9 @@ def _torch_module():
     return _torch
 
 
+INT_MAX = 2 ** 31 - 1   # sizes and leading dimensions are C ints
+
+
 def _matrix(t, name: str, dtype):
     """(rows, cols, leading dimension, device pointer or None) of a row-major
     2-D GPU tensor; raises on anything else.  Runs on every call, so it uses
@@ -151,6 +154,8 @@ def _matrix(t, name: str, dtype):
     if cols > 1 and s1 != 1:
         raise ValueError("%s must have unit stride along its rows (row-major)" % name)
     ld = s0 if rows > 1 and cols > 0 else max(1, cols)
+    if ld > INT_MAX or rows > INT_MAX or cols > INT_MAX:   # (ctypes would cut them off)
+        raise ValueError("%s: sizes and the distance between rows must be below 2^31" % name)
     return rows, cols, ld, (t.data_ptr() if rows and cols else None)
 
 

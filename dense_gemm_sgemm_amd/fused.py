@@ -22,8 +22,8 @@ import ctypes
 import os
 import threading
 
-from . import (ACTS, HERE, _check, _current_stream_handle, _epilogue_args, _matrix, _torch_module,
-               _workspace)
+from . import (ACTS, HERE, INT_MAX, _check, _current_stream_handle, _epilogue_args, _matrix,
+               _torch_module, _workspace)
 
 LIB_PATH = os.path.join(HERE, "libmi355fused.so")
 _lock = threading.Lock()
@@ -85,7 +85,10 @@ def _first(t):
 def _rows(t, name) -> int:
     if not isinstance(t, _Tensor) or t.dim() != 2:
         raise TypeError("%s must be a 2-D torch tensor" % name)
-    return t.shape[0]
+    rows = t.shape[0]
+    if rows > INT_MAX:
+        raise ValueError("%s: sizes must be below 2^31" % name)
+    return rows
 
 
 def _shaped(t, name, dtype, index, rows, cols):
@@ -95,7 +98,7 @@ def _shaped(t, name, dtype, index, rows, cols):
     if isinstance(t, _Tensor) and t.dtype is dtype and t.shape == (rows, cols) and \
             t.get_device() == index and rows > 1 and cols > 1:
         s0, s1 = t.stride()
-        if s1 == 1:
+        if s1 == 1 and s0 <= INT_MAX:
             return t.data_ptr(), s0
     r, c, ld, ptr = _matrix(t, name, dtype)
     if r != rows or c != cols:
@@ -226,8 +229,8 @@ def gemm_w4(X, Wq, scales, C, group: int = 128, zeros=None, bias=None, act: str 
     streamed once for every 64 rows).  Returns C."""
     torch = _torch_module()
     dtype, typ, at, M, K, px, ldx = _first(X)
-    if group <= 0:
-        raise ValueError("group must be a positive multiple of 32")
+    if group <= 0 or group > INT_MAX:
+        raise ValueError("group must be a positive multiple of 32 below 2^31")
     N = _rows(Wq, "Wq")
     groups = -(-K // group)
     pq, ldq = _shaped(Wq, "Wq", torch.uint8, at, N, (K + 1) // 2)

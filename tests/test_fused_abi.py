@@ -210,3 +210,44 @@ def test_xent_bwd_without_rows_reads_no_operand(lib):
         assert size == ws(BF16, 0, N, K, ODD, K + 1, ODD, K + 3, 1, 1)
         Np, Kp = max(N, 128), max((K + 63) // 64 * 64, 128)
         assert size == 128 * ((Np + 63) // 64 * 64) * 2 + 256 + Kp * 128 * 2, (N, K)
+
+
+def fake_gpu(*size_stride, dtype="float16"):
+    """A GPU tensor without memory (none of these calls gets as far as its data)."""
+    torch = pytest.importorskip("torch")
+    fake = pytest.importorskip("torch._subclasses.fake_tensor")
+    with fake.FakeTensorMode():
+        return torch.empty_strided(*size_stride, device="cuda", dtype=getattr(torch, dtype))
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_binding_refuses_what_an_int_does_not_hold(lib):
+    """Rows 2^32 + 64 elements apart or 2^32 + 2 of them would reach the C calls
+    as 64 and 2."""
+    far, small = fake_gpu((2, 64), (2 ** 32 + 64, 1)), fake_gpu((2, 64), (64, 1))
+    many = fake_gpu((2 ** 32 + 2, 64), (64, 1))
+    out = fake_gpu((2, 2), (2, 1))
+    far_out = fake_gpu((2, 2), (2 ** 32 + 2, 1))
+    t, f = fake_gpu((2,), (1,), dtype="int64"), fake_gpu((2,), (1,), dtype="float32")
+    q = fake_gpu((2, 32), (2 ** 32 + 32, 1), dtype="uint8")
+    s = fake_gpu((2, 2), (2, 1))
+    calls = [
+        lambda: dg.gemm_gated(far, small, small, out),
+        lambda: dg.gemm_gated(small, small, far, out),
+        lambda: dg.gemm_gated(small, small, small, far_out),
+        lambda: dg.gemm_gated(small, many, many, fake_gpu((2, 2 ** 32 + 2), (2 ** 32 + 2, 1))),
+        lambda: dg.gated_workspace_bytes(many, small, small),
+        lambda: dg.gemm_gated_bwd(small, small, small, out, out, far_out),
+        lambda: dg.gemm_w4(small, q, s, out, group=32),
+        lambda: dg.gemm_w4(small, fake_gpu((2, 32), (32, 1), dtype="uint8"),
+                           fake_gpu((2, 1), (1, 1)), out, group=2 ** 32 + 64),
+        lambda: dg.gemm_xent(small, far, t, f, f),
+        lambda: dg.gemm_xent(small, many, t, f, f),
+        lambda: dg.gemm_xent_bwd(small, small, t, f, f, dX=far),
+        lambda: dg.gemm_ex(far, small, out),
+        lambda: dg.gemm_f16_nt(small, small, far_out),
+    ]
+    for i, call in enumerate(calls):
+        with pytest.raises(ValueError, match=r"2\^31"):
+            call()
+            pytest.fail("call %d" % i)
