@@ -330,8 +330,7 @@ def _epilogue_args(bias, act, residual, M: int, N: int, dtype=None):
     pbias = None
     if bias is not None:
         if not isinstance(bias, torch.Tensor) or bias.dtype != dtype or \
-                bias.device.type != "cuda" or bias.numel() != N or \
-                (bias.dim() == 1 and N > 1 and bias.stride(0) != 1):
+                bias.device.type != "cuda" or bias.numel() != N or not bias.is_contiguous():
             raise ValueError("bias must be a contiguous %s GPU vector of length N = %d"
                              % (dtype, N))
         pbias = bias.data_ptr()

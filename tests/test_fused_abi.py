@@ -251,3 +251,17 @@ def test_binding_refuses_what_an_int_does_not_hold(lib):
         with pytest.raises(ValueError, match=r"2\^31"):
             call()
             pytest.fail("call %d" % i)
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_binding_refuses_a_strided_bias(lib):
+    """A column of a matrix as the bias, [N, 1]: its values are not N in a row."""
+    x, q, s = fake_gpu((2, 64), (64, 1)), fake_gpu((3, 32), (32, 1), dtype="uint8"), \
+        fake_gpu((3, 2), (2, 1))
+    out, w = fake_gpu((2, 3), (3, 1)), fake_gpu((3, 64), (64, 1))
+    for size_stride in (((3, 1), (5, 1)), ((1, 3), (3, 2)), ((3,), (2,)), ((3,), (0,))):
+        bias = fake_gpu(*size_stride)
+        with pytest.raises(ValueError, match="contiguous"):
+            dg.gemm_w4(x, q, s, out, group=32, bias=bias)
+        with pytest.raises(ValueError, match="contiguous"):
+            dg.gemm_ex(x, w, out, bias=bias)
