@@ -1000,3 +1000,151 @@ def test_what_a_workspace_holds(M, N, K, typ):
             results.append([o.clone() for o in outs])
         for a, b in zip(*results):
             assert bool(torch.isfinite(a).all()) and torch.equal(a, b), (i, M, N, K)
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("pad,shift", [(3, 1), (8, 8), (0, 1), (2, 2)])
+@pytest.mark.parametrize("M,N,K", [(7, 61, 200), (150, 333, 152), (200, 2700, 139)])
+def test_strides_of_both_types(M, N, K, pad, shift, typ):
+    """Every operator with rows further apart than their length or at 2-byte
+    addresses, NaN (255 in bytes) between them."""
+    dt = DT[typ]
+    show("strides", M, N, K, pad, shift, typ)
+    X, Wg, Wu = gated_inputs(M, N, K, dt, 5, pad, shift)
+    H, G, U = (Out(M, N, dt, pad, shift) for _ in range(3))
+    dg.gemm_gated(X, Wg, Wu, H.t, G=G.t, U=U.t)
+    g, u, h, sg, su = gated_ref(X, Wg, Wu, "silu")
+    for o, ref, tol in zip((G, U, H), (g, u, h), gated_tols(g, u, h, sg, su, "silu", K, dt)):
+        close(o.t, ref, tol, "gated")
+        o.check_frame("gated")
+    dH = place(randn((M, N), 1.0, dt, gen(6)), pad, shift)
+    outs = [Out(r, K, dt, pad, shift) for r in (M, N, N)]
+    dg.gemm_gated_bwd(X, Wg, Wu, G.t, U.t, dH, *[o.t for o in outs])
+    for o, (ref, tol) in zip(outs, gated_bwd_ref(X, Wg, Wu, G.t, U.t, dH, "silu", dt)):
+        close(o.t, ref, tol, "gated_bwd")
+        o.check_frame("gated_bwd")
+    for group in (32, 64, 128, 96):
+        X4, Wq, s, z = w4_inputs(M, N, K, group, dt, True, 7, pad, shift)
+        C = Out(M, N, dt, pad, shift)
+        dg.gemm_w4(X4, Wq, s, C.t, group=group, zeros=z)
+        w4_check(C.t, X4, Wq, s, z, group)
+        C.check_frame("w4")
+    X, W, t = xent_inputs(M, N, K, dt, 8, pad, shift)
+    loss, lse = torch.empty((M,), device=DEV), torch.empty((M,), device=DEV)
+    dg.gemm_xent(X, W, t, loss, lse)
+    z, rl, ro = xent_ref(X, W, t, IGN)
+    close(loss, ro, 2 * xent_tol(X, W, z, rl), "loss")
+    dX, dW = Out(M, K, dt, pad, shift), Out(N, K, dt, pad, shift)
+    dloss = torch.rand((M,), generator=gen(9)).to(DEV)
+    dg.gemm_xent_bwd(X, W, t, lse, dloss, dX=dX.t, dW=dW.t)
+    xent_bwd_check(X, W, t, lse, dloss, dX.t, dW.t)
+    dX.check_frame("dX")
+    dW.check_frame("dW")
+
+
+# ---------------------------------------------------------------- past 2^31 elements
+
+def big(shape, sd, dt, seed):
+    """Random values made on the GPU."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return torch.empty(shape, dtype=dt, device=DEV).normal_(0.0, sd, generator=g)
+
+
+def some(n, k=97):
+    """Indices of n: the first, the last, those around element 2^31, and some between."""
+    at = {0, 1, n - 2, n - 1, *range(0, n, max(1, n // k))}
+    return torch.tensor(sorted(i for i in at if 0 <= i < n), device=DEV)
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("M,N,K", [
+    (3, 530000, 4100),        # few rows: weights
+    (200, 530000, 4104),      # tiles, operands in place: weights
+    (130, 1100000, 2001),     # tiles, padded copies of both weights
+    (70000, 32000, 136),      # the outputs
+    (2100000, 130, 1040)])    # X
+def test_gated_past_two_gibi_elements(M, N, K, typ):
+    dt = DT[typ]
+    X, Wg, Wu = big((M, K), 1.0, dt, 1), big((N, K), K ** -0.5, dt, 2), big((N, K), K ** -0.5, dt, 3)
+    H, G, U = (torch.full((M, N), 7.0, dtype=dt, device=DEV) for _ in range(3))
+    show("gated large", M, N, K, typ)
+    dg.gemm_gated(X, Wg, Wu, H, G=G, U=U)
+    m, n = some(M), some(N)
+    g, u, h, sg, su = gated_ref(X[m], Wg[n], Wu[n], "silu")
+    tg, tu, th = gated_tols(g, u, h, sg, su, "silu", K, dt)
+    at = (m[:, None], n[None, :])
+    close(G[at], g, tg, "G")
+    close(U[at], u, tu, "U")
+    close(H[at], h, th, "H")
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("M,N,K", [(70000, 32000, 136), (200, 530000, 4104)])
+def test_gated_bwd_past_two_gibi_elements(M, N, K, typ):
+    dt = DT[typ]
+    X, Wg, Wu = big((M, K), 1.0, dt, 1), big((N, K), N ** -0.5, dt, 2), big((N, K), N ** -0.5, dt, 3)
+    G, U, dH = big((M, N), 1.0, dt, 4), big((M, N), 1.0, dt, 5), big((M, N), M ** -0.5, dt, 6)
+    dX, dWg, dWu = (torch.full_like(q, 7.0) for q in (X, Wg, Wu))
+    show("gated_bwd large", M, N, K, typ)
+    dg.gemm_gated_bwd(X, Wg, Wu, G, U, dH, dX, dWg, dWu)
+    m, n, eps = some(M, 40), some(N, 40), torch.finfo(dt).eps
+    at = gated_bwd_ref(X[m], Wg, Wu, G[m], U[m], dH[m], "silu", dt)[0]
+    norm_close(dX[m], at[0], eps, "dX")
+    refs = gated_bwd_ref(X, Wg[n], Wu[n], *(q[:, n] for q in (G, U, dH)), "silu", dt)
+    for got, (ref, _), what in zip((dWg[n], dWu[n]), refs[1:], ("dWg", "dWu")):
+        norm_close(got, ref, eps, what)
+        rows = (got.double() - ref).norm(dim=1) / ref.norm(dim=1)
+        assert float(rows.max()) <= 2 * eps, (what, int(rows.argmax()))
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("M,N,K", [(1, 300000, 16384), (20, 300000, 16400), (34000, 66000, 64)])
+def test_w4_past_two_gibi_elements(M, N, K, typ):
+    """The packed weights, and the output."""
+    dt, group = DT[typ], 64
+    g = torch.Generator(device=DEV).manual_seed(5)
+    X = big((M, K), 1.0, dt, 1)
+    Wq = torch.randint(0, 256, (N, K // 2), device=DEV, dtype=torch.uint8, generator=g)
+    s = (torch.rand((N, -(-K // group)), device=DEV, generator=g) + 0.5).to(dt)
+    z = torch.randint(0, 16, s.shape, device=DEV, dtype=torch.uint8, generator=g)
+    C = torch.full((M, N), 7.0, dtype=dt, device=DEV)
+    show("w4 large", M, N, K, typ)
+    dg.gemm_w4(X, Wq, s, C, group=group, zeros=z)
+    m, n = some(M), some(N)
+    got = C[m[:, None], n[None, :]]
+    w4_check(got, X[m], Wq[n], s[n], z[n], group)
+    w4_norm_close(got, X[m], *w4_weights(Wq[n], s[n], z[n], group, K), "C")
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("M,N,K", [(150, 530000, 4104), (2100000, 257, 1032)])
+def test_xent_past_two_gibi_elements(M, N, K, typ):
+    """The vocabulary matrix and its gradient; X and its gradient."""
+    dt = DT[typ]
+    X, W = big((M, K), 1.0, dt, 1), big((N, K), 2.0 * K ** -0.5, dt, 2)
+    t = torch.randint(0, N, (M,), generator=gen(3)).to(DEV)
+    t[::7], t[-1] = IGN, N - 1
+    loss, lse = torch.empty((M,), device=DEV), torch.empty((M,), device=DEV)
+    dX, dW = torch.full_like(X, 7.0), torch.full_like(W, 7.0)
+    dloss = torch.rand((M,), generator=gen(4)).to(DEV) + 0.5
+    show("xent large", M, N, K, typ)
+    dg.gemm_xent(X, W, t, loss, lse)
+    dg.gemm_xent_bwd(X, W, t, lse, dloss, dX, dW)
+    m, eps = some(M, 40), torch.finfo(dt).eps
+    for i in m.split(8):   # rows of logits in 64 bits
+        z, a, b = xent_ref(X[i], W, t[i], IGN)
+        tol = xent_tol(X[i], W, z, a)
+        close(lse[i], a, tol, "lse")
+        close(loss[i], b, 2 * tol, "loss")
+        p = torch.exp(z - a[:, None])
+        live = t[i] != IGN
+        p[torch.arange(len(i), device=DEV)[live], t[i][live]] -= 1
+        p *= (live * dloss[i].double())[:, None]
+        norm_close(dX[i], p @ W.double(), eps, "dX")
+        assert bool((dX[i][~live] == 0).all())
+    # columns of the logits for the rows of dW
+    n = some(N, 40)
+    p = torch.exp(X.double() @ W[n].double().T - lse.double()[:, None])
+    p -= (t[:, None] == n[None, :]).double()
+    p *= ((t != IGN) * dloss.double())[:, None]
+    norm_close(dW[n], p.T @ X.double(), eps, "dW")
