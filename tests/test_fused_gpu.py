@@ -600,6 +600,30 @@ def test_xent_bwd_in_pieces(M, N, K):
     assert float(rel.max()) <= 2 * torch.finfo(dt).eps, int(rel.argmax())
 
 
+@pytest.mark.parametrize("M,N,K", [(16384, 262154, 128), (8192, 524400, 72)])
+def test_xent_bwd_last_piece_in_ranges(M, N, K):
+    """A last piece of ten and of 112 columns (two slabs of 64) where the others'
+    128 and 256 slabs are cut into ranges: ranges of one slab."""
+    test_xent_bwd_in_pieces(M, N, K)
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("N", [321, 832, 833, 1088, 1345, 1600])
+def test_gated_bwd_ranges(N, typ):
+    """Few outputs of dX over 12 to 50 slabs: last ranges of every length."""
+    M, K, dt = 128, 128, DT[typ]
+    X, Wg, Wu = gated_inputs(M, N, K, dt, N)
+    r = gen(N)
+    G, U, dH = (randn((M, N), 1.0, dt, r).to(DEV) for _ in range(3))
+    outs = [Out(r, K, dt) for r in (M, N, N)]
+    show("gated_bwd ranges", N, typ)
+    dg.gemm_gated_bwd(X, Wg, Wu, G, U, dH, *[o.t for o in outs])
+    for o, (ref, tol) in zip(outs, gated_bwd_ref(X, Wg, Wu, G, U, dH, "silu", dt)):
+        close(o.t, ref, tol, "gradient")
+        norm_close(o.t, ref, torch.finfo(dt).eps, "gradient")
+        o.check_frame("gated_bwd")
+
+
 @pytest.mark.parametrize("pad,shift", [(3, 1), (8, 8), (0, 1)])
 def test_xent_strides(pad, shift):
     M, N, K, dt = 140, 333, 152, torch.float16
@@ -1000,6 +1024,59 @@ def test_what_a_workspace_holds(M, N, K, typ):
             results.append([o.clone() for o in outs])
         for a, b in zip(*results):
             assert bool(torch.isfinite(a).all()) and torch.equal(a, b), (i, M, N, K)
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("M,N,K", [(256, 512, 128), (200, 333, 136), (70, 1345, 200)])
+def test_some_gradients_captured(M, N, K, typ):
+    """Single gradients and pairs: nothing of a workspace full of NaN is read, and
+    a graph replayed on new inputs, eager calls between, gives the eager bits."""
+    dt = DT[typ]
+    X, Wg, Wu = gated_inputs(M, N, K, dt, M)
+    G, U, dH = (randn((M, N), 1.0, dt, gen(s)).to(DEV) for s in (1, 2, 3))
+    t = torch.randint(0, N, (M,), generator=gen(4)).to(DEV)
+    lse = torch.logsumexp(X.double() @ Wg.double().T, 1).float()
+    dloss = torch.rand((M,), generator=gen(5)).to(DEV)
+    dX, dWg, dWu, dX2, dW2 = (torch.empty_like(q) for q in (X, Wg, Wu, X, Wg))
+    names = dict(dX=dX, dWg=dWg, dWu=dWu)
+    calls = []
+    for want in ("dX", "dWg", "dWu", "dWg dWu", "dX dWu"):
+        kw = {k: names[k] for k in want.split()}
+        size = dg.gated_bwd_workspace_bytes(X, Wg, Wu, "dX" in kw, "dWg" in kw or "dWu" in kw)
+        calls.append((lambda ws, kw=kw: dg.gemm_gated_bwd(X, Wg, Wu, G, U, dH, workspace=ws, **kw),
+                      size, list(kw.values())))
+    for kw in (dict(dX=dX2), dict(dW=dW2)):
+        size = dg.xent_bwd_workspace_bytes(X, Wg, "dX" in kw, "dW" in kw)
+        calls.append((lambda ws, kw=kw: dg.gemm_xent_bwd(X, Wg, t, lse, dloss, workspace=ws, **kw),
+                      size, list(kw.values())))
+    for i, (call, size, outs) in enumerate(calls):
+        show("some gradients", M, N, K, typ, i)
+        results = []
+        for fill in (0, 255):
+            ws = torch.full((size,), fill, dtype=torch.uint8, device=DEV)
+            call(ws)
+            results.append([o.clone() for o in outs])
+        for a, b in zip(*results):
+            assert bool(torch.isfinite(a).all()) and torch.equal(a, b), i
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph):
+            call(ws)
+        for turn in range(3):
+            dH.mul_(-1.0 if turn % 2 else 0.5)
+            dloss.mul_(0.5)
+            call(torch.empty_like(ws))
+            torch.cuda.synchronize()
+            want = [o.clone() for o in outs]
+            for o in outs:
+                o.fill_(7)
+            ws.fill_(255)
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(want, outs):
+                assert torch.equal(a, b), (i, turn)
+        dH.mul_(-4.0)
+        dloss.mul_(8.0)
 
 
 @pytest.mark.parametrize("typ", TYPES)
