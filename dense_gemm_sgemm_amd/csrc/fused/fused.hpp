@@ -159,8 +159,8 @@ inline int choose_shape(const Shape* s, int n, int M, int N, int tiles_mul, int 
 }
 
 // Sizes are limited so that rows made here (d of two parts, transposed X) keep
-// the tiles' 32-bit lane offsets (rows below 2^28 elements) and padded sizes
-// stay ints.
+// the tiles' 32-bit lane offsets (rows of 2^28 elements at most, seven of which
+// are 2^32 - 2^29 bytes) and padded sizes stay ints.
 constexpr int kMaxSize = 1 << 27;
 inline int check_sizes(int M, int N, int K) {
   if (M < 0 || N < 0 || K < 0) return GEMM_ERR_NEGATIVE_DIM;

@@ -2,8 +2,10 @@
 // workgroup, the weights streamed from HBM once).
 //
 // A workgroup owns 16 weight rows (outputs n) and all of K, which its waves
-// share out; no LDS and no barrier until the sums of the waves are added at
-// the end.  A wave multiplies with v_mfma_f32_16x16x32: X rows are the first
+// share out.  Weights go from memory to registers, X through a copy in LDS that
+// is each wave's own (XStage below: no barrier) or, for the fewest rows of
+// gemm_w4, the workgroup's (one barrier before the products); the sums of the
+// waves are added through LDS at the end.  A wave multiplies with v_mfma_f32_16x16x32: X rows are the first
 // operand (lane l: row l % 16, k = 8 (l / 16) .. + 7 of a step's 32), weight
 // rows the second (lane l: row n0 + l % 16, the same k), so a lane's four
 // accumulators are rows 4 (l / 16) .. + 3 of X against its one weight row.

@@ -48,7 +48,12 @@ inline int groups_of(int group) {
 // more registers would spill (64 x 4096 x 16384: 64.9 against 35.5 us); two
 // for up to 16 rows in bf16 with two groups a block, whose 170 registers leave
 // a SIMD too few waves (16 x 10000 x 2432: 10.6 against 8.7 us; not fp16's 130:
-// 8.4 against 8.9); two with sixteen waves.
+// 8.4 against 8.9); two with sixteen waves.  Two instances still spill: bf16
+// with 17 to 32 rows and groups of 64 (6 registers) or of other multiples of 32
+// (26).  Half the blocks end that, but not for the better everywhere, by shape:
+// 24 x 16384 x 4096 27.9 against 33.5 us, 24 x 4096 x 16384 27.5 against 27.4,
+// 32 x 4096 x 4096 10.5 against 9.4 (groups of 64); 50.7 against 56.2, 43.2
+// against 36.1 and 19.4 against 15.2 (groups of 96).
 constexpr int unroll_of(int fmt, int gr, int mt, int most) {
   const bool four = groups_per_block(gr) == 4;
   if (four && mt == 4) return 1;
@@ -59,9 +64,17 @@ constexpr int unroll_of(int fmt, int gr, int mt, int most) {
 // workgroups' LDS a CU), eight, or sixteen: with X in LDS where chunks are two
 // blocks and the registers of sixteen waves do (1 x 4096 x 16384, groups of 32:
 // 15.0 against 13.0 us); with X staged and up to 16 rows where a CU has one
-// workgroup and each wave four chunks (16 x 4096 x 16384, groups of 128, 64 and
-// 32 in fp16: 15.7, 16.1 and 17.1 against 15.1, 15.3 and 16.5 us; bf16 with
-// groups of 32 would spill: 19.1 against 27.7).
+// workgroup and each wave four chunks (bf16 with groups of 32 would spill: 19.1
+// against 27.7).  Eight against sixteen waves with X staged, 4 and 16 rows, 4096
+// weight rows out of HBM, us:
+//             K = 8192               K = 11008              K = 16384
+//   fp16 128  11.0  11.0  11.5 11.4  14.2 11.6  14.9 12.8   17.5 17.1  18.5 19.1
+//   fp16  64  11.1  11.3  11.4 11.7  14.4 12.3  14.9 13.7   18.1 17.7  18.6 19.6
+//   fp16  32  12.4  11.8  12.5 12.2  14.1 13.1  14.8 14.5   20.1 18.4  20.7 20.0
+//   bf16 128  11.9  11.3  12.6 11.5  15.0 11.9  16.3 12.9   18.8 17.7  20.2 19.2
+//   bf16  64  12.0  11.3  12.1 11.9  13.3 12.3  14.5 14.0   19.3 17.8  19.7 19.7
+// so the rule loses up to 5 % in fp16 at 16 rows, and two chunks a wave (K from
+// 8192) would do in most of the other cases.
 constexpr int x_waves(int fmt, int gr) {
   return gr == kFour || (gr == kTwo && fmt == kFmtBF16) ? 16 : 8;
 }

@@ -134,7 +134,8 @@ MI355FUSED_API unsigned long long gemm_gated_bwd_workspace(int type, int M, int 
  *              of NaN is 0)
  *
  * The weights are streamed once for every 64 rows of X, so the time grows in
- * steps of 64 rows: many more rows are faster on weights unpacked to 16 bits.
+ * steps of 64 rows: many more rows are faster with gemm_ex on weights that the
+ * caller has unpacked to 16 bits.
  * K == 0 gives act(bias) + residual.  M == 0 or N == 0 is a no-op.  A group
  * that is not a positive multiple of 32 is GEMM_ERR_BAD_ARG.
  */
