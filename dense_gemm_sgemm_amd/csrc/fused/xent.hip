@@ -75,13 +75,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void join_kernel(JoinArgs p, int64
 }
 
 // ---- The scale of d: {f, 1 / f} with f = size / max |dloss| over the rows that
-// count, so that d = (p - [target]) dloss f has its largest entries at `size`.
-// With one dloss for all rows (a mean) they are p - 1 times `size`, a power of
-// two: rounding dloss itself to 16 bits, the same way in every row, would put
-// all gradients off by up to 2^-9 in bf16 (measured: 0.34 % against 0.17 % of
-// random rounding).  In fp16 the size 2^14 also keeps probabilities down to
-// 2^-38 (binary16's smallest step is 2^-24).  1 where that maximum is 0 or not
-// finite.
+// count and are finite, so that d = (p - [target]) dloss f has its largest
+// entries at `size`.  With one dloss for all rows (a mean) they are p - 1 times
+// `size`, a power of two: rounding dloss itself to 16 bits, the same way in
+// every row, would put all gradients off by up to 2^-9 in bf16 (measured: 0.34 %
+// against 0.17 % of random rounding).  In fp16 the size 2^14 also keeps
+// probabilities down to 2^-38 (binary16's smallest step is 2^-24).  1 where that
+// maximum is 0.
 struct ScaleArgs {
   const float* dloss;
   const long long* targets;
@@ -96,7 +96,7 @@ __device__ __forceinline__ void find_scale(const ScaleArgs& p) {
   float top = 0.f;
   for (int m = threadIdx.x; m < p.M; m += kPrepareThreads) {
     const float v = fabsf(p.dloss[m]);
-    if (p.targets[m] != p.ignore) top = fmaxf(top, v);
+    if (p.targets[m] != p.ignore && v < __builtin_inff()) top = fmaxf(top, v);
   }
 #pragma unroll
   for (int k = 32; k >= 1; k /= 2) top = fmaxf(top, __shfl_xor(top, k));
@@ -105,7 +105,7 @@ __device__ __forceinline__ void find_scale(const ScaleArgs& p) {
   if (threadIdx.x != 0) return;
   for (int w = 1; w < kPrepareThreads / 64; ++w) top = fmaxf(top, part[w]);
   float f = 1.f, r = 1.f;
-  if (top > 0.f && top < __builtin_inff()) {
+  if (top > 0.f) {
     top = fmaxf(top, 0x1p-100f);   // f stays finite
     f = p.size / top;
     r = top / p.size;

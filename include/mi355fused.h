@@ -182,9 +182,9 @@ MI355FUSED_API unsigned long long gemm_xent_workspace(int type, int M, int N, in
  *     dX = d * W     dW = d^T * X
  *
  * computed in pieces of the columns: each piece's d goes to the workspace,
- * rounded to the type after a common factor that brings the largest |dloss| to
- * 1 (bf16) or 2^14 (fp16, so that small probabilities do not underflow); the
- * gradients' fp32 sums are divided by it.
+ * rounded to the type after a common factor that brings the largest finite
+ * |dloss| to 1 (bf16) or 2^14 (fp16, so that small probabilities do not
+ * underflow); the gradients' fp32 sums are divided by it.
  * The sums over N (in fp32 across the pieces) and M are fp32.
  *
  *   lse     : float [M], as gemm_xent stored it   (read)

@@ -783,6 +783,25 @@ def test_xent_bwd_one_dloss_for_all(typ):
         norm_close(got, ref, 1.2 * half / 3 ** 0.5, "one dloss")
 
 
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_xent_bwd_infinite_dloss(value, typ):
+    """A dloss that is no number takes its row of dX (and dW) with it; the other
+    rows of dX keep their bits, also where fp16 needs the common factor."""
+    M, N, K, dt = 150, 2000, 136, DT[typ]
+    X, W, t = xent_inputs(M, N, K, dt, 18, sd=1.0)
+    t[40] = 7
+    loss, lse = torch.empty((M,), device=DEV), torch.empty((M,), device=DEV)
+    dg.gemm_xent(X, W, t, loss, lse)
+    dloss = torch.full((M,), 1e-3, device=DEV)
+    base, dX = torch.empty_like(X), torch.empty_like(X)
+    dg.gemm_xent_bwd(X, W, t, lse, dloss, dX=base)
+    dloss[40] = value
+    dg.gemm_xent_bwd(X, W, t, lse, dloss, dX=dX)
+    rest = torch.arange(M, device=DEV) != 40
+    assert not bool(torch.isfinite(dX[40]).any()) and torch.equal(dX[rest], base[rest])
+
+
 # ---------------------------------------------------------------- how they are called
 
 def test_run_together():
