@@ -22,6 +22,11 @@ the work around them folded in:
     gemm_w4                                  # 4-bit weights with group scales
     gemm_xent / gemm_xent_bwd                # cross entropy over X@W.T, gradients
 
+and, from ``include/mi355tune.h`` (module ``tune``), what fine tuning needs
+next to them:
+
+    gemm_ortho                               # an update orthogonalised
+
 The library allocates no memory.  Where a call's kernels need scratch memory
 (split-K partial sums, gemm_ex's transposed copies and matrix-vector partial
 sums) the caller may pass a ``workspace`` tensor; if it does not, this module
@@ -439,3 +444,4 @@ def ex_path(A, B, C, op_a: str = "n", op_b: str = "t", bias=None, act: str = "no
 from .fused import (gated_bwd_workspace_bytes, gated_workspace_bytes, gemm_gated,  # noqa: E402,F401
                     gemm_gated_bwd, gemm_w4, gemm_xent, gemm_xent_bwd, xent_bwd_workspace_bytes,
                     xent_workspace_bytes)
+from .tune import gemm_ortho, ortho_workspace_bytes  # noqa: E402,F401

@@ -1,5 +1,6 @@
-"""Builds ``libmi355gemm.so`` and ``libmi355fused.so`` (the C-ABI libraries)
-from ``csrc/`` and ``csrc/fused/`` with hipcc for gfx950.
+"""Builds ``libmi355gemm.so``, ``libmi355fused.so`` and ``libmi355tune.so`` (the
+C-ABI libraries) from ``csrc/``, ``csrc/fused/`` and ``csrc/tune/`` with hipcc
+for gfx950.
 
 Usage: ``python -m dense_gemm_sgemm_amd.build`` or ``build()`` from Python.
 Each ``.hip`` file is compiled to an object in ``_build/`` (in parallel), then
@@ -22,6 +23,8 @@ LIB_NAME = "libmi355gemm.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 FUSED_CSRC = os.path.join(CSRC, "fused")
 FUSED_LIB_PATH = os.path.join(HERE, "libmi355fused.so")
+TUNE_CSRC = os.path.join(CSRC, "tune")
+TUNE_LIB_PATH = os.path.join(HERE, "libmi355tune.so")
 ARCH = "gfx950"
 
 # Packed fp32 VALU instructions are kept out of the generated code on purpose;
@@ -52,6 +55,7 @@ FILE_FLAGS = {
     "tiles_gated.hip": ["-mllvm", "--amdgpu-sched-strategy=iterative-minreg"],
     "tiles_logits.hip": ["-mllvm", "--amdgpu-sched-strategy=iterative-minreg"],
     "tiles_grad.hip": ["-mllvm", "--amdgpu-sched-strategy=iterative-minreg"],
+    "tiles_ortho.hip": ["-mllvm", "--amdgpu-sched-strategy=iterative-minreg"],
 }
 
 
@@ -82,11 +86,13 @@ def build(extra_flags: list[str] | None = None, jobs: int | None = None) -> str:
     """Compile every kernel source for gfx950 and link the shared libraries."""
     extra = list(extra_flags or [])
     os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs, fused = sources(), sources(FUSED_CSRC)
-    with ThreadPoolExecutor(max_workers=jobs or min(8, len(srcs) + len(fused))) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra), srcs + fused))
-    _link(objs[:len(srcs)], LIB_PATH)
-    _link(objs[len(srcs):], FUSED_LIB_PATH)
+    srcs, fused, tune = sources(), sources(FUSED_CSRC), sources(TUNE_CSRC)
+    every = srcs + fused + tune
+    with ThreadPoolExecutor(max_workers=jobs or min(8, len(every))) as ex:
+        objs = dict(zip(every, ex.map(lambda s: _compile(s, extra), every)))
+    _link([objs[s] for s in srcs], LIB_PATH)
+    _link([objs[s] for s in fused], FUSED_LIB_PATH)
+    _link([objs[s] for s in tune], TUNE_LIB_PATH)
     return LIB_PATH
 
 

@@ -202,7 +202,13 @@ struct TileArgs {
 //             x.per (the last may be shorter), each a work item of its own
 //             that leaves fp32 sums in x.sum, or adds to those of an earlier
 //             launch.
-enum TileMode { kProduct = 0, kGated, kLse, kDlogit, kGradW, kGradX };
+//   kSym, kMul  the products of an orthogonalised update (tune/ortho.hip), for a
+//             batch of matrices of one size, K in up to three parts with
+//             operands of their own (OrthoExtra).  kSym is symmetric: only
+//             tiles on and below the diagonal are computed, and stored on both
+//             sides of it.
+enum TileMode { kProduct = 0, kGated, kLse, kDlogit, kGradW, kGradX, kSym, kMul };
+constexpr bool is_ortho(int mode) { return mode == kSym || mode == kMul; }
 
 // What these modes need beside the product's arguments.  Operands may be
 // padded past the operator's own sizes: results count for rows m < m_end and
@@ -242,8 +248,40 @@ struct FusedTileArgs {
   int64_t tiles;
   FusedExtra x;
 };
+// kSym and kMul: M, N and K are whole slabs (K of a part; at least two in all),
+// rows start at 16-byte addresses.  Matrices may be held in two 16-bit values
+// an element, hi + lo: products of parts add up the ones that matter.
+//   kSym   hi (, lo) = alpha * acc + beta * q + gamma * [m == n], times the
+//          matrix's own factors coef[3 * matrix .. + 2] if there are any
+//   kMul   v = alpha * acc: to hi (, lo), or rounded to `out`, whose matrices
+//          are m_end x n_end
+struct OrthoExtra {
+  int parts = 1;
+  uint32_t tiles_each = 0;              // tiles of a matrix
+  const half_t* a[3] = {};              // operands of the parts
+  const half_t* b[3] = {};
+  int64_t stride_a = 0, stride_b = 0;   // between matrices
+  half_t* hi = nullptr;
+  half_t* lo = nullptr;                 // or null
+  int64_t stride_c = 0;                 // (rows p.ldc apart)
+  const half_t* q_hi = nullptr;         // laid out as hi
+  const half_t* q_lo = nullptr;
+  float alpha = 1.f, beta = 0.f, gamma = 0.f;
+  const float* coef = nullptr;
+  void* out = nullptr;
+  int out_type = 0;                     // GEMM_TYPE_F16, GEMM_TYPE_BF16 or -1 for fp32
+  int64_t ldo = 0, stride_o = 0;
+  int m_end = 0, n_end = 0;
+};
+struct OrthoTileArgs {
+  Args16 p;
+  int64_t tiles;
+  OrthoExtra x;
+};
 template <int MODE>
-using TileArgsOf = std::conditional_t<MODE == kProduct, TileArgs, FusedTileArgs>;
+using TileArgsOf = std::conditional_t<MODE == kProduct, TileArgs,
+                                      std::conditional_t<is_ortho(MODE), OrthoTileArgs,
+                                                         FusedTileArgs>>;
 
 // Waves of the kernel that share each SIMD: 8-wave workgroups put two on
 // each; 4-wave 128 x 128 tiles run two workgroups per CU (the launcher's
@@ -301,6 +339,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   static_assert((MODE != kLse && MODE != kDlogit) || LAY == 0, "logits from A * B^T");
   static_assert((MODE != kGradW || LAY == 2) && (MODE != kGradX || LAY == 1),
                 "gradients from K-major operands");
+  static_assert(MODE != kSym || (LAY == 0 && BM == BN), "a matrix times its transpose");
   constexpr int kTileN = MODE == kGated ? BN / 2 : BN;   // output columns of a tile
   typedef Config<BM, BN, BK, WAVES_M, WAVES_N, COPY_SEL> C;
   constexpr bool kAT = LAY == 2 || LAY == 3, kBT = LAY == 1 || LAY == 3;   // stored K-major
@@ -364,8 +403,19 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     }
     kb = sp * (SPLIT ? p.sk.per : 0);
     if constexpr (MODE == kGradX) kb = sp * ta.x.per;
+    if constexpr (is_ortho(MODE)) {
+      sp = (int)((uint32_t)item / ta.x.tiles_each);   // the matrix
+      item -= (uint32_t)sp * ta.x.tiles_each;
+    }
     int tm, tn;
-    if constexpr (MODE == kProduct)
+    if constexpr (MODE == kSym) {
+      // tile i of the lower half, row by row: row tm starts at tm (tm + 1) / 2
+      const int i = (int)item;
+      tm = (int)((__builtin_amdgcn_sqrtf(8.f * (float)i + 1.f) - 1.f) * 0.5f);
+      while (tm * (tm + 1) / 2 > i) --tm;
+      while ((tm + 1) * (tm + 2) / 2 <= i) ++tm;
+      tn = i - tm * (tm + 1) / 2;
+    } else if constexpr (MODE == kProduct)
       map_tile<GM>(item, tiles_m, tiles_n, tm, tn);
     else
       tile_at32<GM>((uint32_t)item, tiles_m, tiles_n, tm, tn);
@@ -486,6 +536,21 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       cb.sa = (int64_t)C::kCopyWaves * C::kRowsPerCopy * lda * 2;
       cb.b = (const char*)((h ? ta.x.B2 : p.B) + k0 * p.ldb + n0) + firstTB;
       cb.oa = tail ? offA_x : offA;
+      cb.ob = offB;
+      return cb;
+    }
+    if constexpr (is_ortho(MODE)) {
+      const OrthoExtra& x = ta.x;
+      const int per = p.K / BK;
+      const int h = t < per ? 0 : t < 2 * per ? 1 : 2;
+      const int64_t k0 = (int64_t)(t - h * per) * BK;
+      const half_t* a = (h == 0 ? x.a[0] : h == 1 ? x.a[1] : x.a[2]) + part * x.stride_a;
+      const half_t* b = (h == 0 ? x.b[0] : h == 1 ? x.b[1] : x.b[2]) + part * x.stride_b;
+      cb.a = kAT ? (const char*)(a + k0 * p.lda + m0) + firstTA
+                 : (const char*)(a + (int64_t)m0 * p.lda) + firstA + 2 * k0;
+      cb.b = kBT ? (const char*)(b + k0 * p.ldb + n0) + firstTB
+                 : (const char*)(b + (int64_t)n0 * p.ldb) + firstB + 2 * k0;
+      cb.oa = offA;
       cb.ob = offB;
       return cb;
     }
@@ -1016,6 +1081,120 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
           flush(p.C, p.ldc, m0 + wm + 16 * i, n0 + wn, C::WN, mlo, x.m_end, nlo, x.n_end);
         }
       }
+    } else if constexpr (MODE == kSym) {
+      const OrthoExtra& x = ta.x;
+      float alpha = x.alpha, beta = x.beta, gamma = x.gamma;
+      if (x.coef) {
+        alpha *= x.coef[3 * part];
+        beta *= x.coef[3 * part + 1];
+        gamma *= x.coef[3 * part + 2];
+      }
+      const int64_t at = part * x.stride_c;
+#pragma unroll
+      for (int i = 0; i < C::kBlocksM; ++i) {
+        const int m = m0 + wm + 16 * i + r;
+#pragma unroll
+        for (int j = 0; j < C::kBlocksN; ++j) {
+          const int n = n0 + wn + 16 * j + 4 * g;
+          f4 v = acc[i][j] * alpha;
+          if (x.q_hi) {
+            const int64_t q = at + (int64_t)m * p.ldc + n;
+            h4 qh = *(const h4*)(x.q_hi + q), ql = {};
+            if (x.q_lo) ql = *(const h4*)(x.q_lo + q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              v[e] += beta * ((float)qh[e] + (float)ql[e]);
+              if (m == n + e) v[e] += gamma;
+            }
+          }
+          acc[i][j] = v;
+        }
+        asm volatile("" ::: "memory");   // (q of a row block at a time: registers)
+      }
+      // hi, then lo; on both sides of the diagonal, the other one with the
+      // block's rows and columns exchanged in the staging area: 16 of its rows
+      // (16 columns here) by the wave's rows
+      for (int half = 0; half < (x.lo ? 2 : 1); ++half) {
+        half_t* dst = (half ? x.lo : x.hi) + at;
+        auto value = [&](f4 v) __attribute__((always_inline)) {
+          const h4 o = round4(v);
+          if (!half) return o;
+          f4 d;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[e] = v[e] - (float)o[e];
+          return round4(d);
+        };
+#pragma unroll
+        for (int i = 0; i < C::kBlocksM; ++i) {
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j) put(j, value(acc[i][j]));
+          flush(dst, p.ldc, m0 + wm + 16 * i, n0 + wn, C::WN, mlo, p.M, nlo, p.N);
+        }
+        if (mlo != nlo) {
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j) {
+#pragma unroll
+            for (int i = 0; i < C::kBlocksM; ++i) {
+              const h4 o = value(acc[i][j]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int R = 4 * g + e, c = 2 * i + (r >> 3);
+                *(half_t*)(stage_out + R * C::kOutRowBytes + 16 * (c ^ R) + 2 * (r & 7)) = o[e];
+              }
+            }
+            flush(dst, p.ldc, n0 + wn + 16 * j, m0 + wm, C::WM, nlo, p.N, mlo, p.M);
+          }
+        }
+      }
+    } else if constexpr (MODE == kMul) {
+      const OrthoExtra& x = ta.x;
+#pragma unroll
+      for (int i = 0; i < C::kBlocksM; ++i) {
+        const int m = m0 + wm + 16 * i;
+#pragma unroll
+        for (int j = 0; j < C::kBlocksN; ++j) acc[i][j] *= x.alpha;
+        if (x.hi) {
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j) put(j, round4(acc[i][j]));
+          flush(x.hi + part * x.stride_c, p.ldc, m, n0 + wn, C::WN, mlo, p.M, nlo, p.N);
+          if (x.lo) {
+#pragma unroll
+            for (int j = 0; j < C::kBlocksN; ++j) {
+              const h4 o = round4(acc[i][j]);
+              f4 d;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) d[e] = acc[i][j][e] - (float)o[e];
+              put(j, round4(d));
+            }
+            flush(x.lo + part * x.stride_c, p.ldc, m, n0 + wn, C::WN, mlo, p.M, nlo, p.N);
+          }
+        } else if (x.out_type >= 0) {
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j) {
+            h4 o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o[e] = x.out_type == GEMM_TYPE_BF16 ? f32_to_word<kFmtBF16>(acc[i][j][e])
+                                                  : f32_to_word<kFmtF16>(acc[i][j][e]);
+            put(j, o);
+          }
+          flush((half_t*)x.out + part * x.stride_o, x.ldo, m, n0 + wn, C::WN, mlo, x.m_end, nlo,
+                x.n_end);
+        } else if (m + r >= mlo && m + r < x.m_end) {
+          float* dst = (float*)x.out + part * x.stride_o + (int64_t)(m + r) * x.ldo;
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j) {
+            const int n = n0 + wn + 16 * j + 4 * g;
+            if (n >= nlo && n + 4 <= x.n_end) {
+              __builtin_memcpy(dst + n, &acc[i][j], 16);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if (n + e >= nlo && n + e < x.n_end) dst[n + e] = acc[i][j][e];
+            }
+          }
+        }
+      }
     }
     (void)part;
   };
@@ -1057,7 +1236,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   constexpr int kReadInstr = kReads + (kAT ? C::kBlocksM : 0) + (kBT ? C::kBlocksN : 0);
   constexpr int kCopies = kPerWaveA + kPerWaveB;
   static_assert(kReadInstr <= kMfma && kCopies <= kMfma, "interleave pattern");
-  const int nk = SPLIT ? p.sk.per : RAG ? (p.K + BK - 1) / BK : p.K / BK;   // slabs per work item
+  int nk = SPLIT ? p.sk.per : RAG ? (p.K + BK - 1) / BK : p.K / BK;   // slabs per work item
+  if constexpr (is_ortho(MODE)) nk *= ta.x.parts;
   // The copy target runs two slabs ahead of the compute: slab tc of the tile
   // `ahead` tiles after the current one (origins o[0..2] are refreshed once
   // per tile, outside the MFMA loop).  Past the end of the stream it stays on
@@ -1136,7 +1316,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       const int t = kb + (past ? slabs_of(d) - 1 : tc);
       return slab_base(stage, m0, n0, t, kv < BK && (t == nk_part - 1 || t == nk_all - 1), 0);
     } else {
-      const int part = MODE == kGradW ? (d == 0 ? os[0] : d == 1 ? os[1] : os[2]) : 0;
+      const int part = MODE == kGradW || is_ortho(MODE) ? (d == 0 ? os[0] : d == 1 ? os[1] : os[2]) : 0;
       const int t = past ? nk - 1 : tc;
       return slab_base(stage, m0, n0, kb + t, RAG && kv < BK && t == nk - 1, part);
     }
@@ -1340,6 +1520,27 @@ hipError_t launch_fused(const Args16& a, const FusedExtra& x, int slots, hipStre
   void* args[] = {&ta};
   return hipLaunchKernel((const void*)hgemm_nt_kernel<BM, BN, BK, WAVES_M, WAVES_N, GM, COPY_SEL,
                                                       OPT, false, FMT, false, true, LAY, MODE>,
+                         dim3((unsigned)grid), dim3(C::kThreads), args, 0, stream);
+}
+
+// kSym and kMul over `batch` matrices.
+template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int GM, int COPY_SEL, int OPT, int LAY,
+          int MODE>
+hipError_t launch_ortho(const Args16& a, const OrthoExtra& x, int batch, int slots,
+                        hipStream_t stream) {
+  typedef Config<BM, BN, BK, WAVES_M, WAVES_N, COPY_SEL> C;
+  const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
+  const int64_t each = MODE == kSym ? tm * (tm + 1) / 2 : tm * tn;
+  const int64_t tiles = each * batch;
+  // (xcd_order32; the rows of kSym are found in fp32 within one of the place)
+  if (tiles >= (int64_t(1) << 31) || each >= (int64_t(1) << 24)) return hipErrorInvalidValue;
+  int64_t grid = tiles < slots ? tiles : slots;
+  if (grid < 1) grid = 1;
+  OrthoTileArgs ta{a, tiles, x};
+  ta.x.tiles_each = (uint32_t)each;
+  void* args[] = {&ta};
+  return hipLaunchKernel((const void*)hgemm_nt_kernel<BM, BN, BK, WAVES_M, WAVES_N, GM, COPY_SEL,
+                                                      OPT, false, kFmtF16, false, true, LAY, MODE>,
                          dim3((unsigned)grid), dim3(C::kThreads), args, 0, stream);
 }
 

@@ -1,0 +1,91 @@
+/*
+ * mi355tune -- what fine tuning needs next to a model's products: low-rank
+ * adapters beside a shared projection, their gradients, and updates
+ * orthogonalised by Newton-Schulz products, for AMD Instinct MI355X (gfx950).
+ *
+ * Public C ABI of libmi355tune.so, beside mi355gemm.h and mi355fused.h and with
+ * their conventions: row-major matrices with int leading dimensions and 64-bit
+ * offsets, device pointers owned by the caller, no allocation, work enqueued
+ * on `stream` (a hipStream_t, NULL for the default one) without
+ * synchronising, misaligned pointers and leading dimensions never an error,
+ * thread-safe calls, GEMM_OK or a GEMM_ERR_* code returned (gemm_status_string
+ * of mi355gemm.h names them), nothing enqueued on an error.
+ *
+ * Sums are in fp32 or more; an output is rounded once (nearest, ties to even).
+ * Results repeat bit for bit: there are no atomics.  No output may overlap an
+ * input or another output, except where a call says so.
+ *
+ * Workspaces: a call that takes one needs at least the bytes its size query
+ * reports for the same arguments, at a 16-byte aligned device address, or NULL
+ * when that is 0.  Its kernels write and read it on `stream`, so it must not be
+ * in use by other work until they finish: calls that overlap in time, replays
+ * of two captured graphs among them, need workspaces of their own.  What it
+ * held before does not matter.
+ */
+#ifndef MI355TUNE_H
+#define MI355TUNE_H
+
+#include "mi355gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#if defined(MI355TUNE_BUILDING)
+#define MI355TUNE_API __attribute__((visibility("default")))
+#else
+#define MI355TUNE_API
+#endif
+
+/* Beside GEMM_TYPE_F16 and GEMM_TYPE_BF16, for gemm_ortho only. */
+enum { GEMM_TYPE_F32 = 2 };
+
+/*
+ * An update orthogonalised by Newton-Schulz products, as the Muon optimiser
+ * does, for L matrices of m x n:
+ *
+ *     X = G / (|G| + eps)                       (|G|: Frobenius norm)
+ *     X = a_k X + b_k (X X^T) X + c_k (X X^T)^2 X     for k = 0 .. steps - 1
+ *     O = X
+ *
+ *   G       : [L][m][ldg], type_g (F32, F16 or BF16), ldg >= max(1, n), matrices
+ *             stride_g elements apart                              (read)
+ *   coeffs  : 3 * steps floats a_0, b_0, c_0, a_1, ... in HOST memory, read
+ *             during the call
+ *   O       : [L][m][ldo], type_o (F32, F16 or BF16), matrices stride_o elements
+ *             apart, which must not overlap                        (written)
+ *
+ * m and n may be in either order: the products are taken over the longer side.
+ * A G of zeros gives zeros, one with an infinity or NaN gives NaN throughout;
+ * neither touches the other matrices.
+ *
+ * Products are on the 16-bit matrix cores.  For BF16 outputs the iterates are
+ * binary16, the first three of them in two values (22 bits); for F16 and F32
+ * outputs everything is in two values, at three products for one.  The result
+ * differs from the formula's by about 0.12 % (BF16: beside the output's own
+ * rounding of 0.17 %) or 2^-19, in the 2-norm, for singular values of G that
+ * spread over a factor of a few hundred; what is smaller than that is kept less
+ * well, for F16 and F32 by 2^-11 of the factor.  The singular values of every X
+ * must stay below 7, as they do for coefficients that converge from [0, 1].
+ *
+ * steps is 1 .. 64; m, n and L go up to 2^16; others are GEMM_ERR_BAD_ARG, as is
+ * a negative or NaN eps.  L == 0, m == 0 or n == 0 is a no-op.
+ */
+MI355TUNE_API int gemm_ortho(int type_g, int type_o, int L, int m, int n,
+                             const void* G, int ldg, long long stride_g,
+                             int steps, const float* coeffs, float eps,
+                             void* O, int ldo, long long stride_o,
+                             void* workspace, unsigned long long workspace_bytes,
+                             void* stream);
+
+/* Workspace bytes of gemm_ortho: with s = min(m, n), t = max(m, n), each at least
+ * 128 and a multiple of 64, 4 to 8 bytes for each of L * s * t and of L * s * s,
+ * and the norms. */
+MI355TUNE_API unsigned long long gemm_ortho_workspace(int type_g, int type_o, int L, int m, int n,
+                                                      int steps);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MI355TUNE_H */
