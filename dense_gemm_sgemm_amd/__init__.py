@@ -25,6 +25,7 @@ the work around them folded in:
 and, from ``include/mi355tune.h`` (module ``tune``), what fine tuning needs
 next to them:
 
+    gemm_lora / gemm_lora_bwd                # adapters beside a projection, gradients
     gemm_ortho                               # an update orthogonalised
 
 The library allocates no memory.  Where a call's kernels need scratch memory
@@ -444,4 +445,5 @@ def ex_path(A, B, C, op_a: str = "n", op_b: str = "t", bias=None, act: str = "no
 from .fused import (gated_bwd_workspace_bytes, gated_workspace_bytes, gemm_gated,  # noqa: E402,F401
                     gemm_gated_bwd, gemm_w4, gemm_xent, gemm_xent_bwd, xent_bwd_workspace_bytes,
                     xent_workspace_bytes)
-from .tune import gemm_ortho, ortho_workspace_bytes  # noqa: E402,F401
+from .tune import (gemm_lora, gemm_lora_bwd, gemm_ortho, lora_bwd_workspace_bytes,  # noqa: E402,F401
+                   lora_workspace_bytes, ortho_workspace_bytes)

@@ -92,7 +92,7 @@ def build(extra_flags: list[str] | None = None, jobs: int | None = None) -> str:
         objs = dict(zip(every, ex.map(lambda s: _compile(s, extra), every)))
     _link([objs[s] for s in srcs], LIB_PATH)
     _link([objs[s] for s in fused], FUSED_LIB_PATH)
-    _link([objs[s] for s in tune], TUNE_LIB_PATH)
+    _link([objs[s] for s in tune + [os.path.join(FUSED_CSRC, "pad.hip")]], TUNE_LIB_PATH)
     return LIB_PATH
 
 

@@ -76,6 +76,33 @@ __device__ __forceinline__ f4 mfma16(h8 a, h8 b, f4 c) {
                                                    __builtin_bit_cast(b8, b), c, 0, 0, 0);
   }
 }
+// A product whose one operand is held in two values, hi + lo: in one
+// instruction of half the k (hi holds hi in its first 16 k, lo in the others;
+// the other operand the same 16 twice), or `two`.  SECOND: hi and lo are the
+// instruction's second operand.  An infinity in `b` meets hi alone: lo's sign
+// need not be hi's, and their sum would be NaN.
+template <int FMT, bool SECOND>
+__device__ __forceinline__ f4 mfma_split(h8 hi, h8 lo, h8 b, bool two, int lane) {
+  auto mul = [](h8 t, h8 u, f4 c) __attribute__((always_inline)) {
+    return SECOND ? mfma16<FMT>(u, t, c) : mfma16<FMT>(t, u, c);
+  };
+  const f4 h = mul(hi, b, f4{0.f, 0.f, 0.f, 0.f});
+  f4 s = h;
+  if (two) s = mul(lo, b, h);
+  bool fine = true;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) fine = fine && __builtin_fabsf(s[v]) < __builtin_inff();
+  if (__ballot(!fine)) {
+    f4 first = h;
+    if (!two) {
+      const bool low = (lane & 32) == 0;
+      first = mul(low ? hi : h8{}, low ? b : h8{}, f4{0.f, 0.f, 0.f, 0.f});
+    }
+#pragma unroll
+    for (int v = 0; v < 4; ++v) s[v] = __builtin_fabsf(s[v]) < __builtin_inff() ? s[v] : first[v];
+  }
+  return s;
+}
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(1))) const void gbl_void_t;
 
@@ -207,7 +234,10 @@ struct TileArgs {
 //             operands of their own (OrthoExtra).  kSym is symmetric: only
 //             tiles on and below the diagonal are computed, and stored on both
 //             sides of it.
-enum TileMode { kProduct = 0, kGated, kLse, kDlogit, kGradW, kGradX, kSym, kMul };
+//   kLora     C = act(acc + the row's adapter + bias) + residual: the adapter's
+//             part is a product of few k, made from memory at the tile's end
+//             (LoraExtra).
+enum TileMode { kProduct = 0, kGated, kLse, kDlogit, kGradW, kGradX, kSym, kMul, kLora };
 constexpr bool is_ortho(int mode) { return mode == kSym || mode == kMul; }
 
 // What these modes need beside the product's arguments.  Operands may be
@@ -278,10 +308,30 @@ struct OrthoTileArgs {
   int64_t tiles;
   OrthoExtra x;
 };
+// kLora.  Row m < m_end adds sum_k factor[m][k] (t2[m] block k) . B_a[n], with
+// a = ids[m], where 0 <= a < S; a >= S makes the row NaN, a < 0 adds nothing.
+// A block is w ranks: 16, as 16 values of t2 and 16 more against the same 16
+// of B in one product, or 32, in two products (t2's values are hi + lo).
+struct LoraExtra {
+  const half_t* t2 = nullptr;      // [m_end][ld2]
+  int64_t ld2 = 0;
+  const float* factor = nullptr;   // [m_end][blocks]
+  const half_t* B = nullptr;       // [S][n_end][ldb], R columns
+  int64_t ldb = 0, stride_b = 0;
+  const long long* ids = nullptr;
+  int R = 0, S = 0, w = 0, blocks = 0;
+  int m_end = 0, n_end = 0;
+};
+struct LoraTileArgs {
+  Args16 p;
+  int64_t tiles;
+  LoraExtra x;
+};
 template <int MODE>
-using TileArgsOf = std::conditional_t<MODE == kProduct, TileArgs,
-                                      std::conditional_t<is_ortho(MODE), OrthoTileArgs,
-                                                         FusedTileArgs>>;
+using TileArgsOf = std::conditional_t<
+    MODE == kProduct, TileArgs,
+    std::conditional_t<is_ortho(MODE), OrthoTileArgs,
+                       std::conditional_t<MODE == kLora, LoraTileArgs, FusedTileArgs>>>;
 
 // Waves of the kernel that share each SIMD: 8-wave workgroups put two on
 // each; 4-wave 128 x 128 tiles run two workgroups per CU (the launcher's
@@ -339,6 +389,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   static_assert((MODE != kLse && MODE != kDlogit) || LAY == 0, "logits from A * B^T");
   static_assert((MODE != kGradW || LAY == 2) && (MODE != kGradX || LAY == 1),
                 "gradients from K-major operands");
+  static_assert(MODE != kLora || LAY <= 1, "B as it lies, or K-major");
   static_assert(MODE != kSym || (LAY == 0 && BM == BN), "a matrix times its transpose");
   constexpr int kTileN = MODE == kGated ? BN / 2 : BN;   // output columns of a tile
   typedef Config<BM, BN, BK, WAVES_M, WAVES_N, COPY_SEL> C;
@@ -1195,6 +1246,91 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
           }
         }
       }
+    } else if constexpr (MODE == kLora) {
+      const LoraExtra& x = ta.x;
+      // lane l stands for row l of the wave's
+      const int ml = m0 + wm + lane;
+      int mine = -1;
+      if (lane < C::WM && ml < x.m_end) {
+        const long long id = x.ids[ml];
+        mine = id < 0 ? -1 : id >= x.S ? -2 : (int)id;
+      }
+      const uint64_t unknown = __ballot(mine == -2);
+      uint64_t pending = __ballot(mine >= 0);
+      while (pending) {
+        const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(pending));
+        const uint64_t rows = __ballot(mine == a);
+        pending &= ~rows;
+        const half_t* b = x.B + a * x.stride_b;
+        for (int k = 0; k < x.blocks; ++k) {
+          h8 hi[C::kBlocksM], lo[C::kBlocksM];
+          float f[C::kBlocksM];
+#pragma unroll
+          for (int i = 0; i < C::kBlocksM; ++i) {
+            // (rows of other adapters, and past the end: any values, times 0)
+            const int m = m0 + wm + 16 * i + r, mc = m < x.m_end ? m : x.m_end - 1;
+            const half_t* t2 = x.t2 + (int64_t)mc * x.ld2 + 2 * x.w * k;
+            hi[i] = *(const h8*)(t2 + 8 * g);
+            lo[i] = x.w == 32 ? *(const h8*)(t2 + 32 + 8 * g) : h8{};
+            f[i] = x.factor[(int64_t)mc * x.blocks + k];
+          }
+          const int at = x.w == 16 ? 8 * (g & 1) : 32 * k + 8 * g;
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j) {
+            const int n = n0 + wn + 16 * j + r;
+            const half_t* row = b + (int64_t)(n < x.n_end ? n : x.n_end - 1) * x.ldb;
+            h8 bv = {};
+            if (at + 8 <= x.R) {
+              __builtin_memcpy(&bv, row + at, 16);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (at + e < x.R) bv[e] = row[at + e];
+            }
+#pragma unroll
+            for (int i = 0; i < C::kBlocksM; ++i) {
+              if (!(rows >> (16 * i) & 0xFFFF)) continue;
+              const f4 s = mfma_split<FMT, true>(hi[i], lo[i], bv, x.w == 32, lane);
+              const bool own = rows >> (16 * i + r) & 1;
+#pragma unroll
+              for (int v = 0; v < 4; ++v) acc[i][j][v] += own ? f[i] * s[v] : 0.f;
+            }
+          }
+        }
+      }
+      h4 bq[C::kBlocksN];
+#pragma unroll
+      for (int j = 0; j < C::kBlocksN; ++j) {
+        bq[j] = h4{};
+        const int n = n0 + wn + 16 * j + 4 * g;
+        if (p.bias) {
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (n + v < x.n_end) bq[j][v] = p.bias[n + v];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < C::kBlocksM; ++i) {
+        const int m = m0 + wm + 16 * i + r;
+        const bool nan = unknown >> (16 * i + r) & 1;
+#pragma unroll
+        for (int j = 0; j < C::kBlocksN; ++j) {
+          const int n = n0 + wn + 16 * j + 4 * g;
+          f4 z = acc[i][j];
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            z[v] = gate_act((nan ? __builtin_nanf("") : z[v]) + word_to_f32<FMT>(bq[j][v]), p.act);
+          if (p.res && m >= mlo && m < x.m_end) {
+            // (rows and columns of another tile are left to it: the residual may be C)
+            const half_t* q = p.res + (int64_t)m * p.ldr + n;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (n + v >= nlo && n + v < x.n_end) z[v] += word_to_f32<FMT>(q[v]);
+          }
+          put(j, round4(z));
+        }
+        flush(p.C, p.ldc, m0 + wm + 16 * i, n0 + wn, C::WN, mlo, x.m_end, nlo, x.n_end);
+      }
     }
     (void)part;
   };
@@ -1542,6 +1678,21 @@ hipError_t launch_ortho(const Args16& a, const OrthoExtra& x, int batch, int slo
   return hipLaunchKernel((const void*)hgemm_nt_kernel<BM, BN, BK, WAVES_M, WAVES_N, GM, COPY_SEL,
                                                       OPT, false, kFmtF16, false, true, LAY, MODE>,
                          dim3((unsigned)grid), dim3(C::kThreads), args, 0, stream);
+}
+
+template <int BM, int BN, int BK, int WAVES_M, int WAVES_N, int GM, int COPY_SEL, int OPT, int FMT,
+          int LAY>
+hipError_t launch_lora(const Args16& a, const LoraExtra& x, int slots, hipStream_t stream) {
+  typedef Config<BM, BN, BK, WAVES_M, WAVES_N, COPY_SEL> C;
+  static_assert(C::WM <= 64, "a lane for each of a wave's rows");
+  const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
+  if (tiles >= (int64_t(1) << 31)) return hipErrorInvalidValue;   // xcd_order32
+  LoraTileArgs ta{a, tiles, x};
+  void* args[] = {&ta};
+  return hipLaunchKernel((const void*)hgemm_nt_kernel<BM, BN, BK, WAVES_M, WAVES_N, GM, COPY_SEL,
+                                                      OPT, false, FMT, false, true, LAY, kLora>,
+                         dim3((unsigned)(tiles < slots ? tiles : slots)), dim3(C::kThreads), args,
+                         0, stream);
 }
 
 // Leading dimensions must also keep a lane's 32-bit copy offset (up to 8 rows

@@ -1,0 +1,157 @@
+// A product with adapters for few rows of X (decode steps): W streamed from HBM
+// once for 64 rows, bound by that (skinny.hpp has the layout).  The adapters'
+// second product comes before the waves' sums are added: each wave takes every
+// so many of the adapters that the rows name, multiplies t (tune.hpp) with 16 of
+// the adapter's rows of B and keeps the sums of the rows that are its own.
+#include "fused/skinny.hpp"
+#include "tune.hpp"
+
+namespace mi355gemm {
+namespace tune {
+namespace {
+
+using namespace fused::skinny;
+
+constexpr int kSteps = 4, kChunk = 32 * kSteps, kMaxWaves = 8;
+
+struct RowsArgs {
+  Args16 p;
+  LoraExtra x;
+  int waves;
+};
+
+template <int FMT, int MT>
+__global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args, int64_t base) {
+  constexpr int kS = MT == 4 ? 2 : kSteps, kC = 32 * kS;
+  typedef XStage<MT, kC> Stage;
+  __shared__ __attribute__((aligned(16))) unsigned char
+      lds[kMaxWaves * (Stage::kBytes > MT * 1024 ? Stage::kBytes : MT * 1024)];
+  const Args16& p = args.p;
+  const LoraExtra& y = args.x;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, quarter = lane >> 4;
+  const int64_t id = base + blockIdx.x, groups_n = (p.N + 15) / 16;
+  const int m0 = (int)(id / groups_n) * 64;
+  const int n = (int)(id % groups_n) * 16 + r;
+  const int row = n < p.N ? n : p.N - 1;   // rows past N repeat the last one, unstored
+  const half_t* w = p.B + row * p.ldb + 8 * quarter;
+  f4 acc[MT];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
+
+  // (the pointer and K both moved on by the lane's 8 quarter)
+  const int K = p.K - 8 * quarter, chunks = p.K / kC;
+  h8 cur[kS], nxt[kS], xf[MT][kS];
+  Stage stage;
+  unsigned char* buf = lds + wave * Stage::kBytes;
+  auto load_w = [&](int k, auto tail, h8 (&v)[kS]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < kS; ++s) v[s] = load_x<decltype(tail)::value>(w, k + 32 * s, K);
+  };
+  auto read_x = [&]() __attribute__((always_inline)) {
+    stage.store(buf, lane, [](h8 v) { return v; });
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int s = 0; s < kS; ++s) xf[t][s] = Stage::read(buf, t, r, 32 * s + 8 * quarter);
+  };
+  auto multiply = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int s = 0; s < kS; ++s)
+#pragma unroll
+      for (int t = 0; t < MT; ++t) acc[t] = mfma16<FMT>(xf[t][s], cur[s], acc[t]);
+  };
+  int c = wave;
+  if (c < chunks) {
+    stage.template load<false>(p.A, p.lda, m0, p.M, c * kC, p.K, lane);
+    load_w(c * kC, std::false_type(), cur);
+  }
+  for (; c < chunks; c += args.waves) {
+    read_x();
+    if (c + args.waves < chunks) {
+      stage.template load<false>(p.A, p.lda, m0, p.M, (c + args.waves) * kC, p.K, lane);
+      load_w((c + args.waves) * kC, std::false_type(), nxt);
+    }
+    multiply();
+#pragma unroll
+    for (int s = 0; s < kS; ++s) cur[s] = nxt[s];
+  }
+  if (chunks * kC < p.K && wave == chunks % args.waves) {
+    stage.template load<true>(p.A, p.lda, m0, p.M, chunks * kC, p.K, lane);
+    load_w(chunks * kC, std::true_type(), cur);
+    read_x();
+    multiply();
+  }
+
+  // The adapters: lane l stands for row m0 + l.
+  const int mine = m0 + lane < p.M ? adapter_of(y.ids, m0 + lane, y.S) : -1;
+  uint64_t pending = __ballot(mine >= 0);
+  for (int d = 0; pending; ++d) {
+    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(pending));
+    const uint64_t rows = __ballot(mine == a);
+    pending &= ~rows;
+    if (d % args.waves != wave) continue;
+    const half_t* b = y.B + a * y.stride_b + (int64_t)row * y.ldb;
+    for (int k = 0; k < y.blocks; ++k) {
+      const int at = y.w == 16 ? 8 * (quarter & 1) : 32 * k + 8 * quarter;
+      const h8 bv = load_x<true>(b, at, y.R);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        if (!(rows >> (16 * t) & 0xFFFF)) continue;
+        const int m = m0 + 16 * t + r;
+        const half_t* t2 = y.t2 + (int64_t)(m < p.M ? m : p.M - 1) * y.ld2 + 2 * y.w * k;
+        const h8 hi = *(const h8*)(t2 + 8 * quarter);
+        const h8 lo = y.w == 32 ? *(const h8*)(t2 + 32 + 8 * quarter) : h8{};
+        const f4 s = hgemm::mfma_split<FMT, false>(hi, lo, bv, y.w == 32, lane);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int i = 16 * t + 4 * quarter + v;
+          if (rows >> i & 1) acc[t][v] += y.factor[(int64_t)(m0 + i) * y.blocks + k] * s[v];
+        }
+      }
+    }
+  }
+
+  // (the sums take the place of X)
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  add_waves<MT>(acc, reinterpret_cast<float*>(lds), wave, lane, args.waves);
+  if (wave > 0) return;
+  const uint64_t unknown = __ballot(mine == -2);
+  if (n >= p.N) return;
+  const float bias = p.bias ? word_to_f32<FMT>(p.bias[n]) : 0.f;
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int i = 16 * t + 4 * quarter + v;
+      const int64_t m = m0 + i;
+      if (m >= p.M) continue;
+      float z = unknown >> i & 1 ? __builtin_nanf("") : acc[t][v];
+      z = gate_act(z + bias, p.act);
+      if (p.res) z += word_to_f32<FMT>(p.res[m * p.ldr + n]);
+      p.C[m * p.ldc + n] = f32_to_word<FMT>(z);
+    }
+}
+
+template <int FMT>
+const void* pick(int M) {
+  return M <= 16   ? (const void*)lora_rows_kernel<FMT, 1>
+         : M <= 32 ? (const void*)lora_rows_kernel<FMT, 2>
+                   : (const void*)lora_rows_kernel<FMT, 4>;
+}
+
+}  // namespace
+
+hipError_t launch_lora_rows(const Args16& a, const LoraExtra& x, int cus, hipStream_t stream) {
+  RowsArgs p{a, x, 1};
+  const int64_t wgs = ((int64_t)a.N + 15) / 16 * (((int64_t)a.M + 63) / 64);
+  const int chunk = a.M <= 32 ? kChunk : kChunk / 2;
+  const int chunks = std::max(1, (int)(((int64_t)a.K + chunk - 1) / chunk));
+  p.waves = waves_for(wgs, chunks, kMaxWaves, cus);
+  return launch_tiles(a.fmt == kFmtBF16 ? pick<kFmtBF16>(a.M) : pick<kFmtF16>(a.M), p, wgs,
+                      64 * p.waves, 0, stream);
+}
+
+}  // namespace tune
+}  // namespace mi355gemm

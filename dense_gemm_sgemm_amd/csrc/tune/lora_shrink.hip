@@ -1,0 +1,155 @@
+// t[m][r] = sum_k X[m][k] A_a[r][k] with a the adapter of row m: each adapter's
+// ranks are few, so the product streams X once and the adapters that its rows
+// name once a block of 16 rows (from L2 where neighbours share them).
+//
+// A workgroup takes 16 rows, one of the adapters they name and up to 64 ranks;
+// its waves share K out in turns of 128 and add up through LDS.  Rows of other
+// adapters are multiplied along and dropped.  The launch has 16 places for
+// adapters a block of rows, since only the GPU knows the ids: those past the
+// block's last one end at once.
+#include "fused/skinny.hpp"
+#include "tune.hpp"
+
+namespace mi355gemm {
+namespace tune {
+namespace {
+
+using namespace fused::skinny;
+
+constexpr int kWaves = 8, kSteps = 4, kChunk = 32 * kSteps, kSlots = 16;
+
+template <int FMT, int RB>
+__global__ __launch_bounds__(64 * kWaves) void shrink_kernel(ShrinkArgs p, int64_t base) {
+  __shared__ f4 lds[(kWaves - 1) * RB * 64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, quarter = lane >> 4;
+  const int groups = (p.R + 16 * RB - 1) / (16 * RB);
+  const int64_t id = base + blockIdx.x;
+  const int slot = (int)(id % kSlots);
+  const int64_t rest = id / kSlots;
+  const int first = (int)(rest % groups) * 16 * RB;   // rank
+  const int m0 = (int)(rest / groups) * 16;
+  const int mr = m0 + r < p.M ? m0 + r : p.M - 1;
+  const int mine = m0 + r < p.M ? adapter_of(p.ids, m0 + r, p.S) : -1;
+
+  if (slot == 0 && wave == 0 && p.t32) {
+    // rows without an adapter: zeros (one that does not exist: NaN)
+    for (int q = quarter; q < RB; q += 4)
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int other = __builtin_amdgcn_readlane(mine, i), c = first + 16 * q + r;
+        if (other < 0 && m0 + i < p.M && c < p.cols32)
+          p.t32[(int64_t)(m0 + i) * p.ldt + c] = other == -1 ? 0.f : __builtin_nanf("");
+      }
+  }
+  // the slot's adapter
+  uint32_t pending = (uint32_t)__ballot(mine >= 0) & 0xFFFFu, rows = 0;
+  int a = -1;
+  for (int d = 0; d <= slot && pending; ++d) {
+    a = __builtin_amdgcn_readlane(mine, __builtin_ctz(pending));
+    rows = (uint32_t)__ballot(mine == a) & 0xFFFFu;
+    pending &= ~rows;
+    if (d == slot) break;
+    a = -1;
+  }
+  if (a < 0) return;
+
+  const half_t* x = p.X + (int64_t)mr * p.ldx + 8 * quarter;
+  const half_t* w[RB];
+#pragma unroll
+  for (int q = 0; q < RB; ++q) {
+    const int n = first + 16 * q + r;   // ranks past R repeat the last one and count as zeros
+    w[q] = p.A + a * p.stride_a + (int64_t)(n < p.R ? n : p.R - 1) * p.lda + 8 * quarter;
+  }
+  f4 acc[RB];
+#pragma unroll
+  for (int q = 0; q < RB; ++q) acc[q] = f4{0.f, 0.f, 0.f, 0.f};
+  // (pointers and K both moved on by the lane's 8 quarter)
+  const int K = p.K - 8 * quarter, chunks = p.K / kChunk;
+  auto turn = [&](int k, auto tail) __attribute__((always_inline)) {
+    constexpr bool kTail = decltype(tail)::value;
+    h8 xv[kSteps], wv[RB][kSteps];
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      xv[s] = load_x<kTail>(x, k + 32 * s, K);
+#pragma unroll
+      for (int q = 0; q < RB; ++q) wv[q][s] = load_x<kTail>(w[q], k + 32 * s, K);
+    }
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int q = 0; q < RB; ++q) acc[q] = mfma16<FMT>(xv[s], wv[q][s], acc[q]);
+  };
+  for (int c = wave; c < chunks; c += kWaves) turn(c * kChunk, std::false_type());
+  if (chunks * kChunk < p.K && wave == chunks % kWaves) turn(chunks * kChunk, std::true_type());
+  add_waves<RB>(acc, reinterpret_cast<float*>(lds), wave, lane, kWaves);
+  if (wave > 0) return;
+
+  // acc[q][v]: row 4 quarter + v, rank first + 16 q + r
+#pragma unroll
+  for (int q = 0; q < RB; ++q)
+    if (first + 16 * q + r >= p.R) acc[q] = f4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int i = 4 * quarter + v;
+    const int64_t m = m0 + i;
+    const bool live = rows >> i & 1;
+    if (p.t32 && live) {
+#pragma unroll
+      for (int q = 0; q < RB; ++q)
+        if (first + 16 * q + r < p.cols32) p.t32[m * p.ldt + first + 16 * q + r] = acc[q][v];
+    }
+    if (!p.t2) continue;
+    const float scale = p.scales ? p.scales[a] : 1.f;
+    constexpr int kPer = RB == 1 ? 1 : 2;   // 16-rank groups of a block (w / 16)
+#pragma unroll
+    for (int b = 0; b < RB / kPer; ++b) {
+      const int block = first / p.w + b;
+      float top = 0.f;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const float t = fabsf(acc[kPer * b + u][v]);
+        top = fmaxf(top, t < __builtin_inff() ? t : 0.f);
+      }
+#pragma unroll
+      for (int k = 8; k >= 1; k /= 2) top = fmaxf(top, __shfl_xor(top, k));
+      // 2^(13 - floor(log2 top)), within what fp32 holds
+      const int e = top == 0.f ? 13 : (int)(__float_as_uint(fmaxf(top, 0x1p-100f)) >> 23) - 127;
+      const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+      const float down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+      if (live && block < p.blocks) {
+        half_t* dst = p.t2 + m * p.ld2 + 2 * p.w * (int64_t)block + r;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          const float t = acc[kPer * b + u][v] * up;
+          const half_t hi = f32_to_word<FMT>(t);
+          const float left = t - word_to_f32<FMT>(hi);
+          dst[16 * u] = hi;
+          // (infinite and NaN: hi says it)
+          dst[p.w + 16 * u] = f32_to_word<FMT>(fabsf(t) < __builtin_inff() ? left : 0.f);
+        }
+        if (r == 0) p.factor[m * p.blocks + block] = down * scale;
+      }
+    }
+  }
+}
+
+template <int FMT>
+const void* pick(int rb) {
+  return rb == 1   ? (const void*)shrink_kernel<FMT, 1>
+         : rb == 2 ? (const void*)shrink_kernel<FMT, 2>
+                   : (const void*)shrink_kernel<FMT, 4>;
+}
+
+}  // namespace
+
+hipError_t launch_shrink(int fmt, const ShrinkArgs& p, hipStream_t stream) {
+  const int rb = p.R <= 16 ? 1 : p.R <= 32 ? 2 : 4;
+  const int64_t wgs = ((int64_t)p.M + 15) / 16 * ((p.R + 16 * rb - 1) / (16 * rb)) * kSlots;
+  return launch_tiles(fmt == kFmtBF16 ? pick<kFmtBF16>(rb) : pick<kFmtF16>(rb), p, wgs,
+                      64 * kWaves, 0, stream);
+}
+
+}  // namespace tune
+}  // namespace mi355gemm

@@ -8,6 +8,7 @@ namespace mi355gemm {
 namespace tune {
 
 using fused::Mat;
+using hgemm::LoraExtra;
 using hgemm::OrthoExtra;
 
 // Products of an orthogonalised update over `batch` matrices (tiles_ortho.hip):
@@ -16,6 +17,117 @@ hipError_t launch_sym_tiles(const Args16& a, const OrthoExtra& x, int batch, int
                             hipStream_t stream);
 hipError_t launch_mul_tiles(const Args16& a, const OrthoExtra& x, bool a_kmajor, int batch, int cus,
                             hipStream_t stream);
+
+// ---- Low-rank adapters.
+//
+// A row's product with its adapter's first factor, t[m][r] = sum_k X[m][k]
+// A_a[r][k], is needed as an operand of the matrix cores.  Rounded to the type
+// it would carry an error of its own as large as the output's; so it is kept
+// in two 16-bit values, hi + lo, which in the second product are 32 more k a
+// block of ranks.  Both are stored times a power of two for the row's block
+// that brings the largest of its ranks to 2^13 .. 2^14, so that neither leaves
+// binary16's normal range; the factor that undoes it, times the adapter's
+// scale, is applied to the block's sums in fp32.
+//
+//   t2      : [M][ld2], for each block of w ranks w hi values, then w lo
+//   factor  : float [M][blocks]
+//   w       : 16 for up to 16 ranks (hi and lo share the 32 k of one product),
+//             else 32
+// Rows without an adapter are left as they were: what reads t2 or the factors
+// drops the sums of rows that are not the adapter's, whatever they are.
+constexpr int kMaxRank = 1024;
+struct Ranks {
+  int R, w, blocks, padded;   // padded: w * blocks
+  explicit Ranks(int r) : R(r), w(r <= 16 ? 16 : 32), blocks((r + w - 1) / w), padded(w * blocks) {}
+  int64_t ld2() const { return 2 * (int64_t)padded; }
+};
+
+struct ShrinkArgs {
+  const half_t* X;     // [M][ldx]
+  const half_t* A;     // [S][R][lda], matrices stride_a apart
+  int64_t ldx, lda, stride_a;
+  const long long* ids;
+  const float* scales;   // [S] or null
+  half_t* t2;            // or null, with factor
+  float* factor;
+  int64_t ld2;
+  float* t32;            // [M][ldt] or null: the sums themselves
+  int64_t ldt;
+  int M, K, R, S, w, blocks, cols32;   // cols32: columns of t32 written (zeros past R)
+};
+hipError_t launch_shrink(int fmt, const ShrinkArgs& p, hipStream_t stream);
+
+// The adapters' part beside a product of few rows (lora_rows.hip), operands as
+// they are; x as for the tiles.
+hipError_t launch_lora_rows(const Args16& a, const LoraExtra& x, int cus, hipStream_t stream);
+// C = A B^T (kmajor: A B) with the adapters' part.
+hipError_t launch_lora_tiles(const Args16& a, const LoraExtra& x, bool kmajor, int cus,
+                             hipStream_t stream);
+
+// ---- Gradients of the adapters (lora_grad.hip).
+//
+// dA_a[r][k] = sum_m dt[m][r] X[m][k] over the rows of adapter a, and dB alike
+// with dC and t: sums over rows, which lie in any order.  The rows are listed
+// adapter by adapter, each adapter's list filled up to whole steps of 32 with
+// -1, so that a matrix-core step of 32 rows belongs to one adapter.
+struct GroupArgs {
+  const long long* ids;
+  int M, S;
+  int* counts;         // [S] rows of an adapter
+  int* rows;           // [32 * steps]
+  int* step_adapter;   // [steps], -1 past the last one
+  int steps;           // as many as there can be
+};
+inline int max_steps(int M, int S) { return (int)(((int64_t)M + 31) / 32 + std::min(M, S)); }
+hipError_t launch_group(const GroupArgs& p, hipStream_t stream);
+
+// One of the two gradients: `left` [rows][ld_left] fp32 (dt or t) times `right`
+// [rows][ld_right] 16-bit (X or dC).
+struct GradJob {
+  const float* left = nullptr;
+  int64_t ld_left = 0;
+  const half_t* right = nullptr;
+  int64_t ld_right = 0;
+  int cols = 0;             // of right
+  half_t* out = nullptr;    // null: not asked for
+  int64_t ldo = 0, stride_o = 0;
+  int transposed = 0;       // out[a][col][rank] (dB) instead of out[a][rank][col]
+  half_t* pack = nullptr;   // left's ranks in list order, [hi, lo][padded][32 * steps]
+  float* step_factor = nullptr;   // [steps]
+  float* partial = nullptr;
+  int blocks = 0;           // of 128 columns
+};
+struct GradArgs {
+  GroupArgs g;
+  GradJob job[2];
+  const float* scales;      // [S] or null
+  int R, padded;            // ranks, and in whole groups of 16
+  int groups;               // of 16 * RB ranks
+  int chunks, chunk_steps;  // the steps are cut into chunks, each a workgroup's
+};
+struct GradPlan {
+  int steps, rb, groups, chunks, chunk_steps, padded;
+  size_t pack, partial[2];   // bytes of one job's
+};
+GradPlan plan_grad(int M, int N, int K, int R, int S);
+hipError_t launch_adapter_grads(int fmt, const GradArgs& p, const GradPlan& plan,
+                                hipStream_t stream);
+
+// dst[l][o][i] = src[l][i][o] for i < inner (zeros up to inner_p, a multiple of
+// 8) and o < outer, in `count` matrices.
+struct TurnArgs {
+  const half_t* src;
+  half_t* dst;
+  int64_t lds, stride_s, ldd, stride_d;
+  int inner, inner_p, outer, count;
+};
+hipError_t launch_turn(const TurnArgs& first, const TurnArgs* second, hipStream_t stream);
+
+// Row m's adapter: its number, -1 for none, -2 for one that does not exist.
+__device__ __forceinline__ int adapter_of(const long long* ids, int64_t m, int S) {
+  const long long id = ids[m];
+  return id < 0 ? -1 : id >= S ? -2 : (int)id;
+}
 
 }  // namespace tune
 }  // namespace mi355gemm

@@ -1,6 +1,11 @@
 """Bindings of ``libmi355tune.so`` (``include/mi355tune.h``): what fine tuning
 needs next to a model's products.
 
+    gemm_lora(X, W, A, B, ids, C, scales=None, T=None, ...)
+                                  # C[m] = act(X[m]@W.T + scales[a] X[m]@A[a].T@B[a].T + bias)
+                                  #        + residual[m], a = ids[m]
+    gemm_lora_bwd(X, W, A, B, ids, T, dC, dX=None, dA=None, dB=None, scales=None)
+                                  # its gradients, W frozen
     gemm_ortho(G, O, steps=5, coeffs=(a, b, c), eps=1e-7)
                                   # O = G orthogonalised by Newton-Schulz products
 
@@ -15,8 +20,8 @@ import ctypes
 import os
 import threading
 
-from . import HERE, INT_MAX, _torch_module
-from .fused import _run
+from . import HERE, INT_MAX, _epilogue_args, _torch_module
+from .fused import _act, _first, _optional, _rows, _run, _shaped, _vector
 
 LIB_PATH = os.path.join(HERE, "libmi355tune.so")
 _lock = threading.Lock()
@@ -42,6 +47,12 @@ def load_library() -> ctypes.CDLL:
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, restype
 
+        mat, stack = [p, i], [p, i, i64]
+        declare("gemm_lora", [i] * 6 + mat * 2 + stack * 2 + [p, p, p, i] + mat * 3 + [p, u64, p])
+        declare("gemm_lora_workspace", [i] * 6 + mat * 2, u64)
+        declare("gemm_lora_bwd",
+                [i] * 6 + mat * 2 + stack * 2 + [p, p] + mat * 3 + stack * 2 + [p, u64, p])
+        declare("gemm_lora_bwd_workspace", [i] * 6 + mat * 2 + [i] * 3, u64)
         declare("gemm_ortho", [i] * 5 + [p, i, i64, i, ctypes.POINTER(f), f, p, i, i64, p, u64, p])
         declare("gemm_ortho_workspace", [i] * 6, u64)
         _lib = lib
@@ -80,6 +91,115 @@ def _stack(t, name):
     if max(L, rows, cols, ld) > INT_MAX:
         raise ValueError("%s: sizes and the distance between rows must be below 2^31" % name)
     return L, rows, cols, ld, (stride[0] if L > 1 else 0), (t.data_ptr() if t.numel() else None)
+
+
+def _adapters(t, name, dtype, index, rows, cols, count=None):
+    """(adapters, pointer, leading dimension, distance between adapters) of a stack
+    [S, rows, cols]; None of rows, cols or count is free."""
+    torch = _torch_module()
+    if not isinstance(t, torch.Tensor) or t.dim() != 3:
+        raise TypeError("%s must be a 3-D tensor, one matrix an adapter" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    S, r, c, ld, stride, ptr = _stack(t, name)
+    for have, want in ((S, count), (r, rows), (c, cols)):
+        if want is not None and have != want:
+            raise ValueError("%s must be %s, got %s" % (name, [
+                "adapters" if count is None else count, "ranks" if rows is None else rows,
+                "ranks" if cols is None else cols], tuple(t.shape)))
+    if t.get_device() != index:
+        raise ValueError("all tensors of a call must live on one GPU")
+    return S, ptr, max(ld, c), stride
+
+
+def _scales(scales, index, S):
+    return None if scales is None else _vector(scales, "scales", _torch_module().float32, index, S)
+
+
+def gemm_lora(X, W, A, B, ids, C, scales=None, bias=None, act: str = "none", residual=None, T=None,
+              workspace=None, stream=None):
+    """``C[m] = act(X[m] @ W.T + scales[a] * X[m] @ A[a].T @ B[a].T + bias) + residual[m]``
+    with ``a = ids[m]``: a projection shared by all rows beside the low-rank
+    adapter that each row names.  float16 or bfloat16 X[M,K], W[N,K], A[S,R,K],
+    B[S,N,R], C[M,N]; ``ids``: int64 [M], below 0 for rows without an adapter
+    (S and more give NaN); ``scales``: float32 [S] or None for 1.  ``T``: float32
+    [M,R] or None, receives ``X[m] @ A[a].T`` for ``gemm_lora_bwd``.  ``bias``,
+    ``act`` and ``residual`` (which may be C) as for ``gemm_ex``.  ``workspace``:
+    ``lora_workspace_bytes`` bytes, or None.  Returns C."""
+    torch = _torch_module()
+    dtype, typ, at, M, K, px, ldx = _first(X)
+    N = _rows(W, "W")
+    pw, ldw = _shaped(W, "W", dtype, at, N, K)
+    S, pa, lda, sa = _adapters(A, "A", dtype, at, None, K)
+    R = A.shape[1]
+    _, pb, ldb, sb = _adapters(B, "B", dtype, at, N, R, S)
+    pi = _vector(ids, "ids", torch.int64, at, M)
+    ps = _scales(scales, at, S)
+    pc, ldc = _shaped(C, "C", dtype, at, M, N)
+    pt, ldt = _optional(T, "T", torch.float32, at, M, R)
+    if bias is None and residual is None:
+        pbias, code, pres, ldr = None, _act(act), None, 0
+    else:
+        for t in (bias, residual):
+            if t is not None and t.get_device() != at:
+                raise ValueError("all tensors of a call must live on one GPU")
+        pbias, code, pres, ldr = _epilogue_args(bias, act, residual, M, N, dtype)
+    lib = _lib or load_library()
+    _run(at, stream, lib.gemm_lora,
+         (typ, M, N, K, R, S, px, ldx, pw, ldw, pa, lda, sa, pb, ldb, sb, pi, ps, pbias, code, pres,
+          ldr, pc, ldc, pt, ldt),
+         lambda: lib.gemm_lora_workspace(typ, M, N, K, R, S, px, ldx, pw, ldw), workspace)
+    return C
+
+
+def lora_workspace_bytes(X, W, A) -> int:
+    """Workspace bytes ``gemm_lora`` needs for these tensors."""
+    dtype, typ, at, M, K, px, ldx = _first(X)
+    N = _rows(W, "W")
+    S = _adapters(A, "A", dtype, at, None, K)[0]
+    return load_library().gemm_lora_workspace(typ, M, N, K, A.shape[1], S, px, ldx,
+                                              *_shaped(W, "W", dtype, at, N, K))
+
+
+def gemm_lora_bwd(X, W, A, B, ids, T, dC, dX=None, dA=None, dB=None, scales=None, workspace=None,
+                  stream=None):
+    """The gradients of ``gemm_lora`` (act "none", W frozen) for the gradient dC
+    [M,N] of its result and the T it stored: ``dX`` [M,K], ``dA`` [S,R,K] and
+    ``dB`` [S,N,R], each computed if given; adapters that no row names get zeros.
+    ``workspace``: ``lora_bwd_workspace_bytes`` bytes, or None.  Returns
+    (dX, dA, dB)."""
+    torch = _torch_module()
+    dtype, typ, at, M, K, px, ldx = _first(X)
+    N = _rows(W, "W")
+    pw, ldw = _shaped(W, "W", dtype, at, N, K)
+    S, pa, lda, sa = _adapters(A, "A", dtype, at, None, K)
+    R = A.shape[1]
+    _, pb, ldb, sb = _adapters(B, "B", dtype, at, N, R, S)
+    pi = _vector(ids, "ids", torch.int64, at, M)
+    ps = _scales(scales, at, S)
+    pt, ldt = _shaped(T, "T", torch.float32, at, M, R)
+    pc, ldc = _shaped(dC, "dC", dtype, at, M, N)
+    pdx, lddx = _optional(dX, "dX", dtype, at, M, K)
+    pda, ldda, sda = (None, 0, 0) if dA is None else _adapters(dA, "dA", dtype, at, R, K, S)[1:]
+    pdb, lddb, sdb = (None, 0, 0) if dB is None else _adapters(dB, "dB", dtype, at, N, R, S)[1:]
+    lib = _lib or load_library()
+    _run(at, stream, lib.gemm_lora_bwd,
+         (typ, M, N, K, R, S, px, ldx, pw, ldw, pa, lda, sa, pb, ldb, sb, pi, ps, pt, ldt, pc, ldc,
+          pdx, lddx, pda, ldda, sda, pdb, lddb, sdb),
+         lambda: lib.gemm_lora_bwd_workspace(typ, M, N, K, R, S, pc, ldc, pw, ldw, pdx is not None,
+                                             pda is not None, pdb is not None), workspace)
+    return dX, dA, dB
+
+
+def lora_bwd_workspace_bytes(X, W, A, dC, want_dx: bool = True, want_da: bool = True,
+                             want_db: bool = True) -> int:
+    """Workspace bytes ``gemm_lora_bwd`` needs for these tensors and gradients."""
+    dtype, typ, at, M, K, _, _ = _first(X)
+    N = _rows(W, "W")
+    S = _adapters(A, "A", dtype, at, None, K)[0]
+    return load_library().gemm_lora_bwd_workspace(
+        typ, M, N, K, A.shape[1], S, *_shaped(dC, "dC", dtype, at, M, N),
+        *_shaped(W, "W", dtype, at, N, K), bool(want_dx), bool(want_da), bool(want_db))
 
 
 MUON = (3.4445, -4.7750, 2.0315)

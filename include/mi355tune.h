@@ -37,6 +37,98 @@ extern "C" {
 #define MI355TUNE_API
 #endif
 
+/*
+ * A projection shared by all rows beside the low-rank adapter that each row
+ * names:
+ *
+ *     t[m] = X[m] * A[a]^T,  a = ids[m]
+ *     C[m] = act(X[m] * W^T + scales[a] * t[m] * B[a]^T + bias) + residual[m]
+ *
+ *   type    : GEMM_TYPE_F16 or GEMM_TYPE_BF16, of X, W, A, B, bias, residual, C
+ *   X       : [M][ldx], ldx >= max(1, K)                            (read)
+ *   W       : [N][ldw], ldw >= max(1, K)                            (read)
+ *   A       : [S][R][lda], lda >= max(1, K), adapters stride_a elements
+ *             apart                                                 (read)
+ *   B       : [S][N][ldb], ldb >= R, adapters stride_b apart        (read)
+ *   ids     : 64-bit integers [M], in any order: the row's adapter, below 0 for
+ *             none (the projection alone); S and more make the row of C NaN
+ *   scales  : float [S], or NULL for 1 everywhere                   (read)
+ *   bias, act, residual, ldr, C, ldc : as for gemm_ex (residual may be C; ReLU
+ *             of NaN is NaN)
+ *   T       : float [M][ldt], ldt >= R, or NULL: t, as gemm_lora_bwd takes it;
+ *             0 for rows without an adapter                         (written)
+ *
+ * t is an operand of the second product in two 16-bit values of the type (16
+ * bits in bf16, 22 in fp16, of the largest of 16 or 32 ranks), so C is rounded
+ * once.  An adapter of fewer ranks than R has zeros in the others.  What one
+ * row's adapter holds, infinities and NaN too, reaches no other row.
+ *
+ * Rows whose neighbours have the same adapter share its reads; in any other
+ * order each block of 16 rows reads every adapter that it names.
+ *
+ * R is 1 .. 1024, M, N, K and S go up to 2^27; others are GEMM_ERR_BAD_ARG.
+ * K == 0 gives act(bias) + residual.  M == 0 is a no-op, and so is N == 0
+ * without T.
+ */
+MI355TUNE_API int gemm_lora(int type, int M, int N, int K, int R, int S,
+                            const void* X, int ldx, const void* W, int ldw,
+                            const void* A, int lda, long long stride_a,
+                            const void* B, int ldb, long long stride_b,
+                            const long long* ids, const float* scales,
+                            const void* bias, int act, const void* residual, int ldr,
+                            void* C, int ldc, float* T, int ldt,
+                            void* workspace, unsigned long long workspace_bytes,
+                            void* stream);
+
+/* Workspace bytes of gemm_lora: t (4 bytes a row and rank, ranks in blocks of
+ * 16, or of 32 above 16), and padded copies of X and W where many rows meet
+ * operands that are not whole 16-byte rows (as for gemm_gated). */
+MI355TUNE_API unsigned long long gemm_lora_workspace(int type, int M, int N, int K, int R, int S,
+                                                     const void* X, int ldx,
+                                                     const void* W, int ldw);
+
+/*
+ * The gradients of gemm_lora without an activation, for the gradient dC of its
+ * result and the T it stored; W is frozen:
+ *
+ *     dt[m] = scales[a] * dC[m] * B[a]          a = ids[m]
+ *     dX[m] = dC[m] * W + dt[m] * A[a]
+ *     dA[a] = sum over the rows of a: dt[m]^T * X[m]
+ *     dB[a] = scales[a] * sum over the rows of a: dC[m]^T * T[m]
+ *
+ *   dC      : [M][lddc], lddc >= max(1, N)                          (read)
+ *   dX      : [M][lddx], lddx >= max(1, K), or NULL                 (written)
+ *   dA, dB  : laid out like A and B, or NULL each; adapters must not
+ *             overlap                                               (written)
+ *
+ * dt and T are operands in two 16-bit values, as t above; sums over rows, K and
+ * N are fp32.  Rows without an adapter (any id below 0, or S and more) reach
+ * no adapter's gradient, whatever they hold; an id of S and more makes the row
+ * of dX NaN.  An adapter without rows has gradients of zero.
+ *
+ * X is read only for dA, T only for dB, W and A only for dX, B for dX and dA;
+ * they may be NULL otherwise.  An empty sum is zero.
+ */
+MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S,
+                                const void* X, int ldx, const void* W, int ldw,
+                                const void* A, int lda, long long stride_a,
+                                const void* B, int ldb, long long stride_b,
+                                const long long* ids, const float* scales,
+                                const float* T, int ldt, const void* dC, int lddc,
+                                void* dX, int lddx,
+                                void* dA, int ldda, long long stride_da,
+                                void* dB, int lddb, long long stride_db,
+                                void* workspace, unsigned long long workspace_bytes,
+                                void* stream);
+
+/* Workspace bytes of gemm_lora_bwd: B and A with rows and columns exchanged, dt,
+ * the rows listed by adapter, fp32 sums of adapters' parts, and padded copies
+ * of dC and W.  want_*: the gradient is asked for. */
+MI355TUNE_API unsigned long long gemm_lora_bwd_workspace(int type, int M, int N, int K, int R,
+                                                         int S, const void* dC, int lddc,
+                                                         const void* W, int ldw, int want_dx,
+                                                         int want_da, int want_db);
+
 /* Beside GEMM_TYPE_F16 and GEMM_TYPE_BF16, for gemm_ortho only. */
 enum { GEMM_TYPE_F32 = 2 };
 
