@@ -894,17 +894,31 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   // The operators' epilogues (MODE).  flush stores the 16 staged rows of row
   // block i, `cols` columns from n_first, to dst: rows [mlo, mhi) and columns
   // [nlo, nhi) only, at any 2-byte address.
+  // (xl, xr, xg: the lane, its l % 16 and l / 16.  kSym, kMul and kLora find them
+  // again at the end of each tile: kept across the slab loop, they and what is
+  // computed from them cost spills inside it)
+  constexpr bool kFresh = is_ortho(MODE) || MODE == kLora;
+  int xl = 0, xr = 0, xg = 0;
   auto put = [&](int j, h4 o) __attribute__((always_inline)) {
-    const int c = 2 * j + (g >> 1);
-    *(h4*)(stage_out + r * C::kOutRowBytes + 16 * (c ^ r) + 8 * (g & 1)) = o;
+    if constexpr (kFresh) {
+      const int c = 2 * j + (xg >> 1);
+      *(h4*)(stage_out + xr * C::kOutRowBytes + 16 * (c ^ xr) + 8 * (xg & 1)) = o;
+    } else {
+      const int c = 2 * j + (g >> 1);
+      *(h4*)(stage_out + r * C::kOutRowBytes + 16 * (c ^ r) + 8 * (g & 1)) = o;
+    }
   };
   auto flush = [&](half_t* dst, int64_t ld, int m_first, int n_first, int cols, int mlo, int mhi,
                    int nlo, int nhi) __attribute__((always_inline)) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    const int cc = lane & 15;
+    auto at = [&]() __attribute__((always_inline)) {
+      if constexpr (kFresh) return xl;
+      else return lane;
+    };
+    const int cc = at() & 15;
 #pragma unroll
     for (int q = 0; q < kOutRows / 4; ++q) {
-      const int R = 4 * q + (lane >> 4);
+      const int R = 4 * q + (at() >> 4);
       const h8 v = *(const h8*)(stage_out + R * C::kOutRowBytes + 16 * (cc ^ R));
       const int m = m_first + R, n = n_first + 8 * cc;
       if (cc < cols / 8 && m >= mlo && m < mhi && n + 8 > nlo && n < nhi) {
@@ -937,6 +951,11 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   };
   auto epilogue_fused = [&](int m0, int n0, int mlo, int nlo, int part)
                             __attribute__((always_inline)) {
+    if constexpr (kFresh) {
+      asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(xl));
+      xr = xl & 15;
+      xg = xl >> 4;
+    }
     if constexpr (MODE == kGated) {
       const FusedExtra& x = ta.x;
       const int nw = n0 + wn / 2;
@@ -1143,10 +1162,10 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       const int64_t at = part * x.stride_c;
 #pragma unroll
       for (int i = 0; i < C::kBlocksM; ++i) {
-        const int m = m0 + wm + 16 * i + r;
+        const int m = m0 + wm + 16 * i + xr;
 #pragma unroll
         for (int j = 0; j < C::kBlocksN; ++j) {
-          const int n = n0 + wn + 16 * j + 4 * g;
+          const int n = n0 + wn + 16 * j + 4 * xg;
           f4 v = acc[i][j] * alpha;
           if (x.q_hi) {
             const int64_t q = at + (int64_t)m * p.ldc + n;
@@ -1189,8 +1208,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
               const h4 o = value(acc[i][j]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const int R = 4 * g + e, c = 2 * i + (r >> 3);
-                *(half_t*)(stage_out + R * C::kOutRowBytes + 16 * (c ^ R) + 2 * (r & 7)) = o[e];
+                const int R = 4 * xg + e, c = 2 * i + (xr >> 3);
+                *(half_t*)(stage_out + R * C::kOutRowBytes + 16 * (c ^ R) + 2 * (xr & 7)) = o[e];
               }
             }
             flush(dst, p.ldc, n0 + wn + 16 * j, m0 + wm, C::WM, nlo, p.N, mlo, p.M);
@@ -1231,11 +1250,11 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
           }
           flush((half_t*)x.out + part * x.stride_o, x.ldo, m, n0 + wn, C::WN, mlo, x.m_end, nlo,
                 x.n_end);
-        } else if (m + r >= mlo && m + r < x.m_end) {
-          float* dst = (float*)x.out + part * x.stride_o + (int64_t)(m + r) * x.ldo;
+        } else if (m + xr >= mlo && m + xr < x.m_end) {
+          float* dst = (float*)x.out + part * x.stride_o + (int64_t)(m + xr) * x.ldo;
 #pragma unroll
           for (int j = 0; j < C::kBlocksN; ++j) {
-            const int n = n0 + wn + 16 * j + 4 * g;
+            const int n = n0 + wn + 16 * j + 4 * xg;
             if (n >= nlo && n + 4 <= x.n_end) {
               __builtin_memcpy(dst + n, &acc[i][j], 16);
             } else {
@@ -1249,9 +1268,9 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     } else if constexpr (MODE == kLora) {
       const LoraExtra& x = ta.x;
       // lane l stands for row l of the wave's
-      const int ml = m0 + wm + lane;
+      const int ml = m0 + wm + xl;
       int mine = -1;
-      if (lane < C::WM && ml < x.m_end) {
+      if (xl < C::WM && ml < x.m_end) {
         const long long id = x.ids[ml];
         mine = id < 0 ? -1 : id >= x.S ? -2 : (int)id;
       }
@@ -1268,16 +1287,16 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
 #pragma unroll
           for (int i = 0; i < C::kBlocksM; ++i) {
             // (rows of other adapters, and past the end: any values, times 0)
-            const int m = m0 + wm + 16 * i + r, mc = m < x.m_end ? m : x.m_end - 1;
+            const int m = m0 + wm + 16 * i + xr, mc = m < x.m_end ? m : x.m_end - 1;
             const half_t* t2 = x.t2 + (int64_t)mc * x.ld2 + 2 * x.w * k;
-            hi[i] = *(const h8*)(t2 + 8 * g);
-            lo[i] = x.w == 32 ? *(const h8*)(t2 + 32 + 8 * g) : h8{};
+            hi[i] = *(const h8*)(t2 + 8 * xg);
+            lo[i] = x.w == 32 ? *(const h8*)(t2 + 32 + 8 * xg) : h8{};
             f[i] = x.factor[(int64_t)mc * x.blocks + k];
           }
-          const int at = x.w == 16 ? 8 * (g & 1) : 32 * k + 8 * g;
+          const int at = x.w == 16 ? 8 * (xg & 1) : 32 * k + 8 * xg;
 #pragma unroll
           for (int j = 0; j < C::kBlocksN; ++j) {
-            const int n = n0 + wn + 16 * j + r;
+            const int n = n0 + wn + 16 * j + xr;
             const half_t* row = b + (int64_t)(n < x.n_end ? n : x.n_end - 1) * x.ldb;
             h8 bv = {};
             if (at + 8 <= x.R) {
@@ -1290,8 +1309,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
 #pragma unroll
             for (int i = 0; i < C::kBlocksM; ++i) {
               if (!(rows >> (16 * i) & 0xFFFF)) continue;
-              const f4 s = mfma_split<FMT, true>(hi[i], lo[i], bv, x.w == 32, lane);
-              const bool own = rows >> (16 * i + r) & 1;
+              const f4 s = mfma_split<FMT, true>(hi[i], lo[i], bv, x.w == 32, xl);
+              const bool own = rows >> (16 * i + xr) & 1;
 #pragma unroll
               for (int v = 0; v < 4; ++v) acc[i][j][v] += own ? f[i] * s[v] : 0.f;
             }
@@ -1302,7 +1321,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
 #pragma unroll
       for (int j = 0; j < C::kBlocksN; ++j) {
         bq[j] = h4{};
-        const int n = n0 + wn + 16 * j + 4 * g;
+        const int n = n0 + wn + 16 * j + 4 * xg;
         if (p.bias) {
 #pragma unroll
           for (int v = 0; v < 4; ++v)
@@ -1311,11 +1330,11 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       }
 #pragma unroll
       for (int i = 0; i < C::kBlocksM; ++i) {
-        const int m = m0 + wm + 16 * i + r;
-        const bool nan = unknown >> (16 * i + r) & 1;
+        const int m = m0 + wm + 16 * i + xr;
+        const bool nan = unknown >> (16 * i + xr) & 1;
 #pragma unroll
         for (int j = 0; j < C::kBlocksN; ++j) {
-          const int n = n0 + wn + 16 * j + 4 * g;
+          const int n = n0 + wn + 16 * j + 4 * xg;
           f4 z = acc[i][j];
 #pragma unroll
           for (int v = 0; v < 4; ++v)
@@ -1466,7 +1485,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   auto slab = [&](int gs, auto next, auto is_copier, bool zero_next) __attribute__((always_inline)) {
     auto sync = [&]() __attribute__((always_inline)) {
       // kGradX needs no zeros in LDS: its A side of a tail slab has them in memory
-      if constexpr (RAG && MODE != kGradX) wait_zero_sync(zero_next, (gs + 1) & 1);
+      // (and kSym's and kMul's K is whole slabs)
+      if constexpr (RAG && MODE != kGradX && !is_ortho(MODE)) wait_zero_sync(zero_next, (gs + 1) & 1);
       else wait_and_sync();
     };
     constexpr bool kCp = decltype(is_copier)::value;

@@ -26,8 +26,10 @@ __global__ __launch_bounds__(64 * kWaves) void shrink_kernel(ShrinkArgs p, int64
   const int r = lane & 15, quarter = lane >> 4;
   const int groups = (p.R + 16 * RB - 1) / (16 * RB);
   const int64_t id = base + blockIdx.x;
-  const int slot = (int)(id % kSlots);
-  const int64_t rest = id / kSlots;
+  // (a place's blocks of rows one after another: dealt out the other way round,
+  // the places that have an adapter would all be on one XCD)
+  const int64_t per = ((int64_t)p.M + 15) / 16 * groups, rest = id % per;
+  const int slot = (int)(id / per);
   const int first = (int)(rest % groups) * 16 * RB;   // rank
   const int m0 = (int)(rest / groups) * 16;
   const int mr = m0 + r < p.M ? m0 + r : p.M - 1;
