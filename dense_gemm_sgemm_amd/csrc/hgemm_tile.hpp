@@ -283,11 +283,17 @@ struct FusedTileArgs {
 // an element, hi + lo: products of parts add up the ones that matter.
 //   kSym   hi (, lo) = alpha * acc + beta * q + gamma * [m == n], times the
 //          matrix's own factors coef[3 * matrix .. + 2] if there are any
+//          The first `whole` tiles (of all matrices) are made so; the slabs of
+//          the `rest` are cut into ranges, each a work item that leaves acc *
+//          alpha in `sum`, [range][tile - whole][BM][BM].
 //   kMul   v = alpha * acc: to hi (, lo), or rounded to `out`, whose matrices
 //          are m_end x n_end
 struct OrthoExtra {
   int parts = 1;
   uint32_t tiles_each = 0;              // tiles of a matrix
+  uint32_t whole = 0, rest = 0;         // kSym (whole is a multiple of 8 if there is a rest)
+  int splits = 1, per = 0;              // ranges, slabs of each (the last may be shorter)
+  float* sum = nullptr;
   const half_t* a[3] = {};              // operands of the parts
   const half_t* b[3] = {};
   int64_t stride_a = 0, stride_b = 0;   // between matrices
@@ -444,7 +450,21 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       sp = (int)(item / tiles);
       item -= sp * tiles;
     }
-    if constexpr (MODE != kProduct) item = xcd_order32((uint32_t)item, (uint32_t)ta.tiles);
+    if constexpr (MODE == kSym) {
+      // (each XCD its share of the whole tiles and of the ranges)
+      const uint32_t whole = ta.x.whole, rest = ta.x.rest;
+      kb = -1;
+      if ((uint32_t)item < whole) {
+        item = xcd_order32((uint32_t)item, whole);
+      } else {
+        const uint32_t e = xcd_order32((uint32_t)item - whole, rest * ta.x.splits);
+        const uint32_t range = e / rest;
+        kb = (int)range * ta.x.per;
+        item = whole + e - range * rest;
+      }
+    } else if constexpr (MODE != kProduct) {
+      item = xcd_order32((uint32_t)item, (uint32_t)ta.tiles);
+    }
     // (an XCD's tiles of a range share its slabs of d and W: 333 x 50001 x 768
     // fp16, a step: 213 against 223 us dealt out tile by tile)
     if constexpr (MODE == kGradX) {
@@ -452,7 +472,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       sp = (int)((uint32_t)item / tiles);
       item -= (uint32_t)sp * tiles;
     }
-    kb = sp * (SPLIT ? p.sk.per : 0);
+    if constexpr (MODE != kSym) kb = sp * (SPLIT ? p.sk.per : 0);
     if constexpr (MODE == kGradX) kb = sp * ta.x.per;
     if constexpr (is_ortho(MODE)) {
       sp = (int)((uint32_t)item / ta.x.tiles_each);   // the matrix
@@ -891,6 +911,10 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     }
   };
 
+  // Work items ahead of the current one (the stream below): tile origins, first
+  // slab, part or matrix or range.
+  int om[3], on[3], ok[3], os[3];
+
   // The operators' epilogues (MODE).  flush stores the 16 staged rows of row
   // block i, `cols` columns from n_first, to dst: rows [mlo, mhi) and columns
   // [nlo, nhi) only, at any 2-byte address.
@@ -1159,6 +1183,17 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         beta *= x.coef[3 * part + 1];
         gamma *= x.coef[3 * part + 2];
       }
+      if (ok[0] >= 0) {
+        const uint32_t tm = (uint32_t)mlo / BM;   // (mlo and nlo are whole tiles)
+        const uint32_t tile = part * x.tiles_each + tm * (tm + 1) / 2 + (uint32_t)nlo / BN - x.whole;
+        float* sum = x.sum + ((int64_t)(ok[0] / x.per) * x.rest + tile) * (BM * BN);
+#pragma unroll
+        for (int i = 0; i < C::kBlocksM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j)
+            *(f4*)(sum + (wm + 16 * i + xr) * BN + wn + 16 * j + 4 * xg) = acc[i][j] * x.alpha;
+        return;
+      }
       const int64_t at = part * x.stride_c;
 #pragma unroll
       for (int i = 0; i < C::kBlocksM; ++i) {
@@ -1391,21 +1426,27 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   constexpr int kReadInstr = kReads + (kAT ? C::kBlocksM : 0) + (kBT ? C::kBlocksN : 0);
   constexpr int kCopies = kPerWaveA + kPerWaveB;
   static_assert(kReadInstr <= kMfma && kCopies <= kMfma, "interleave pattern");
-  int nk = SPLIT ? p.sk.per : RAG ? (p.K + BK - 1) / BK : p.K / BK;   // slabs per work item
-  if constexpr (is_ortho(MODE)) nk *= ta.x.parts;
+  const int nk = SPLIT ? p.sk.per : RAG ? (p.K + BK - 1) / BK : p.K / BK;   // slabs per work item
   // The copy target runs two slabs ahead of the compute: slab tc of the tile
   // `ahead` tiles after the current one (origins o[0..2] are refreshed once
   // per tile, outside the MFMA loop).  Past the end of the stream it stays on
   // the last slab of the last tile.
   int tc = 0, ahead = 0, cur = 0;
-  int om[3], on[3], ok[3], os[3];
   int mlo0 = 0, nlo0 = 0;   // the current tile's first stored row and column
   // slabs of the work item `ahead` items after the current one (kGradX: the
   // last range of K may be shorter)
   int nk_all = nk;
   if constexpr (MODE == kGradX) nk_all = ta.x.parts * nk_part;
+  if constexpr (is_ortho(MODE)) nk_all = ta.x.parts * nk;
   auto slabs_of = [&](int d) __attribute__((always_inline)) {
-    if constexpr (MODE == kGradX) {
+    if constexpr (MODE == kSym) {
+      const int from = d == 0 ? ok[0] : d == 1 ? ok[1] : ok[2];
+      const int left = nk_all - from;
+      return from < 0 ? nk_all : left < ta.x.per ? left : ta.x.per;
+    } else if constexpr (MODE == kMul) {
+      (void)d;
+      return nk_all;
+    } else if constexpr (MODE == kGradX) {
       const int left = nk_all - (d == 0 ? ok[0] : d == 1 ? ok[1] : ok[2]);
       return left < ta.x.per ? left : ta.x.per;
     } else {
@@ -1454,7 +1495,51 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     }
   };
   refresh_origins(0);
+  // kSym, kMul and kLora keep the copy target's addresses and move them on by a
+  // slab; they are found from the origins only where a run of slabs that lie
+  // behind each other begins (an item, a part of K, a last slab that reaches
+  // past K).  That is a third of the loop's scalar work, all of it in the copying
+  // waves, which the others wait for.
+  const char *run_a = nullptr, *run_b = nullptr;
+  int run_left = 0;         // slabs left of the run, the next one among them
+  bool run_tail = false;
+  constexpr bool kRuns = kFresh;
+  auto begin_run = [&]() __attribute__((always_inline)) {
+    const int d = ahead < 2 ? ahead : 2;
+    const int m0 = d == 0 ? om[0] : d == 1 ? om[1] : om[2];
+    const int n0 = d == 0 ? on[0] : d == 1 ? on[1] : on[2];
+    const int kb = d == 0 ? ok[0] : d == 1 ? ok[1] : ok[2];
+    const int part = d == 0 ? os[0] : d == 1 ? os[1] : os[2];
+    const int t = (kb > 0 ? kb : 0) + tc, left = slabs_of(d) - tc;
+    run_tail = MODE == kLora && kv < BK && t == nk - 1;
+    const CopyBaseT cb = slab_base(0, m0, n0, t, run_tail, part);
+    run_a = cb.a;
+    run_b = cb.b;
+    int len = left;
+    if constexpr (is_ortho(MODE)) {
+      const int part_left = (t < nk ? nk : t < 2 * nk ? 2 * nk : 3 * nk) - t;
+      len = left < part_left ? left : part_left;
+    } else {
+      if (kv < BK && !run_tail) len = left - 1;
+    }
+    run_left = __builtin_amdgcn_readfirstlane(len);
+  };
   auto advance_copy = [&]() __attribute__((always_inline)) {
+    if constexpr (kRuns) {
+      ++tc;
+      if (--run_left > 0) {
+        run_a += kAT ? BK * p.lda * 2 : BK * 2;
+        run_b += kBT ? BK * p.ldb * 2 : BK * 2;
+      } else if (cur + ahead < ntiles) {
+        if (tc == slabs_of(ahead < 2 ? ahead : 2)) {
+          tc = 0;
+          ++ahead;
+        }
+        // past the end: the last slab again
+        if (cur + ahead < ntiles) begin_run();
+      }
+      return;
+    }
     if (++tc == slabs_of(ahead < 2 ? ahead : 2)) {
       tc = 0;
       ++ahead;
@@ -1462,6 +1547,15 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   };
   // The copy target's sources and LDS stage.
   auto next_base = [&](int stage) __attribute__((always_inline)) {
+    if constexpr (kRuns) {
+      CopyBaseT cb;
+      cb.a = run_a;
+      cb.b = run_b;
+      cb.l = lds + stage * kStage;
+      cb.oa = MODE == kLora && LAY == 0 && run_tail ? offA_tail : offA;
+      cb.ob = MODE == kLora && LAY == 0 && run_tail ? offB_tail : offB;
+      return cb;
+    }
     const bool past = cur + ahead >= ntiles;
     const int d = ahead < 2 ? ahead : 2;
     const int m0 = d == 0 ? om[0] : d == 1 ? om[1] : om[2];
@@ -1472,8 +1566,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       return slab_base(stage, m0, n0, t, kv < BK && (t == nk_part - 1 || t == nk_all - 1), 0);
     } else {
       const int part = MODE == kGradW || is_ortho(MODE) ? (d == 0 ? os[0] : d == 1 ? os[1] : os[2]) : 0;
-      const int t = past ? nk - 1 : tc;
-      return slab_base(stage, m0, n0, kb + t, RAG && kv < BK && t == nk - 1, part);
+      const int t = past ? (is_ortho(MODE) ? slabs_of(d) : nk) - 1 : tc;
+      return slab_base(stage, m0, n0, (MODE == kSym && kb < 0 ? 0 : kb) + t, RAG && kv < BK && t == nk - 1, part);
     }
   };
   auto copy_next = [&](int stage) __attribute__((always_inline)) {
@@ -1552,7 +1646,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         }
         __builtin_amdgcn_sched_barrier(0);
       });
-      advance_copy();
+      if constexpr (kCp || !kRuns) advance_copy();
       return;
     }
     // First half: step 0 of slab gs, with the loads of step 1.
@@ -1582,12 +1676,13 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    advance_copy();
+    if constexpr (kCp || !kRuns) advance_copy();
   };
   typedef std::integral_constant<bool, true> yes;
   typedef std::integral_constant<bool, false> no;
 
   // Prologue: slab 0 (tile 0), then slab 1 in flight.
+  if constexpr (kRuns) begin_run();
   if (copier) copy_next(0);
   advance_copy();
   wait_and_sync();
@@ -1687,12 +1782,13 @@ hipError_t launch_ortho(const Args16& a, const OrthoExtra& x, int batch, int slo
   typedef Config<BM, BN, BK, WAVES_M, WAVES_N, COPY_SEL> C;
   const int64_t tm = (a.M + BM - 1) / BM, tn = (a.N + BN - 1) / BN;
   const int64_t each = MODE == kSym ? tm * (tm + 1) / 2 : tm * tn;
-  const int64_t tiles = each * batch;
+  const int64_t items = MODE == kSym ? x.whole + (int64_t)x.rest * x.splits : each * batch;
   // (xcd_order32; the rows of kSym are found in fp32 within one of the place)
-  if (tiles >= (int64_t(1) << 31) || each >= (int64_t(1) << 24)) return hipErrorInvalidValue;
-  int64_t grid = tiles < slots ? tiles : slots;
-  if (grid < 1) grid = 1;
-  OrthoTileArgs ta{a, tiles, x};
+  if (items >= (int64_t(1) << 31) || each >= (int64_t(1) << 24) ||
+      (MODE == kSym && x.whole + (int64_t)x.rest != each * batch))
+    return hipErrorInvalidValue;
+  const int64_t grid = items < slots ? items : slots;
+  OrthoTileArgs ta{a, items, x};
   ta.x.tiles_each = (uint32_t)each;
   void* args[] = {&ta};
   return hipLaunchKernel((const void*)hgemm_nt_kernel<BM, BN, BK, WAVES_M, WAVES_N, GM, COPY_SEL,

@@ -195,8 +195,21 @@ struct Plan {
   bool x_lo, x0_lo;      // iterates, the first one, have a second value
   size_t x, a, sums, coef;   // bytes of one buffer
   int x_count, a_count;
-  size_t total() const { return x_count * x + a_count * a + sums + coef; }
+  size_t cut;            // fp32 sums of tiles whose K is cut into ranges
+  size_t total() const { return x_count * x + a_count * a + sums + coef + cut; }
 };
+
+// The parts of a step's products (see `parts` below) depend on which iterates
+// are held in two values: iterate i, of `steps` steps.
+bool held(const Plan& p, int i, int steps) {
+  // (an iterate that only the last step reads needs no second value)
+  return p.fine ? i > 0 || p.x0_lo : i + 1 < steps && i < kSplitSteps && (i > 0 || p.x0_lo);
+}
+// X X^T and A^2 of a step.
+SymPlan plan_gram(const Plan& p, int L, bool lo) {
+  return plan_sym(p.sp, (p.fine && lo ? 3 : 1) * (p.tp / 64), L);
+}
+SymPlan plan_square(const Plan& p, int L) { return plan_sym(p.sp, (p.fine ? 3 : 1) * (p.sp / 64), L); }
 
 Plan make_plan(int type_g, int type_o, int L, int m, int n, int steps) {
   Plan p;
@@ -216,6 +229,8 @@ Plan make_plan(int type_g, int type_o, int L, int m, int n, int steps) {
   p.coef = round256((size_t)L * 3 * sizeof(float));
   p.x_count = 2 + (p.x_lo || p.x0_lo ? 2 : 0);
   p.a_count = p.fine ? 4 : 2;
+  p.cut = plan_square(p, L).sum_bytes();
+  for (bool lo : {false, true}) p.cut = std::max(p.cut, plan_gram(p, L, lo).sum_bytes());
   return p;
 }
 
@@ -290,6 +305,7 @@ MI355TUNE_API int gemm_ortho(int type_g, int type_o, int L, int m, int n, const 
                reinterpret_cast<float*>(ws + p.sums), (double)eps, x[0][0],
                p.x0_lo ? x[0][1] : nullptr, (int64_t)p.sp * p.tp,
                (int64_t)(p.sp / 64) * (p.tp / 64), p.sp, p.tp};
+  float* cut = reinterpret_cast<float*>(ws + p.sums + p.coef);
   hipError_t e = launch_tiles((const void*)norm_kernel, st, (int64_t)L * p.blocks, kThreads, 0, s);
   if (e != hipSuccess) return to_status(e);
   const int64_t per = ((int64_t)p.sp * (p.tp / 8) + kThreads - 1) / kThreads;
@@ -313,11 +329,7 @@ MI355TUNE_API int gemm_ortho(int type_g, int type_o, int L, int m, int n, const 
   for (int k = 0; k < steps; ++k) {
     const float* f = coeffs + 3 * k;
     const bool last = k + 1 == steps;
-    // (an iterate that only the last step reads needs no second value)
-    auto held = [&](int i) {
-      return p.fine ? i > 0 || p.x0_lo : i + 1 < steps && i < kSplitSteps && (i > 0 || p.x0_lo);
-    };
-    const bool lo = held(k);
+    const bool lo = held(p, k, steps);
     Args16 g{nullptr, nullptr, nullptr, p.tp, p.tp, p.sp, p.sp, p.sp, p.tp};
     OrthoExtra y;
     parts(y, x[cur], x[cur], p.fine && lo, p.fine && lo);
@@ -326,7 +338,8 @@ MI355TUNE_API int gemm_ortho(int type_g, int type_o, int L, int m, int n, const 
     y.hi = a[0];
     y.lo = a[1];
     y.alpha = ldexpf(1.f, kScaleA - 2 * kScaleX);
-    e = launch_sym_tiles(g, y, L, cus, s);
+    y.sum = cut;
+    e = launch_sym_tiles(g, y, plan_gram(p, L, lo), L, cus, s);
     if (e != hipSuccess) return to_status(e);
 
     g.lda = g.ldb = p.sp;
@@ -342,7 +355,8 @@ MI355TUNE_API int gemm_ortho(int type_g, int type_o, int L, int m, int n, const 
     y.beta = f[1];
     y.gamma = ldexpf(f[0], kScaleA);
     y.coef = k == 0 ? st.coef : nullptr;
-    e = launch_sym_tiles(g, y, L, cus, s);
+    y.sum = cut;
+    e = launch_sym_tiles(g, y, plan_square(p, L), L, cus, s);
     if (e != hipSuccess) return to_status(e);
 
     y = OrthoExtra();
@@ -369,7 +383,7 @@ MI355TUNE_API int gemm_ortho(int type_g, int type_o, int L, int m, int n, const 
     } else {
       y.alpha = ldexpf(1.f, -kScaleA);
       y.hi = x[1 - cur][0];
-      y.lo = held(k + 1) ? x[1 - cur][1] : nullptr;
+      y.lo = held(p, k + 1, steps) ? x[1 - cur][1] : nullptr;
       y.stride_c = stride_x;
     }
     e = launch_mul_tiles(g, y, turned, L, cus, s);
