@@ -76,33 +76,6 @@ __device__ __forceinline__ f4 mfma16(h8 a, h8 b, f4 c) {
                                                    __builtin_bit_cast(b8, b), c, 0, 0, 0);
   }
 }
-// A product whose one operand is held in two values, hi + lo: in one
-// instruction of half the k (hi holds hi in its first 16 k, lo in the others;
-// the other operand the same 16 twice), or `two`.  SECOND: hi and lo are the
-// instruction's second operand.  An infinity in `b` meets hi alone: lo's sign
-// need not be hi's, and their sum would be NaN.
-template <int FMT, bool SECOND>
-__device__ __forceinline__ f4 mfma_split(h8 hi, h8 lo, h8 b, bool two, int lane) {
-  auto mul = [](h8 t, h8 u, f4 c) __attribute__((always_inline)) {
-    return SECOND ? mfma16<FMT>(u, t, c) : mfma16<FMT>(t, u, c);
-  };
-  const f4 h = mul(hi, b, f4{0.f, 0.f, 0.f, 0.f});
-  f4 s = h;
-  if (two) s = mul(lo, b, h);
-  bool fine = true;
-#pragma unroll
-  for (int v = 0; v < 4; ++v) fine = fine && __builtin_fabsf(s[v]) < __builtin_inff();
-  if (__ballot(!fine)) {
-    f4 first = h;
-    if (!two) {
-      const bool low = (lane & 32) == 0;
-      first = mul(low ? hi : h8{}, low ? b : h8{}, f4{0.f, 0.f, 0.f, 0.f});
-    }
-#pragma unroll
-    for (int v = 0; v < 4; ++v) s[v] = __builtin_fabsf(s[v]) < __builtin_inff() ? s[v] : first[v];
-  }
-  return s;
-}
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(1))) const void gbl_void_t;
 
@@ -316,16 +289,17 @@ struct OrthoTileArgs {
 };
 // kLora.  Row m < m_end adds sum_k factor[m][k] (t2[m] block k) . B_a[n], with
 // a = ids[m], where 0 <= a < S; a >= S makes the row NaN, a < 0 adds nothing.
-// A block is w ranks: 16, as 16 values of t2 and 16 more against the same 16
-// of B in one product, or 32, in two products (t2's values are hi + lo).
+// A block is 16 ranks: 16 values of t2 and 16 more (hi and lo) against the same
+// 16 of B, the 32 k of one matrix-core product.
 struct LoraExtra {
   const half_t* t2 = nullptr;      // [m_end][ld2]
   int64_t ld2 = 0;
   const float* factor = nullptr;   // [m_end][blocks]
-  const half_t* B = nullptr;       // [S][n_end][ldb], R columns
+  const half_t* B = nullptr;       // [S][n_end][ldb], R columns, a multiple of 8;
+                                   //   ldb < 2^22 (32-bit offsets of 128 rows)
   int64_t ldb = 0, stride_b = 0;
   const long long* ids = nullptr;
-  int R = 0, S = 0, w = 0, blocks = 0;
+  int R = 0, S = 0, blocks = 0;
   int m_end = 0, n_end = 0;
 };
 struct LoraTileArgs {
@@ -607,21 +581,6 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       cb.sa = (int64_t)C::kCopyWaves * C::kRowsPerCopy * lda * 2;
       cb.b = (const char*)((h ? ta.x.B2 : p.B) + k0 * p.ldb + n0) + firstTB;
       cb.oa = tail ? offA_x : offA;
-      cb.ob = offB;
-      return cb;
-    }
-    if constexpr (is_ortho(MODE)) {
-      const OrthoExtra& x = ta.x;
-      const int per = p.K / BK;
-      const int h = t < per ? 0 : t < 2 * per ? 1 : 2;
-      const int64_t k0 = (int64_t)(t - h * per) * BK;
-      const half_t* a = (h == 0 ? x.a[0] : h == 1 ? x.a[1] : x.a[2]) + part * x.stride_a;
-      const half_t* b = (h == 0 ? x.b[0] : h == 1 ? x.b[1] : x.b[2]) + part * x.stride_b;
-      cb.a = kAT ? (const char*)(a + k0 * p.lda + m0) + firstTA
-                 : (const char*)(a + (int64_t)m0 * p.lda) + firstA + 2 * k0;
-      cb.b = kBT ? (const char*)(b + k0 * p.ldb + n0) + firstTB
-                 : (const char*)(b + (int64_t)n0 * p.ldb) + firstB + 2 * k0;
-      cb.oa = offA;
       cb.ob = offB;
       return cb;
     }
@@ -923,6 +882,14 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   // computed from them cost spills inside it)
   constexpr bool kFresh = is_ortho(MODE) || MODE == kLora;
   int xl = 0, xr = 0, xg = 0;
+  // (and the kernel's arguments, which the compiler would otherwise hold in
+  // scalar registers throughout, and spill)
+  typedef const __attribute__((address_space(4))) TileArgsOf<MODE> KernArgs;
+  auto fresh_args = [&]() __attribute__((always_inline)) {
+    KernArgs* k = (KernArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(k));
+    return k;
+  };
   auto put = [&](int j, h4 o) __attribute__((always_inline)) {
     if constexpr (kFresh) {
       const int c = 2 * j + (xg >> 1);
@@ -1176,7 +1143,9 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         }
       }
     } else if constexpr (MODE == kSym) {
-      const OrthoExtra& x = ta.x;
+      KernArgs* args = fresh_args();
+      const auto& x = args->x;
+      const auto& p = args->p;
       float alpha = x.alpha, beta = x.beta, gamma = x.gamma;
       if (x.coef) {
         alpha *= x.coef[3 * part];
@@ -1252,7 +1221,9 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         }
       }
     } else if constexpr (MODE == kMul) {
-      const OrthoExtra& x = ta.x;
+      KernArgs* args = fresh_args();
+      const auto& x = args->x;
+      const auto& p = args->p;
 #pragma unroll
       for (int i = 0; i < C::kBlocksM; ++i) {
         const int m = m0 + wm + 16 * i;
@@ -1301,7 +1272,9 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         }
       }
     } else if constexpr (MODE == kLora) {
-      const LoraExtra& x = ta.x;
+      KernArgs* args = fresh_args();
+      const auto& x = args->x;
+      const auto& p = args->p;
       // lane l stands for row l of the wave's
       const int ml = m0 + wm + xl;
       int mine = -1;
@@ -1315,74 +1288,114 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(pending));
         const uint64_t rows = __ballot(mine == a);
         pending &= ~rows;
-        const half_t* b = x.B + a * x.stride_b;
+        // scalar bases, and 32-bit offsets of the lanes from them (rows past the
+        // end: the last one)
+        const int mb = m0 + wm < x.m_end ? m0 + wm : x.m_end - 1, m_last = x.m_end - 1 - mb;
+        const int nb = n0 + wn < x.n_end ? n0 + wn : x.n_end - 1, n_last = x.n_end - 1 - nb;
+        const char* t2 = (const char*)(x.t2 + (int64_t)mb * x.ld2);
+        const char* factor = (const char*)(x.factor + (int64_t)mb * x.blocks);
+        const char* b = (const char*)(x.B + a * x.stride_b + (int64_t)nb * x.ldb);
+        const uint32_t ld2 = (uint32_t)x.ld2 * 2, ldb = (uint32_t)x.ldb * 2;
         for (int k = 0; k < x.blocks; ++k) {
-          h8 hi[C::kBlocksM], lo[C::kBlocksM];
+          h8 tv[C::kBlocksM];
           float f[C::kBlocksM];
 #pragma unroll
           for (int i = 0; i < C::kBlocksM; ++i) {
-            // (rows of other adapters, and past the end: any values, times 0)
-            const int m = m0 + wm + 16 * i + xr, mc = m < x.m_end ? m : x.m_end - 1;
-            const half_t* t2 = x.t2 + (int64_t)mc * x.ld2 + 2 * x.w * k;
-            hi[i] = *(const h8*)(t2 + 8 * xg);
-            lo[i] = x.w == 32 ? *(const h8*)(t2 + 32 + 8 * xg) : h8{};
-            f[i] = x.factor[(int64_t)mc * x.blocks + k];
+            // (rows of other adapters, and past the end: any values, dropped below)
+            const uint32_t m = min(16 * i + xr, m_last);
+            tv[i] = *(const h8*)(t2 + (m * ld2 + 64 * k + 16 * xg));
+            const float v = *(const float*)(factor + 4 * (m * x.blocks + k));
+            f[i] = rows >> (16 * i + xr) & 1 ? v : 0.f;
           }
-          const int at = x.w == 16 ? 8 * (xg & 1) : 32 * k + 8 * xg;
-#pragma unroll
-          for (int j = 0; j < C::kBlocksN; ++j) {
-            const int n = n0 + wn + 16 * j + xr;
-            const half_t* row = b + (int64_t)(n < x.n_end ? n : x.n_end - 1) * x.ldb;
-            h8 bv = {};
-            if (at + 8 <= x.R) {
-              __builtin_memcpy(&bv, row + at, 16);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (at + e < x.R) bv[e] = row[at + e];
-            }
+          const int at = 16 * k + 8 * (xg & 1);
+          auto load_b = [&](int j) __attribute__((always_inline)) {
+            const uint32_t n = min(16 * j + xr, n_last);
+            h8 v = {};
+            if (at < x.R) __builtin_memcpy(&v, b + (n * ldb + 2 * at), 16);
+            return v;
+          };
+          // (one block of columns ahead and no more, and no branches: the
+          // accumulators leave few registers)
+          h8 next = load_b(0);
+          static_for<C::kBlocksN>([&](auto jc) __attribute__((always_inline)) {
+            constexpr int j = decltype(jc)::value;
+            const h8 bv = next;
+            if constexpr (j + 1 < C::kBlocksN) next = load_b(j + 1);
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int i = 0; i < C::kBlocksM; ++i) {
-              if (!(rows >> (16 * i) & 0xFFFF)) continue;
-              const f4 s = mfma_split<FMT, true>(hi[i], lo[i], bv, x.w == 32, xl);
+              const f4 s = mfma16<FMT>(bv, tv[i], f4{0.f, 0.f, 0.f, 0.f});
               const bool own = rows >> (16 * i + xr) & 1;
 #pragma unroll
-              for (int v = 0; v < 4; ++v) acc[i][j][v] += own ? f[i] * s[v] : 0.f;
+              for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(f[i], own ? s[v] : 0.f, acc[i][j][v]);
             }
-          }
+            __builtin_amdgcn_sched_barrier(0);
+          });
         }
       }
-      h4 bq[C::kBlocksN];
+      if (unknown) {
 #pragma unroll
-      for (int j = 0; j < C::kBlocksN; ++j) {
-        bq[j] = h4{};
-        const int n = n0 + wn + 16 * j + 4 * xg;
-        if (p.bias) {
+        for (int i = 0; i < C::kBlocksM; ++i)
+          if (unknown >> (16 * i + xr) & 1) {
+#pragma unroll
+            for (int j = 0; j < C::kBlocksN; ++j) acc[i][j] = acc[i][j] * __builtin_nanf("");
+          }
+      }
+      // The write-back, each part for the whole tile at once if it is asked for.
+      if (p.bias) {
+#pragma unroll
+        for (int j = 0; j < C::kBlocksN; ++j) {
+          const int n = n0 + wn + 16 * j + 4 * xg;
+          f4 bias;
 #pragma unroll
           for (int v = 0; v < 4; ++v)
-            if (n + v < x.n_end) bq[j][v] = p.bias[n + v];
+            bias[v] = word_to_f32<FMT>(p.bias[n + v < x.n_end ? n + v : x.n_end - 1]);
+#pragma unroll
+          for (int i = 0; i < C::kBlocksM; ++i) acc[i][j] += bias;
+        }
+      }
+      if (p.act == GEMM_ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < C::kBlocksM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[i][j][v] = epi_silu(acc[i][j][v]);
+      } else if (p.act == GEMM_ACT_RELU) {
+#pragma unroll
+        for (int i = 0; i < C::kBlocksM; ++i)
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[i][j][v] = gate_relu(acc[i][j][v]);
+      }
+      if (p.res) {
+        // (rows and columns of another tile are left to it: the residual may be C)
+#pragma unroll
+        for (int i = 0; i < C::kBlocksM; ++i) {
+          const int m = m0 + wm + 16 * i + xr;
+          if (m < mlo || m >= x.m_end) continue;
+          const half_t* res = p.res + (int64_t)m * p.ldr;
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j) {
+            const int n = n0 + wn + 16 * j + 4 * xg;
+            h4 q = {};
+            if (n >= nlo && n + 4 <= x.n_end) {
+              __builtin_memcpy(&q, res + n, 8);
+            } else {
+#pragma unroll
+              for (int v = 0; v < 4; ++v)
+                if (n + v >= nlo && n + v < x.n_end) q[v] = res[n + v];
+            }
+#pragma unroll
+            for (int v = 0; v < 4; ++v) acc[i][j][v] += word_to_f32<FMT>(q[v]);
+          }
         }
       }
 #pragma unroll
       for (int i = 0; i < C::kBlocksM; ++i) {
-        const int m = m0 + wm + 16 * i + xr;
-        const bool nan = unknown >> (16 * i + xr) & 1;
 #pragma unroll
-        for (int j = 0; j < C::kBlocksN; ++j) {
-          const int n = n0 + wn + 16 * j + 4 * xg;
-          f4 z = acc[i][j];
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            z[v] = gate_act((nan ? __builtin_nanf("") : z[v]) + word_to_f32<FMT>(bq[j][v]), p.act);
-          if (p.res && m >= mlo && m < x.m_end) {
-            // (rows and columns of another tile are left to it: the residual may be C)
-            const half_t* q = p.res + (int64_t)m * p.ldr + n;
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              if (n + v >= nlo && n + v < x.n_end) z[v] += word_to_f32<FMT>(q[v]);
-          }
-          put(j, round4(z));
-        }
+        for (int j = 0; j < C::kBlocksN; ++j) put(j, round4(acc[i][j]));
         flush(p.C, p.ldc, m0 + wm + 16 * i, n0 + wn, C::WN, mlo, x.m_end, nlo, x.n_end);
       }
     }
@@ -1511,17 +1524,31 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     const int kb = d == 0 ? ok[0] : d == 1 ? ok[1] : ok[2];
     const int part = d == 0 ? os[0] : d == 1 ? os[1] : os[2];
     const int t = (kb > 0 ? kb : 0) + tc, left = slabs_of(d) - tc;
-    run_tail = MODE == kLora && kv < BK && t == nk - 1;
-    const CopyBaseT cb = slab_base(0, m0, n0, t, run_tail, part);
-    run_a = cb.a;
-    run_b = cb.b;
+    KernArgs* args = fresh_args();
+    const auto& p = args->p;
+    const half_t *a, *b;
+    int64_t k0;
     int len = left;
     if constexpr (is_ortho(MODE)) {
-      const int part_left = (t < nk ? nk : t < 2 * nk ? 2 * nk : 3 * nk) - t;
+      const auto& x = args->x;
+      const int h = t < nk ? 0 : t < 2 * nk ? 1 : 2;
+      k0 = (int64_t)(t - h * nk) * BK;
+      a = x.a[h] + part * x.stride_a;
+      b = x.b[h] + part * x.stride_b;
+      const int part_left = (h + 1) * nk - t;
       len = left < part_left ? left : part_left;
     } else {
+      // (LAY 1 with a K tail: the last slab from K - 64, see slab_base)
+      run_tail = kv < BK && t == nk - 1;
+      k0 = LAY != 0 && run_tail ? (int64_t)p.K - BK : (int64_t)t * BK;
+      a = p.A;
+      b = p.B;
       if (kv < BK && !run_tail) len = left - 1;
     }
+    run_a = kAT ? (const char*)(a + k0 * p.lda + m0) + firstTA
+                : (const char*)(a + (int64_t)m0 * p.lda + k0) + firstA;
+    run_b = kBT ? (const char*)(b + k0 * p.ldb + n0) + firstTB
+                : (const char*)(b + (int64_t)n0 * p.ldb + k0) + firstB;
     run_left = __builtin_amdgcn_readfirstlane(len);
   };
   auto advance_copy = [&]() __attribute__((always_inline)) {

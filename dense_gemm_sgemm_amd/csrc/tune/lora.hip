@@ -36,17 +36,18 @@ bool by_rows(int M, int N, Mat x, Mat w) {
 }
 
 struct Plan {
-  size_t t2, factor, x = 0, w = 0;
-  size_t total() const { return t2 + factor + x + w; }
+  size_t t2, factor, x = 0, w = 0, b = 0;
+  size_t total() const { return t2 + factor + x + w + b; }
 };
-Plan make_plan(int M, int N, int K, int R, Mat x, Mat w) {
-  const Ranks ranks(R);
+Plan make_plan(int M, int N, int K, int R, int S, Mat x, Mat w, int ldb) {
   Plan p;
-  p.t2 = round256((size_t)M * ranks.ld2() * 2);
-  p.factor = round256((size_t)M * ranks.blocks * sizeof(float));
+  p.t2 = round256((size_t)M * rank_ld2(R) * 2);
+  p.factor = round256((size_t)M * rank_blocks(R) * sizeof(float));
   if (N > 0 && !by_rows(M, N, x, w)) {
     if (needs_copy(x.p, x.ld, M, K)) p.x = copy_bytes(M, K);
     if (needs_copy(w.p, w.ld, N, K)) p.w = copy_bytes(N, K);
+    // (the tiles read B's ranks eight at a time, at 32-bit offsets)
+    if (R % 8 != 0 || ldb >= 1 << 22) p.b = round256((size_t)S * N * 16 * rank_blocks(R) * 2);
   }
   return p;
 }
@@ -69,7 +70,6 @@ size_t copy_bytes_w(int N, int K) {
   return round256((size_t)pad_k(pad_rows(N)) * line_ld(pad_k(K)) * 2);
 }
 BwdPlan plan_bwd(int M, int N, int K, int R, int S, Mat c, Mat w, bool dx, bool da, bool db) {
-  const Ranks ranks(R);
   BwdPlan p;
   p.dx = dx && M > 0 && K > 0;
   p.da = da && S > 0 && K > 0;
@@ -79,9 +79,9 @@ BwdPlan plan_bwd(int M, int N, int K, int R, int S, Mat c, Mat w, bool dx, bool 
     if (p.da) p.dt = round256((size_t)M * R * sizeof(float));
   }
   if (p.dx) {
-    p.t2 = round256((size_t)M * ranks.ld2() * 2);
-    p.factor = round256((size_t)M * ranks.blocks * sizeof(float));
-    p.at = round256((size_t)S * K * ranks.padded * 2);
+    p.t2 = round256((size_t)M * rank_ld2(R) * 2);
+    p.factor = round256((size_t)M * rank_blocks(R) * sizeof(float));
+    p.at = round256((size_t)S * K * 16 * rank_blocks(R) * 2);
     const int Kd = pad_k(N);
     if (needs_copy(c.p, c.ld, M, N)) p.copy_c = copy_bytes(M, N);
     if (needs_copy(w.p, w.ld, N, K) || Kd != N) p.copy_w = copy_bytes_w(N, K);
@@ -116,11 +116,11 @@ extern "C" {
 
 MI355TUNE_API unsigned long long gemm_lora_workspace(int type, int M, int N, int K, int R, int S,
                                                      const void* X, int ldx, const void* W,
-                                                     int ldw) {
+                                                     int ldw, int ldb) {
   if (check(type, M, N, K, R, S) != GEMM_OK || M == 0 || bad_ld(ldx, K) ||
       (N > 0 && bad_ld(ldw, K)))
     return 0;
-  return make_plan(M, N, K, R, Mat{in16(X), ldx}, Mat{in16(W), ldw}).total();
+  return make_plan(M, N, K, R, S, Mat{in16(X), ldx}, Mat{in16(W), ldw}, ldb).total();
 }
 
 MI355TUNE_API int gemm_lora(int type, int M, int N, int K, int R, int S, const void* X, int ldx,
@@ -142,19 +142,18 @@ MI355TUNE_API int gemm_lora(int type, int M, int N, int K, int R, int S, const v
       (N > 0 && (C == nullptr || (K > 0 && W == nullptr) || (S > 0 && B == nullptr))))
     return GEMM_ERR_NULL_POINTER;
   const Mat x0{in16(X), ldx}, w0{in16(W), ldw};
-  const Plan p = make_plan(M, N, K, R, x0, w0);
+  const Plan p = make_plan(M, N, K, R, S, x0, w0, ldb);
   if (!workspace_ok(p.total(), workspace, workspace_bytes)) return GEMM_ERR_WORKSPACE;
   const int cus = check_device();
   if (cus < 0) return cus;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int fmt = type == GEMM_TYPE_BF16 ? kFmtBF16 : kFmtF16;
-  const Ranks ranks(R);
   char* ws = static_cast<char*>(workspace);
   half_t* t2 = reinterpret_cast<half_t*>(ws);
   float* factor = reinterpret_cast<float*>(ws + p.t2);
   ws += p.t2 + p.factor;
-  const ShrinkArgs sh{in16(X), in16(A), ldx, lda, stride_a, ids, scales, t2, factor, ranks.ld2(),
-                      T, ldt, M, K, R, S, ranks.w, ranks.blocks, R};
+  const ShrinkArgs sh{in16(X), in16(A), ldx, lda, stride_a, ids, scales, t2, factor, rank_ld2(R),
+                      T, ldt, M, K, R, S};
   hipError_t e = launch_shrink(fmt, sh, s);
   if (e != hipSuccess || N == 0) return to_status(e);
   Args16 a{x0.p, w0.p, out16(C), ldx, ldw, ldc, M, N, K};
@@ -163,13 +162,21 @@ MI355TUNE_API int gemm_lora(int type, int M, int N, int K, int R, int S, const v
   a.ldr = ldr;
   a.act = act;
   a.fmt = fmt;
-  const LoraExtra y{t2, ranks.ld2(), factor, in16(B), ldb, stride_b, ids, R, S, ranks.w,
-                    ranks.blocks, M, N};
+  LoraExtra y{t2, rank_ld2(R), factor, in16(B), ldb, stride_b, ids, R, S,
+                    rank_blocks(R), M, N};
   if (by_rows(M, N, x0, w0)) return to_status(launch_lora_rows(a, y, cus, s));
   PadJobs jobs;
   const Mat x = jobs.add(x0, M, K, ws), w = jobs.add(w0, N, K, ws);
   e = launch_pad(jobs, s);
   if (e != hipSuccess) return to_status(e);
+  if (p.b) {
+    y.B = reinterpret_cast<half_t*>(ws);
+    y.ldb = y.R = 16 * rank_blocks(R);
+    y.stride_b = N * y.ldb;
+    e = launch_widen(WidenArgs{in16(B), reinterpret_cast<half_t*>(ws), ldb, stride_b, N, R, y.R, S},
+                     s);
+    if (e != hipSuccess) return to_status(e);
+  }
   a.A = x.p;
   a.lda = x.ld;
   a.B = w.p;
@@ -221,7 +228,6 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S, con
   if (cus < 0) return cus;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int fmt = type == GEMM_TYPE_BF16 ? kFmtBF16 : kFmtF16;
-  const Ranks ranks(R);
   char* ws = static_cast<char*>(workspace);
   auto take = [&](size_t bytes) {
     char* at = bytes ? ws : nullptr;
@@ -249,12 +255,12 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S, con
     // B^T as the second operand of dt = dC B, A^T of dX's part
     const TurnArgs tb{in16(B), bt, ldb, stride_b, ldbt, (int64_t)R * ldbt,
                       N, (int)round_up(N, 8), R, S};
-    const TurnArgs ta{in16(A), at, lda, stride_a, ranks.padded, (int64_t)K * ranks.padded,
-                      R, ranks.padded, K, S};
+    const TurnArgs ta{in16(A), at, lda, stride_a, 16 * rank_blocks(R), (int64_t)K * 16 * rank_blocks(R),
+                      R, 16 * rank_blocks(R), K, S};
     if (N > 0 || p.dx) e = launch_turn(N > 0 ? tb : ta, N > 0 && p.dx ? &ta : nullptr, s);
     if (e != hipSuccess) return to_status(e);
     const ShrinkArgs sh{c0.p, bt, lddc, ldbt, (int64_t)R * ldbt, ids, scales, t2, factor,
-                        ranks.ld2(), dt32, R, M, N, R, S, ranks.w, ranks.blocks, R};
+                        rank_ld2(R), dt32, R, M, N, R, S};
     e = launch_shrink(fmt, sh, s);
     if (e != hipSuccess) return to_status(e);
   }
@@ -295,8 +301,8 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S, con
     if (e != hipSuccess) return to_status(e);
     Args16 a{c.p, w.p, out16(dX), c.ld, w.ld, lddx, pad_rows(M), pad_k(K), pad_k(N)};
     a.fmt = fmt;
-    const LoraExtra y{t2, ranks.ld2(), factor, at, ranks.padded, (int64_t)K * ranks.padded, ids,
-                      ranks.padded, S, ranks.w, ranks.blocks, M, K};
+    const LoraExtra y{t2, rank_ld2(R), factor, at, 16 * rank_blocks(R), (int64_t)K * 16 * rank_blocks(R), ids,
+                      16 * rank_blocks(R), S, rank_blocks(R), M, K};
     e = launch_lora_tiles(a, y, true, cus, s);
   }
   return to_status(e);

@@ -19,6 +19,7 @@ namespace {
 
 using hgemm::f4;
 using hgemm::h8;
+using hgemm::mfma16;
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int i4 __attribute__((ext_vector_type(4)));
 
@@ -104,9 +105,8 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(GradArgs p, int64_t base
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
   __syncthreads();
   top = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
-  const int e = top == 0.f ? 13 : (int)(__float_as_uint(fmaxf(top, 0x1p-100f)) >> 23) - 127;
-  const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
-  const float down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+  float up, down;
+  scale_for(top, up, down);
   if (threadIdx.x == 0) job.step_factor[step] = down * (p.scales ? p.scales[a] : 1.f);
   const int64_t ld = 32 * (int64_t)p.g.steps, half = ld * p.padded;
   // a thread a rank and 8 rows
@@ -117,9 +117,10 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(GradArgs p, int64_t base
     for (int i = 0; i < 8; ++i) {
       const int m = row[8 * q + i];
       if (m < 0 || rank >= p.R) continue;
-      const float v = job.left[m * job.ld_left + rank] * up;
-      hi[i] = f32_to_word<FMT>(v);
-      lo[i] = f32_to_word<FMT>(fabsf(v) < __builtin_inff() ? v - word_to_f32<FMT>(hi[i]) : 0.f);
+      half_t a, b;
+      split_value<FMT>(job.left[m * job.ld_left + rank] * up, a, b);
+      hi[i] = a;
+      lo[i] = b;
     }
     half_t* dst = job.pack + rank * ld + 32 * (int64_t)step + 8 * q;
     *(h8*)dst = hi;
@@ -266,7 +267,9 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(GradArgs p, int64_t base
       for (int e = 0; e < 8; ++e)
 #pragma unroll
         for (int q = 0; q < RB; ++q) {
-          acc[q][e] += hgemm::mfma_split<FMT, false>(hi[q], lo[q], x[e], true, lane) * f;
+          f4 d = mfma16<FMT>(hi[q], x[e], f4{0.f, 0.f, 0.f, 0.f});
+          d = mfma16<FMT>(lo[q], x[e], d);
+          acc[q][e] += d * f;
         }
     }
     // the waves' sums, 16 ranks at a time
@@ -363,6 +366,19 @@ __global__ __launch_bounds__(kThreads) void turn_kernel(TurnJobs jobs, int64_t b
     if (i + e < p.inner) v[e] = src[e * p.lds];
   *(h8*)(p.dst + l * p.stride_d + (int64_t)o * p.ldd + i) = v;
 }
+__global__ __launch_bounds__(kThreads) void widen_kernel(WidenArgs p, int64_t base) {
+  int64_t t = (base + blockIdx.x) * kThreads + threadIdx.x;
+  const int c = (int)(t % (p.cols_p / 8)) * 8;
+  t /= p.cols_p / 8;
+  const int64_t l = t / p.rows;
+  if (l >= p.count) return;
+  const half_t* src = p.src + l * p.stride_s + (t - l * p.rows) * p.lds;
+  h8 v = {};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (c + e < p.cols) v[e] = src[c + e];
+  *(h8*)(p.dst + t * p.cols_p + c) = v;
+}
 int64_t turn_blocks(const TurnArgs& p) {
   return ((int64_t)p.outer * (p.inner_p / 8) * p.count + kThreads - 1) / kThreads;
 }
@@ -424,6 +440,12 @@ hipError_t launch_turn(const TurnArgs& first, const TurnArgs* second, hipStream_
   TurnJobs jobs{{first, second ? *second : first}, turn_blocks(first)};
   return launch_tiles((const void*)turn_kernel, jobs,
                       jobs.blocks0 + (second ? turn_blocks(*second) : 0), kThreads, 0, stream);
+}
+
+hipError_t launch_widen(const WidenArgs& p, hipStream_t stream) {
+  const int64_t threads = (int64_t)p.count * p.rows * (p.cols_p / 8);
+  return launch_tiles((const void*)widen_kernel, p, (threads + kThreads - 1) / kThreads, kThreads,
+                      0, stream);
 }
 
 }  // namespace tune

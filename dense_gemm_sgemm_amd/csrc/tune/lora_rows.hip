@@ -20,6 +20,29 @@ struct RowsArgs {
   int waves;
 };
 
+// Columns at .. at + 7 of a row of R, zeros past it.  `room`: elements from the
+// row's start to the end of its matrix, up to which a whole 16-byte piece may
+// be loaded; what lies past the row is masked.
+__device__ __forceinline__ h8 load_ranks(const half_t* row, int at, int R, int64_t room) {
+  h8 v = {};
+  if (at + 8 <= room) {
+    __builtin_memcpy(&v, row + at, 16);
+    if (at + 8 > R) {
+      typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+      u32x4 w = __builtin_bit_cast(u32x4, v);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = at + 2 * e + 1 < R ? w[e] : at + 2 * e < R ? w[e] & 0xFFFFu : 0u;
+      v = __builtin_bit_cast(h8, w);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (at + e < R) v[e] = row[at + e];
+  }
+  return v;
+}
+
 template <int FMT, int MT>
 __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args, int64_t base) {
   constexpr int kS = MT == 4 ? 2 : kSteps, kC = 32 * kS;
@@ -94,16 +117,14 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
     if (d % args.waves != wave) continue;
     const half_t* b = y.B + a * y.stride_b + (int64_t)row * y.ldb;
     for (int k = 0; k < y.blocks; ++k) {
-      const int at = y.w == 16 ? 8 * (quarter & 1) : 32 * k + 8 * quarter;
-      const h8 bv = load_x<true>(b, at, y.R);
+      const h8 bv = load_ranks(b, 16 * k + 8 * (quarter & 1), y.R,
+                               (int64_t)(p.N - 1 - row) * y.ldb + y.R);
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         if (!(rows >> (16 * t) & 0xFFFF)) continue;
         const int m = m0 + 16 * t + r;
-        const half_t* t2 = y.t2 + (int64_t)(m < p.M ? m : p.M - 1) * y.ld2 + 2 * y.w * k;
-        const h8 hi = *(const h8*)(t2 + 8 * quarter);
-        const h8 lo = y.w == 32 ? *(const h8*)(t2 + 32 + 8 * quarter) : h8{};
-        const f4 s = hgemm::mfma_split<FMT, false>(hi, lo, bv, y.w == 32, lane);
+        const h8 tv = *(const h8*)(y.t2 + (m < p.M ? m : p.M - 1) * y.ld2 + 32 * k + 8 * quarter);
+        const f4 s = mfma16<FMT>(tv, bv, f4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int i = 16 * t + 4 * quarter + v;

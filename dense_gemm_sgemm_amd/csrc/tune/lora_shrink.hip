@@ -41,7 +41,7 @@ __global__ __launch_bounds__(64 * kWaves) void shrink_kernel(ShrinkArgs p, int64
 #pragma unroll 4
       for (int i = 0; i < 16; ++i) {
         const int other = __builtin_amdgcn_readlane(mine, i), c = first + 16 * q + r;
-        if (other < 0 && m0 + i < p.M && c < p.cols32)
+        if (other < 0 && m0 + i < p.M && c < p.R)
           p.t32[(int64_t)(m0 + i) * p.ldt + c] = other == -1 ? 0.f : __builtin_nanf("");
       }
   }
@@ -88,6 +88,7 @@ __global__ __launch_bounds__(64 * kWaves) void shrink_kernel(ShrinkArgs p, int64
   add_waves<RB>(acc, reinterpret_cast<float*>(lds), wave, lane, kWaves);
   if (wave > 0) return;
 
+  const int blocks = rank_blocks(p.R);
   // acc[q][v]: row 4 quarter + v, rank first + 16 q + r
 #pragma unroll
   for (int q = 0; q < RB; ++q)
@@ -100,38 +101,23 @@ __global__ __launch_bounds__(64 * kWaves) void shrink_kernel(ShrinkArgs p, int64
     if (p.t32 && live) {
 #pragma unroll
       for (int q = 0; q < RB; ++q)
-        if (first + 16 * q + r < p.cols32) p.t32[m * p.ldt + first + 16 * q + r] = acc[q][v];
+        if (first + 16 * q + r < p.R) p.t32[m * p.ldt + first + 16 * q + r] = acc[q][v];
     }
     if (!p.t2) continue;
     const float scale = p.scales ? p.scales[a] : 1.f;
-    constexpr int kPer = RB == 1 ? 1 : 2;   // 16-rank groups of a block (w / 16)
 #pragma unroll
-    for (int b = 0; b < RB / kPer; ++b) {
-      const int block = first / p.w + b;
-      float top = 0.f;
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const float t = fabsf(acc[kPer * b + u][v]);
-        top = fmaxf(top, t < __builtin_inff() ? t : 0.f);
-      }
+    for (int q = 0; q < RB; ++q) {
+      const float t = acc[q][v];
+      float top = fabsf(t), up, down;
+      if (!(top < __builtin_inff())) top = 0.f;
 #pragma unroll
       for (int k = 8; k >= 1; k /= 2) top = fmaxf(top, __shfl_xor(top, k));
-      // 2^(13 - floor(log2 top)), within what fp32 holds
-      const int e = top == 0.f ? 13 : (int)(__float_as_uint(fmaxf(top, 0x1p-100f)) >> 23) - 127;
-      const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
-      const float down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
-      if (live && block < p.blocks) {
-        half_t* dst = p.t2 + m * p.ld2 + 2 * p.w * (int64_t)block + r;
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-          const float t = acc[kPer * b + u][v] * up;
-          const half_t hi = f32_to_word<FMT>(t);
-          const float left = t - word_to_f32<FMT>(hi);
-          dst[16 * u] = hi;
-          // (infinite and NaN: hi says it)
-          dst[p.w + 16 * u] = f32_to_word<FMT>(fabsf(t) < __builtin_inff() ? left : 0.f);
-        }
-        if (r == 0) p.factor[m * p.blocks + block] = down * scale;
+      scale_for(top, up, down);
+      const int block = first / 16 + q;
+      if (live && block < blocks) {
+        half_t* dst = p.t2 + m * p.ld2 + 32 * block + r;
+        split_value<FMT>(t * up, dst[0], dst[16]);
+        if (r == 0) p.factor[m * blocks + block] = down * scale;
       }
     }
   }

@@ -33,24 +33,42 @@ hipError_t launch_mul_tiles(const Args16& a, const OrthoExtra& x, bool a_kmajor,
 // A row's product with its adapter's first factor, t[m][r] = sum_k X[m][k]
 // A_a[r][k], is needed as an operand of the matrix cores.  Rounded to the type
 // it would carry an error of its own as large as the output's; so it is kept
-// in two 16-bit values, hi + lo, which in the second product are 32 more k a
-// block of ranks.  Both are stored times a power of two for the row's block
-// that brings the largest of its ranks to 2^13 .. 2^14, so that neither leaves
-// binary16's normal range; the factor that undoes it, times the adapter's
-// scale, is applied to the block's sums in fp32.
+// in two 16-bit values, hi + lo, against the same values of the other factor:
+// 16 ranks are the 32 k of one instruction.  Both are stored times a power of
+// two for the row's block of 16 ranks that brings the largest of them to 2^13
+// .. 2^14, so that neither leaves binary16's normal range; the factor that
+// undoes it, times the adapter's scale, is applied to the block's sums in fp32.
 //
-//   t2      : [M][ld2], for each block of w ranks w hi values, then w lo
+// hi is cut off, not rounded, and lo is never zero beside a value that is not:
+// both then have the value's sign, and an infinity that they meet in the other
+// factor gives one infinity, not a NaN.
+//
+//   t2      : [M][ld2], for each block 16 hi values, then 16 lo
 //   factor  : float [M][blocks]
-//   w       : 16 for up to 16 ranks (hi and lo share the 32 k of one product),
-//             else 32
 // Rows without an adapter are left as they were: what reads t2 or the factors
 // drops the sums of rows that are not the adapter's, whatever they are.
 constexpr int kMaxRank = 1024;
-struct Ranks {
-  int R, w, blocks, padded;   // padded: w * blocks
-  explicit Ranks(int r) : R(r), w(r <= 16 ? 16 : 32), blocks((r + w - 1) / w), padded(w * blocks) {}
-  int64_t ld2() const { return 2 * (int64_t)padded; }
-};
+__host__ __device__ inline int rank_blocks(int R) { return (R + 15) / 16; }
+__host__ __device__ inline int64_t rank_ld2(int R) { return 32 * (int64_t)rank_blocks(R); }
+
+// v = hi + lo but for 2^-15 (bf16) or 2^-21 (fp16) of it, |v| < 2^14 (or not
+// finite), as above.
+template <int FMT>
+__device__ __forceinline__ void split_value(float v, half_t& hi, half_t& lo) {
+  hi = f32_to_word<FMT>(v);
+  uint16_t bits = __builtin_bit_cast(uint16_t, hi);
+  if (fabsf(word_to_f32<FMT>(hi)) > fabsf(v)) --bits;   // towards zero
+  hi = __builtin_bit_cast(half_t, bits);
+  float left = v - word_to_f32<FMT>(hi);
+  if (left == 0.f) left = copysignf(v == 0.f ? 0.f : 0x1p-14f, v);
+  lo = fabsf(v) < __builtin_inff() ? f32_to_word<FMT>(left) : hi;
+}
+// 2^(13 - floor(log2 top)) and its inverse, within what fp32 holds.
+__device__ __forceinline__ void scale_for(float top, float& up, float& down) {
+  const int e = top == 0.f ? 13 : (int)(__float_as_uint(fmaxf(top, 0x1p-100f)) >> 23) - 127;
+  up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+  down = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+}
 
 struct ShrinkArgs {
   const half_t* X;     // [M][ldx]
@@ -63,7 +81,7 @@ struct ShrinkArgs {
   int64_t ld2;
   float* t32;            // [M][ldt] or null: the sums themselves
   int64_t ldt;
-  int M, K, R, S, w, blocks, cols32;   // cols32: columns of t32 written (zeros past R)
+  int M, K, R, S;
 };
 hipError_t launch_shrink(int fmt, const ShrinkArgs& p, hipStream_t stream);
 
@@ -132,6 +150,15 @@ struct TurnArgs {
   int inner, inner_p, outer, count;
 };
 hipError_t launch_turn(const TurnArgs& first, const TurnArgs* second, hipStream_t stream);
+// dst[l][r][0 .. cols_p) = src[l][r][0 .. cols), zeros past cols (cols_p a
+// multiple of 8, rows of dst cols_p apart).
+struct WidenArgs {
+  const half_t* src;
+  half_t* dst;
+  int64_t lds, stride_s;
+  int rows, cols, cols_p, count;
+};
+hipError_t launch_widen(const WidenArgs& p, hipStream_t stream);
 
 // Row m's adapter: its number, -1 for none, -2 for one that does not exist.
 __device__ __forceinline__ int adapter_of(const long long* ids, int64_t m, int S) {

@@ -49,7 +49,7 @@ def load_library() -> ctypes.CDLL:
 
         mat, stack = [p, i], [p, i, i64]
         declare("gemm_lora", [i] * 6 + mat * 2 + stack * 2 + [p, p, p, i] + mat * 3 + [p, u64, p])
-        declare("gemm_lora_workspace", [i] * 6 + mat * 2, u64)
+        declare("gemm_lora_workspace", [i] * 6 + mat * 2 + [i], u64)
         declare("gemm_lora_bwd",
                 [i] * 6 + mat * 2 + stack * 2 + [p, p] + mat * 3 + stack * 2 + [p, u64, p])
         declare("gemm_lora_bwd_workspace", [i] * 6 + mat * 2 + [i] * 3, u64)
@@ -148,17 +148,19 @@ def gemm_lora(X, W, A, B, ids, C, scales=None, bias=None, act: str = "none", res
     _run(at, stream, lib.gemm_lora,
          (typ, M, N, K, R, S, px, ldx, pw, ldw, pa, lda, sa, pb, ldb, sb, pi, ps, pbias, code, pres,
           ldr, pc, ldc, pt, ldt),
-         lambda: lib.gemm_lora_workspace(typ, M, N, K, R, S, px, ldx, pw, ldw), workspace)
+         lambda: lib.gemm_lora_workspace(typ, M, N, K, R, S, px, ldx, pw, ldw, ldb), workspace)
     return C
 
 
-def lora_workspace_bytes(X, W, A) -> int:
+def lora_workspace_bytes(X, W, A, B) -> int:
     """Workspace bytes ``gemm_lora`` needs for these tensors."""
     dtype, typ, at, M, K, px, ldx = _first(X)
     N = _rows(W, "W")
     S = _adapters(A, "A", dtype, at, None, K)[0]
-    return load_library().gemm_lora_workspace(typ, M, N, K, A.shape[1], S, px, ldx,
-                                              *_shaped(W, "W", dtype, at, N, K))
+    R = A.shape[1]
+    ldb = _adapters(B, "B", dtype, at, N, R, S)[2]
+    return load_library().gemm_lora_workspace(typ, M, N, K, R, S, px, ldx,
+                                              *_shaped(W, "W", dtype, at, N, K), ldb)
 
 
 def gemm_lora_bwd(X, W, A, B, ids, T, dC, dX=None, dA=None, dB=None, scales=None, workspace=None,

@@ -59,8 +59,7 @@ extern "C" {
  *             0 for rows without an adapter                         (written)
  *
  * t is an operand of the second product in two 16-bit values of the type (16
- * bits in bf16, 22 in fp16, of the largest of 16 or 32 ranks), so C is rounded
- * once.  An adapter of fewer ranks than R has zeros in the others.  What one
+ * bits in bf16, 22 in fp16, of the largest of 16 ranks), so C is rounded once.  An adapter of fewer ranks than R has zeros in the others.  What one
  * row's adapter holds, infinities and NaN too, reaches no other row.
  *
  * Rows whose neighbours have the same adapter share its reads; in any other
@@ -81,11 +80,11 @@ MI355TUNE_API int gemm_lora(int type, int M, int N, int K, int R, int S,
                             void* stream);
 
 /* Workspace bytes of gemm_lora: t (4 bytes a row and rank, ranks in blocks of
- * 16, or of 32 above 16), and padded copies of X and W where many rows meet
- * operands that are not whole 16-byte rows (as for gemm_gated). */
+ * 16), and, for many rows, padded copies of X and W where they are not whole
+ * 16-byte rows (as for gemm_gated) and of B where R % 8 != 0 or ldb >= 2^22. */
 MI355TUNE_API unsigned long long gemm_lora_workspace(int type, int M, int N, int K, int R, int S,
                                                      const void* X, int ldx,
-                                                     const void* W, int ldw);
+                                                     const void* W, int ldw, int ldb);
 
 /*
  * The gradients of gemm_lora without an activation, for the gradient dC of its
