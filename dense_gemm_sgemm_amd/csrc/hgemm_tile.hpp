@@ -1182,15 +1182,16 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
             }
           }
           acc[i][j] = v;
+          asm volatile("" : "+v"(acc[i][j]));   // (one quad after another: registers)
         }
-        asm volatile("" ::: "memory");   // (q of a row block at a time: registers)
       }
       // hi, then lo; on both sides of the diagonal, the other one with the
       // block's rows and columns exchanged in the staging area: 16 of its rows
       // (16 columns here) by the wave's rows
       for (int half = 0; half < (x.lo ? 2 : 1); ++half) {
         half_t* dst = (half ? x.lo : x.hi) + at;
-        auto value = [&](f4 v) __attribute__((always_inline)) {
+        auto value = [&](f4& v) __attribute__((always_inline)) {
+          asm volatile("" : "+v"(v));   // (rounded where it is stored, not kept from one to the other)
           const h4 o = round4(v);
           if (!half) return o;
           f4 d;
@@ -1309,28 +1310,27 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
           }
           const int at = 16 * k + 8 * (xg & 1);
           auto load_b = [&](int j) __attribute__((always_inline)) {
+            // (no ranks there: the eight before, as zeros)
             const uint32_t n = min(16 * j + xr, n_last);
-            h8 v = {};
-            if (at < x.R) __builtin_memcpy(&v, b + (n * ldb + 2 * at), 16);
-            return v;
+            h8 v;
+            __builtin_memcpy(&v, b + (n * ldb + 2 * (at < x.R ? at : at - 8)), 16);
+            return at < x.R ? v : h8{};
           };
-          // (one block of columns ahead and no more, and no branches: the
-          // accumulators leave few registers)
-          h8 next = load_b(0);
-          static_for<C::kBlocksN>([&](auto jc) __attribute__((always_inline)) {
-            constexpr int j = decltype(jc)::value;
-            const h8 bv = next;
-            if constexpr (j + 1 < C::kBlocksN) next = load_b(j + 1);
-            __builtin_amdgcn_sched_barrier(0);
+          // (no branches, and each sum added up at once: the accumulators leave few
+          // registers)
+          h8 bv[C::kBlocksN];
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j) bv[j] = load_b(j);
+#pragma unroll
+          for (int j = 0; j < C::kBlocksN; ++j)
 #pragma unroll
             for (int i = 0; i < C::kBlocksM; ++i) {
-              const f4 s = mfma16<FMT>(bv, tv[i], f4{0.f, 0.f, 0.f, 0.f});
+              const f4 s = mfma16<FMT>(bv[j], tv[i], f4{0.f, 0.f, 0.f, 0.f});
               const bool own = rows >> (16 * i + xr) & 1;
 #pragma unroll
               for (int v = 0; v < 4; ++v) acc[i][j][v] = fmaf(f[i], own ? s[v] : 0.f, acc[i][j][v]);
+              asm volatile("" : "+v"(acc[i][j]));
             }
-            __builtin_amdgcn_sched_barrier(0);
-          });
         }
       }
       if (unknown) {
@@ -1389,6 +1389,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
             }
 #pragma unroll
             for (int v = 0; v < 4; ++v) acc[i][j][v] += word_to_f32<FMT>(q[v]);
+            asm volatile("" : "+v"(acc[i][j]));
           }
         }
       }
