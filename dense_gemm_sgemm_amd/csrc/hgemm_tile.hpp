@@ -301,6 +301,9 @@ struct LoraExtra {
   const long long* ids = nullptr;
   int R = 0, S = 0, blocks = 0;
   int m_end = 0, n_end = 0;
+  // LAY 1 with p.K % 64 != 0: A's columns p.K - 64 .. p.K - 1, [p.M][64], zeros
+  // for those of a slab before the last
+  const half_t* tail = nullptr;
 };
 struct LoraTileArgs {
   Args16 p;
@@ -554,9 +557,11 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   struct CopyBaseX : CopyBase {   // kGradX
     int64_t sa;        // bytes between A's copies
   };
-  typedef std::conditional_t<MODE == kGradX, CopyBaseX, CopyBase> CopyBaseT;
+  constexpr bool kTailA = MODE == kLora && LAY == 1;   // A's last slab from a copy, as kGradX's
+  typedef std::conditional_t<MODE == kGradX || kTailA, CopyBaseX, CopyBase> CopyBaseT;
   // kGradX: this lane's offset in x.tail; slabs of each part of K
   uint32_t offA_x = 0;
+  if constexpr (kTailA) offA_x = (uint32_t)(lane_row * BK + 8 * lane_chunk) * 2;
   int nk_part = 0;
   if constexpr (MODE == kGradX) {
     offA_x = (uint32_t)(lane_row * ta.x.ldt + 8 * lane_chunk) * 2;
@@ -609,7 +614,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
         if constexpr (kAT)
           issue(cb.a + c * copy_strideTA, t_hi(kTPA, c) ? offTA1 : offTA0,
                 cb.l + (c * C::kCopyWaves + cw) * 1024);
-        else if constexpr (MODE == kGradX)
+        else if constexpr (MODE == kGradX || kTailA)
           issue(cb.a + c * cb.sa, cb.oa, cb.l + (c * C::kCopyWaves + cw) * 1024);
         else
           issue(cb.a + c * copy_strideA, cb.oa, cb.l + (c * C::kCopyWaves + cw) * 1024);
@@ -1517,6 +1522,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   const char *run_a = nullptr, *run_b = nullptr;
   int run_left = 0;         // slabs left of the run, the next one among them
   bool run_tail = false;
+  int64_t run_sa = 0;       // bytes between A's copies
   constexpr bool kRuns = kFresh;
   auto begin_run = [&]() __attribute__((always_inline)) {
     const int d = ahead < 2 ? ahead : 2;
@@ -1539,7 +1545,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       const int part_left = (h + 1) * nk - t;
       len = left < part_left ? left : part_left;
     } else {
-      // (LAY 1 with a K tail: the last slab from K - 64, see slab_base)
+      // (LAY 1 with a K tail: the last slab from K - 64)
       run_tail = kv < BK && t == nk - 1;
       k0 = LAY != 0 && run_tail ? (int64_t)p.K - BK : (int64_t)t * BK;
       a = p.A;
@@ -1548,6 +1554,13 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     }
     run_a = kAT ? (const char*)(a + k0 * p.lda + m0) + firstTA
                 : (const char*)(a + (int64_t)m0 * p.lda + k0) + firstA;
+    if constexpr (kTailA) {
+      run_sa = copy_strideA;
+      if (run_tail) {
+        run_a = (const char*)(args->x.tail + (int64_t)(m0 + cwp * C::kRowsPerCopy) * BK);
+        run_sa = (int64_t)C::kCopyWaves * C::kRowsPerCopy * BK * 2;
+      }
+    }
     run_b = kBT ? (const char*)(b + k0 * p.ldb + n0) + firstTB
                 : (const char*)(b + (int64_t)n0 * p.ldb + k0) + firstB;
     run_left = __builtin_amdgcn_readfirstlane(len);
@@ -1580,7 +1593,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       cb.a = run_a;
       cb.b = run_b;
       cb.l = lds + stage * kStage;
-      cb.oa = MODE == kLora && LAY == 0 && run_tail ? offA_tail : offA;
+      cb.oa = MODE == kLora && run_tail ? (LAY == 0 ? offA_tail : offA_x) : offA;
+      if constexpr (kTailA) cb.sa = run_sa;
       cb.ob = MODE == kLora && LAY == 0 && run_tail ? offB_tail : offB;
       return cb;
     }
@@ -1608,7 +1622,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     auto sync = [&]() __attribute__((always_inline)) {
       // kGradX needs no zeros in LDS: its A side of a tail slab has them in memory
       // (and kSym's and kMul's K is whole slabs)
-      if constexpr (RAG && MODE != kGradX && !is_ortho(MODE)) wait_zero_sync(zero_next, (gs + 1) & 1);
+      // (and kLora's with B K-major has zeros in memory too)
+      if constexpr (RAG && MODE != kGradX && !is_ortho(MODE) && !(MODE == kLora && LAY == 1)) wait_zero_sync(zero_next, (gs + 1) & 1);
       else wait_and_sync();
     };
     constexpr bool kCp = decltype(is_copier)::value;

@@ -59,11 +59,11 @@ struct BwdPlan {
   bool dx, da, db;
   size_t t2 = 0, factor = 0, dt = 0, at = 0, bt = 0;
   size_t counts = 0, rows = 0, steps = 0, pack = 0, step_factor = 0, partial[2] = {0, 0};
-  size_t copy_c = 0, copy_w = 0;
+  size_t copy_c = 0, copy_w = 0, tail = 0;
   GradPlan grad{};
   size_t total() const {
     return t2 + factor + dt + at + bt + counts + rows + steps + 2 * pack + 2 * step_factor +
-           partial[0] + partial[1] + copy_c + copy_w;
+           partial[0] + partial[1] + copy_c + copy_w + tail;
   }
 };
 size_t copy_bytes_w(int N, int K) {
@@ -85,6 +85,7 @@ BwdPlan plan_bwd(int M, int N, int K, int R, int S, Mat c, Mat w, bool dx, bool 
     const int Kd = pad_k(N);
     if (needs_copy(c.p, c.ld, M, N)) p.copy_c = copy_bytes(M, N);
     if (needs_copy(w.p, w.ld, N, K) || Kd != N) p.copy_w = copy_bytes_w(N, K);
+    if (Kd % 64 != 0) p.tail = (size_t)pad_rows(M) * 64 * 2;
   }
   if (p.da || p.db) {
     p.grad = plan_grad(M, p.db ? N : 0, p.da ? K : 0, R, S);
@@ -301,8 +302,13 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S, con
     if (e != hipSuccess) return to_status(e);
     Args16 a{c.p, w.p, out16(dX), c.ld, w.ld, lddx, pad_rows(M), pad_k(K), pad_k(N)};
     a.fmt = fmt;
-    const LoraExtra y{t2, rank_ld2(R), factor, at, 16 * rank_blocks(R), (int64_t)K * 16 * rank_blocks(R), ids,
+    LoraExtra y{t2, rank_ld2(R), factor, at, 16 * rank_blocks(R), (int64_t)K * 16 * rank_blocks(R), ids,
                       16 * rank_blocks(R), S, rank_blocks(R), M, K};
+    if (p.tail) {
+      y.tail = reinterpret_cast<half_t*>(ws);
+      e = launch_tail(TailArgs{c0.p, reinterpret_cast<half_t*>(ws), lddc, M, a.M, a.K}, s);
+      if (e != hipSuccess) return to_status(e);
+    }
     e = launch_lora_tiles(a, y, true, cus, s);
   }
   return to_status(e);

@@ -379,6 +379,20 @@ __global__ __launch_bounds__(kThreads) void widen_kernel(WidenArgs p, int64_t ba
     if (c + e < p.cols) v[e] = src[c + e];
   *(h8*)(p.dst + t * p.cols_p + c) = v;
 }
+__global__ __launch_bounds__(kThreads) void tail_kernel(TailArgs p, int64_t base) {
+  const int64_t t = (base + blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t row = t / 8;
+  const int c = (int)(t % 8) * 8;
+  if (row >= p.rows_p) return;
+  h8 v = {};
+  if (row < p.rows) {
+    const half_t* src = p.src + row * p.lds + p.K - 64 + c;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e >= 64 - p.K % 64) v[e] = src[e];
+  }
+  *(h8*)(p.dst + row * 64 + c) = v;
+}
 int64_t turn_blocks(const TurnArgs& p) {
   return ((int64_t)p.outer * (p.inner_p / 8) * p.count + kThreads - 1) / kThreads;
 }
@@ -440,6 +454,11 @@ hipError_t launch_turn(const TurnArgs& first, const TurnArgs* second, hipStream_
   TurnJobs jobs{{first, second ? *second : first}, turn_blocks(first)};
   return launch_tiles((const void*)turn_kernel, jobs,
                       jobs.blocks0 + (second ? turn_blocks(*second) : 0), kThreads, 0, stream);
+}
+
+hipError_t launch_tail(const TailArgs& p, hipStream_t stream) {
+  return launch_tiles((const void*)tail_kernel, p, ((int64_t)p.rows_p * 8 + kThreads - 1) / kThreads,
+                      kThreads, 0, stream);
 }
 
 hipError_t launch_widen(const WidenArgs& p, hipStream_t stream) {

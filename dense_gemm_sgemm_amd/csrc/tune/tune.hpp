@@ -159,6 +159,15 @@ struct WidenArgs {
   int rows, cols, cols_p, count;
 };
 hipError_t launch_widen(const WidenArgs& p, hipStream_t stream);
+// The last 64 of K columns (K % 64 != 0) of src [rows][lds] for the tiles: dst
+// [rows_p][64], zeros for those of a slab of 64 before the last and past `rows`.
+struct TailArgs {
+  const half_t* src;
+  half_t* dst;
+  int64_t lds;
+  int rows, rows_p, K;
+};
+hipError_t launch_tail(const TailArgs& p, hipStream_t stream);
 
 // Row m's adapter: its number, -1 for none, -2 for one that does not exist.
 __device__ __forceinline__ int adapter_of(const long long* ids, int64_t m, int S) {
