@@ -26,55 +26,13 @@
 // binary16 and fp32 outputs take two values for X, A and C throughout and
 // three products for each one.
 #define MI355TUNE_BUILDING 1
-#include "tune.hpp"
+#include "ortho.hpp"
 
 namespace mi355gemm {
 namespace tune {
 namespace {
 
-typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-constexpr int kThreads = 256;
-constexpr int kScaleX = 12, kScaleA = 10;   // powers of two of what is stored
-constexpr int kNormBlocks = 256;            // partial sums of a matrix, at most
-constexpr int kSplitSteps = 3;              // iterates 0 .. 2 are held in two values
-enum { kF32 = -1 };                         // beside GEMM_TYPE_F16 and GEMM_TYPE_BF16
-
-__device__ __forceinline__ float load_one(const void* g, int64_t i, int type) {
-  if (type == kF32) return static_cast<const float*>(g)[i];
-  const half_t w = static_cast<const half_t*>(g)[i];
-  return type == GEMM_TYPE_BF16 ? word_to_f32<kFmtBF16>(w) : word_to_f32<kFmtF16>(w);
-}
-
-// Eight values of a row at columns c .., zeros past n; any alignment.
-__device__ __forceinline__ void load8(const void* g, int64_t row, int c, int n, int type,
-                                      float (&v)[8]) {
-  if (c + 8 <= n) {
-    if (type == kF32) {
-      __builtin_memcpy(v, static_cast<const float*>(g) + row + c, 32);
-    } else {
-      h8 w;
-      __builtin_memcpy(&w, static_cast<const half_t*>(g) + row + c, 16);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[e] = type == GEMM_TYPE_BF16 ? word_to_f32<kFmtBF16>(w[e]) : word_to_f32<kFmtF16>(w[e]);
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c + e < n ? load_one(g, row + c + e, type) : 0.f;
-  }
-}
-
-struct StartArgs {
-  const void* G;
-  int64_t ldg, stride_g;
-  int type, m, n, L, blocks;   // blocks: partial sums of a matrix
-  double* sums;                // [L][blocks]
-  float* coef;                 // [L][3]
-  double eps;
-  half_t *hi, *lo;             // [L][sp][tp]
-  int64_t stride_x, tiles;     // tiles: 64 x 64 ones of a matrix (transposed start)
-  int sp, tp;
-};
+using namespace ortho;
 
 // Sums of squares, in 64 bits: the squares of fp32 values neither overflow nor
 // vanish there, and their sum is as good as exact.  Bound by HBM.
@@ -104,22 +62,6 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(StartArgs p, int64_t bas
   p.sums[block] = s;
 }
 
-// The power of two a matrix is stored with and what is left of 1 / (|G| + eps):
-// |G| = f 2^e with f in [0.5, 1), X0 = G 2^-e, rho = 2^e / (|G| + eps).
-__device__ __forceinline__ void start_of(const StartArgs& p, int64_t l, double& up, double& rho) {
-  double s = 0.;
-  for (int i = threadIdx.x & 63; i < p.blocks; i += 64) s += p.sums[l * p.blocks + i];
-#pragma unroll
-  for (int k = 32; k >= 1; k /= 2) s += __shfl_xor(s, k);
-  const double norm = sqrt(s);
-  int e = 0;
-  if (norm > 0. && norm < __builtin_inf()) (void)frexp(norm, &e);
-  up = ldexp(1., kScaleX - e);
-  rho = norm > 0. ? ldexp(1., e) / (norm + p.eps) : 1.;
-  // an infinite or NaN norm: every value of the result is NaN
-  if (!(norm < __builtin_inf())) up = rho = __builtin_nan("");
-}
-
 __device__ __forceinline__ void put_start(const StartArgs& p, int64_t at, const float (&v)[8],
                                           double up) {
   h8 hi, lo;
@@ -131,13 +73,6 @@ __device__ __forceinline__ void put_start(const StartArgs& p, int64_t at, const 
   }
   *(h8*)(p.hi + at) = hi;
   if (p.lo) *(h8*)(p.lo + at) = lo;
-}
-
-__device__ __forceinline__ void put_coef(const StartArgs& p, int64_t l, double rho) {
-  // step 0 sees X0, which is the normalised matrix / rho
-  p.coef[3 * l] = (float)(rho * rho * rho * rho * rho);
-  p.coef[3 * l + 1] = (float)(rho * rho * rho);
-  p.coef[3 * l + 2] = (float)rho;
 }
 
 // X0 as it lies: a thread 8 columns.  Bound by HBM.
@@ -196,7 +131,11 @@ struct Plan {
   size_t x, a, sums, coef;   // bytes of one buffer
   int x_count, a_count;
   size_t cut;            // fp32 sums of tiles whose K is cut into ranges
-  size_t total() const { return x_count * x + a_count * a + sums + coef + cut; }
+  bool small;
+  SmallPlan few;
+  size_t total() const {
+    return sums + coef + (small ? few.total() : x_count * x + a_count * a + cut);
+  }
 };
 
 // The parts of a step's products (see `parts` below) depend on which iterates
@@ -212,7 +151,7 @@ SymPlan plan_gram(const Plan& p, int L, bool lo) {
 SymPlan plan_square(const Plan& p, int L) { return plan_sym(p.sp, (p.fine ? 3 : 1) * (p.sp / 64), L); }
 
 Plan make_plan(int type_g, int type_o, int L, int m, int n, int steps) {
-  Plan p;
+  Plan p{};
   p.tall = m > n;
   p.s = p.tall ? n : m;
   p.t = p.tall ? m : n;
@@ -227,6 +166,11 @@ Plan make_plan(int type_g, int type_o, int L, int m, int n, int steps) {
   p.a = round256((size_t)L * p.sp * p.sp * 2);
   p.sums = round256((size_t)L * p.blocks * sizeof(double));
   p.coef = round256((size_t)L * 3 * sizeof(float));
+  p.small = p.s <= kSmallSide;
+  if (p.small) {
+    p.few = plan_small(L, p.s, p.t);
+    return p;
+  }
   p.x_count = 2 + (p.x_lo || p.x0_lo ? 2 : 0);
   p.a_count = p.fine ? 4 : 2;
   p.cut = plan_square(p, L).sum_bytes();
@@ -289,6 +233,14 @@ MI355TUNE_API int gemm_ortho(int type_g, int type_o, int L, int m, int n, const 
   hipStream_t s = static_cast<hipStream_t>(stream);
 
   char* ws = static_cast<char*>(workspace);
+  StartArgs st{G, ldg, stride_g, tg, m, n, L, p.blocks, reinterpret_cast<double*>(ws),
+               reinterpret_cast<float*>(ws + p.sums), (double)eps, nullptr, nullptr,
+               (int64_t)p.sp * p.tp, (int64_t)(p.sp / 64) * (p.tp / 64), p.sp, p.tp};
+  ws += p.sums + p.coef;
+  hipError_t e = launch_tiles((const void*)norm_kernel, st, (int64_t)L * p.blocks, kThreads, 0, s);
+  if (e != hipSuccess) return to_status(e);
+  if (p.small)
+    return to_status(launch_small(st, p.few, steps, coeffs, SmallOut{O, ldo, stride_o, to}, ws, s));
   half_t* x[2][2];   // [iterate][hi, lo]
   for (int v = 0; v < 2; ++v)
     for (int i = 0; i < 2; ++i) {
@@ -301,13 +253,9 @@ MI355TUNE_API int gemm_ortho(int type_g, int type_o, int L, int m, int n, const 
     c[v] = a[v] ? reinterpret_cast<half_t*>(ws + p.a) : nullptr;
     if (a[v]) ws += 2 * p.a;
   }
-  StartArgs st{G,   ldg, stride_g, tg, m, n, L, p.blocks, reinterpret_cast<double*>(ws),
-               reinterpret_cast<float*>(ws + p.sums), (double)eps, x[0][0],
-               p.x0_lo ? x[0][1] : nullptr, (int64_t)p.sp * p.tp,
-               (int64_t)(p.sp / 64) * (p.tp / 64), p.sp, p.tp};
-  float* cut = reinterpret_cast<float*>(ws + p.sums + p.coef);
-  hipError_t e = launch_tiles((const void*)norm_kernel, st, (int64_t)L * p.blocks, kThreads, 0, s);
-  if (e != hipSuccess) return to_status(e);
+  float* cut = reinterpret_cast<float*>(ws);
+  st.hi = x[0][0];
+  st.lo = p.x0_lo ? x[0][1] : nullptr;
   const int64_t per = ((int64_t)p.sp * (p.tp / 8) + kThreads - 1) / kThreads;
   e = p.tall ? launch_tiles((const void*)start_t_kernel, st, L * st.tiles, kThreads, 0, s)
              : launch_tiles((const void*)start_kernel, st, L * per, kThreads, 0, s);

@@ -1,0 +1,97 @@
+// Shared by the two forms of gemm_ortho: ortho.hip, on the tile kernel, and
+// ortho_small.hip, for a shorter side of up to 64.
+#pragma once
+
+#include "tune.hpp"
+
+namespace mi355gemm {
+namespace tune {
+namespace ortho {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+constexpr int kThreads = 256;
+constexpr int kScaleX = 12, kScaleA = 10;   // powers of two of what is stored
+constexpr int kNormBlocks = 256;            // partial sums of a matrix, at most
+constexpr int kSplitSteps = 3;              // iterates 0 .. 2 are held in two values
+enum { kF32 = -1 };                         // beside GEMM_TYPE_F16 and GEMM_TYPE_BF16
+
+__device__ __forceinline__ float load_one(const void* g, int64_t i, int type) {
+  if (type == kF32) return static_cast<const float*>(g)[i];
+  const half_t w = static_cast<const half_t*>(g)[i];
+  return type == GEMM_TYPE_BF16 ? word_to_f32<kFmtBF16>(w) : word_to_f32<kFmtF16>(w);
+}
+
+// Eight values of a row at columns c .., zeros past n; any alignment.
+__device__ __forceinline__ void load8(const void* g, int64_t row, int c, int n, int type,
+                                      float (&v)[8]) {
+  if (c + 8 <= n) {
+    if (type == kF32) {
+      __builtin_memcpy(v, static_cast<const float*>(g) + row + c, 32);
+    } else {
+      h8 w;
+      __builtin_memcpy(&w, static_cast<const half_t*>(g) + row + c, 16);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        v[e] = type == GEMM_TYPE_BF16 ? word_to_f32<kFmtBF16>(w[e]) : word_to_f32<kFmtF16>(w[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = c + e < n ? load_one(g, row + c + e, type) : 0.f;
+  }
+}
+
+struct StartArgs {
+  const void* G;
+  int64_t ldg, stride_g;
+  int type, m, n, L, blocks;   // blocks: partial sums of a matrix
+  double* sums;                // [L][blocks]
+  float* coef;                 // [L][3]
+  double eps;
+  half_t *hi, *lo;             // [L][sp][tp]
+  int64_t stride_x, tiles;     // tiles: 64 x 64 ones of a matrix (transposed start)
+  int sp, tp;
+};
+
+// The power of two a matrix is stored with and what is left of 1 / (|G| + eps):
+// |G| = f 2^e with f in [0.5, 1), X0 = G 2^-e, rho = 2^e / (|G| + eps).
+__device__ __forceinline__ void start_of(const StartArgs& p, int64_t l, double& up, double& rho) {
+  double s = 0.;
+  for (int i = threadIdx.x & 63; i < p.blocks; i += 64) s += p.sums[l * p.blocks + i];
+#pragma unroll
+  for (int k = 32; k >= 1; k /= 2) s += __shfl_xor(s, k);
+  const double norm = sqrt(s);
+  int e = 0;
+  if (norm > 0. && norm < __builtin_inf()) (void)frexp(norm, &e);
+  up = ldexp(1., kScaleX - e);
+  rho = norm > 0. ? ldexp(1., e) / (norm + p.eps) : 1.;
+  // an infinite or NaN norm: every value of the result is NaN
+  if (!(norm < __builtin_inf())) up = rho = __builtin_nan("");
+}
+
+__device__ __forceinline__ void put_coef(const StartArgs& p, int64_t l, double rho) {
+  // step 0 sees X0, which is the normalised matrix / rho
+  p.coef[3 * l] = (float)(rho * rho * rho * rho * rho);
+  p.coef[3 * l + 1] = (float)(rho * rho * rho);
+  p.coef[3 * l + 2] = (float)rho;
+}
+
+// A shorter side of up to kSmallSide (ortho_small.hip).
+constexpr int kSmallSide = 64, kMaxSlabs = 16;
+struct SmallPlan {
+  int side, slabs, slab;   // the padded side, and the slabs that the longer one is cut into
+  size_t x, gram;          // bytes of an iterate's hi (or lo) values, of partial products
+  size_t total() const { return 4 * x + 2 * gram; }
+};
+SmallPlan plan_small(int L, int s, int t);
+struct SmallOut {
+  void* O;
+  int64_t ldo, stride_o;
+  int type;
+};
+// Everything after the norms; st's hi, lo and tiles are not used.
+hipError_t launch_small(const StartArgs& st, const SmallPlan& p, int steps, const float* coeffs,
+                        const SmallOut& out, char* ws, hipStream_t stream);
+
+}  // namespace ortho
+}  // namespace tune
+}  // namespace mi355gemm
