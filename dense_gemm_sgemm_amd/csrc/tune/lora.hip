@@ -88,13 +88,15 @@ BwdPlan plan_bwd(int M, int N, int K, int R, int S, Mat c, Mat w, bool dx, bool 
     if (Kd % 64 != 0) p.tail = (size_t)pad_rows(M) * 64 * 2;
   }
   if (p.da || p.db) {
-    p.grad = plan_grad(M, p.db ? N : 0, p.da ? K : 0, R, S);
+    // (the same whatever is asked for, so that each gradient has the same bits)
+    p.grad = plan_grad(M, N, K, R, S);
     p.counts = round256((size_t)S * sizeof(int));
     p.rows = round256((size_t)p.grad.steps * 32 * sizeof(int));
     p.steps = round256((size_t)p.grad.steps * sizeof(int));
     p.pack = p.grad.pack;
     p.step_factor = round256((size_t)p.grad.steps * sizeof(float));
-    for (int i = 0; i < 2; ++i) p.partial[i] = p.grad.partial[i];
+    if (p.da) p.partial[0] = p.grad.partial[0];
+    if (p.db) p.partial[1] = p.grad.partial[1];
   }
   return p;
 }

@@ -2,7 +2,9 @@
 // once for 64 rows, bound by that (skinny.hpp has the layout).  The adapters'
 // second product comes before the waves' sums are added: each wave takes every
 // so many of the adapters that the rows name, multiplies t (tune.hpp) with 16 of
-// the adapter's rows of B and keeps the sums of the rows that are its own.
+// the adapter's rows of B and keeps the sums of the rows that are its own, apart
+// from the projection's: one wave has them, so that a row's result does not
+// depend on the rows beside it.
 #include "fused/skinny.hpp"
 #include "tune.hpp"
 
@@ -48,7 +50,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
   constexpr int kS = MT == 4 ? 2 : kSteps, kC = 32 * kS;
   typedef XStage<MT, kC> Stage;
   __shared__ __attribute__((aligned(16))) unsigned char
-      lds[kMaxWaves * (Stage::kBytes > MT * 1024 ? Stage::kBytes : MT * 1024)];
+      lds[kMaxWaves * (Stage::kBytes > 2 * MT * 1024 ? Stage::kBytes : 2 * MT * 1024)];
   const Args16& p = args.p;
   const LoraExtra& y = args.x;
   const int lane = threadIdx.x & 63;
@@ -59,9 +61,9 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
   const int n = (int)(id % groups_n) * 16 + r;
   const int row = n < p.N ? n : p.N - 1;   // rows past N repeat the last one, unstored
   const half_t* w = p.B + row * p.ldb + 8 * quarter;
-  f4 acc[MT];
+  f4 acc[2 * MT];   // the projection's, then the adapters'
 #pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < 2 * MT; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
 
   // (the pointer and K both moved on by the lane's 8 quarter)
   const int K = p.K - 8 * quarter, chunks = p.K / kC;
@@ -128,7 +130,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int i = 16 * t + 4 * quarter + v;
-          if (rows >> i & 1) acc[t][v] += y.factor[(int64_t)(m0 + i) * y.blocks + k] * s[v];
+          if (rows >> i & 1) acc[MT + t][v] += y.factor[(int64_t)(m0 + i) * y.blocks + k] * s[v];
         }
       }
     }
@@ -136,7 +138,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
 
   // (the sums take the place of X)
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  add_waves<MT>(acc, reinterpret_cast<float*>(lds), wave, lane, args.waves);
+  add_waves<2 * MT>(acc, reinterpret_cast<float*>(lds), wave, lane, args.waves);
   if (wave > 0) return;
   const uint64_t unknown = __ballot(mine == -2);
   if (n >= p.N) return;
@@ -148,7 +150,7 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
       const int i = 16 * t + 4 * quarter + v;
       const int64_t m = m0 + i;
       if (m >= p.M) continue;
-      float z = unknown >> i & 1 ? __builtin_nanf("") : acc[t][v];
+      float z = unknown >> i & 1 ? __builtin_nanf("") : acc[t][v] + acc[MT + t][v];
       z = gate_act(z + bias, p.act);
       if (p.res) z += word_to_f32<FMT>(p.res[m * p.ldr + n]);
       p.C[m * p.ldc + n] = f32_to_word<FMT>(z);
