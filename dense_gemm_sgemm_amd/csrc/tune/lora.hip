@@ -254,14 +254,19 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S, con
   }
   hipError_t e = hipSuccess;
   const int64_t ldbt = line_ld(round_up(N, 8));
+  // B^T as the second operand of dt = dC B, A^T of dX's part, and the lists
+  TurnArgs turns[2];
+  int count = 0;
+  if (M > 0 && dt && N > 0)
+    turns[count++] = TurnArgs{in16(B), bt, ldb, stride_b, ldbt, (int64_t)R * ldbt,
+                              N, (int)round_up(N, 8), R, S};
+  if (p.dx && S > 0)
+    turns[count++] = TurnArgs{in16(A), at, lda, stride_a, 16 * rank_blocks(R),
+                              (int64_t)K * 16 * rank_blocks(R), R, 16 * rank_blocks(R), K, S};
+  const bool listed = p.da || p.db;
+  if (listed || count) e = launch_lists(listed ? &group : nullptr, turns, count, s);
+  if (e != hipSuccess) return to_status(e);
   if (M > 0 && dt) {
-    // B^T as the second operand of dt = dC B, A^T of dX's part
-    const TurnArgs tb{in16(B), bt, ldb, stride_b, ldbt, (int64_t)R * ldbt,
-                      N, (int)round_up(N, 8), R, S};
-    const TurnArgs ta{in16(A), at, lda, stride_a, 16 * rank_blocks(R), (int64_t)K * 16 * rank_blocks(R),
-                      R, 16 * rank_blocks(R), K, S};
-    if (N > 0 || p.dx) e = launch_turn(N > 0 ? tb : ta, N > 0 && p.dx ? &ta : nullptr, s);
-    if (e != hipSuccess) return to_status(e);
     const ShrinkArgs sh{c0.p, bt, lddc, ldbt, (int64_t)R * ldbt, ids, scales, t2, factor,
                         rank_ld2(R), dt32, R, M, N, R, S};
     e = launch_shrink(fmt, sh, s);
@@ -284,8 +289,7 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S, con
       ga.job[1] = GradJob{T, ldt, c0.p, lddc, N, out16(dB), lddb, stride_db, 1, pack[1],
                           step_factor[1], partial[1], (N + 127) / 128};
     }
-    e = launch_group(group, s);
-    if (e == hipSuccess) e = launch_adapter_grads(fmt, ga, p.grad, s);
+    e = launch_adapter_grads(fmt, ga, p.grad, s);
     if (e != hipSuccess) return to_status(e);
   }
   if (p.dx) {

@@ -7,7 +7,7 @@
 // lane loads 8 rows x 8 columns in 16-byte pieces and exchanges them, so that
 // its eight fragments are eight neighbouring columns.  No LDS, any alignment.
 //
-// A workgroup takes 128 columns, up to 64 ranks and a chunk of the steps, which
+// A workgroup takes 128 columns, up to 32 ranks and a chunk of the steps, which
 // its waves share; the waves' sums are added through LDS at the end of each
 // adapter's steps in the chunk.  An adapter that lies in one chunk is stored at
 // once, the others' chunks leave fp32 sums that a second kernel adds in order.
@@ -25,57 +25,113 @@ typedef int i4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256, kWaves = kThreads / 64, kCols = 128;
 
-// Sum over the threads of a workgroup.
+constexpr int kListThreads = 1024, kListWaves = kListThreads / 64;
+
+// Sum over the threads of a workgroup of kListThreads.
 __device__ __forceinline__ int sum_all(int v, int* lds) {
 #pragma unroll
   for (int k = 32; k >= 1; k /= 2) v += __shfl_xor(v, k);
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
   __syncthreads();
-  return lds[0] + lds[1] + lds[2] + lds[3];
+  v = 0;
+#pragma unroll
+  for (int w = 0; w < kListWaves; ++w) v += lds[w];
+  return v;
 }
 
-// Workgroup a counts the rows of adapter a.
-__global__ __launch_bounds__(kThreads) void count_kernel(GroupArgs p, int64_t base) {
-  __shared__ int lds[kWaves];
+// Workgroup a counts the rows of adapter a (more adapters than kHistogram).
+__global__ __launch_bounds__(kListThreads) void count_kernel(GroupArgs p, int64_t base) {
+  __shared__ int lds[kListWaves];
   const int a = (int)(base + blockIdx.x);
   int n = 0;
-  for (int m = threadIdx.x; m < p.M; m += kThreads) n += p.ids[m] == a;
+  for (int m = threadIdx.x; m < p.M; m += kListThreads) n += p.ids[m] == a;
   n = sum_all(n, lds);
   if (threadIdx.x == 0) p.counts[a] = n;
 }
 
 // Workgroup a lists the rows of adapter a, behind those of the adapters before
-// it; workgroup S marks the steps that are left over.
-__global__ __launch_bounds__(kThreads) void list_kernel(GroupArgs p, int64_t base) {
-  __shared__ int lds[kWaves];
-  const int a = (int)(base + blockIdx.x);
-  int before = 0;   // steps
-  for (int i = threadIdx.x; i < a; i += kThreads) before += (p.counts[i] + 31) / 32;
+// it; workgroup S marks the steps that are left over.  Up to kHistogram adapters
+// each workgroup counts all of them for itself (whole numbers: in any order).
+// The workgroups past S turn the factors' stacks (below), which needs none of it.
+struct ListJobs {
+  GroupArgs g;
+  int groups;   // workgroups of the lists, or 0
+  TurnArgs turn[2];
+  int64_t turns0;   // workgroups of the first
+};
+__device__ void list_rows(const GroupArgs& p, int a, int* lds, int* bins) {
+  int before = 0, count = 0;   // before: steps
+  if (p.S <= kHistogram) {
+    for (int i = threadIdx.x; i < p.S; i += kListThreads) bins[i] = 0;
+    __syncthreads();
+    for (int m = threadIdx.x; m < p.M; m += kListThreads) {
+      const long long id = p.ids[m];
+      if (id >= 0 && id < p.S) atomicAdd(bins + (int)id, 1);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < a; i += kListThreads) before += (bins[i] + 31) / 32;
+    if (a < p.S) count = bins[a];
+    if (a < p.S && threadIdx.x == 0) p.counts[a] = count;
+  } else {
+    for (int i = threadIdx.x; i < a; i += kListThreads) before += (p.counts[i] + 31) / 32;
+    if (a < p.S) count = p.counts[a];
+  }
   before = sum_all(before, lds);
   if (a == p.S) {
-    for (int i = before + threadIdx.x; i < p.steps; i += kThreads) p.step_adapter[i] = -1;
+    for (int i = before + threadIdx.x; i < p.steps; i += kListThreads) p.step_adapter[i] = -1;
     return;
   }
-  const int count = p.counts[a], steps = (count + 31) / 32;
-  if (count == 0) return;
-  for (int i = threadIdx.x; i < steps; i += kThreads) p.step_adapter[before + i] = a;
+  const int steps = (count + 31) / 32;
+  for (int i = threadIdx.x; i < steps; i += kListThreads) p.step_adapter[before + i] = a;
   int* rows = p.rows + 32 * (int64_t)before;
-  for (int i = count + threadIdx.x; i < 32 * steps; i += kThreads) rows[i] = -1;
+  for (int i = count + threadIdx.x; i < 32 * steps; i += kListThreads) rows[i] = -1;
   int at = 0;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  for (int m0 = 0; m0 < p.M && at < count; m0 += kThreads) {
-    const int m = m0 + threadIdx.x;
+  for (int64_t m0 = 0; m0 < p.M && at < count; m0 += kListThreads) {
+    const int64_t m = m0 + threadIdx.x;
     const bool mine = m < p.M && p.ids[m] == a;
     const uint64_t votes = __ballot(mine);
     __syncthreads();
     if (lane == 0) lds[wave] = __popcll(votes);
     __syncthreads();
     int pos = at;
-    for (int w = 0; w < wave; ++w) pos += lds[w];
-    if (mine) rows[pos + __popcll(votes & ((uint64_t(1) << lane) - 1))] = m;
-    at += lds[0] + lds[1] + lds[2] + lds[3];
+#pragma unroll
+    for (int w = 0; w < kListWaves; ++w) {
+      pos += w < wave ? lds[w] : 0;
+      at += lds[w];
+    }
+    if (mine) rows[pos + __popcll(votes & ((uint64_t(1) << lane) - 1))] = (int)m;
   }
+}
+
+// A thread 8 inner values of one outer index; neighbouring threads neighbouring
+// outer indices.
+__device__ __forceinline__ void turn(const TurnArgs& p, int64_t id) {
+  int64_t t = id * kListThreads + threadIdx.x;
+  const int o = (int)(t % p.outer);
+  t /= p.outer;
+  const int i = (int)(t % (p.inner_p / 8)) * 8;
+  const int64_t l = t / (p.inner_p / 8);
+  if (l >= p.count) return;
+  const half_t* src = p.src + l * p.stride_s + (int64_t)i * p.lds + o;
+  h8 v = {};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (i + e < p.inner) v[e] = src[e * p.lds];
+  *(h8*)(p.dst + l * p.stride_d + (int64_t)o * p.ldd + i) = v;
+}
+
+__global__ __launch_bounds__(kListThreads) void list_kernel(ListJobs p, int64_t base) {
+  __shared__ int lds[kListWaves], bins[kHistogram];
+  int64_t id = base + blockIdx.x;
+  if (id < p.groups) {
+    list_rows(p.g, (int)id, lds, bins);
+    return;
+  }
+  id -= p.groups;
+  const bool second = id >= p.turns0;
+  turn(second ? p.turn[1] : p.turn[0], second ? id - p.turns0 : id);
 }
 
 // A step's 32 rows of `left`, ranks as rows, in two 16-bit values times a power
@@ -144,6 +200,25 @@ __device__ __forceinline__ void turn8(h8 (&v)[8]) {
   }
 }
 
+// The waves' sums, 16 ranks at a time, in the order of the waves; complete in wave 0.
+template <int RB>
+__device__ __forceinline__ void add_up(f4 (&acc)[RB][8], f4* lds, int wave, int lane) {
+#pragma unroll
+  for (int q = 0; q < RB; ++q) {
+    __syncthreads();
+    if (wave > 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) lds[((wave - 1) * 8 + e) * 64 + lane] = acc[q][e];
+    }
+    __syncthreads();
+    if (wave == 0) {
+      for (int w = 0; w + 1 < kWaves; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[q][e] += lds[(w * 8 + e) * 64 + lane];
+    }
+  }
+}
+
 // Where a workgroup's sums of an adapter go: 16 RB ranks x 128 columns, lane
 // (g, j) holding ranks 16 q + 4 g + v, columns c0 + 8 j + e.
 template <int FMT, int RB>
@@ -207,10 +282,10 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(GradArgs p, int64_t base
   const int g = lane >> 4, j = lane & 15;
   int64_t id = base + blockIdx.x;
   const int blocks0 = p.job[0].blocks, blocks = blocks0 + p.job[1].blocks;
-  const int group = (int)(id % p.groups);
-  id /= p.groups;
   int block = (int)(id % blocks);
-  const int chunk = (int)(id / blocks);
+  id /= blocks;
+  const int group = (int)(id % p.groups);
+  const int chunk = (int)(id / p.groups);
   const int which = block >= blocks0;
   if (which) block -= blocks0;
   const GradJob& job = p.job[which];
@@ -270,23 +345,10 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(GradArgs p, int64_t base
           f4 d = mfma16<FMT>(hi[q], x[e], f4{0.f, 0.f, 0.f, 0.f});
           d = mfma16<FMT>(lo[q], x[e], d);
           acc[q][e] += d * f;
+          asm volatile("" : "+v"(acc[q][e]));   // (each at once: registers)
         }
     }
-    // the waves' sums, 16 ranks at a time
-#pragma unroll
-    for (int q = 0; q < RB; ++q) {
-      __syncthreads();
-      if (wave > 0) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) lds[((wave - 1) * 8 + e) * 64 + lane] = acc[q][e];
-      }
-      __syncthreads();
-      if (wave == 0) {
-        for (int w = 0; w + 1 < kWaves; ++w)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) acc[q][e] += lds[(w * 8 + e) * 64 + lane];
-      }
-    }
+    add_up<RB>(acc, lds, wave, lane);
     if (wave == 0) {
       const bool whole = (s == 0 || p.g.step_adapter[s - 1] != a) &&
                          (end == p.g.steps || p.g.step_adapter[end] != a);
@@ -305,10 +367,12 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(GradArgs p, int64_t base
 }
 
 // The adapters that lie in several chunks, and those without rows (zeros): a
-// wave for 128 columns and 16 RB ranks.
+// workgroup for 128 columns and 16 RB ranks, its waves every so many of the chunks.
 template <int FMT, int RB>
-__global__ __launch_bounds__(64) void join_kernel(GradArgs p, int64_t base) {
-  const int lane = threadIdx.x;
+__global__ __launch_bounds__(kThreads) void join_kernel(GradArgs p, int64_t base) {
+  __shared__ f4 lds[(kWaves - 1) * 8 * 64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int64_t id = base + blockIdx.x;
   const int blocks0 = p.job[0].blocks, blocks = blocks0 + p.job[1].blocks;
   const int group = (int)(id % p.groups);
@@ -332,40 +396,18 @@ __global__ __launch_bounds__(64) void join_kernel(GradArgs p, int64_t base) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) acc[q][e] = f4{0.f, 0.f, 0.f, 0.f};
   if (steps)
-    for (int c = from; c <= to; ++c) {
+    for (int c = from + wave; c <= to; c += kWaves) {
       const f4* src = partial_at(p, job, c + a, block, group, RB);
 #pragma unroll
       for (int q = 0; q < RB; ++q)
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[q][e] += src[(q * 8 + e) * 64 + lane];
     }
+  add_up<RB>(acc, lds, wave, lane);
+  if (wave > 0) return;
   store_out<FMT, RB>(p, job, a, group * 16 * RB, block * kCols, lane, acc);
 }
 
-// A thread 8 inner values of one outer index; neighbouring threads neighbouring
-// outer indices.
-struct TurnJobs {
-  TurnArgs job[2];
-  int64_t blocks0;
-};
-__global__ __launch_bounds__(kThreads) void turn_kernel(TurnJobs jobs, int64_t base) {
-  int64_t id = base + blockIdx.x;
-  const int which = id >= jobs.blocks0;
-  if (which) id -= jobs.blocks0;
-  const TurnArgs& p = jobs.job[which];
-  int64_t t = id * kThreads + threadIdx.x;
-  const int o = (int)(t % p.outer);
-  t /= p.outer;
-  const int i = (int)(t % (p.inner_p / 8)) * 8;
-  const int64_t l = t / (p.inner_p / 8);
-  if (l >= p.count) return;
-  const half_t* src = p.src + l * p.stride_s + (int64_t)i * p.lds + o;
-  h8 v = {};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (i + e < p.inner) v[e] = src[e * p.lds];
-  *(h8*)(p.dst + l * p.stride_d + (int64_t)o * p.ldd + i) = v;
-}
 __global__ __launch_bounds__(kThreads) void widen_kernel(WidenArgs p, int64_t base) {
   int64_t t = (base + blockIdx.x) * kThreads + threadIdx.x;
   const int c = (int)(t % (p.cols_p / 8)) * 8;
@@ -394,7 +436,7 @@ __global__ __launch_bounds__(kThreads) void tail_kernel(TailArgs p, int64_t base
   *(h8*)(p.dst + row * 64 + c) = v;
 }
 int64_t turn_blocks(const TurnArgs& p) {
-  return ((int64_t)p.outer * (p.inner_p / 8) * p.count + kThreads - 1) / kThreads;
+  return ((int64_t)p.outer * (p.inner_p / 8) * p.count + kListThreads - 1) / kListThreads;
 }
 
 template <int FMT, int RB>
@@ -403,16 +445,31 @@ hipError_t launch_rb(const GradArgs& p, hipStream_t stream) {
   hipError_t e = launch_tiles((const void*)grad_kernel<FMT, RB>, p, blocks * p.groups * p.chunks,
                               kThreads, 0, stream);
   if (e != hipSuccess) return e;
-  return launch_tiles((const void*)join_kernel<FMT, RB>, p, blocks * p.groups * p.g.S, 64, 0,
+  return launch_tiles((const void*)join_kernel<FMT, RB>, p, blocks * p.groups * p.g.S, kThreads, 0,
                       stream);
 }
 
 }  // namespace
 
-hipError_t launch_group(const GroupArgs& p, hipStream_t stream) {
-  hipError_t e = launch_tiles((const void*)count_kernel, p, p.S, kThreads, 0, stream);
-  if (e != hipSuccess) return e;
-  return launch_tiles((const void*)list_kernel, p, (int64_t)p.S + 1, kThreads, 0, stream);
+hipError_t launch_lists(const GroupArgs* group, const TurnArgs* turns, int count,
+                        hipStream_t stream) {
+  ListJobs jobs{};
+  int64_t blocks = 0;
+  if (group) {
+    jobs.g = *group;
+    jobs.groups = group->S + 1;
+    if (group->S > kHistogram) {
+      const hipError_t e =
+          launch_tiles((const void*)count_kernel, *group, group->S, kListThreads, 0, stream);
+      if (e != hipSuccess) return e;
+    }
+  }
+  for (int i = 0; i < count; ++i) {
+    jobs.turn[i] = turns[i];
+    if (i == 0) jobs.turns0 = turn_blocks(turns[i]);
+    blocks += turn_blocks(turns[i]);
+  }
+  return launch_tiles((const void*)list_kernel, jobs, jobs.groups + blocks, kListThreads, 0, stream);
 }
 
 // Chunks so that some 1024 workgroups share the work, of at least four steps
@@ -421,7 +478,7 @@ GradPlan plan_grad(int M, int N, int K, int R, int S) {
   GradPlan p;
   p.steps = max_steps(M, S);
   p.padded = (int)round_up(R, 16);
-  p.rb = R <= 16 ? 1 : R <= 32 ? 2 : 4;
+  p.rb = R <= 16 ? 1 : 2;
   p.groups = (R + 16 * p.rb - 1) / (16 * p.rb);
   const int64_t cols[2] = {K, N};
   const int64_t blocks = ((cols[0] + kCols - 1) / kCols + (cols[1] + kCols - 1) / kCols) * p.groups;
@@ -442,18 +499,8 @@ hipError_t launch_adapter_grads(int fmt, const GradArgs& p, const GradPlan& plan
                                     p, 2 * (int64_t)p.g.steps, kThreads, 0, stream);
   if (e != hipSuccess) return e;
   if (fmt == kFmtBF16)
-    return plan.rb == 1   ? launch_rb<kFmtBF16, 1>(p, stream)
-           : plan.rb == 2 ? launch_rb<kFmtBF16, 2>(p, stream)
-                          : launch_rb<kFmtBF16, 4>(p, stream);
-  return plan.rb == 1   ? launch_rb<kFmtF16, 1>(p, stream)
-         : plan.rb == 2 ? launch_rb<kFmtF16, 2>(p, stream)
-                        : launch_rb<kFmtF16, 4>(p, stream);
-}
-
-hipError_t launch_turn(const TurnArgs& first, const TurnArgs* second, hipStream_t stream) {
-  TurnJobs jobs{{first, second ? *second : first}, turn_blocks(first)};
-  return launch_tiles((const void*)turn_kernel, jobs,
-                      jobs.blocks0 + (second ? turn_blocks(*second) : 0), kThreads, 0, stream);
+    return plan.rb == 1 ? launch_rb<kFmtBF16, 1>(p, stream) : launch_rb<kFmtBF16, 2>(p, stream);
+  return plan.rb == 1 ? launch_rb<kFmtF16, 1>(p, stream) : launch_rb<kFmtF16, 2>(p, stream);
 }
 
 hipError_t launch_tail(const TailArgs& p, hipStream_t stream) {

@@ -3,10 +3,13 @@
 // name once a block of 16 rows (from L2 where neighbours share them).
 //
 // A workgroup takes 16 rows, one of the adapters they name and up to 64 ranks;
-// its waves share K out in turns of 128 and add up through LDS.  Rows of other
-// adapters are multiplied along and dropped.  The launch has 16 places for
-// adapters a block of rows, since only the GPU knows the ids: those past the
-// block's last one end at once.
+// its sixteen waves share K out in turns of 128 (64, 32 for more ranks), the next
+// turn's loads in flight, and add up through LDS: with few rows the time is a few
+// memory latencies.  Rows of other adapters are multiplied along and dropped.
+// Only the GPU knows the ids, so a block of rows has places for adapters, up to
+// 16 while the launch is small: a workgroup takes its place's adapter and every
+// so many after it, and ends if there is none (256 blocks of 4096 rows with 16
+// places: 10 us for workgroups that end at once).
 #include "fused/skinny.hpp"
 #include "tune.hpp"
 
@@ -16,47 +19,14 @@ namespace {
 
 using namespace fused::skinny;
 
-constexpr int kWaves = 8, kSteps = 4, kChunk = 32 * kSteps, kSlots = 16;
+constexpr int kWaves = 16, kMaxSlots = 16, kWorkgroups = 512;
 
+// One adapter's ranks first .. of the 16 rows from m0 (`rows`: its own).
 template <int FMT, int RB>
-__global__ __launch_bounds__(64 * kWaves) void shrink_kernel(ShrinkArgs p, int64_t base) {
-  __shared__ f4 lds[(kWaves - 1) * RB * 64];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+__device__ __forceinline__ void shrink_one(const ShrinkArgs& p, f4* lds, int a, uint32_t rows,
+                                           int m0, int mr, int first, int lane, int wave) {
+  constexpr int kSteps = 4 / RB, kChunk = 32 * kSteps;
   const int r = lane & 15, quarter = lane >> 4;
-  const int groups = (p.R + 16 * RB - 1) / (16 * RB);
-  const int64_t id = base + blockIdx.x;
-  // (a place's blocks of rows one after another: dealt out the other way round,
-  // the places that have an adapter would all be on one XCD)
-  const int64_t per = ((int64_t)p.M + 15) / 16 * groups, rest = id % per;
-  const int slot = (int)(id / per);
-  const int first = (int)(rest % groups) * 16 * RB;   // rank
-  const int m0 = (int)(rest / groups) * 16;
-  const int mr = m0 + r < p.M ? m0 + r : p.M - 1;
-  const int mine = m0 + r < p.M ? adapter_of(p.ids, m0 + r, p.S) : -1;
-
-  if (slot == 0 && wave == 0 && p.t32) {
-    // rows without an adapter: zeros (one that does not exist: NaN)
-    for (int q = quarter; q < RB; q += 4)
-#pragma unroll 4
-      for (int i = 0; i < 16; ++i) {
-        const int other = __builtin_amdgcn_readlane(mine, i), c = first + 16 * q + r;
-        if (other < 0 && m0 + i < p.M && c < p.R)
-          p.t32[(int64_t)(m0 + i) * p.ldt + c] = other == -1 ? 0.f : __builtin_nanf("");
-      }
-  }
-  // the slot's adapter
-  uint32_t pending = (uint32_t)__ballot(mine >= 0) & 0xFFFFu, rows = 0;
-  int a = -1;
-  for (int d = 0; d <= slot && pending; ++d) {
-    a = __builtin_amdgcn_readlane(mine, __builtin_ctz(pending));
-    rows = (uint32_t)__ballot(mine == a) & 0xFFFFu;
-    pending &= ~rows;
-    if (d == slot) break;
-    a = -1;
-  }
-  if (a < 0) return;
-
   const half_t* x = p.X + (int64_t)mr * p.ldx + 8 * quarter;
   const half_t* w[RB];
 #pragma unroll
@@ -69,22 +39,36 @@ __global__ __launch_bounds__(64 * kWaves) void shrink_kernel(ShrinkArgs p, int64
   for (int q = 0; q < RB; ++q) acc[q] = f4{0.f, 0.f, 0.f, 0.f};
   // (pointers and K both moved on by the lane's 8 quarter)
   const int K = p.K - 8 * quarter, chunks = p.K / kChunk;
-  auto turn = [&](int k, auto tail) __attribute__((always_inline)) {
+  h8 xv[2][kSteps], wv[2][RB][kSteps];
+  auto load = [&](int set, int k, auto tail) __attribute__((always_inline)) {
     constexpr bool kTail = decltype(tail)::value;
-    h8 xv[kSteps], wv[RB][kSteps];
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      xv[s] = load_x<kTail>(x, k + 32 * s, K);
+      xv[set][s] = load_x<kTail>(x, k + 32 * s, K);
 #pragma unroll
-      for (int q = 0; q < RB; ++q) wv[q][s] = load_x<kTail>(w[q], k + 32 * s, K);
+      for (int q = 0; q < RB; ++q) wv[set][q][s] = load_x<kTail>(w[q], k + 32 * s, K);
     }
+  };
+  auto multiply = [&](int set) __attribute__((always_inline)) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-      for (int q = 0; q < RB; ++q) acc[q] = mfma16<FMT>(xv[s], wv[q][s], acc[q]);
+      for (int q = 0; q < RB; ++q) acc[q] = mfma16<FMT>(xv[set][s], wv[set][q][s], acc[q]);
   };
-  for (int c = wave; c < chunks; c += kWaves) turn(c * kChunk, std::false_type());
-  if (chunks * kChunk < p.K && wave == chunks % kWaves) turn(chunks * kChunk, std::true_type());
+  // two turns at a time, so that the sets are named by constants
+  int c = wave;
+  if (c < chunks) load(0, c * kChunk, std::false_type());
+  for (; c < chunks; c += 2 * kWaves) {
+    const bool second = c + kWaves < chunks;
+    if (second) load(1, (c + kWaves) * kChunk, std::false_type());
+    multiply(0);
+    if (c + 2 * kWaves < chunks) load(0, (c + 2 * kWaves) * kChunk, std::false_type());
+    if (second) multiply(1);
+  }
+  if (chunks * kChunk < p.K && wave == chunks % kWaves) {
+    load(0, chunks * kChunk, std::true_type());
+    multiply(0);
+  }
   add_waves<RB>(acc, reinterpret_cast<float*>(lds), wave, lane, kWaves);
   if (wave > 0) return;
 
@@ -123,6 +107,45 @@ __global__ __launch_bounds__(64 * kWaves) void shrink_kernel(ShrinkArgs p, int64
   }
 }
 
+template <int FMT, int RB>
+__global__ __launch_bounds__(64 * kWaves) void shrink_kernel(ShrinkArgs p, int64_t base) {
+  __shared__ f4 lds[(kWaves - 1) * RB * 64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, quarter = lane >> 4;
+  const int groups = (p.R + 16 * RB - 1) / (16 * RB);
+  const int64_t id = base + blockIdx.x;
+  // (a place's blocks of rows one after another: dealt out the other way round,
+  // the places that have an adapter would all be on one XCD)
+  const int64_t per = ((int64_t)p.M + 15) / 16 * groups, rest = id % per;
+  const int slot = (int)(id / per);
+  const int first = (int)(rest % groups) * 16 * RB;   // rank
+  const int m0 = (int)(rest / groups) * 16;
+  const int mr = m0 + r < p.M ? m0 + r : p.M - 1;
+  const int mine = m0 + r < p.M ? adapter_of(p.ids, m0 + r, p.S) : -1;
+
+  if (slot == 0 && wave == 0 && p.t32) {
+    // rows without an adapter: zeros (one that does not exist: NaN)
+    for (int q = quarter; q < RB; q += 4)
+#pragma unroll 4
+      for (int i = 0; i < 16; ++i) {
+        const int other = __builtin_amdgcn_readlane(mine, i), c = first + 16 * q + r;
+        if (other < 0 && m0 + i < p.M && c < p.R)
+          p.t32[(int64_t)(m0 + i) * p.ldt + c] = other == -1 ? 0.f : __builtin_nanf("");
+      }
+  }
+  uint32_t pending = (uint32_t)__ballot(mine >= 0) & 0xFFFFu;
+  for (int d = 0; pending; ++d) {
+    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(pending));
+    const uint32_t rows = (uint32_t)__ballot(mine == a) & 0xFFFFu;
+    pending &= ~rows;
+    if (d % p.slots == slot) {
+      if (d >= p.slots) __syncthreads();   // the sums before have been read
+      shrink_one<FMT, RB>(p, lds, a, rows, m0, mr, first, lane, wave);
+    }
+  }
+}
+
 template <int FMT>
 const void* pick(int rb) {
   return rb == 1   ? (const void*)shrink_kernel<FMT, 1>
@@ -134,8 +157,11 @@ const void* pick(int rb) {
 
 hipError_t launch_shrink(int fmt, const ShrinkArgs& p, hipStream_t stream) {
   const int rb = p.R <= 16 ? 1 : p.R <= 32 ? 2 : 4;
-  const int64_t wgs = ((int64_t)p.M + 15) / 16 * ((p.R + 16 * rb - 1) / (16 * rb)) * kSlots;
-  return launch_tiles(fmt == kFmtBF16 ? pick<kFmtBF16>(rb) : pick<kFmtF16>(rb), p, wgs,
+  const int64_t wgs = ((int64_t)p.M + 15) / 16 * ((p.R + 16 * rb - 1) / (16 * rb));
+  ShrinkArgs a = p;
+  a.slots = (int)std::max<int64_t>(
+      1, std::min<int64_t>(std::min(kMaxSlots, p.M), kWorkgroups / std::max<int64_t>(1, wgs)));
+  return launch_tiles(fmt == kFmtBF16 ? pick<kFmtBF16>(rb) : pick<kFmtF16>(rb), a, wgs * a.slots,
                       64 * kWaves, 0, stream);
 }
 

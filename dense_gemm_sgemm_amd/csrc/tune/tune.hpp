@@ -82,6 +82,7 @@ struct ShrinkArgs {
   float* t32;            // [M][ldt] or null: the sums themselves
   int64_t ldt;
   int M, K, R, S;
+  int slots = 1;   // (set by the launcher)
 };
 hipError_t launch_shrink(int fmt, const ShrinkArgs& p, hipStream_t stream);
 
@@ -107,7 +108,7 @@ struct GroupArgs {
   int steps;           // as many as there can be
 };
 inline int max_steps(int M, int S) { return (int)(((int64_t)M + 31) / 32 + std::min(M, S)); }
-hipError_t launch_group(const GroupArgs& p, hipStream_t stream);
+constexpr int kHistogram = 2048;   // adapters that one workgroup counts
 
 // One of the two gradients: `left` [rows][ld_left] fp32 (dt or t) times `right`
 // [rows][ld_right] 16-bit (X or dC).
@@ -149,7 +150,9 @@ struct TurnArgs {
   int64_t lds, stride_s, ldd, stride_d;
   int inner, inner_p, outer, count;
 };
-hipError_t launch_turn(const TurnArgs& first, const TurnArgs* second, hipStream_t stream);
+// The lists (group: or null) and up to two stacks, in one launch.
+hipError_t launch_lists(const GroupArgs* group, const TurnArgs* turns, int count,
+                        hipStream_t stream);
 // dst[l][r][0 .. cols_p) = src[l][r][0 .. cols), zeros past cols (cols_p a
 // multiple of 8, rows of dst cols_p apart).
 struct WidenArgs {

@@ -94,9 +94,19 @@ def _stack(t, name):
 
 
 def _adapters(t, name, dtype, index, rows, cols, count=None):
-    """(adapters, pointer, leading dimension, distance between adapters) of a stack
-    [S, rows, cols]; None of rows, cols or count is free."""
+    """(adapters, ranks or rows, pointer, leading dimension, distance between
+    adapters) of a stack [S, rows, cols]; None of rows, cols or count is free.
+    Runs for every stack of every call: the usual case is told by the cheapest
+    queries."""
     torch = _torch_module()
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.dim() == 3 and \
+            t.get_device() == index:
+        S, r, c = t.shape
+        if r > 1 and c > 1 and S > 1 and (rows is None or r == rows) and \
+                (cols is None or c == cols) and (count is None or S == count):
+            s0, s1, s2 = t.stride()
+            if s2 == 1 and c <= s1 <= INT_MAX:
+                return S, r, t.data_ptr(), s1, s0
     if not isinstance(t, torch.Tensor) or t.dim() != 3:
         raise TypeError("%s must be a 3-D tensor, one matrix an adapter" % name)
     if t.dtype != dtype:
@@ -109,7 +119,7 @@ def _adapters(t, name, dtype, index, rows, cols, count=None):
                 "ranks" if cols is None else cols], tuple(t.shape)))
     if t.get_device() != index:
         raise ValueError("all tensors of a call must live on one GPU")
-    return S, ptr, max(ld, c), stride
+    return S, r, ptr, max(ld, c), stride
 
 
 def _scales(scales, index, S):
@@ -130,9 +140,8 @@ def gemm_lora(X, W, A, B, ids, C, scales=None, bias=None, act: str = "none", res
     dtype, typ, at, M, K, px, ldx = _first(X)
     N = _rows(W, "W")
     pw, ldw = _shaped(W, "W", dtype, at, N, K)
-    S, pa, lda, sa = _adapters(A, "A", dtype, at, None, K)
-    R = A.shape[1]
-    _, pb, ldb, sb = _adapters(B, "B", dtype, at, N, R, S)
+    S, R, pa, lda, sa = _adapters(A, "A", dtype, at, None, K)
+    _, _, pb, ldb, sb = _adapters(B, "B", dtype, at, N, R, S)
     pi = _vector(ids, "ids", torch.int64, at, M)
     ps = _scales(scales, at, S)
     pc, ldc = _shaped(C, "C", dtype, at, M, N)
@@ -156,9 +165,8 @@ def lora_workspace_bytes(X, W, A, B) -> int:
     """Workspace bytes ``gemm_lora`` needs for these tensors."""
     dtype, typ, at, M, K, px, ldx = _first(X)
     N = _rows(W, "W")
-    S = _adapters(A, "A", dtype, at, None, K)[0]
-    R = A.shape[1]
-    ldb = _adapters(B, "B", dtype, at, N, R, S)[2]
+    S, R = _adapters(A, "A", dtype, at, None, K)[:2]
+    ldb = _adapters(B, "B", dtype, at, N, R, S)[3]
     return load_library().gemm_lora_workspace(typ, M, N, K, R, S, px, ldx,
                                               *_shaped(W, "W", dtype, at, N, K), ldb)
 
@@ -174,16 +182,15 @@ def gemm_lora_bwd(X, W, A, B, ids, T, dC, dX=None, dA=None, dB=None, scales=None
     dtype, typ, at, M, K, px, ldx = _first(X)
     N = _rows(W, "W")
     pw, ldw = _shaped(W, "W", dtype, at, N, K)
-    S, pa, lda, sa = _adapters(A, "A", dtype, at, None, K)
-    R = A.shape[1]
-    _, pb, ldb, sb = _adapters(B, "B", dtype, at, N, R, S)
+    S, R, pa, lda, sa = _adapters(A, "A", dtype, at, None, K)
+    _, _, pb, ldb, sb = _adapters(B, "B", dtype, at, N, R, S)
     pi = _vector(ids, "ids", torch.int64, at, M)
     ps = _scales(scales, at, S)
     pt, ldt = _shaped(T, "T", torch.float32, at, M, R)
     pc, ldc = _shaped(dC, "dC", dtype, at, M, N)
     pdx, lddx = _optional(dX, "dX", dtype, at, M, K)
-    pda, ldda, sda = (None, 0, 0) if dA is None else _adapters(dA, "dA", dtype, at, R, K, S)[1:]
-    pdb, lddb, sdb = (None, 0, 0) if dB is None else _adapters(dB, "dB", dtype, at, N, R, S)[1:]
+    pda, ldda, sda = (None, 0, 0) if dA is None else _adapters(dA, "dA", dtype, at, R, K, S)[2:]
+    pdb, lddb, sdb = (None, 0, 0) if dB is None else _adapters(dB, "dB", dtype, at, N, R, S)[2:]
     lib = _lib or load_library()
     _run(at, stream, lib.gemm_lora_bwd,
          (typ, M, N, K, R, S, px, ldx, pw, ldw, pa, lda, sa, pb, ldb, sb, pi, ps, pt, ldt, pc, ldc,
@@ -198,9 +205,9 @@ def lora_bwd_workspace_bytes(X, W, A, dC, want_dx: bool = True, want_da: bool = 
     """Workspace bytes ``gemm_lora_bwd`` needs for these tensors and gradients."""
     dtype, typ, at, M, K, _, _ = _first(X)
     N = _rows(W, "W")
-    S = _adapters(A, "A", dtype, at, None, K)[0]
+    S, R = _adapters(A, "A", dtype, at, None, K)[:2]
     return load_library().gemm_lora_bwd_workspace(
-        typ, M, N, K, A.shape[1], S, *_shaped(dC, "dC", dtype, at, M, N),
+        typ, M, N, K, R, S, *_shaped(dC, "dC", dtype, at, M, N),
         *_shaped(W, "W", dtype, at, N, K), bool(want_dx), bool(want_da), bool(want_db))
 
 
