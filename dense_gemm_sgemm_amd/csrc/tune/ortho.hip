@@ -131,10 +131,12 @@ struct Plan {
   size_t x, a, sums, coef;   // bytes of one buffer
   int x_count, a_count;
   size_t cut;            // fp32 sums of tiles whose K is cut into ranges
-  bool small;
+  bool small, mid;
   SmallPlan few;
+  MidPlan between;
   size_t total() const {
-    return sums + coef + (small ? few.total() : x_count * x + a_count * a + cut);
+    return sums + coef +
+           (small ? few.total() : mid ? between.total() : x_count * x + a_count * a + cut);
   }
 };
 
@@ -149,6 +151,18 @@ SymPlan plan_gram(const Plan& p, int L, bool lo) {
   return plan_sym(p.sp, (p.fine && lo ? 3 : 1) * (p.tp / 64), L);
 }
 SymPlan plan_square(const Plan& p, int L) { return plan_sym(p.sp, (p.fine ? 3 : 1) * (p.sp / 64), L); }
+
+// The short tiles of ortho_mid.hip, where the tile kernel's launches would be
+// mostly their beginning and end; they do three products for one throughout, so
+// they are worth it for twice as much where the others would too (bf16, fp16; us
+// on short and large tiles: 128 x 128 92 and 132, 92 and 190; 256 x 4096 163 and
+// 310, 164 and 431; four of 512 x 1024 243 and 253, 242 and 337; sixteen of 384 x
+// 512 297 and 217, 297 and 374; 1024 x 1024 264 and 315, 263 and 440; 1024 x 2048
+// 354 and 322, 353 and 457; four of 768 x 1024 420 and 291, 420 and 424).
+bool by_mid(bool fine, int L, int s, int t) {
+  const int64_t size = (int64_t)L * s * t;
+  return s <= 1024 && (s > 512 ? size + size / 2 : size) <= (fine ? 5 : 2.5) * (1 << 20);
+}
 
 Plan make_plan(int type_g, int type_o, int L, int m, int n, int steps) {
   Plan p{};
@@ -169,6 +183,11 @@ Plan make_plan(int type_g, int type_o, int L, int m, int n, int steps) {
   p.small = p.s <= kSmallSide;
   if (p.small) {
     p.few = plan_small(L, p.s, p.t);
+    return p;
+  }
+  p.mid = by_mid(p.fine, L, p.s, p.t);
+  if (p.mid) {
+    p.between = plan_mid(L, p.s, p.t);
     return p;
   }
   p.x_count = 2 + (p.x_lo || p.x0_lo ? 2 : 0);
@@ -241,6 +260,8 @@ MI355TUNE_API int gemm_ortho(int type_g, int type_o, int L, int m, int n, const 
   if (e != hipSuccess) return to_status(e);
   if (p.small)
     return to_status(launch_small(st, p.few, steps, coeffs, SmallOut{O, ldo, stride_o, to}, ws, s));
+  if (p.mid)
+    return to_status(launch_mid(st, p.between, steps, coeffs, SmallOut{O, ldo, stride_o, to}, ws, s));
   half_t* x[2][2];   // [iterate][hi, lo]
   for (int v = 0; v < 2; ++v)
     for (int i = 0; i < 2; ++i) {

@@ -1,5 +1,5 @@
-// Shared by the two forms of gemm_ortho: ortho.hip, on the tile kernel, and
-// ortho_small.hip, for a shorter side of up to 64.
+// Shared by the forms of gemm_ortho: ortho.hip, on the tile kernel,
+// ortho_small.hip, for a shorter side of up to 64, and ortho_mid.hip between them.
 #pragma once
 
 #include "tune.hpp"
@@ -88,9 +88,48 @@ struct SmallOut {
   int64_t ldo, stride_o;
   int type;
 };
+// Eight values of the result's row m < m_end, columns n .. (those below n_end).
+__device__ __forceinline__ void store_out8(const SmallOut& o, int64_t l, int m, int n, int m_end,
+                                           int n_end, const float (&v)[8]) {
+  if (m >= m_end || n >= n_end) return;
+  const int64_t at = l * o.stride_o + (int64_t)m * o.ldo + n;
+  if (o.type == kF32) {
+    float* d = static_cast<float*>(o.O) + at;
+    if (n + 8 <= n_end) {
+      __builtin_memcpy(d, v, 32);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (n + e < n_end) d[e] = v[e];
+    }
+    return;
+  }
+  h8 w;
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    w[e] = o.type == GEMM_TYPE_BF16 ? f32_to_word<kFmtBF16>(v[e]) : f32_to_word<kFmtF16>(v[e]);
+  half_t* d = static_cast<half_t*>(o.O) + at;
+  if (n + 8 <= n_end) {
+    __builtin_memcpy(d, &w, 16);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (n + e < n_end) d[e] = w[e];
+  }
+}
 // Everything after the norms; st's hi, lo and tiles are not used.
 hipError_t launch_small(const StartArgs& st, const SmallPlan& p, int steps, const float* coeffs,
                         const SmallOut& out, char* ws, hipStream_t stream);
+
+// Middling sizes (ortho_mid.hip).
+struct MidPlan {
+  int sp, tp, splits, per;
+  size_t x, a, sum;        // bytes of a buffer: hi (or lo) of an iterate, of A or C; sums
+  size_t total() const { return 8 * x + 4 * a + sum; }
+};
+MidPlan plan_mid(int L, int s, int t);
+hipError_t launch_mid(const StartArgs& st, const MidPlan& p, int steps, const float* coeffs,
+                      const SmallOut& out, char* ws, hipStream_t stream);
 
 }  // namespace ortho
 }  // namespace tune

@@ -150,13 +150,12 @@ enum { GEMM_TYPE_F32 = 2 };
  * A G of zeros gives zeros, one with an infinity or NaN gives NaN throughout;
  * neither touches the other matrices.
  *
- * Products are on the 16-bit matrix cores.  For BF16 outputs the iterates are
- * binary16, the first three of them in two values (22 bits); for F16 and F32
- * outputs everything is in two values, at three products for one.  The result
- * differs from the formula's by about 0.12 % (BF16: beside the output's own
- * rounding of 0.17 %) or 2^-19, in the 2-norm, for singular values of G that
- * spread over a factor of a few hundred; what is smaller than that is kept less
- * well, for F16 and F32 by 2^-11 of the factor.  The singular values of every X
+ * Products are on the 16-bit matrix cores, of values held in two binary16 ones (22
+ * bits) at three products for one; for BF16 outputs of large matrices one value
+ * is enough for all but the first three iterates.  The result differs from the
+ * formula's by about 2^-19, or there by 0.12 % (beside the output's own rounding
+ * of 0.17 %), in the 2-norm, for singular values of G that spread over a factor
+ * of a few hundred; what is smaller than that is kept less well.  The singular values of every X
  * must stay below 7, as they do for coefficients that converge from [0, 1].
  *
  * steps is 1 .. 64; m, n and L go up to 2^16; others are GEMM_ERR_BAD_ARG, as is
@@ -169,9 +168,10 @@ MI355TUNE_API int gemm_ortho(int type_g, int type_o, int L, int m, int n,
                              void* workspace, unsigned long long workspace_bytes,
                              void* stream);
 
-/* Workspace bytes of gemm_ortho: with s = min(m, n), t = max(m, n), each at least
- * 128 and a multiple of 64, 4 to 8 bytes for each of L * s * t and of L * s * s,
- * and the norms. */
+/* Workspace bytes of gemm_ortho: with s = min(m, n), t = max(m, n), padded to
+ * multiples of 64 (128 at least for the large ones), 4 to 16 bytes for each of
+ * L * s * t, 4 to 8 for each of L * s * s, fp32 sums of products over a long
+ * side, and the norms. */
 MI355TUNE_API unsigned long long gemm_ortho_workspace(int type_g, int type_o, int L, int m, int n,
                                                       int steps);
 

@@ -154,7 +154,9 @@ def rounded(G, fine, steps=5, coeffs=MUON, eps=1e-7):
 def ortho_check(got, G, what, steps=5, coeffs=MUON, eps=1e-7):
     """Matrix by matrix, in the 2-norm."""
     fine = got.dtype != torch.bfloat16
-    small = min(G.shape[-2:]) <= 64        # two values throughout, whatever the output's type
+    # two values throughout for the smaller ones, whatever the output's type
+    low = min(G.shape[-2:])
+    small = low <= 64 or (low <= 1024 and G.numel() * (1.5 if low > 512 else 1) <= 2.5 * 2 ** 20)
     ref = ortho_ref(G, steps, coeffs, eps)
     off = (rounded(G, fine or small, steps, coeffs, eps) - ref).flatten(1).norm(dim=1) + \
         (in_32_bits(G, steps, coeffs, eps).double() - ref).flatten(1).norm(dim=1)
