@@ -56,14 +56,16 @@ Plan make_plan(int M, int N, int K, int R, int S, Mat x, Mat w, int ldb) {
 // stacks of factors turned, the rows by adapter, dt and t packed, their steps'
 // factors, partial sums; padded copies of dC and W.
 struct BwdPlan {
-  bool dx, da, db;
+  bool dx, da, db, few = false;   // few: dX by the kernel for few rows
+  DxPlan sums;
   size_t t2 = 0, factor = 0, dt = 0, at = 0, bt = 0;
   size_t counts = 0, rows = 0, steps = 0, pack = 0, step_factor = 0, partial[2] = {0, 0};
   size_t copy_c = 0, copy_w = 0, tail = 0;
   GradPlan grad{};
   size_t total() const {
     return t2 + factor + dt + at + bt + counts + rows + steps + 2 * pack + 2 * step_factor +
-           partial[0] + partial[1] + copy_c + copy_w + tail;
+           partial[0] + partial[1] + copy_c + copy_w + tail +
+           sums.bytes;
   }
 };
 size_t copy_bytes_w(int N, int K) {
@@ -82,10 +84,15 @@ BwdPlan plan_bwd(int M, int N, int K, int R, int S, Mat c, Mat w, bool dx, bool 
     p.t2 = round256((size_t)M * rank_ld2(R) * 2);
     p.factor = round256((size_t)M * rank_blocks(R) * sizeof(float));
     p.at = round256((size_t)S * K * 16 * rank_blocks(R) * 2);
-    const int Kd = pad_k(N);
-    if (needs_copy(c.p, c.ld, M, N)) p.copy_c = copy_bytes(M, N);
-    if (needs_copy(w.p, w.ld, N, K) || Kd != N) p.copy_w = copy_bytes_w(N, K);
-    if (Kd % 64 != 0) p.tail = (size_t)pad_rows(M) * 64 * 2;
+    p.few = by_rows(M, K, c, w);
+    if (p.few) {
+      p.sums = plan_dx(M, N, K);
+    } else {
+      const int Kd = pad_k(N);
+      if (needs_copy(c.p, c.ld, M, N)) p.copy_c = copy_bytes(M, N);
+      if (needs_copy(w.p, w.ld, N, K) || Kd != N) p.copy_w = copy_bytes_w(N, K);
+      if (Kd % 64 != 0) p.tail = (size_t)pad_rows(M) * 64 * 2;
+    }
   }
   if (p.da || p.db) {
     // (the same whatever is asked for, so that each gradient has the same bits)
@@ -167,7 +174,7 @@ MI355TUNE_API int gemm_lora(int type, int M, int N, int K, int R, int S, const v
   a.fmt = fmt;
   LoraExtra y{t2, rank_ld2(R), factor, in16(B), ldb, stride_b, ids, R, S,
                     rank_blocks(R), M, N};
-  if (by_rows(M, N, x0, w0)) return to_status(launch_lora_rows(a, y, cus, s));
+  if (by_rows(M, N, x0, w0)) return to_status(launch_lora_rows(a, y, RowSums(), cus, s));
   PadJobs jobs;
   const Mat x = jobs.add(x0, M, K, ws), w = jobs.add(w0, N, K, ws);
   e = launch_pad(jobs, s);
@@ -292,7 +299,16 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S, con
     e = launch_adapter_grads(fmt, ga, p.grad, s);
     if (e != hipSuccess) return to_status(e);
   }
-  if (p.dx) {
+  LoraExtra y{t2, rank_ld2(R), factor, at, 16 * rank_blocks(R), (int64_t)K * 16 * rank_blocks(R),
+              ids, 16 * rank_blocks(R), S, rank_blocks(R), M, K};
+  if (p.dx && p.few) {
+    float* sum = reinterpret_cast<float*>(ws);
+    e = launch_dx(fmt, c0.p, lddc, w0.p, ldw, M, N, K, p.sums, sum, s);
+    if (e != hipSuccess) return to_status(e);
+    Args16 a{c0.p, w0.p, out16(dX), lddc, ldw, lddx, M, K, 0};
+    a.fmt = fmt;
+    e = launch_lora_rows(a, y, RowSums{sum, p.sums.ld, p.sums.splits}, cus, s);
+  } else if (p.dx) {
     PadJobs jobs;
     Mat c = c0, w = w0;
     if (p.copy_c) c = jobs.copy(c0, M, N, ws);
@@ -308,8 +324,6 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S, con
     if (e != hipSuccess) return to_status(e);
     Args16 a{c.p, w.p, out16(dX), c.ld, w.ld, lddx, pad_rows(M), pad_k(K), pad_k(N)};
     a.fmt = fmt;
-    LoraExtra y{t2, rank_ld2(R), factor, at, 16 * rank_blocks(R), (int64_t)K * 16 * rank_blocks(R), ids,
-                      16 * rank_blocks(R), S, rank_blocks(R), M, K};
     if (p.tail) {
       y.tail = reinterpret_cast<half_t*>(ws);
       e = launch_tail(TailArgs{c0.p, reinterpret_cast<half_t*>(ws), lddc, M, a.M, a.K}, s);

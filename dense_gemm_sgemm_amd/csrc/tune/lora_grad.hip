@@ -184,41 +184,6 @@ __global__ __launch_bounds__(kThreads) void pack_kernel(GradArgs p, int64_t base
   }
 }
 
-// A lane's 8 x 8 block of 16-bit values with rows and columns exchanged.
-__device__ __forceinline__ void turn8(h8 (&v)[8]) {
-  u32x4 x[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = __builtin_bit_cast(u32x4, v[e]);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    u32x4 w;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)   // bytes of {second, first}: the low or the high halves
-      w[q] = __builtin_amdgcn_perm(x[2 * q + 1][k >> 1], x[2 * q][k >> 1],
-                                   k & 1 ? 0x07060302u : 0x05040100u);
-    v[k] = __builtin_bit_cast(h8, w);
-  }
-}
-
-// The waves' sums, 16 ranks at a time, in the order of the waves; complete in wave 0.
-template <int RB>
-__device__ __forceinline__ void add_up(f4 (&acc)[RB][8], f4* lds, int wave, int lane) {
-#pragma unroll
-  for (int q = 0; q < RB; ++q) {
-    __syncthreads();
-    if (wave > 0) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) lds[((wave - 1) * 8 + e) * 64 + lane] = acc[q][e];
-    }
-    __syncthreads();
-    if (wave == 0) {
-      for (int w = 0; w + 1 < kWaves; ++w)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[q][e] += lds[(w * 8 + e) * 64 + lane];
-    }
-  }
-}
-
 // Where a workgroup's sums of an adapter go: 16 RB ranks x 128 columns, lane
 // (g, j) holding ranks 16 q + 4 g + v, columns c0 + 8 j + e.
 template <int FMT, int RB>

@@ -19,6 +19,7 @@ constexpr int kSteps = 4, kChunk = 32 * kSteps, kMaxWaves = 8;
 struct RowsArgs {
   Args16 p;
   LoraExtra x;
+  RowSums sums;
   int waves;
 };
 
@@ -87,6 +88,17 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[t] = mfma16<FMT>(xf[t][s], cur[s], acc[t]);
   };
+  if (args.sums.sum) {
+    // (the waves share the ranges)
+    for (int s = wave; s < args.sums.ranges; s += args.waves)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int m = m0 + 16 * t + 4 * quarter + v;
+          if (m < p.M) acc[t][v] += args.sums.sum[((int64_t)s * p.M + m) * args.sums.ld_sum + row];
+        }
+  }
   int c = wave;
   if (c < chunks) {
     stage.template load<false>(p.A, p.lda, m0, p.M, c * kC, p.K, lane);
@@ -166,12 +178,14 @@ const void* pick(int M) {
 
 }  // namespace
 
-hipError_t launch_lora_rows(const Args16& a, const LoraExtra& x, int cus, hipStream_t stream) {
-  RowsArgs p{a, x, 1};
+hipError_t launch_lora_rows(const Args16& a, const LoraExtra& x, const RowSums& sums, int cus,
+                            hipStream_t stream) {
+  RowsArgs p{a, x, sums, 1};
+  if (sums.sum) p.p.K = 0;
   const int64_t wgs = ((int64_t)a.N + 15) / 16 * (((int64_t)a.M + 63) / 64);
   const int chunk = a.M <= 32 ? kChunk : kChunk / 2;
   const int chunks = std::max(1, (int)(((int64_t)a.K + chunk - 1) / chunk));
-  p.waves = waves_for(wgs, chunks, kMaxWaves, cus);
+  p.waves = sums.sum ? 4 : waves_for(wgs, chunks, kMaxWaves, cus);
   return launch_tiles(a.fmt == kFmtBF16 ? pick<kFmtBF16>(a.M) : pick<kFmtF16>(a.M), p, wgs,
                       64 * p.waves, 0, stream);
 }

@@ -87,8 +87,25 @@ struct ShrinkArgs {
 hipError_t launch_shrink(int fmt, const ShrinkArgs& p, hipStream_t stream);
 
 // The adapters' part beside a product of few rows (lora_rows.hip), operands as
-// they are; x as for the tiles.
-hipError_t launch_lora_rows(const Args16& a, const LoraExtra& x, int cus, hipStream_t stream);
+// they are; x as for the tiles but for B, whose ranks may be any number.  `sums`:
+// the product is there already, in `ranges` fp32 sums [M][ld_sum] behind each
+// other.
+struct RowSums {
+  const float* sum = nullptr;
+  int64_t ld_sum = 0;
+  int ranges = 0;
+};
+hipError_t launch_lora_rows(const Args16& a, const LoraExtra& x, const RowSums& sums, int cus,
+                            hipStream_t stream);
+// dC W for few rows, in ranges of N (lora_dx.hip).
+struct DxPlan {
+  int splits = 0, per = 0;
+  int64_t ld = 0;
+  size_t bytes = 0;
+};
+DxPlan plan_dx(int M, int N, int K);
+hipError_t launch_dx(int fmt, const half_t* dC, int64_t lddc, const half_t* W, int64_t ldw, int M,
+                     int N, int K, const DxPlan& plan, float* sum, hipStream_t stream);
 // C = A B^T (kmajor: A B) with the adapters' part.
 hipError_t launch_lora_tiles(const Args16& a, const LoraExtra& x, bool kmajor, int cus,
                              hipStream_t stream);
@@ -171,6 +188,43 @@ struct TailArgs {
   int rows, rows_p, K;
 };
 hipError_t launch_tail(const TailArgs& p, hipStream_t stream);
+
+// A lane's 8 x 8 block of 16-bit values with rows and columns exchanged.
+__device__ __forceinline__ void turn8(hgemm::h8 (&v)[8]) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  u32x4 x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = __builtin_bit_cast(u32x4, v[e]);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    u32x4 w;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)   // bytes of {second, first}: the low or the high halves
+      w[q] = __builtin_amdgcn_perm(x[2 * q + 1][k >> 1], x[2 * q][k >> 1],
+                                   k & 1 ? 0x07060302u : 0x05040100u);
+    v[k] = __builtin_bit_cast(hgemm::h8, w);
+  }
+}
+
+// The four waves' sums, 16 rows at a time, in the order of the waves; complete in
+// wave 0.
+template <int RB>
+__device__ __forceinline__ void add_up(hgemm::f4 (&acc)[RB][8], hgemm::f4* lds, int wave, int lane) {
+#pragma unroll
+  for (int q = 0; q < RB; ++q) {
+    __syncthreads();
+    if (wave > 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) lds[((wave - 1) * 8 + e) * 64 + lane] = acc[q][e];
+    }
+    __syncthreads();
+    if (wave == 0) {
+      for (int w = 0; w + 1 < 4; ++w)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[q][e] += lds[(w * 8 + e) * 64 + lane];
+    }
+  }
+}
 
 // Row m's adapter: its number, -1 for none, -2 for one that does not exist.
 __device__ __forceinline__ int adapter_of(const long long* ids, int64_t m, int S) {
