@@ -25,7 +25,7 @@ struct DxArgs {
 };
 
 template <int FMT, int MT>
-__global__ __launch_bounds__(kThreads) void dx_kernel(DxArgs p, int64_t base) {
+__global__ __launch_bounds__(kThreads, MT == 4 ? 2 : 1) void dx_kernel(DxArgs p, int64_t base) {
   __shared__ f4 lds[(kWaves - 1) * 8 * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -67,20 +67,25 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(DxArgs p, int64_t base) {
 #pragma unroll
     for (int t = 0; t < MT; ++t) d[t] = load_x<true>(c[t], n, p.N);
   };
+  // (64 rows leave no registers for a step ahead, but two waves a SIMD)
+  constexpr bool kAhead = MT < 4;
   h8 x[8], nx[8], d[MT], nd[MT];
   int s = s0 + wave;
-  if (s < s1) load(s, x, d);
+  if (kAhead && s < s1) load(s, x, d);
   for (; s < s1; s += kWaves) {
-    if (s + kWaves < s1) load(s + kWaves, nx, nd);
+    if (!kAhead) load(s, x, d);
+    if (kAhead && s + kWaves < s1) load(s + kWaves, nx, nd);
     turn8(x);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
 #pragma unroll
       for (int t = 0; t < MT; ++t) acc[t][e] = mfma16<FMT>(d[t], x[e], acc[t][e]);
+    if (kAhead) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = nx[i];
+      for (int i = 0; i < 8; ++i) x[i] = nx[i];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) d[t] = nd[t];
+      for (int t = 0; t < MT; ++t) d[t] = nd[t];
+    }
   }
   add_up<MT>(acc, lds, wave, lane);
   if (wave > 0 || col >= p.K) return;
@@ -113,13 +118,14 @@ const void* pick(int M) {
 
 }  // namespace
 
-// Ranges for some 512 workgroups, of at least two turns of the waves each.
+// Ranges for some 512 workgroups, of at least two turns of the waves each; fewer
+// where their sums are many.
 DxPlan plan_dx(int M, int N, int K) {
   const int64_t blocks = ((int64_t)K + kCols - 1) / kCols * (((int64_t)M + 63) / 64);
   const int steps = (N + 31) / 32;
   DxPlan p;
   p.splits = (int)std::max<int64_t>(
-      1, std::min<int64_t>({16, 512 / std::max<int64_t>(1, blocks), steps / (2 * kWaves)}));
+      1, std::min<int64_t>({M > 32 ? 8 : 16, 512 / std::max<int64_t>(1, blocks), steps / (2 * kWaves)}));
   p.per = (steps + p.splits - 1) / p.splits;
   p.splits = p.per ? (steps + p.per - 1) / p.per : 1;
   p.ld = round_up(K, 8);

@@ -437,8 +437,8 @@ hipError_t launch_lists(const GroupArgs* group, const TurnArgs* turns, int count
   return launch_tiles((const void*)list_kernel, jobs, jobs.groups + blocks, kListThreads, 0, stream);
 }
 
-// Chunks so that some 1024 workgroups share the work, of at least four steps
-// (one a wave).
+// Chunks so that some 1024 workgroups share the work (adapters of few rows are a
+// step each: a chunk of several would take them one after another).
 GradPlan plan_grad(int M, int N, int K, int R, int S) {
   GradPlan p;
   p.steps = max_steps(M, S);
@@ -448,7 +448,7 @@ GradPlan plan_grad(int M, int N, int K, int R, int S) {
   const int64_t cols[2] = {K, N};
   const int64_t blocks = ((cols[0] + kCols - 1) / kCols + (cols[1] + kCols - 1) / kCols) * p.groups;
   const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, blocks));
-  p.chunk_steps = std::max<int>(kWaves, (int)((p.steps + want - 1) / want));
+  p.chunk_steps = std::max<int>(1, (int)((p.steps + want - 1) / want));
   p.chunks = (p.steps + p.chunk_steps - 1) / p.chunk_steps;
   p.pack = round256((size_t)2 * p.padded * p.steps * 64);
   for (int i = 0; i < 2; ++i)

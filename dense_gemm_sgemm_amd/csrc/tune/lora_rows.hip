@@ -89,15 +89,62 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
       for (int t = 0; t < MT; ++t) acc[t] = mfma16<FMT>(xf[t][s], cur[s], acc[t]);
   };
   if (args.sums.sum) {
-    // (the waves share the ranges)
+    // (the waves share the ranges; rows past M repeat the last one, unstored)
     for (int s = wave; s < args.sums.ranges; s += args.waves)
 #pragma unroll
       for (int t = 0; t < MT; ++t)
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const int m = m0 + 16 * t + 4 * quarter + v;
-          if (m < p.M) acc[t][v] += args.sums.sum[((int64_t)s * p.M + m) * args.sums.ld_sum + row];
+          acc[t][v] +=
+              args.sums.sum[((int64_t)s * p.M + (m < p.M ? m : p.M - 1)) * args.sums.ld_sum + row];
         }
+  }
+  // The adapters: lane l stands for row m0 + l.  What the first block of ranks and
+  // the wave's first adapters need is loaded before the products.
+  const int mine = m0 + lane < p.M ? adapter_of(y.ids, m0 + lane, y.S) : -1;
+  const uint64_t named = __ballot(mine >= 0);
+  uint64_t pending = named;
+  int turn = 0, block = 0;
+  constexpr int kAhead = 4;
+  h8 tv[MT], bv[kAhead];
+  float factor[MT][4];
+  uint64_t rows[kAhead] = {};
+  auto load_t = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      // (rows without an adapter, and past M: any values, dropped below)
+      const int m = m0 + 16 * t + r;
+      tv[t] = *(const h8*)(y.t2 + (m < p.M ? m : p.M - 1) * y.ld2 + 32 * block + 8 * quarter);
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int64_t i = m0 + 16 * t + 4 * quarter + v;
+        factor[t][v] = y.factor[(i < p.M ? i : p.M - 1) * y.blocks + block];
+      }
+    }
+  };
+  // the wave's next adapters: every so many of those that the rows name
+  auto load_b = [&]() __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      rows[q] = 0;
+      bv[q] = h8{};
+      int a = 0;
+      while (pending && !rows[q]) {
+        a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(pending));
+        const uint64_t own = __ballot(mine == a);
+        pending &= ~own;
+        if (turn++ % args.waves == wave) rows[q] = own;
+      }
+      if (rows[q])
+        bv[q] = load_ranks(y.B + a * y.stride_b + (int64_t)row * y.ldb,
+                           16 * block + 8 * (quarter & 1), y.R,
+                           (int64_t)(p.N - 1 - row) * y.ldb + y.R);
+    }
+  };
+  if (named) {
+    load_t();
+    load_b();
   }
   int c = wave;
   if (c < chunks) {
@@ -121,31 +168,24 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
     multiply();
   }
 
-  // The adapters: lane l stands for row m0 + l.
-  const int mine = m0 + lane < p.M ? adapter_of(y.ids, m0 + lane, y.S) : -1;
-  uint64_t pending = __ballot(mine >= 0);
-  for (int d = 0; pending; ++d) {
-    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(pending));
-    const uint64_t rows = __ballot(mine == a);
-    pending &= ~rows;
-    if (d % args.waves != wave) continue;
-    const half_t* b = y.B + a * y.stride_b + (int64_t)row * y.ldb;
-    for (int k = 0; k < y.blocks; ++k) {
-      const h8 bv = load_ranks(b, 16 * k + 8 * (quarter & 1), y.R,
-                               (int64_t)(p.N - 1 - row) * y.ldb + y.R);
+  while (named) {
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
-        if (!(rows >> (16 * t) & 0xFFFF)) continue;
-        const int m = m0 + 16 * t + r;
-        const h8 tv = *(const h8*)(y.t2 + (m < p.M ? m : p.M - 1) * y.ld2 + 32 * k + 8 * quarter);
-        const f4 s = mfma16<FMT>(tv, bv, f4{0.f, 0.f, 0.f, 0.f});
+        if (!(rows[q] >> (16 * t) & 0xFFFF)) continue;
+        const f4 s = mfma16<FMT>(tv[t], bv[q], f4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int i = 16 * t + 4 * quarter + v;
-          if (rows >> i & 1) acc[MT + t][v] += y.factor[(int64_t)(m0 + i) * y.blocks + k] * s[v];
-        }
+        for (int v = 0; v < 4; ++v)
+          if (rows[q] >> (16 * t + 4 * quarter + v) & 1) acc[MT + t][v] += factor[t][v] * s[v];
       }
+    if (!pending) {
+      if (++block == y.blocks) break;
+      pending = named;
+      turn = 0;
+      load_t();
     }
+    load_b();
   }
 
   // (the sums take the place of X)
@@ -185,7 +225,7 @@ hipError_t launch_lora_rows(const Args16& a, const LoraExtra& x, const RowSums& 
   const int64_t wgs = ((int64_t)a.N + 15) / 16 * (((int64_t)a.M + 63) / 64);
   const int chunk = a.M <= 32 ? kChunk : kChunk / 2;
   const int chunks = std::max(1, (int)(((int64_t)a.K + chunk - 1) / chunk));
-  p.waves = sums.sum ? 4 : waves_for(wgs, chunks, kMaxWaves, cus);
+  p.waves = sums.sum ? std::max(1, std::min(kMaxWaves, sums.ranges)) : waves_for(wgs, chunks, kMaxWaves, cus);
   return launch_tiles(a.fmt == kFmtBF16 ? pick<kFmtBF16>(a.M) : pick<kFmtF16>(a.M), p, wgs,
                       64 * p.waves, 0, stream);
 }

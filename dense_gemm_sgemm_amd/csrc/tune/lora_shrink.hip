@@ -3,9 +3,9 @@
 // name once a block of 16 rows (from L2 where neighbours share them).
 //
 // A workgroup takes 16 rows, one of the adapters they name and up to 64 ranks;
-// its sixteen waves share K out in turns of 128 (64, 32 for more ranks), the next
-// turn's loads in flight, and add up through LDS: with few rows the time is a few
-// memory latencies.  Rows of other adapters are multiplied along and dropped.
+// its eight or sixteen waves share K out in turns of 128 or 64, the next turn's
+// loads in flight, and add up through LDS: with few rows the time is a few memory
+// latencies.  Rows of other adapters are multiplied along and dropped.
 // Only the GPU knows the ids, so a block of rows has places for adapters, up to
 // 16 while the launch is small: a workgroup takes its place's adapter and every
 // so many after it, and ends if there is none (256 blocks of 4096 rows with 16
@@ -19,13 +19,16 @@ namespace {
 
 using namespace fused::skinny;
 
-constexpr int kWaves = 16, kMaxSlots = 16, kWorkgroups = 512;
+constexpr int kMaxSlots = 16, kWorkgroups = 512;
+// (64 ranks' operands take the registers of two waves)
+constexpr int waves_of(int rb) { return rb == 4 ? 8 : 16; }
+constexpr int steps_of(int rb) { return rb == 1 ? 4 : 2; }
 
 // One adapter's ranks first .. of the 16 rows from m0 (`rows`: its own).
 template <int FMT, int RB>
 __device__ __forceinline__ void shrink_one(const ShrinkArgs& p, f4* lds, int a, uint32_t rows,
                                            int m0, int mr, int first, int lane, int wave) {
-  constexpr int kSteps = 4 / RB, kChunk = 32 * kSteps;
+  constexpr int kWaves = waves_of(RB), kSteps = steps_of(RB), kChunk = 32 * kSteps;
   const int r = lane & 15, quarter = lane >> 4;
   const half_t* x = p.X + (int64_t)mr * p.ldx + 8 * quarter;
   const half_t* w[RB];
@@ -108,7 +111,8 @@ __device__ __forceinline__ void shrink_one(const ShrinkArgs& p, f4* lds, int a, 
 }
 
 template <int FMT, int RB>
-__global__ __launch_bounds__(64 * kWaves) void shrink_kernel(ShrinkArgs p, int64_t base) {
+__global__ __launch_bounds__(64 * waves_of(RB)) void shrink_kernel(ShrinkArgs p, int64_t base) {
+  constexpr int kWaves = waves_of(RB);
   __shared__ f4 lds[(kWaves - 1) * RB * 64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -162,7 +166,7 @@ hipError_t launch_shrink(int fmt, const ShrinkArgs& p, hipStream_t stream) {
   a.slots = (int)std::max<int64_t>(
       1, std::min<int64_t>(std::min(kMaxSlots, p.M), kWorkgroups / std::max<int64_t>(1, wgs)));
   return launch_tiles(fmt == kFmtBF16 ? pick<kFmtBF16>(rb) : pick<kFmtF16>(rb), a, wgs * a.slots,
-                      64 * kWaves, 0, stream);
+                      64 * waves_of(rb), 0, stream);
 }
 
 }  // namespace tune
