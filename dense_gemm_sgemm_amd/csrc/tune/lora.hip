@@ -27,12 +27,25 @@ int check(int type, int M, int N, int K, int R, int S) {
                                                                               : GEMM_OK;
 }
 
-// Few rows, or too few tiles to fill the chip: the kernel that streams W once
-// for 64 rows (gemm_gated's rule, for half of the bytes).
+// Rows in blocks of 64 times columns: what the kernels for few rows (lora_rows.hip,
+// lora_dx.hip) take their time for; the tiles' is the same up to 256 of them.
+int64_t row_work(int M, int cols) { return ((int64_t)M + 63) / 64 * cols; }
+
+// Forward: the kernel for few rows streams W once for 64 of them.  bf16, K and N of
+// 4096, M = 128: 30 us against 45 of the tiles, 192: 43 against 44, 256: 56 against
+// 44; N 8192, K 2048, M = 96: 38 against 33.  Odd widths cost it more and the tiles
+// their copies: N 2305, K 769, M = 192: 18 against 24, 256: 29 against 24.
 bool by_rows(int M, int N, Mat x, Mat w) {
-  const int64_t work = ((int64_t)M + 63) / 64 * N;
   auto even = [](Mat m) { return m.ld % 2 == 0 && (reinterpret_cast<uintptr_t>(m.p) & 3) == 0; };
-  return M <= 64 || work <= (even(x) && even(w) ? 20000 : 8000);
+  return M <= 64 || row_work(M, N) <= (even(x) && even(w) ? 12288 : 8192);
+}
+// dX = dC W: its kernel for few rows cuts N, the sum's length, which the tiles walk
+// whole, but writes and reads its ranges' sums.  bf16, N 4096 and K 4096, M = 256: 40
+// us against 44, 320: 47 against 45; N 8192, K 2048, M = 640: 62 against 78; N 1024, K
+// 4096, M = 96: 20 against 18 (128: 23 against 18); N 2305, K 769, M = 448: 39 against
+// 41, 640: 42 against 40.
+bool dx_by_rows(int M, int N, int K) {
+  return M <= 64 || row_work(M, K) <= std::min<int64_t>(5 * (int64_t)N - 3000, 40000);
 }
 
 struct Plan {
@@ -84,7 +97,7 @@ BwdPlan plan_bwd(int M, int N, int K, int R, int S, Mat c, Mat w, bool dx, bool 
     p.t2 = round256((size_t)M * rank_ld2(R) * 2);
     p.factor = round256((size_t)M * rank_blocks(R) * sizeof(float));
     p.at = round256((size_t)S * K * 16 * rank_blocks(R) * 2);
-    p.few = by_rows(M, K, c, w);
+    p.few = dx_by_rows(M, N, K);
     if (p.few) {
       p.sums = plan_dx(M, N, K);
     } else {

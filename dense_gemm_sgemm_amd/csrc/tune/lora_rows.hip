@@ -134,7 +134,8 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
         a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(pending));
         const uint64_t own = __ballot(mine == a);
         pending &= ~own;
-        if (turn++ % args.waves == wave) rows[q] = own;
+        if (turn == wave) rows[q] = own;
+        turn = turn + 1 == args.waves ? 0 : turn + 1;
       }
       if (rows[q])
         bv[q] = load_ranks(y.B + a * y.stride_b + (int64_t)row * y.ldb,
