@@ -3,9 +3,13 @@
 // name once a block of 16 rows (from L2 where neighbours share them).
 //
 // A workgroup takes 16 rows, one of the adapters they name and up to 64 ranks;
-// its eight or sixteen waves share K out in turns of 128 or 64, the next turn's
+// its eight waves share K out in turns of 128 (64 for more ranks), the next turn's
 // loads in flight, and add up through LDS: with few rows the time is a few memory
-// latencies.  Rows of other adapters are multiplied along and dropped.
+// latencies.  Both operands go through a copy in LDS that is each wave's own, so that
+// a load covers whole lines: read straight into the fragments' layout, 16 rows x 64
+// bytes, the loads themselves were the time (bf16, K 4096, 16 ranks: 64 rows 12.8 ->
+// 8.6 us, 4096 rows 20 -> 9.6 us, 3.5 TB/s; 19 odd rows of 5669: 47 -> 18 us), and
+// sixteen waves with half of the registers spilled (9.6 -> 20 us).  Rows of other adapters are multiplied along and dropped.
 // Only the GPU knows the ids, so a block of rows has places for adapters, up to
 // 16 while the launch is small: a workgroup takes its place's adapter and every
 // so many after it, and ends if there is none (256 blocks of 4096 rows with 16
@@ -19,44 +23,60 @@ namespace {
 
 using namespace fused::skinny;
 
-constexpr int kMaxSlots = 16, kWorkgroups = 512;
-// (64 ranks' operands take the registers of two waves)
-constexpr int waves_of(int rb) { return rb == 4 ? 8 : 16; }
+constexpr int kWaves = 8, kMaxSlots = 16, kWorkgroups = 512;
 constexpr int steps_of(int rb) { return rb == 1 ? 4 : 2; }
 
 // One adapter's ranks first .. of the 16 rows from m0 (`rows`: its own).
 template <int FMT, int RB>
-__device__ __forceinline__ void shrink_one(const ShrinkArgs& p, f4* lds, int a, uint32_t rows,
-                                           int m0, int mr, int first, int lane, int wave) {
-  constexpr int kWaves = waves_of(RB), kSteps = steps_of(RB), kChunk = 32 * kSteps;
+__device__ __forceinline__ void shrink_one(const ShrinkArgs& p, unsigned char* lds, int a,
+                                           uint32_t rows, int m0, int first, int lane, int wave) {
+  constexpr int kSteps = steps_of(RB), kChunk = 32 * kSteps;
+  typedef XStage<1, kChunk> Stage;
   const int r = lane & 15, quarter = lane >> 4;
-  const half_t* x = p.X + (int64_t)mr * p.ldx + 8 * quarter;
-  const half_t* w[RB];
-#pragma unroll
-  for (int q = 0; q < RB; ++q) {
-    const int n = first + 16 * q + r;   // ranks past R repeat the last one and count as zeros
-    w[q] = p.A + a * p.stride_a + (int64_t)(n < p.R ? n : p.R - 1) * p.lda + 8 * quarter;
-  }
+  const half_t* w = p.A + a * p.stride_a;
   f4 acc[RB];
 #pragma unroll
   for (int q = 0; q < RB; ++q) acc[q] = f4{0.f, 0.f, 0.f, 0.f};
-  // (pointers and K both moved on by the lane's 8 quarter)
-  const int K = p.K - 8 * quarter, chunks = p.K / kChunk;
-  h8 xv[2][kSteps], wv[2][RB][kSteps];
-  auto load = [&](int set, int k, auto tail) __attribute__((always_inline)) {
-    constexpr bool kTail = decltype(tail)::value;
+  const int chunks = p.K / kChunk;
+  Stage stage[2][1 + RB];   // X, then the ranks
+  unsigned char* buf = lds + wave * (1 + RB) * Stage::kBytes;
+  // where the lane's pieces of a turn begin (rows past M and ranks past R repeat the
+  // last one and count as zeros)
+  constexpr int kLoads = Stage::kLoads;
+  const half_t* at[1 + RB][kLoads];
+  const int column = lane % Stage::kPieces * 8;
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      xv[set][s] = load_x<kTail>(x, k + 32 * s, K);
+  for (int e = 0; e < kLoads; ++e) {
+    const int i = e * Stage::kRows + lane / Stage::kPieces, m = m0 + i;
+    at[0][e] = p.X + (m < p.M ? m : p.M - 1) * p.ldx + column;
 #pragma unroll
-      for (int q = 0; q < RB; ++q) wv[set][q][s] = load_x<kTail>(w[q], k + 32 * s, K);
+    for (int q = 0; q < RB; ++q) {
+      const int n = first + 16 * q + i;
+      at[1 + q][e] = w + (n < p.R ? n : p.R - 1) * p.lda + column;
     }
+  }
+  auto load = [&](int set, int k, auto tail) __attribute__((always_inline)) {
+    // (k of unknown origin: one address kept a piece, not one a piece and set)
+    asm volatile("" : "+s"(k));
+#pragma unroll
+    for (int q = 0; q < 1 + RB; ++q)
+#pragma unroll
+      for (int e = 0; e < kLoads; ++e)
+        stage[set][q].v[e] = load_x<decltype(tail)::value>(at[q][e], k, p.K - column);
   };
   auto multiply = [&](int set) __attribute__((always_inline)) {
+    auto as_is = [](h8 v) { return v; };
 #pragma unroll
-    for (int s = 0; s < kSteps; ++s)
+    for (int q = 0; q < 1 + RB; ++q) stage[set][q].store(buf + q * Stage::kBytes, lane, as_is);
 #pragma unroll
-      for (int q = 0; q < RB; ++q) acc[q] = mfma16<FMT>(xv[set][s], wv[set][q][s], acc[q]);
+    for (int s = 0; s < kSteps; ++s) {
+      const h8 xv = Stage::read(buf, 0, r, 32 * s + 8 * quarter);
+#pragma unroll
+      for (int q = 0; q < RB; ++q)
+        acc[q] = mfma16<FMT>(
+            xv, Stage::read(buf + (1 + q) * Stage::kBytes, 0, r, 32 * s + 8 * quarter), acc[q]);
+    }
+    asm volatile("" ::: "memory");
   };
   // two turns at a time, so that the sets are named by constants
   int c = wave;
@@ -72,6 +92,7 @@ __device__ __forceinline__ void shrink_one(const ShrinkArgs& p, f4* lds, int a, 
     load(0, chunks * kChunk, std::true_type());
     multiply(0);
   }
+  __syncthreads();   // the sums take the place of the operands
   add_waves<RB>(acc, reinterpret_cast<float*>(lds), wave, lane, kWaves);
   if (wave > 0) return;
 
@@ -111,9 +132,10 @@ __device__ __forceinline__ void shrink_one(const ShrinkArgs& p, f4* lds, int a, 
 }
 
 template <int FMT, int RB>
-__global__ __launch_bounds__(64 * waves_of(RB)) void shrink_kernel(ShrinkArgs p, int64_t base) {
-  constexpr int kWaves = waves_of(RB);
-  __shared__ f4 lds[(kWaves - 1) * RB * 64];
+__global__ __launch_bounds__(64 * kWaves) void shrink_kernel(ShrinkArgs p, int64_t base) {
+  constexpr int kBytes = XStage<1, 32 * steps_of(RB)>::kBytes;
+  static_assert((1 + RB) * kBytes >= RB * 1024, "room for the sums");
+  __shared__ __attribute__((aligned(16))) unsigned char lds[kWaves * (1 + RB) * kBytes];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, quarter = lane >> 4;
@@ -125,7 +147,6 @@ __global__ __launch_bounds__(64 * waves_of(RB)) void shrink_kernel(ShrinkArgs p,
   const int slot = (int)(id / per);
   const int first = (int)(rest % groups) * 16 * RB;   // rank
   const int m0 = (int)(rest / groups) * 16;
-  const int mr = m0 + r < p.M ? m0 + r : p.M - 1;
   const int mine = m0 + r < p.M ? adapter_of(p.ids, m0 + r, p.S) : -1;
 
   if (slot == 0 && wave == 0 && p.t32) {
@@ -145,7 +166,7 @@ __global__ __launch_bounds__(64 * waves_of(RB)) void shrink_kernel(ShrinkArgs p,
     pending &= ~rows;
     if (d % p.slots == slot) {
       if (d >= p.slots) __syncthreads();   // the sums before have been read
-      shrink_one<FMT, RB>(p, lds, a, rows, m0, mr, first, lane, wave);
+      shrink_one<FMT, RB>(p, lds, a, rows, m0, first, lane, wave);
     }
   }
 }
@@ -166,7 +187,7 @@ hipError_t launch_shrink(int fmt, const ShrinkArgs& p, hipStream_t stream) {
   a.slots = (int)std::max<int64_t>(
       1, std::min<int64_t>(std::min(kMaxSlots, p.M), kWorkgroups / std::max<int64_t>(1, wgs)));
   return launch_tiles(fmt == kFmtBF16 ? pick<kFmtBF16>(rb) : pick<kFmtF16>(rb), a, wgs * a.slots,
-                      64 * waves_of(rb), 0, stream);
+                      64 * kWaves, 0, stream);
 }
 
 }  // namespace tune
