@@ -34,7 +34,7 @@ int64_t row_work(int M, int cols) { return ((int64_t)M + 63) / 64 * cols; }
 // Forward: the kernel for few rows streams W once for 64 of them.  bf16, K and N of
 // 4096, M = 128: 30 us against 45 of the tiles, 192: 43 against 44, 256: 56 against
 // 44; N 8192, K 2048, M = 96: 38 against 33.  Odd widths cost it more and the tiles
-// their copies: N 2305, K 769, M = 192: 18 against 24, 256: 29 against 24.
+// their copies: N 2305, K 769, M = 192: 20 against 24, 256: 29 against 24.
 bool by_rows(int M, int N, Mat x, Mat w) {
   auto even = [](Mat m) { return m.ld % 2 == 0 && (reinterpret_cast<uintptr_t>(m.p) & 3) == 0; };
   return M <= 64 || row_work(M, N) <= (even(x) && even(w) ? 12288 : 8192);

@@ -1,5 +1,9 @@
 // A product with adapters for few rows of X (decode steps): W streamed from HBM
-// once for 64 rows, bound by that (skinny.hpp has the layout).  The adapters'
+// once for 64 rows, bound by that (skinny.hpp has the layout; here W goes through a
+// wave's own copy in LDS too, so that its loads cover whole lines: fp16, N and K of
+// 4096, 1 row 8.8 -> 7.2 us, 4.7 TB/s; 32 rows 11.5 -> 10.5; 64 x 8192 x 8192 47 ->
+// 42; 19 odd rows of 5669, N 2545: 29 -> 19).  64 values of K a turn for more than 16
+// rows, so that LDS holds two workgroups (N 14336, 32 rows: 36 -> 29 us).  The adapters'
 // second product comes before the waves' sums are added: each wave takes every
 // so many of the adapters that the rows name, multiplies t (tune.hpp) with 16 of
 // the adapter's rows of B and keeps the sums of the rows that are its own, apart
@@ -48,10 +52,12 @@ __device__ __forceinline__ h8 load_ranks(const half_t* row, int at, int R, int64
 
 template <int FMT, int MT>
 __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args, int64_t base) {
-  constexpr int kS = MT == 4 ? 2 : kSteps, kC = 32 * kS;
+  constexpr int kS = MT == 1 ? kSteps : 2, kC = 32 * kS;
   typedef XStage<MT, kC> Stage;
+  typedef XStage<1, kC> WStage;
+  constexpr int kBytes = Stage::kBytes + WStage::kBytes;
   __shared__ __attribute__((aligned(16))) unsigned char
-      lds[kMaxWaves * (Stage::kBytes > 2 * MT * 1024 ? Stage::kBytes : 2 * MT * 1024)];
+      lds[kMaxWaves * (kBytes > 2 * MT * 1024 ? kBytes : 2 * MT * 1024)];
   const Args16& p = args.p;
   const LoraExtra& y = args.x;
   const int lane = threadIdx.x & 63;
@@ -61,32 +67,34 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
   const int m0 = (int)(id / groups_n) * 64;
   const int n = (int)(id % groups_n) * 16 + r;
   const int row = n < p.N ? n : p.N - 1;   // rows past N repeat the last one, unstored
-  const half_t* w = p.B + row * p.ldb + 8 * quarter;
   f4 acc[2 * MT];   // the projection's, then the adapters'
 #pragma unroll
   for (int t = 0; t < 2 * MT; ++t) acc[t] = f4{0.f, 0.f, 0.f, 0.f};
 
-  // (the pointer and K both moved on by the lane's 8 quarter)
-  const int K = p.K - 8 * quarter, chunks = p.K / kC;
-  h8 cur[kS], nxt[kS], xf[MT][kS];
+  const int chunks = p.K / kC;
   Stage stage;
-  unsigned char* buf = lds + wave * Stage::kBytes;
-  auto load_w = [&](int k, auto tail, h8 (&v)[kS]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int s = 0; s < kS; ++s) v[s] = load_x<decltype(tail)::value>(w, k + 32 * s, K);
+  WStage wstage;
+  unsigned char* buf = lds + wave * kBytes;
+  const int n0 = (int)(id % groups_n) * 16;
+  auto load = [&](int k, auto tail) __attribute__((always_inline)) {
+    constexpr bool kTail = decltype(tail)::value;
+    wstage.template load<kTail>(p.B, p.ldb, n0, p.N, k, p.K, lane);
+    stage.template load<kTail>(p.A, p.lda, m0, p.M, k, p.K, lane);
   };
-  auto read_x = [&]() __attribute__((always_inline)) {
-    stage.store(buf, lane, [](h8 v) { return v; });
-#pragma unroll
-    for (int t = 0; t < MT; ++t)
-#pragma unroll
-      for (int s = 0; s < kS; ++s) xf[t][s] = Stage::read(buf, t, r, 32 * s + 8 * quarter);
+  auto store = [&]() __attribute__((always_inline)) {
+    auto as_is = [](h8 v) { return v; };
+    stage.store(buf, lane, as_is);
+    wstage.store(buf + Stage::kBytes, lane, as_is);
   };
   auto multiply = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int s = 0; s < kS; ++s)
+    for (int s = 0; s < kS; ++s) {
+      const h8 wv = WStage::read(buf + Stage::kBytes, 0, r, 32 * s + 8 * quarter);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) acc[t] = mfma16<FMT>(xf[t][s], cur[s], acc[t]);
+      for (int t = 0; t < MT; ++t)
+        acc[t] = mfma16<FMT>(Stage::read(buf, t, r, 32 * s + 8 * quarter), wv, acc[t]);
+    }
+    asm volatile("" ::: "memory");
   };
   if (args.sums.sum) {
     // (the waves share the ranges; rows past M repeat the last one, unstored)
@@ -148,24 +156,15 @@ __global__ __launch_bounds__(64 * kMaxWaves) void lora_rows_kernel(RowsArgs args
     load_b();
   }
   int c = wave;
-  if (c < chunks) {
-    stage.template load<false>(p.A, p.lda, m0, p.M, c * kC, p.K, lane);
-    load_w(c * kC, std::false_type(), cur);
-  }
+  if (c < chunks) load(c * kC, std::false_type());
   for (; c < chunks; c += args.waves) {
-    read_x();
-    if (c + args.waves < chunks) {
-      stage.template load<false>(p.A, p.lda, m0, p.M, (c + args.waves) * kC, p.K, lane);
-      load_w((c + args.waves) * kC, std::false_type(), nxt);
-    }
+    store();
+    if (c + args.waves < chunks) load((c + args.waves) * kC, std::false_type());
     multiply();
-#pragma unroll
-    for (int s = 0; s < kS; ++s) cur[s] = nxt[s];
   }
   if (chunks * kC < p.K && wave == chunks % args.waves) {
-    stage.template load<true>(p.A, p.lda, m0, p.M, chunks * kC, p.K, lane);
-    load_w(chunks * kC, std::true_type(), cur);
-    read_x();
+    load(chunks * kC, std::true_type());
+    store();
     multiply();
   }
 
@@ -224,7 +223,7 @@ hipError_t launch_lora_rows(const Args16& a, const LoraExtra& x, const RowSums& 
   RowsArgs p{a, x, sums, 1};
   if (sums.sum) p.p.K = 0;
   const int64_t wgs = ((int64_t)a.N + 15) / 16 * (((int64_t)a.M + 63) / 64);
-  const int chunk = a.M <= 32 ? kChunk : kChunk / 2;
+  const int chunk = a.M <= 16 ? kChunk : kChunk / 2;
   const int chunks = std::max(1, (int)(((int64_t)a.K + chunk - 1) / chunk));
   p.waves = sums.sum ? std::max(1, std::min(kMaxWaves, sums.ranges)) : waves_for(wgs, chunks, kMaxWaves, cus);
   return launch_tiles(a.fmt == kFmtBF16 ? pick<kFmtBF16>(a.M) : pick<kFmtF16>(a.M), p, wgs,
