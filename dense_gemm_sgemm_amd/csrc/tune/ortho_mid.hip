@@ -29,7 +29,7 @@ struct Two {
 struct MidArgs {
   Two a, b;                    // rows of the product's two sides
   int64_t lda, ldb, stride_a, stride_b;
-  int slabs, rows, cols;       // of 64 each: K, and the tiles of a matrix
+  int slabs, cols;             // of 64 each: K, and the tiles across a matrix
   int sym, tiles;              // sym: tiles on and below the diagonal
   int splits, per;             // ranges of K (1: none)
   float* sum;                  // [matrix][range][tile][64][64]
@@ -287,7 +287,6 @@ hipError_t launch_mid(const StartArgs& st, const MidPlan& p, int steps, const fl
   const int rows = p.sp / BT, cols = p.tp / BT, half = rows * (rows + 1) / 2;
   const int64_t stride_x = (int64_t)p.sp * p.tp, stride_a = (int64_t)p.sp * p.sp;
   MidArgs m{};
-  m.rows = rows;
   m.cols = cols;
   m.tiles = rows * cols;
   m.splits = 1;
@@ -326,7 +325,7 @@ hipError_t launch_mid(const StartArgs& st, const MidPlan& p, int steps, const fl
     m.lda = m.ldb = p.tp;
     m.stride_a = m.stride_b = stride_x;
     m.slabs = cols;
-    m.rows = m.cols = rows;
+    m.cols = rows;
     m.sym = 1;
     m.tiles = half;
     m.splits = p.splits;
@@ -357,8 +356,7 @@ hipError_t launch_mid(const StartArgs& st, const MidPlan& p, int steps, const fl
     m.stride_a = stride_a;
     m.stride_b = stride_x;
     m.slabs = m.per = rows;
-    m.rows = rows;
-    m.cols = cols;
+      m.cols = cols;
     m.tiles = rows * cols;
     m.splits = 1;
     m.to = x[1 - i];

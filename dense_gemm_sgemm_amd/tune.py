@@ -217,13 +217,15 @@ _coeff_cache: dict = {}
 
 def _coeffs(coeffs, steps):
     """The C array of ``coeffs``: one triple for all steps, or one for each."""
-    key = (coeffs if isinstance(coeffs, tuple) else tuple(map(tuple, coeffs)), steps)
+    if coeffs is not MUON:
+        coeffs = tuple(tuple(v) if isinstance(v, (tuple, list)) else v for v in coeffs)
+    key = (coeffs, steps)
     array = _coeff_cache.get(key)
     if array is None:
         flat = key[0]
-        if len(flat) == 3 and not any(isinstance(v, (tuple, list)) for v in flat):
+        if len(flat) == 3 and not any(isinstance(v, tuple) for v in flat):
             flat = (flat,) * steps
-        if len(flat) != steps or any(len(v) != 3 for v in flat):
+        if len(flat) != steps or any(not isinstance(v, tuple) or len(v) != 3 for v in flat):
             raise ValueError("coeffs must be three numbers, or three for each of the steps")
         array = (ctypes.c_float * (3 * steps))(*[float(v) for t in flat for v in t])
         if len(_coeff_cache) > 64:

@@ -56,11 +56,12 @@ extern "C" {
  *   bias, act, residual, ldr, C, ldc : as for gemm_ex (residual may be C; ReLU
  *             of NaN is NaN)
  *   T       : float [M][ldt], ldt >= R, or NULL: t, as gemm_lora_bwd takes it;
- *             0 for rows without an adapter                         (written)
+ *             0 for rows without an adapter, NaN for unknown ones   (written)
  *
  * t is an operand of the second product in two 16-bit values of the type (16
- * bits in bf16, 22 in fp16, of the largest of 16 ranks), so C is rounded once.  An adapter of fewer ranks than R has zeros in the others.  What one
- * row's adapter holds, infinities and NaN too, reaches no other row.
+ * bits in bf16, 22 in fp16, of the largest of 16 ranks), so C is rounded once.
+ * An adapter of fewer ranks than R has zeros in the others.  What one row's
+ * adapter holds, infinities and NaN too, reaches no other row.
  *
  * Rows whose neighbours have the same adapter share its reads; in any other
  * order each block of 16 rows reads every adapter that it names.

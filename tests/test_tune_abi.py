@@ -247,3 +247,15 @@ def test_binding_checks(lib):
         with pytest.raises(ValueError):
             dg.gemm_ortho(g, g.clone(), **kw)
             pytest.fail(str(kw))
+
+
+def test_coefficients_in_any_sequence():
+    from dense_gemm_sgemm_amd import tune
+    one = [3.0, -4.0, 2.0]
+    for coeffs in (tuple(one), one):
+        assert list(tune._coeffs(coeffs, 2)) == one * 2
+    for coeffs in ((one, one), [one, one], [tuple(one), one], (tuple(one), tuple(one))):
+        assert list(tune._coeffs(coeffs, 2)) == one * 2
+    for coeffs in ((one, 1.0), [one], (1.0, 2.0), [one, one, one]):
+        with pytest.raises(ValueError):
+            tune._coeffs(coeffs, 2)

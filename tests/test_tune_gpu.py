@@ -710,3 +710,52 @@ def test_stacks_past_two_gibi_elements():
         dg.gemm_ortho(far_g, far_o)
         assert torch.equal(O, far_o)
     del buf
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("M,N,K,R,S", [(300, 64, 72, 4, 2500), (20, 136, 200, 16, 2049),
+                                       (900, 2600, 64, 4, 2300)])
+def test_lora_thousands_of_adapters(M, N, K, R, S, typ):
+    """More adapters than one workgroup counts, and ids past 32 bits."""
+    dt = DT[typ]
+    X, W, A, B, ids, scales = lora_inputs(M, N, K, R, S, dt, M + S)
+    ids[0], ids[M // 2], ids[M - 1] = (1 << 32) + 1, -(1 << 40), S - 1
+    C, T = Out(M, N, dt), Out(M, R, torch.float32)
+    show("lora", M, N, K, R, S, typ)
+    dg.gemm_lora(X, W, A, B, ids, C.t, scales=scales, T=T.t)
+    y, t, off, dt_sum = lora_ref(X, W, A, B, ids, scales)
+    assert bool(C.t[0].isnan().all()) and bool(T.t[0].isnan().all())
+    close(T.t[1:], t[1:], dt_sum[1:], "T")
+    ref, tol = lora_result(y, off, dt)
+    close(C.t[1:], ref[1:], tol[1:], "C")
+    dC = randn((M, N), 0.1, dt, gen(M)).to(DEV)
+    T = t.float()
+    T[0] = 0
+    dX, dA, dB = Out(M, K, dt), Out3(S, R, K, dt), Out3(S, N, R, dt)
+    dg.gemm_lora_bwd(X, W, A, B, ids, T, dC, dX.t, dA.t, dB.t, scales=scales)
+    (rx, tx), (ra, ta), (rb, tb) = lora_bwd_ref(X, W, A, B, ids, T, dC, scales)
+    assert bool(dX.t[0].isnan().all())
+    close(dX.t[1:], rx[1:], tx[1:], "dX")
+    close(dA.t, ra, ta, "dA")
+    close(dB.t, rb, tb, "dB")
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("M,N,K", [(192, 4096, 264), (193, 4096, 264), (640, 264, 1024),
+                                   (200, 2000, 7000), (641, 1000, 200), (65, 600, 64)])
+def test_lora_at_the_rules(M, N, K, typ):
+    """Sizes on both sides of what chooses the kernels for few rows."""
+    dt = DT[typ]
+    X, W, A, B, ids, scales = lora_inputs(M, N, K, 16, 6, dt, M + K)
+    C, T = Out(M, N, dt), Out(M, 16, torch.float32)
+    show("lora", M, N, K, typ)
+    dg.gemm_lora(X, W, A, B, ids, C.t, scales=scales, T=T.t)
+    y, t, off, dt_sum = lora_ref(X, W, A, B, ids, scales)
+    close(C.t, *lora_result(y, off, dt), "C")
+    close(T.t, t, dt_sum, "T")
+    dC = randn((M, N), 0.1, dt, gen(M)).to(DEV)
+    dX = Out(M, K, dt)
+    dg.gemm_lora_bwd(X, W, A, B, ids, T.t, dC, dX.t, scales=scales)
+    grads_check(X, W, A, B, ids, T.t, dC, scales, dX.t)
+    C.check_frame("C")
+    dX.check_frame("dX")
