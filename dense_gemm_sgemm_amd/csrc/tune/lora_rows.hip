@@ -225,7 +225,8 @@ hipError_t launch_lora_rows(const Args16& a, const LoraExtra& x, const RowSums& 
   const int64_t wgs = ((int64_t)a.N + 15) / 16 * (((int64_t)a.M + 63) / 64);
   const int chunk = a.M <= 16 ? kChunk : kChunk / 2;
   const int chunks = std::max(1, (int)(((int64_t)a.K + chunk - 1) / chunk));
-  p.waves = sums.sum ? std::max(1, std::min(kMaxWaves, sums.ranges)) : waves_for(wgs, chunks, kMaxWaves, cus);
+  p.waves = sums.sum ? std::max(1, std::min(kMaxWaves, sums.ranges))
+                     : waves_for(wgs, chunks, kMaxWaves, cus);
   return launch_tiles(a.fmt == kFmtBF16 ? pick<kFmtBF16>(a.M) : pick<kFmtF16>(a.M), p, wgs,
                       64 * p.waves, 0, stream);
 }

@@ -9,7 +9,8 @@
 // a load covers whole lines: read straight into the fragments' layout, 16 rows x 64
 // bytes, the loads themselves were the time (bf16, K 4096, 16 ranks: 64 rows 12.8 ->
 // 8.6 us, 4096 rows 20 -> 9.6 us, 3.5 TB/s; 19 odd rows of 5669: 47 -> 18 us), and
-// sixteen waves with half of the registers spilled (9.6 -> 20 us).  Rows of other adapters are multiplied along and dropped.
+// sixteen waves with half of the registers spilled (9.6 -> 20 us).  Rows of other
+// adapters are multiplied along and dropped.
 // Only the GPU knows the ids, so a block of rows has places for adapters, up to
 // 16 while the launch is small: a workgroup takes its place's adapter and every
 // so many after it, and ends if there is none (256 blocks of 4096 rows with 16

