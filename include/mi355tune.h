@@ -122,8 +122,9 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S,
                                 void* stream);
 
 /* Workspace bytes of gemm_lora_bwd: B and A with rows and columns exchanged, dt,
- * the rows listed by adapter, fp32 sums of adapters' parts, and padded copies
- * of dC and W.  want_*: the gradient is asked for. */
+ * the rows listed by adapter, dt and T in their order, fp32 sums of adapters'
+ * parts and (few rows) of dX over ranges of N, and padded copies of dC and W.
+ * want_*: the gradient is asked for. */
 MI355TUNE_API unsigned long long gemm_lora_bwd_workspace(int type, int M, int N, int K, int R,
                                                          int S, const void* dC, int lddc,
                                                          const void* W, int ldw, int want_dx,
