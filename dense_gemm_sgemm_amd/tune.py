@@ -119,7 +119,9 @@ def _adapters(t, name, dtype, index, rows, cols, count=None):
                 "ranks" if cols is None else cols], tuple(t.shape)))
     if t.get_device() != index:
         raise ValueError("all tensors of a call must live on one GPU")
-    return S, r, ptr, max(ld, c), stride
+    if ld < c and ptr is not None:
+        raise ValueError("%s: the rows of an adapter must not overlap" % name)
+    return S, r, ptr, max(ld, c), stride   # (no element: any distance)
 
 
 def _scales(scales, index, S):

@@ -1,0 +1,54 @@
+"""Calls of the operators of fine tuning that the binding or the plans have to
+answer rightly, without a GPU: none of them reaches a kernel."""
+from __future__ import annotations
+
+import os
+
+import pytest
+
+import dense_gemm_sgemm_amd as dg
+from dense_gemm_sgemm_amd import tune
+from test_fused_abi import fake_gpu
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if not os.path.exists(tune.LIB_PATH):
+        from dense_gemm_sgemm_amd import build
+        build.build()
+    return tune.load_library()
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+@pytest.mark.parametrize("S", [1, 5])
+def test_stacks_whose_rows_overlap(lib, S):
+    """Rows closer than their length (one row expanded to all, a sliding window)
+    are no matrix that the kernels can read, and none that they may write."""
+    x, w, out = fake_gpu((2, 64), (64, 1)), fake_gpu((3, 64), (64, 1)), fake_gpu((2, 3), (3, 1))
+    a, b = fake_gpu((S, 4, 64), (256, 64, 1)), fake_gpu((S, 3, 4), (12, 4, 1))
+    ids = fake_gpu((2,), (1,), dtype="int64")
+    t = fake_gpu((2, 4), (4, 1), dtype="float32")
+    for row in (0, 1, 63):
+        A, B = fake_gpu((S, 4, 64), (1 << 20, row, 1)), fake_gpu((S, 3, 4), (1 << 20, row % 4, 1))
+        for call in (lambda: dg.gemm_lora(x, w, A, b, ids, out),
+                     lambda: dg.gemm_lora(x, w, a, B, ids, out),
+                     lambda: dg.lora_workspace_bytes(x, w, A, b),
+                     lambda: dg.lora_workspace_bytes(x, w, a, B),
+                     lambda: dg.lora_bwd_workspace_bytes(x, w, A, out),
+                     lambda: dg.gemm_lora_bwd(x, w, A, b, ids, t, out, dX=x),
+                     lambda: dg.gemm_lora_bwd(x, w, a, B, ids, t, out, dX=x),
+                     lambda: dg.gemm_lora_bwd(x, w, a, b, ids, t, out, dA=A),
+                     lambda: dg.gemm_lora_bwd(x, w, a, b, ids, t, out, dB=B)):
+            with pytest.raises(ValueError, match="overlap"):
+                call()
+                pytest.fail("rows %d elements apart" % row)
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_stacks_with_one_row_or_no_element():
+    """Where no row has another behind it, the distance between rows says nothing."""
+    half, at = fake_gpu((1, 1), (1, 1)).dtype, 0
+    assert tune._adapters(fake_gpu((3, 1, 64), (64, 0, 1)), "A", half, at, 1, 64)[3] == 64
+    assert tune._adapters(fake_gpu((3, 4, 1), (4, 1, 1)), "B", half, at, 4, 1)[3] == 1
+    assert tune._adapters(fake_gpu((0, 4, 64), (0, 0, 1)), "A", half, at, 4, 64)[:2] == (0, 4)
+    assert tune._adapters(fake_gpu((2, 4, 0), (0, 0, 1)), "A", half, at, 4, 0)[:2] == (2, 4)
