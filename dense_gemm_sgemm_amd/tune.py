@@ -217,10 +217,20 @@ MUON = (3.4445, -4.7750, 2.0315)
 _coeff_cache: dict = {}
 
 
+def _numbers(v):
+    """A number as a float, a sequence of them as a tuple of floats."""
+    if isinstance(v, (tuple, list)) or getattr(v, "ndim", 0) == 1:
+        return tuple(float(x) for x in v)
+    if getattr(v, "ndim", 0) > 1:
+        raise ValueError("coeffs must be three numbers, or three for each of the steps")
+    return float(v)
+
+
 def _coeffs(coeffs, steps):
-    """The C array of ``coeffs``: one triple for all steps, or one for each."""
+    """The C array of ``coeffs``: one triple for all steps, or one for each.  Arrays
+    are kept by the values alone: what holds them may change from call to call."""
     if coeffs is not MUON:
-        coeffs = tuple(tuple(v) if isinstance(v, (tuple, list)) else v for v in coeffs)
+        coeffs = tuple(_numbers(v) for v in coeffs)
     key = (coeffs, steps)
     array = _coeff_cache.get(key)
     if array is None:
@@ -229,7 +239,7 @@ def _coeffs(coeffs, steps):
             flat = (flat,) * steps
         if len(flat) != steps or any(not isinstance(v, tuple) or len(v) != 3 for v in flat):
             raise ValueError("coeffs must be three numbers, or three for each of the steps")
-        array = (ctypes.c_float * (3 * steps))(*[float(v) for t in flat for v in t])
+        array = (ctypes.c_float * (3 * steps))(*[v for t in flat for v in t])
         if len(_coeff_cache) > 64:
             _coeff_cache.clear()
         _coeff_cache[key] = array

@@ -52,3 +52,41 @@ def test_stacks_with_one_row_or_no_element():
     assert tune._adapters(fake_gpu((3, 4, 1), (4, 1, 1)), "B", half, at, 4, 1)[3] == 1
     assert tune._adapters(fake_gpu((0, 4, 64), (0, 0, 1)), "A", half, at, 4, 64)[:2] == (0, 4)
     assert tune._adapters(fake_gpu((2, 4, 0), (0, 0, 1)), "A", half, at, 4, 0)[:2] == (2, 4)
+
+
+def test_coefficients_by_their_values():
+    """Numbers held in tensors count as they are at the call, not as they were at an
+    earlier one; a whole matrix of them, and numpy's, are taken too."""
+    torch = pytest.importorskip("torch")
+    np = pytest.importorskip("numpy")
+    own = [torch.tensor(v) for v in (3.0, -4.0, 2.0)]
+    assert list(tune._coeffs(own, 2)) == [3.0, -4.0, 2.0] * 2
+    own[0].fill_(9.0)
+    assert list(tune._coeffs(own, 2)) == [9.0, -4.0, 2.0] * 2
+    own[1] -= 1.0
+    assert list(tune._coeffs([own, own], 2)) == [9.0, -5.0, 2.0] * 2
+    own[2].fill_(0.5)
+    assert list(tune._coeffs([tuple(own), own], 2)) == [9.0, -5.0, 0.5] * 2
+    rows = torch.tensor([[1.0, 2.0, 3.0], [4.0, 5.0, 6.0]])
+    for held in (rows, rows.numpy(), list(rows), tuple(rows.numpy())):
+        assert list(tune._coeffs(held, 2)) == [1.0, 2.0, 3.0, 4.0, 5.0, 6.0]
+    rows[1, 2] = 7.0
+    assert list(tune._coeffs(rows, 2)) == [1.0, 2.0, 3.0, 4.0, 5.0, 7.0]
+    assert list(tune._coeffs(np.array([1.0, 2.0, 3.0]), 2)) == [1.0, 2.0, 3.0] * 2
+    assert list(tune._coeffs(tune.MUON, 1)) == list(tune._coeffs(tuple(tune.MUON), 1))
+    for wrong in (rows.T, torch.ones(2, 3, 1), torch.ones(2), torch.ones(4, 3)):
+        with pytest.raises((ValueError, TypeError)):
+            tune._coeffs(wrong, 2)
+            pytest.fail(str(wrong))
+
+
+def test_coefficients_do_not_hold_the_callers_objects():
+    torch = pytest.importorskip("torch")
+    import gc
+    import weakref
+    t = torch.tensor(2.0)
+    alive = weakref.ref(t)
+    tune._coeffs((t, 0.5, 0.25), 3)
+    del t
+    gc.collect()
+    assert alive() is None
