@@ -1518,7 +1518,10 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   // slab; they are found from the origins only where a run of slabs that lie
   // behind each other begins (an item, a part of K, a last slab that reaches
   // past K).  That is a third of the loop's scalar work, all of it in the copying
-  // waves, which the others wait for.
+  // waves, which the others wait for.  A run begins when the slab before it has been
+  // copied, with the origins of the current item and of two more: the slab three on
+  // from an item's last one must lie in them, so two items behind each other have
+  // three slabs at least (the launchers see to that).
   const char *run_a = nullptr, *run_b = nullptr;
   int run_left = 0;         // slabs left of the run, the next one among them
   bool run_tail = false;
@@ -1830,6 +1833,10 @@ hipError_t launch_ortho(const Args16& a, const OrthoExtra& x, int batch, int slo
   if (items >= (int64_t(1) << 31) || each >= (int64_t(1) << 24) ||
       (MODE == kSym && x.whole + (int64_t)x.rest != each * batch))
     return hipErrorInvalidValue;
+  // (at least two slabs an item, see the copies' runs in the kernel)
+  const int64_t slabs = (int64_t)x.parts * ((a.K + BK - 1) / BK);
+  if (slabs < 2 || (MODE == kSym && x.rest && slabs - (int64_t)(x.splits - 1) * x.per < 2))
+    return hipErrorInvalidValue;
   const int64_t grid = items < slots ? items : slots;
   OrthoTileArgs ta{a, items, x};
   ta.x.tiles_each = (uint32_t)each;
@@ -1845,7 +1852,8 @@ hipError_t launch_lora(const Args16& a, const LoraExtra& x, int slots, hipStream
   typedef Config<BM, BN, BK, WAVES_M, WAVES_N, COPY_SEL> C;
   static_assert(C::WM <= 64, "a lane for each of a wave's rows");
   const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
-  if (tiles >= (int64_t(1) << 31)) return hipErrorInvalidValue;   // xcd_order32
+  // (xcd_order32; two slabs a tile, see the copies' runs in the kernel)
+  if (tiles >= (int64_t(1) << 31) || a.K <= BK) return hipErrorInvalidValue;
   LoraTileArgs ta{a, tiles, x};
   void* args[] = {&ta};
   return hipLaunchKernel((const void*)hgemm_nt_kernel<BM, BN, BK, WAVES_M, WAVES_N, GM, COPY_SEL,

@@ -146,11 +146,14 @@ bool held(const Plan& p, int i, int steps) {
   // (an iterate that only the last step reads needs no second value)
   return p.fine ? i > 0 || p.x0_lo : i + 1 < steps && i < kSplitSteps && (i > 0 || p.x0_lo);
 }
-// X X^T and A^2 of a step.
+// X X^T and A^2 of a step, planned for kPlanCus CUs: the workspace is sized before
+// a device is asked.
 SymPlan plan_gram(const Plan& p, int L, bool lo) {
-  return plan_sym(p.sp, (p.fine && lo ? 3 : 1) * (p.tp / 64), L);
+  return plan_sym(p.sp, (p.fine && lo ? 3 : 1) * (p.tp / 64), L, fused::kPlanCus);
 }
-SymPlan plan_square(const Plan& p, int L) { return plan_sym(p.sp, (p.fine ? 3 : 1) * (p.sp / 64), L); }
+SymPlan plan_square(const Plan& p, int L) {
+  return plan_sym(p.sp, (p.fine ? 3 : 1) * (p.sp / 64), L, fused::kPlanCus);
+}
 
 // The short tiles of ortho_mid.hip, where the tile kernel's launches would be
 // mostly their beginning and end; they do three products for one throughout, so

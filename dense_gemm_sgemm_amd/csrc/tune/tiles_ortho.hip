@@ -33,65 +33,11 @@ int choose(const Shape* s, int n, int M, int N, int batch, int cus, F each) {
   return best;
 }
 
-// kSym's: the time of a slab and of a tile's end in microseconds, from launches of
-// each shape.
-struct SymShape {
-  int bm, per_cu;
-  double slab, alone, end;   // alone: tiles do not outnumber the CUs
-};
-constexpr SymShape kSymShapes[] = {
-    {256, 1, 1.5, 1.5, 10.},
-    {128, 2, 0.92, 0.6, 4.},
-    {192, 1, 1.0, 1.0, 6.},
-};
 constexpr Shape kMulShapes[] = {
     {256, 256, 1, 256 * 256, 256 * 256},
     {128, 128, 2, 2 * 128 * 128 * 6 / 5, 128 * 128 * 8 / 5},
     {192, 256, 1, 192 * 256 * 11 / 10, 192 * 256 * 11 / 10},
 };
-
-}  // namespace
-
-SymPlan plan_sym(int M, int slabs, int batch) {
-  SymPlan best;
-  double best_cost = 0;
-  auto consider = [&](int i, int64_t tiles, int64_t whole, int splits) {
-    const SymShape& s = kSymShapes[i];
-    const int64_t slots = (int64_t)s.per_cu * fused::kPlanCus, rest = tiles - whole;
-    const int per = (slabs + splits - 1) / splits;
-    splits = (slabs + per - 1) / per;
-    if (rest * splits >= (int64_t(1) << 31)) return;
-    double cost = 0;
-    if (whole)
-      cost += (double)((whole + slots - 1) / slots) *
-              (slabs * (whole <= fused::kPlanCus ? s.alone : s.slab) + s.end);
-    if (rest) {
-      const int64_t items = rest * splits;
-      cost += (double)((items + slots - 1) / slots) *
-                  (per * (items <= fused::kPlanCus ? s.alone : s.slab) + 3.) +
-              (double)items * s.bm * s.bm * 8 * 2.5e-7 + 6.;
-    }
-    if (best.shape < 0 || cost < best_cost) {
-      best = SymPlan{i, s.bm, (uint32_t)whole, (uint32_t)rest, splits, per};
-      best_cost = cost;
-    }
-  };
-  for (int i = 0; i < 3; ++i) {
-    const SymShape& s = kSymShapes[i];
-    if (M < s.bm) continue;
-    const int64_t t = (M + s.bm - 1) / s.bm, tiles = t * (t + 1) / 2 * batch;
-    const int64_t slots = (int64_t)s.per_cu * fused::kPlanCus, whole = tiles / slots * slots;
-    consider(i, tiles, tiles, 1);
-    if (whole == tiles) continue;
-    for (int splits = 2; splits <= 64 && 2 * splits <= slabs; ++splits) {
-      consider(i, tiles, whole, splits);
-      if ((tiles - whole) * splits >= 2 * slots) break;
-    }
-  }
-  return best;
-}
-
-namespace {
 
 typedef float f4 __attribute__((ext_vector_type(4)));
 typedef _Float16 h4 __attribute__((ext_vector_type(4)));

@@ -3,6 +3,7 @@
 
 #include "fused/fused.hpp"
 #include "mi355tune.h"
+#include "sym_plan.hpp"
 
 namespace mi355gemm {
 namespace tune {
@@ -13,15 +14,6 @@ using hgemm::OrthoExtra;
 
 // Products of an orthogonalised update over `batch` matrices (tiles_ortho.hip):
 // kSym, and kMul with the second operand K-major or (a_kmajor) the first one.
-// kSym's tile shape, and what is cut into ranges of K (made for kPlanCus CUs,
-// since the workspace is sized before a device is asked).
-struct SymPlan {
-  int shape = -1, bm = 0;
-  uint32_t whole = 0, rest = 0;
-  int splits = 1, per = 0;
-  size_t sum_bytes() const { return (size_t)rest * splits * bm * bm * sizeof(float); }
-};
-SymPlan plan_sym(int M, int slabs, int batch);
 // x.sum: room for the plan's sums, which are joined and stored here too.
 hipError_t launch_sym_tiles(const Args16& a, const OrthoExtra& x, const SymPlan& plan, int batch,
                             int cus, hipStream_t stream);
