@@ -302,7 +302,7 @@ struct LoraExtra {
   int R = 0, S = 0, blocks = 0;
   int m_end = 0, n_end = 0;
   // LAY 1 with p.K % 64 != 0: A's columns p.K - 64 .. p.K - 1, [p.M][64], zeros
-  // for those of a slab before the last
+  // for those of a slab before the last (B's rows there are zeroed in LDS)
   const half_t* tail = nullptr;
 };
 struct LoraTileArgs {
@@ -1620,13 +1620,39 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
 #pragma unroll
     for (int c = 0; c < kCopies; ++c) copy_one(cb, c);
   };
+  // kTailA: A's side of the last slab has zeros in memory where B's rows repeat the
+  // slab before, and the copying waves zero those rows here, since an infinity in
+  // them times zero would be NaN.  In the last slab but one, which has code of its own
+  // for it: a branch for it in the slab loop costs spills there (4096^3, whether or not
+  // there is such a slab: 122 -> 154 us).
+  auto wait_tail_b_sync = [&](int stage) __attribute__((always_inline)) {
+    __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);
+    const int ks = (BK - fresh_args()->p.K % BK) % BK;   // 8 .. 56, or 0: whole slabs
+    int l;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+    volatile uint32_t* at = (volatile uint32_t*)(lds + stage * kStage + kAreaA + cw * 1024) + l;
+    // copy i of this wave: rows R (4 i + cw) .. + R - 1, all of them below ks or none
+    constexpr int R = 1024 / kTPB;
+    static_assert(8 % R == 0, "ks is a multiple of 8");
+#pragma unroll
+    for (int i = 0; i < kPerWaveB; ++i)
+      if (R * (i * C::kCopyWaves + cw) < ks) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) at[i * C::kCopyWaves * 256 + 64 * q] = 0;
+      }
+    __builtin_amdgcn_s_waitcnt(kWaitLgkm0);
+    asm volatile("s_barrier" ::: "memory");
+  };
   // zero_next (RAG): the next slab is the last of its tile and reaches past K.
-  auto slab = [&](int gs, auto next, auto is_copier, bool zero_next) __attribute__((always_inline)) {
+  // tail_next (kTailA): the next slab is the last of its tile.
+  auto slab = [&](int gs, auto next, auto is_copier, bool zero_next, auto tail_next)
+                  __attribute__((always_inline)) {
     auto sync = [&]() __attribute__((always_inline)) {
       // kGradX needs no zeros in LDS: its A side of a tail slab has them in memory
-      // (and kSym's and kMul's K is whole slabs)
-      // (and kLora's with B K-major has zeros in memory too)
-      if constexpr (RAG && MODE != kGradX && !is_ortho(MODE) && !(MODE == kLora && LAY == 1)) wait_zero_sync(zero_next, (gs + 1) & 1);
+      // (and kSym's and kMul's K is whole slabs); kLora with B K-major zeroes B alone
+      if constexpr (decltype(tail_next)::value) wait_tail_b_sync((gs + 1) & 1);
+      else if constexpr (kTailA) wait_and_sync();
+      else if constexpr (RAG && MODE != kGradX && !is_ortho(MODE)) wait_zero_sync(zero_next, (gs + 1) & 1);
       else wait_and_sync();
     };
     constexpr bool kCp = decltype(is_copier)::value;
@@ -1756,11 +1782,17 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
     const int zt = RAG && kv < BK ? nk - 2 : -1;
     const int nk_item = slabs_of(0);
     if (copies) {
-      for (int t = 0; t + 1 < nk_item; ++t, ++gs) slab(gs, yes(), yes(), t == zt);
-      slab(gs, no(), yes(), false);
+      if constexpr (kTailA) {
+        for (int t = 0; t + 2 < nk_item; ++t, ++gs) slab(gs, yes(), yes(), false, no());
+        slab(gs, yes(), yes(), false, yes());
+        ++gs;
+      } else {
+        for (int t = 0; t + 1 < nk_item; ++t, ++gs) slab(gs, yes(), yes(), t == zt, no());
+      }
+      slab(gs, no(), yes(), false, no());
     } else {
-      for (int t = 0; t + 1 < nk_item; ++t, ++gs) slab(gs, yes(), no(), t == zt);
-      slab(gs, no(), no(), false);
+      for (int t = 0; t + 1 < nk_item; ++t, ++gs) slab(gs, yes(), no(), t == zt, no());
+      slab(gs, no(), no(), false, no());
     }
     ++gs;
     if constexpr (SPLIT) {
