@@ -31,9 +31,10 @@ hipError_t launch_mul_tiles(const Args16& a, const OrthoExtra& x, bool a_kmajor,
 // .. 2^14, so that neither leaves binary16's normal range; the factor that
 // undoes it, times the adapter's scale, is applied to the block's sums in fp32.
 //
-// hi is cut off, not rounded, and lo is never zero beside a value that is not:
-// both then have the value's sign, and an infinity that they meet in the other
-// factor gives one infinity, not a NaN.
+// hi is cut off, not rounded, and neither is zero for a value that is not: both
+// then have the value's sign, and an infinity that they meet in the other factor
+// gives one infinity, not a NaN.  What stands for such a zero is binary16's least
+// value, 2^-37 of the block's largest, and in bf16 2^-73 of it.
 //
 //   t2      : [M][ld2], for each block 16 hi values, then 16 lo
 //   factor  : float [M][blocks]
@@ -47,13 +48,15 @@ __host__ __device__ inline int64_t rank_ld2(int R) { return 32 * (int64_t)rank_b
 // finite), as above.
 template <int FMT>
 __device__ __forceinline__ void split_value(float v, half_t& hi, half_t& lo) {
+  const half_t least = f32_to_word<FMT>(copysignf(FMT == kFmtF16 ? 0x1p-24f : 0x1p-60f, v));
+  auto zero = [](half_t w) { return (__builtin_bit_cast(uint16_t, w) & 0x7FFF) == 0; };
   hi = f32_to_word<FMT>(v);
   uint16_t bits = __builtin_bit_cast(uint16_t, hi);
   if (fabsf(word_to_f32<FMT>(hi)) > fabsf(v)) --bits;   // towards zero
   hi = __builtin_bit_cast(half_t, bits);
-  float left = v - word_to_f32<FMT>(hi);
-  if (left == 0.f) left = copysignf(v == 0.f ? 0.f : 0x1p-14f, v);
-  lo = fabsf(v) < __builtin_inff() ? f32_to_word<FMT>(left) : hi;
+  lo = fabsf(v) < __builtin_inff() ? f32_to_word<FMT>(v - word_to_f32<FMT>(hi)) : hi;
+  if (v != 0.f && zero(hi)) hi = least;
+  if (v != 0.f && zero(lo)) lo = least;
 }
 // 2^(13 - floor(log2 top)) and its inverse, within what fp32 holds.
 __device__ __forceinline__ void scale_for(float top, float& up, float& down) {

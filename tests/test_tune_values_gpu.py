@@ -67,3 +67,55 @@ def test_infinite_gradients(M, N, K, typ):
     show("infinite gradients", M, N, K, typ)
     dg.gemm_lora_bwd(X, W, A, B, ids, T, dC, dX, scales=scales)
     close(dX, want, tol, "dX")
+
+
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("M,N,K", [(24, 96, 64), (500, 5000, 128)])
+def test_small_values_beside_large_ones(M, N, K, typ):
+    """What a rank adds is its own, however small it is beside the other ranks of its
+    block: an infinity that it meets is one, and without the large one it is there to
+    the last bits (fp16 holds values down to 2^-37 of the largest, bf16 all of them)."""
+    dt, inf, R, S = DT[typ], float("inf"), 4, 1
+    X, W, A, B, ids, scales = lora_inputs(M, N, K, R, S, dt, 5, "one")
+    ids[0] = -1
+    W[:] = 0
+    scales[:] = 1.0
+    X[:, 0], X[:, 1] = 1.0, 2.0 ** -14
+    A[:] = 0
+    A[0, 0, 0] = 8192.0                                  # t: 2^13,
+    A[0, 1, 0], A[0, 1, 1] = 2.0 ** -9, 2.0 ** -16       # 2^-9 + 2^-30,
+    A[0, 2, 0] = -2.0 ** -24                             # -2^-24,
+    A[0, 3, 1] = 2.0 ** -20                              # 2^-34
+    B[:] = 0
+    B[0, 5, 1], B[0, 6, 2], B[0, 7, 3] = inf, inf, -inf
+    B[0, 8, 1], B[0, 9, 2] = 512.0, 4096.0
+    C, T = torch.empty((M, N), dtype=dt, device=DEV), torch.empty((M, R), device=DEV)
+    show("small beside large", M, N, K, typ)
+    dg.gemm_lora(X, W, A, B, ids, C, scales=scales, T=T)
+    want = torch.zeros((M, N), dtype=torch.float64, device=DEV)
+    want[1:, 5], want[1:, 6], want[1:, 7] = inf, -inf, -inf
+    want[1:, 8], want[1:, 9] = 1.0 + 2.0 ** -21, -2.0 ** -12
+    # the second product's values: 2^-37 of the largest, 2^13, times B
+    tol = torch.zeros_like(want)
+    tol[:, 8], tol[:, 9] = 512.0 * 2.0 ** -24, 4096.0 * 2.0 ** -24
+    close(C, want, tol + torch.finfo(dt).eps / 2 * want.abs().clamp(max=2.0), "C")
+    # gradients: dt = dC B and T of all rows of an adapter are scaled together
+    d = torch.zeros((M, N), dtype=dt, device=DEV)
+    B[:] = 0
+    B[0, 0, 0], B[0, 1, 1], B[0, 2, 2], B[0, 3, 3] = 8192.0, 2.0 ** -9, -2.0 ** -24, 2.0 ** -14
+    B[0, 4, 1], B[0, 5, 3] = 2.0 ** -14, 2.0 ** -14
+    d[:, :4] = 1.0
+    d[:, 4], d[:, 3], d[:, 5] = 2.0 ** -16, 2.0 ** -14, 2.0 ** -14
+    X[:, 2:] = 0
+    X[1, 2], X[2, 3] = inf, 0.0
+    dA, dB = torch.empty_like(A), torch.empty_like(B)
+    dg.gemm_lora_bwd(X, W, A, B, ids, T, d, None, dA, dB, scales=scales)
+    assert dA[0, :, 2].tolist() == [inf, inf, -inf, inf]
+    assert bool((dA[0, :, 3:] == 0).all())
+    d[1, 11], d[1, 12] = inf, -inf
+    dg.gemm_lora_bwd(X, W, A, B, ids, T, d, None, None, dB, scales=scales)
+    assert dB[0, 11].tolist() == [inf, inf, -inf, inf] and dB[0, 12].tolist() == [-inf, -inf, inf, -inf]
+    # (sums of 2^13 over the rows are past binary16's largest value, and no other one is)
+    rest = (d[1:, :11].double().T @ T[1:].double()).to(dt)
+    assert torch.equal(torch.isinf(dB[0, :11]), torch.isinf(rest))
+    assert not bool(torch.isnan(dB[0, :11]).any()) and bool((dB[0, 13:] == 0).all())
