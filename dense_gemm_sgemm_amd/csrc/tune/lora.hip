@@ -302,6 +302,7 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S, con
     ga.groups = p.grad.groups;
     ga.chunks = p.grad.chunks;
     ga.chunk_steps = p.grad.chunk_steps;
+    ga.by_adapter = p.grad.by_adapter;
     if (p.da) {
       ga.job[0] = GradJob{dt32, R, in16(X), ldx, K, out16(dA), ldda, stride_da, 0, pack[0],
                           step_factor[0], partial[0], (K + 127) / 128};

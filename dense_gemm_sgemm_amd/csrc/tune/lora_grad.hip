@@ -233,12 +233,15 @@ __device__ __forceinline__ void store_out(const GradArgs& p, const GradJob& job,
 }
 
 // Partial sums: the f4 of (slot, block of columns, group of ranks), [q][e][lane].
-// An adapter's place in a chunk is slot chunk + a: no two share one, since each
-// next place in the order of the steps has a later chunk or adapter.
-__device__ __forceinline__ f4* partial_at(const GradArgs& p, const GradJob& job, int slot,
-                                          int block, int group, int rb) {
+// A chunk leaves two at most, of an adapter that goes on from the chunk before
+// and of one that begins in it and goes on to the next: slots 2 chunk and 2 chunk
+// + 1.  With fewer adapters than chunks it is slot chunk + a: no two share one,
+// since each next place in the order of the steps has a later chunk or adapter.
+__device__ __forceinline__ f4* partial_at(const GradArgs& p, const GradJob& job, int chunk, int a,
+                                          bool begins, int block, int group, int rb) {
+  const int64_t slot = p.by_adapter ? (int64_t)chunk + a : 2 * (int64_t)chunk + begins;
   return reinterpret_cast<f4*>(job.partial) +
-         (((int64_t)slot * job.blocks + block) * p.groups + group) * (rb * 8 * 64);
+         ((slot * job.blocks + block) * p.groups + group) * (rb * 8 * 64);
 }
 
 template <int FMT, int RB>
@@ -317,12 +320,12 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(GradArgs p, int64_t base
     }
     add_up<RB>(acc, lds, wave, lane);
     if (wave == 0) {
-      const bool whole = (s == 0 || p.g.step_adapter[s - 1] != a) &&
-                         (end == p.g.steps || p.g.step_adapter[end] != a);
+      const bool begins = s == 0 || p.g.step_adapter[s - 1] != a;
+      const bool whole = begins && (end == p.g.steps || p.g.step_adapter[end] != a);
       if (whole) {
         store_out<FMT, RB>(p, job, a, first, c0, lane, acc);
       } else {
-        f4* dst = partial_at(p, job, chunk + a, block, group, RB);
+        f4* dst = partial_at(p, job, chunk, a, begins, block, group, RB);
 #pragma unroll
         for (int q = 0; q < RB; ++q)
 #pragma unroll
@@ -364,7 +367,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(GradArgs p, int64_t base
     for (int e = 0; e < 8; ++e) acc[q][e] = f4{0.f, 0.f, 0.f, 0.f};
   if (steps)
     for (int c = from + wave; c <= to; c += kWaves) {
-      const f4* src = partial_at(p, job, c + a, block, group, RB);
+      const f4* src = partial_at(p, job, c, a, c == from, block, group, RB);
 #pragma unroll
       for (int q = 0; q < RB; ++q)
 #pragma unroll
@@ -452,10 +455,11 @@ GradPlan plan_grad(int M, int N, int K, int R, int S) {
   const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(1, blocks));
   p.chunk_steps = std::max<int>(1, (int)((p.steps + want - 1) / want));
   p.chunks = (p.steps + p.chunk_steps - 1) / p.chunk_steps;
+  p.by_adapter = S < p.chunks;
   p.pack = round256((size_t)2 * p.padded * p.steps * 64);
   for (int i = 0; i < 2; ++i)
-    p.partial[i] = (size_t)(p.chunks + S) * ((cols[i] + kCols - 1) / kCols) * p.groups * p.rb * 8 *
-                   64 * sizeof(f4);
+    p.partial[i] = (size_t)(p.by_adapter ? p.chunks + S : 2 * p.chunks) *
+                   ((cols[i] + kCols - 1) / kCols) * p.groups * p.rb * 8 * 64 * sizeof(f4);
   return p;
 }
 

@@ -145,9 +145,11 @@ struct GradArgs {
   int R, padded;            // ranks, and in whole groups of 16
   int groups;               // of 16 * RB ranks
   int chunks, chunk_steps;  // the steps are cut into chunks, each a workgroup's
+  bool by_adapter;          // how partial sums are numbered
 };
 struct GradPlan {
   int steps, rb, groups, chunks, chunk_steps, padded;
+  bool by_adapter;
   size_t pack, partial[2];   // bytes of one job's
 };
 GradPlan plan_grad(int M, int N, int K, int R, int S);

@@ -90,3 +90,23 @@ def test_coefficients_do_not_hold_the_callers_objects():
     del t
     gc.collect()
     assert alive() is None
+
+
+A, F16, BF16 = 0x100000, 0, 1     # a fake device address
+
+
+def bwd_bytes(lib, M, N, K, R, S, dx=0, da=0, db=0):
+    return lib.gemm_lora_bwd_workspace(BF16, M, N, K, R, S, A, max(1, N), A, max(1, K), dx, da, db)
+
+
+def test_partial_sums_by_the_chunks(lib):
+    """Only an adapter that goes on from one workgroup's steps to the next one's
+    leaves partial sums, two of them a workgroup at most: the workspace does not
+    grow by gradients in fp32 with the adapters that no row names."""
+    M, N, K, R = 300, 4096, 4096, 64
+    few, many = (bwd_bytes(lib, M, N, K, R, S, db=1) for S in (M, 8 * M))
+    assert 0 <= many - few <= 2 * 4 * (7 * M + 128)              # rows of each, first steps
+    few, many = (bwd_bytes(lib, M, N, K, R, S, da=1) for S in (M, 8 * M))
+    assert 0 <= many - few <= 2 * 4 * (7 * M + 128) + 7 * M * R * 4096 * 2   # and B turned
+    # one adapter keeps what it had: a place a chunk and one
+    assert bwd_bytes(lib, 4096, 4096, 4096, 16, 1, da=1, db=1) < 10 << 20
