@@ -73,11 +73,11 @@ struct BwdPlan {
   bool dx, da, db, few = false;   // few: dX by the kernel for few rows
   DxPlan sums;
   size_t t2 = 0, factor = 0, dt = 0, at = 0, bt = 0;
-  size_t counts = 0, rows = 0, steps = 0, pack = 0, step_factor = 0, partial[2] = {0, 0};
+  size_t first = 0, rows = 0, steps = 0, pack = 0, step_factor = 0, partial[2] = {0, 0};
   size_t copy_c = 0, copy_w = 0, tail = 0;
   GradPlan grad{};
   size_t total() const {
-    return t2 + factor + dt + at + bt + counts + rows + steps + 2 * pack + 2 * step_factor +
+    return t2 + factor + dt + at + bt + first + rows + steps + 2 * pack + 2 * step_factor +
            partial[0] + partial[1] + copy_c + copy_w + tail +
            sums.bytes;
   }
@@ -111,7 +111,7 @@ BwdPlan plan_bwd(int M, int N, int K, int R, int S, Mat c, Mat w, bool dx, bool 
   if (p.da || p.db) {
     // (the same whatever is asked for, so that each gradient has the same bits)
     p.grad = plan_grad(M, N, K, R, S);
-    p.counts = round256((size_t)S * sizeof(int));
+    p.first = round256(((size_t)S + 1) * sizeof(int));
     p.rows = round256((size_t)p.grad.steps * 32 * sizeof(int));
     p.steps = round256((size_t)p.grad.steps * sizeof(int));
     p.pack = p.grad.pack;
@@ -216,7 +216,8 @@ MI355TUNE_API unsigned long long gemm_lora_bwd_workspace(int type, int M, int N,
                                                          const void* W, int ldw, int want_dx,
                                                          int want_da, int want_db) {
   if (check(type, M, N, K, R, S) != GEMM_OK || bad_ld(lddc, N) ||
-      (want_dx && M > 0 && K > 0 && bad_ld(ldw, K)))
+      (want_dx && M > 0 && K > 0 && bad_ld(ldw, K)) ||
+      ((want_da || want_db) && !can_list(M, S)))
     return 0;
   return plan_bwd(M, N, K, R, S, Mat{in16(dC), lddc}, Mat{in16(W), ldw}, want_dx, want_da, want_db)
       .total();
@@ -235,6 +236,7 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S, con
   const Mat c0{in16(dC), lddc}, w0{in16(W), ldw};
   const BwdPlan p = plan_bwd(M, N, K, R, S, c0, w0, dX != nullptr, dA != nullptr, dB != nullptr);
   if (!p.dx && !p.da && !p.db) return GEMM_OK;
+  if ((p.da || p.db) && !can_list(M, S)) return GEMM_ERR_BAD_ARG;
   const bool dt = S > 0 && (p.dx || p.da);   // B is read
   if (bad_ld(lddc, N) || (p.dx && (bad_ld(ldw, K) || bad_ld(lddx, K))) ||
       (p.da && (bad_ld(ldx, K) || bad_ld(ldda, K) || bad_out_stride(stride_da, S, R, ldda, K))) ||
@@ -263,7 +265,7 @@ MI355TUNE_API int gemm_lora_bwd(int type, int M, int N, int K, int R, int S, con
   float* dt32 = reinterpret_cast<float*>(take(p.dt));
   half_t* at = reinterpret_cast<half_t*>(take(p.at));
   half_t* bt = reinterpret_cast<half_t*>(take(p.bt));
-  GroupArgs group{ids, M, S, reinterpret_cast<int*>(take(p.counts)),
+  GroupArgs group{ids, M, S, reinterpret_cast<int*>(take(p.first)),
                   reinterpret_cast<int*>(take(p.rows)), reinterpret_cast<int*>(take(p.steps)),
                   p.grad.steps};
   half_t* pack[2];

@@ -42,14 +42,48 @@ __device__ __forceinline__ int sum_all(int v, int* lds) {
   return v;
 }
 
-// Workgroup a counts the rows of adapter a (more adapters than kHistogram).
-__global__ __launch_bounds__(kListThreads) void count_kernel(GroupArgs p, int64_t base) {
+// More adapters than kHistogram: one workgroup counts their rows in p.first (whole
+// numbers: in any order) and adds up the steps.  An adapter's count goes where its
+// rows will be listed.
+__global__ __launch_bounds__(kListThreads) void count_kernel(GroupArgs p, int64_t) {
   __shared__ int lds[kListWaves];
-  const int a = (int)(base + blockIdx.x);
-  int n = 0;
-  for (int m = threadIdx.x; m < p.M; m += kListThreads) n += p.ids[m] == a;
-  n = sum_all(n, lds);
-  if (threadIdx.x == 0) p.counts[a] = n;
+  for (int i = threadIdx.x; i < p.S; i += kListThreads) p.first[i] = 0;
+  __threadfence();
+  __syncthreads();
+  for (int m = threadIdx.x; m < p.M; m += kListThreads) {
+    const long long id = p.ids[m];
+    if (id >= 0 && id < p.S) atomicAdd(p.first + id, 1);
+  }
+  __threadfence();
+  __syncthreads();
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  int before = 0;
+  for (int a0 = 0; a0 < p.S; a0 += kListThreads) {
+    const int a = a0 + threadIdx.x;
+    // (from where the atomics left it)
+    const int count = a < p.S ? __hip_atomic_load(p.first + a, __ATOMIC_RELAXED,
+                                                  __HIP_MEMORY_SCOPE_AGENT) : 0;
+    const int n = (count + 31) / 32;
+    int sum = n;
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) {
+      const int v = __shfl_up(sum, k);
+      if (lane >= k) sum += v;
+    }
+    __syncthreads();
+    if (lane == 63) lds[wave] = sum;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < kListWaves; ++w) {
+      sum += w < wave ? lds[w] : 0;
+      all += lds[w];
+    }
+    if (a < p.S) p.first[a] = before + sum - n;
+    if (count) p.rows[32 * (int64_t)(before + sum - n)] = count;
+    before += all;
+  }
+  if (threadIdx.x == 0) p.first[p.S] = before;
 }
 
 // Workgroup a lists the rows of adapter a, behind those of the adapters before
@@ -74,12 +108,13 @@ __device__ void list_rows(const GroupArgs& p, int a, int* lds, int* bins) {
     __syncthreads();
     for (int i = threadIdx.x; i < a; i += kListThreads) before += (bins[i] + 31) / 32;
     if (a < p.S) count = bins[a];
-    if (a < p.S && threadIdx.x == 0) p.counts[a] = count;
+    before = sum_all(before, lds);
+    if (threadIdx.x == 0) p.first[a] = before;
   } else {
-    for (int i = threadIdx.x; i < a; i += kListThreads) before += (p.counts[i] + 31) / 32;
-    if (a < p.S) count = p.counts[a];
+    before = p.first[a];
+    if (a < p.S && p.first[a + 1] != before) count = p.rows[32 * (int64_t)before];
+    __syncthreads();   // (its place is written below)
   }
-  before = sum_all(before, lds);
   if (a == p.S) {
     for (int i = before + threadIdx.x; i < p.steps; i += kListThreads) p.step_adapter[i] = -1;
     return;
@@ -237,11 +272,13 @@ __device__ __forceinline__ void store_out(const GradArgs& p, const GradJob& job,
 // and of one that begins in it and goes on to the next: slots 2 chunk and 2 chunk
 // + 1.  With fewer adapters than chunks it is slot chunk + a: no two share one,
 // since each next place in the order of the steps has a later chunk or adapter.
-__device__ __forceinline__ f4* partial_at(const GradArgs& p, const GradJob& job, int chunk, int a,
-                                          bool begins, int block, int group, int rb) {
-  const int64_t slot = p.by_adapter ? (int64_t)chunk + a : 2 * (int64_t)chunk + begins;
+__device__ __forceinline__ int partial_slot(const GradArgs& p, int chunk, int a, bool begins) {
+  return p.by_adapter ? chunk + a : 2 * chunk + begins;
+}
+__device__ __forceinline__ f4* partial_at(const GradArgs& p, const GradJob& job, int slot,
+                                          int block, int group, int rb) {
   return reinterpret_cast<f4*>(job.partial) +
-         ((slot * job.blocks + block) * p.groups + group) * (rb * 8 * 64);
+         (((int64_t)slot * job.blocks + block) * p.groups + group) * (rb * 8 * 64);
 }
 
 template <int FMT, int RB>
@@ -325,7 +362,7 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(GradArgs p, int64_t base
       if (whole) {
         store_out<FMT, RB>(p, job, a, first, c0, lane, acc);
       } else {
-        f4* dst = partial_at(p, job, chunk, a, begins, block, group, RB);
+        f4* dst = partial_at(p, job, partial_slot(p, chunk, a, begins), block, group, RB);
 #pragma unroll
         for (int q = 0; q < RB; ++q)
 #pragma unroll
@@ -352,11 +389,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(GradArgs p, int64_t base
   const int which = block >= blocks0;
   if (which) block -= blocks0;
   const GradJob& job = p.job[which];
-  int before = 0;
-  for (int i = lane; i < a; i += 64) before += (p.g.counts[i] + 31) / 32;
-#pragma unroll
-  for (int k = 32; k >= 1; k /= 2) before += __shfl_xor(before, k);
-  const int steps = (p.g.counts[a] + 31) / 32;
+  const int before = p.g.first[a], steps = p.g.first[a + 1] - before;
   const int from = before / p.chunk_steps;
   const int to = steps ? (before + steps - 1) / p.chunk_steps : from;
   if (steps && from == to) return;   // stored already
@@ -367,11 +400,17 @@ __global__ __launch_bounds__(kThreads) void join_kernel(GradArgs p, int64_t base
     for (int e = 0; e < 8; ++e) acc[q][e] = f4{0.f, 0.f, 0.f, 0.f};
   if (steps)
     for (int c = from + wave; c <= to; c += kWaves) {
-      const f4* src = partial_at(p, job, c, a, c == from, block, group, RB);
+      const f4* src = partial_at(p, job, partial_slot(p, c, a, c == from), block, group, RB);
+      f4 v[RB][8];
 #pragma unroll
       for (int q = 0; q < RB; ++q)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[q][e] += src[(q * 8 + e) * 64 + lane];
+        for (int e = 0; e < 8; ++e) v[q][e] = src[(q * 8 + e) * 64 + lane];
+      __builtin_amdgcn_sched_barrier(0);   // (all loads, then the sums)
+#pragma unroll
+      for (int q = 0; q < RB; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[q][e] += v[q][e];
     }
   add_up<RB>(acc, lds, wave, lane);
   if (wave > 0) return;
@@ -430,7 +469,7 @@ hipError_t launch_lists(const GroupArgs* group, const TurnArgs* turns, int count
     jobs.groups = group->S + 1;
     if (group->S > kHistogram) {
       const hipError_t e =
-          launch_tiles((const void*)count_kernel, *group, group->S, kListThreads, 0, stream);
+          launch_tiles((const void*)count_kernel, *group, 1, kListThreads, 0, stream);
       if (e != hipSuccess) return e;
     }
   }

@@ -114,13 +114,16 @@ hipError_t launch_lora_tiles(const Args16& a, const LoraExtra& x, bool kmajor, i
 struct GroupArgs {
   const long long* ids;
   int M, S;
-  int* counts;         // [S] rows of an adapter
+  int* first;          // [S + 1] an adapter's first step, and the number of all
   int* rows;           // [32 * steps]
   int* step_adapter;   // [steps], -1 past the last one
   int steps;           // as many as there can be
 };
 inline int max_steps(int M, int S) { return (int)(((int64_t)M + 31) / 32 + std::min(M, S)); }
 constexpr int kHistogram = 2048;   // adapters that one workgroup counts
+// Each adapter's rows are found among all M: what a call may ask for.  2^40 is 2^30
+// turns of a workgroup of 1024, half a second.
+inline bool can_list(int M, int S) { return (int64_t)M * std::min(M, S) <= int64_t(1) << 40; }
 
 // One of the two gradients: `left` [rows][ld_left] fp32 (dt or t) times `right`
 // [rows][ld_right] 16-bit (X or dC).

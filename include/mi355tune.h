@@ -12,7 +12,7 @@
  * of mi355gemm.h names them), nothing enqueued on an error.
  *
  * Sums are in fp32 or more; an output is rounded once (nearest, ties to even).
- * Results repeat bit for bit: there are no atomics.  No output may overlap an
+ * Results repeat bit for bit: nothing is summed in an order that changes.  No output may overlap an
  * input or another output, except where a call says so.
  *
  * Workspaces: a call that takes one needs at least the bytes its size query
@@ -105,6 +105,9 @@ MI355TUNE_API unsigned long long gemm_lora_workspace(int type, int M, int N, int
  * N are fp32.  Rows without an adapter (any id below 0, or S and more) reach
  * no adapter's gradient, whatever they hold; an id of S and more makes the row
  * of dX NaN.  An adapter without rows has gradients of zero.
+ *
+ * For dA and dB, M * min(M, S) goes up to 2^40 (rows are looked for adapter by
+ * adapter); more is GEMM_ERR_BAD_ARG.
  *
  * X is read only for dA, T only for dB, W and A only for dX, B for dX and dA;
  * they may be NULL otherwise.  An empty sum is zero.

@@ -110,3 +110,25 @@ def test_partial_sums_by_the_chunks(lib):
     assert 0 <= many - few <= 2 * 4 * (7 * M + 128) + 7 * M * R * 4096 * 2   # and B turned
     # one adapter keeps what it had: a place a chunk and one
     assert bwd_bytes(lib, 4096, 4096, 4096, 16, 1, da=1, db=1) < 10 << 20
+
+
+def test_rows_times_adapters(lib):
+    """Rows are listed by adapter in time that goes as M * min(M, S): where that is no
+    longer a moment's work the gradients of adapters are refused, dX is not."""
+    from ctypes import c_void_p
+    a = c_void_p(A)
+
+    def call(M, S, dx, da, db, ws=None, bytes=0):
+        return lib.gemm_lora_bwd(F16, M, 8, 8, 1, S, a, 8, a, 8, a, 8, 8, a, 1, 8, a, None, a, 1, a,
+                                 8, a if dx else None, 8, a if da else None, 8, 8, a if db else None,
+                                 1, 8, ws, bytes, None)
+
+    big = 1 << 20
+    for da, db in ((1, 0), (0, 1), (1, 1)):
+        assert call(big, big, 1, da, db) == -7                   # a workspace is missing
+        assert call(big + 1, big, 1, da, db) == -6
+        assert call(1 << 27, 1 << 13, 0, da, db) == -7 and call(1 << 27, 8193, 0, da, db) == -6
+        assert bwd_bytes(lib, big, 8, 8, 1, big, 0, da, db) > 0
+        assert bwd_bytes(lib, big + 1, 8, 8, 1, big, 0, da, db) == 0
+    assert call(1 << 22, 1 << 22, 1, 0, 0) == -7 and bwd_bytes(lib, 1 << 22, 8, 8, 1, 1 << 22, 1) > 0
+    assert call(4, 1 << 27, 0, 1, 1) == -7                       # few rows, any adapters

@@ -119,3 +119,33 @@ def test_small_values_beside_large_ones(M, N, K, typ):
     rest = (d[1:, :11].double().T @ T[1:].double()).to(dt)
     assert torch.equal(torch.isinf(dB[0, :11]), torch.isinf(rest))
     assert not bool(torch.isnan(dB[0, :11]).any()) and bool((dB[0, 13:] == 0).all())
+
+
+@pytest.mark.parametrize("M,S", [(300, 1 << 20), (5000, 40000), (3000, 2049), (2, 1 << 22)])
+def test_a_million_adapters(M, S):
+    """Gradients of as many adapters as fit take the time of writing them."""
+    dt, N, K, R = torch.bfloat16, 8, 16, 1
+    g = gen(S)
+    X, dC = randn((M, K), 1.0, dt, g).to(DEV), randn((M, N), 1.0, dt, g).to(DEV)
+    W = randn((N, K), 1.0, dt, g).to(DEV)
+    B = torch.ones((S, N, R), dtype=dt, device=DEV)
+    A = torch.ones((S, R, K), dtype=dt, device=DEV)
+    ids = torch.randint(-1, S, (M,), generator=g)
+    ids[M // 3:M // 2] = S - 1                 # more than one step of 32 rows
+    ids[0] = 0
+    ids = ids.to(DEV)
+    T = torch.rand((M, R), generator=g).to(DEV)
+    dA, dB = torch.full_like(A, 3.0), torch.full_like(B, 3.0)
+    show("many adapters", M, S)
+    dg.gemm_lora_bwd(X, W, A, B, ids, T, dC, None, dA, dB)
+    at, have = ids.clamp(min=0), (ids >= 0).double()[:, None]
+    x, d = X.double(), dC.double() * have
+    dt64 = d.sum(1, keepdim=True)
+    each = lambda v: torch.zeros((S, v.shape[1]), dtype=torch.float64, device=DEV).index_add_(0, at, v)
+    # (one step of bf16 for the result, and t's two values of 2^-15 each)
+    wantA, sizeA = each(dt64 * x), each(dt64.abs() * x.abs())
+    wantB, sizeB = each(d * T.double()), each(d.abs() * T.double())
+    most = float(d.abs().sum(1).max())
+    close(dA[:, 0], wantA, 2.0 ** -8 * wantA.abs() + 2.0 ** -14 * (sizeA + most * each(x.abs() * have)),
+          "dA")
+    close(dB[:, :, 0], wantB, 2.0 ** -8 * wantB.abs() + 2.0 ** -14 * each(d.abs()), "dB")
