@@ -255,12 +255,38 @@ struct FusedTileArgs {
 // rows start at 16-byte addresses.  Matrices may be held in two 16-bit values
 // an element, hi + lo: products of parts add up the ones that matter.
 //   kSym   hi (, lo) = alpha * acc + beta * q + gamma * [m == n], times the
-//          matrix's own factors coef[3 * matrix .. + 2] if there are any
+//          matrix's own factors (Growth) if there are any
 //          The first `whole` tiles (of all matrices) are made so; the slabs of
 //          the `rest` are cut into ranges, each a work item that leaves acc *
 //          alpha in `sum`, [range][tile - whole][BM][BM].
-//   kMul   v = alpha * acc: to hi (, lo), or rounded to `out`, whose matrices
-//          are m_end x n_end
+//   kMul   v = alpha * acc: to hi (, lo), or, times the matrix's own factor, rounded
+//          to `out`, whose matrices are m_end x n_end
+//
+// The matrices' own factors.  A matrix far below eps is kept as it would be with a
+// norm of one: iterate k is r_k times what is stored, r_0 = 2^e / (|G| + eps) for a
+// matrix stored times 2^-e, and r_k = min(1, r_0 a_0 .. a_k-1) after that, as it
+// grows while it is small (1 at once for r_0 >= 1, which is what there is if eps does
+// not count).  With A of what is stored,
+//     stored_k+1 = (r_k / r_k+1) (a + b r_k^2 A + c r_k^4 A^2) stored_k.
+struct Growth {
+  const float* coef = nullptr;   // [matrix][4]: step 0's factors of c, b and a, then
+                                 // 2^64 r_0 or an infinity (r_k = 1 for k > 0)
+  int first = 0;                 // step 0
+  float now = 0.f, next = 0.f;   // 2^-64 a_0 .. a_k-1, and with a_k
+  float inverse = 0.f;           // 1 / a_k
+};
+// r of a matrix whose a_0 .. a_k-1 make `grown`; own: the matrix's of coef.
+__device__ __forceinline__ float growth_rate(const float* own, float grown) {
+  return fminf(own[3] * grown, 1.f);
+}
+__device__ __forceinline__ void growth_factors(const Growth& g, const float* own, float& fc,
+                                               float& fb, float& fa) {
+  const float c = own[0], b = own[1], a = own[2], r = growth_rate(own, g.now);
+  const float f = growth_rate(own, g.next) < 1.f ? g.inverse : r;
+  fc = g.first ? c : f * r * r * r * r;
+  fb = g.first ? b : f * r * r;
+  fa = g.first ? a : f;
+}
 struct OrthoExtra {
   int parts = 1;
   uint32_t tiles_each = 0;              // tiles of a matrix
@@ -276,7 +302,7 @@ struct OrthoExtra {
   const half_t* q_hi = nullptr;         // laid out as hi
   const half_t* q_lo = nullptr;
   float alpha = 1.f, beta = 0.f, gamma = 0.f;
-  const float* coef = nullptr;
+  Growth growth;                        // (kMul: coef and now alone)
   void* out = nullptr;
   int out_type = 0;                     // GEMM_TYPE_F16, GEMM_TYPE_BF16 or -1 for fp32
   int64_t ldo = 0, stride_o = 0;
@@ -1152,10 +1178,14 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       const auto& x = args->x;
       const auto& p = args->p;
       float alpha = x.alpha, beta = x.beta, gamma = x.gamma;
-      if (x.coef) {
-        alpha *= x.coef[3 * part];
-        beta *= x.coef[3 * part + 1];
-        gamma *= x.coef[3 * part + 2];
+      if (x.growth.coef) {
+        const Growth own = {x.growth.coef, x.growth.first, x.growth.now, x.growth.next,
+                            x.growth.inverse};
+        float fc, fb, fa;
+        growth_factors(own, own.coef + 4 * part, fc, fb, fa);
+        alpha *= fc;
+        beta *= fb;
+        gamma *= fa;
       }
       if (ok[0] >= 0) {
         const uint32_t tm = (uint32_t)mlo / BM;   // (mlo and nlo are whole tiles)
@@ -1230,11 +1260,13 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       KernArgs* args = fresh_args();
       const auto& x = args->x;
       const auto& p = args->p;
+      float alpha = x.alpha;
+      if (x.growth.coef) alpha *= growth_rate(x.growth.coef + 4 * part, x.growth.now);
 #pragma unroll
       for (int i = 0; i < C::kBlocksM; ++i) {
         const int m = m0 + wm + 16 * i;
 #pragma unroll
-        for (int j = 0; j < C::kBlocksN; ++j) acc[i][j] *= x.alpha;
+        for (int j = 0; j < C::kBlocksN; ++j) acc[i][j] *= alpha;
         if (x.hi) {
 #pragma unroll
           for (int j = 0; j < C::kBlocksN; ++j) put(j, round4(acc[i][j]));

@@ -45,8 +45,9 @@ struct StartArgs {
   int64_t ldg, stride_g;
   int type, m, n, L, blocks;   // blocks: partial sums of a matrix
   double* sums;                // [L][blocks]
-  float* coef;                 // [L][3]
+  float* coef;                 // [L][4] (Growth)
   double eps;
+  double grows;                // a_0 as grown() has it
   half_t *hi, *lo;             // [L][sp][tp]
   int64_t stride_x, tiles;     // tiles: 64 x 64 ones of a matrix (transposed start)
   int sp, tp;
@@ -70,9 +71,30 @@ __device__ __forceinline__ void start_of(const StartArgs& p, int64_t l, double& 
 
 __device__ __forceinline__ void put_coef(const StartArgs& p, int64_t l, double rho) {
   // step 0 sees X0, which is the normalised matrix / rho
-  p.coef[3 * l] = (float)(rho * rho * rho * rho * rho);
-  p.coef[3 * l + 1] = (float)(rho * rho * rho);
-  p.coef[3 * l + 2] = (float)rho;
+  const bool below = rho > 0. && rho < 1.;
+  const double back = below ? fmax(1., 1. / (rho * p.grows)) : 1.;   // 1 / r_1
+  p.coef[4 * l] = (float)(rho * rho * rho * rho * rho * back);
+  p.coef[4 * l + 1] = (float)(rho * rho * rho * back);
+  p.coef[4 * l + 2] = (float)(rho * back);
+  // (under 2^-190 the result is zero in any type)
+  p.coef[4 * l + 3] = below ? (float)fmax(rho * 0x1p64, 0x1p-126) : __builtin_inff();
+}
+// What a small singular value grows by in a step (a coefficient of next to nothing:
+// by something, so that it can be divided by).
+inline double grown(float a) { return fmax(fabs((double)a), 0x1p-10); }
+// The factors of step k, and of the result (k = steps).
+inline hgemm::Growth growth_of(const float* coef, const float* coeffs, int k, int steps) {
+  double now = 0x1p-64;
+  for (int i = 0; i < k; ++i) now *= grown(coeffs[3 * i]);
+  hgemm::Growth g;
+  g.coef = coef;
+  g.first = k == 0;
+  g.now = (float)now;
+  if (k < steps) {
+    g.next = (float)(now * grown(coeffs[3 * k]));
+    g.inverse = (float)(1. / grown(coeffs[3 * k]));
+  }
+  return g;
 }
 
 // A shorter side of up to kSmallSide (ortho_small.hip).

@@ -33,12 +33,12 @@ struct MidArgs {
   int sym, tiles;              // sym: tiles on and below the diagonal
   int splits, per;             // ranges of K (1: none)
   float* sum;                  // [matrix][range][tile][64][64]
-  // out = alpha acc + beta q + gamma [m == n], times coef's of the matrix, to
-  // `to` and turned to `turned`
+  // out = alpha acc + beta q + gamma [m == n], times the matrix's own factors (the
+  // last one: factor), to `to` and turned to `turned`
   Two to, turned, q;
   int64_t ldt, ldtt, stride_t;
   float alpha, beta, gamma;
-  const float* coef;
+  hgemm::Growth growth;
   // the last one: rounded to the result instead, turned or not
   SmallOut out;
   int last, tall, m_end, n_end;   // (of the result as it lies)
@@ -73,10 +73,14 @@ __device__ __forceinline__ void finish_tile(const MidArgs& p, float* t, int64_t 
   const int row = threadIdx.x >> 2, c0 = (threadIdx.x & 3) * 16;
   const int m0 = tm * BT, n0 = tn * BT;
   float alpha = p.alpha, beta = p.beta, gamma = p.gamma;
-  if (p.coef) {
-    alpha *= p.coef[3 * l];
-    beta *= p.coef[3 * l + 1];
-    gamma *= p.coef[3 * l + 2];
+  if (p.last) {
+    alpha *= hgemm::growth_rate(p.growth.coef + 4 * l, p.growth.now);
+  } else if (p.growth.coef) {
+    float fc, fb, fa;
+    hgemm::growth_factors(p.growth, p.growth.coef + 4 * l, fc, fb, fa);
+    alpha *= fc;
+    beta *= fb;
+    gamma *= fa;
   }
   __syncthreads();
   if (!p.last || !p.tall) {
@@ -346,7 +350,7 @@ hipError_t launch_mid(const StartArgs& st, const MidPlan& p, int steps, const fl
     m.alpha = ldexpf(f[2], -kScaleA);
     m.beta = f[1];
     m.gamma = ldexpf(f[0], kScaleA);
-    m.coef = k == 0 ? st.coef : nullptr;
+    m.growth = growth_of(st.coef, coeffs, k, steps);
     e = launch(m);
     if (e != hipSuccess) return e;
     m = MidArgs{};
@@ -365,6 +369,7 @@ hipError_t launch_mid(const StartArgs& st, const MidPlan& p, int steps, const fl
     m.ldtt = p.sp;
     m.stride_t = stride_x;
     m.last = k + 1 == steps;
+    if (m.last) m.growth = growth_of(st.coef, coeffs, steps, steps);
     m.alpha = ldexpf(1.f, -kScaleA - (m.last ? kScaleX : 0));
     m.out = out;
     m.tall = tall;

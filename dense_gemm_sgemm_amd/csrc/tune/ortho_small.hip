@@ -36,7 +36,8 @@ struct SmallArgs {
   float* gram_to;
   int slabs, slab, steps;
   float alpha, beta, gamma;
-  int first, last;
+  hgemm::Growth growth;
+  int last;
   SmallOut out;
 };
 
@@ -161,6 +162,12 @@ __global__ __launch_bounds__(kThreads) void small_step_kernel(SmallArgs p, int64
   const int slab = (int)(id % p.slabs);
   const StartArgs& st = p.st;
 
+  // (a vector load, ahead of the parts': a scalar one would be waited for on its own,
+  // 0.5 us a step)
+  int64_t at_own = 4 * l;
+  asm volatile("" : "+v"(at_own));
+  const f4 own = *(const f4*)(p.growth.coef + at_own);
+
   // A, from the slabs' parts in order
   constexpr int kQuads = SP * SP / 4 / kThreads;
   static_assert(kQuads * kThreads * 4 == SP * SP, "a quad a thread");
@@ -182,11 +189,12 @@ __global__ __launch_bounds__(kThreads) void small_step_kernel(SmallArgs p, int64
     *(h4*)(mat[1] + e / SP * kPitch + e % SP) = lo;
   }
   float alpha = p.alpha, beta = p.beta, gamma = p.gamma;
-  if (p.first) {
-    alpha *= st.coef[3 * l];
-    beta *= st.coef[3 * l + 1];
-    gamma *= st.coef[3 * l + 2];
-  }
+  const float values[4] = {own[0], own[1], own[2], own[3]};
+  float fc, fb, fa;
+  hgemm::growth_factors(p.growth, values, fc, fb, fa);
+  alpha *= fc;
+  beta *= fb;
+  gamma *= fa;
   auto frag = [&](int which, int block, int k) __attribute__((always_inline)) {
     return *(const h8*)(mat[which] + (16 * block + r) * kPitch + 32 * k + 8 * g);
   };
@@ -263,7 +271,9 @@ __global__ __launch_bounds__(kThreads) void small_step_kernel(SmallArgs p, int64
       }
     }
   };
-  const float down = ldexpf(1.f, -kScaleA), end = ldexpf(1.f, -kScaleA - kScaleX);
+  const float down = ldexpf(1.f, -kScaleA);
+  const float end = ldexpf(1.f, -kScaleA - kScaleX) *
+                    (p.last ? hgemm::growth_rate(values, p.growth.next) : 1.f);
   for (int c = wave * kCols; c < p.slab; c += kWaves * kCols) {
     const int n0 = slab * p.slab + c;
     h8 xh[2][KS], xl[2][KS];
@@ -371,7 +381,7 @@ hipError_t launch_small(const StartArgs& st, const SmallPlan& p, int steps, cons
     a.alpha = ldexpf(coeffs[3 * k + 2], -kScaleA);
     a.beta = coeffs[3 * k + 1];
     a.gamma = ldexpf(coeffs[3 * k], kScaleA);
-    a.first = k == 0;
+    a.growth = growth_of(st.coef, coeffs, k, steps);
     a.last = k + 1 == steps;
     e = launch_tiles(p.side == 32 ? (const void*)small_step_kernel<32>
                                   : (const void*)small_step_kernel<64>,

@@ -68,10 +68,11 @@ __global__ __launch_bounds__(256) void join_kernel(JoinArgs p, int64_t base) {
   // (blocks of an earlier tile, and those above the diagonal: by the other ones)
   if (m0 < tm * p.bm || n0 < tn * p.bm || n0 > m0) return;
   float beta = x.beta, gamma = x.gamma, alpha = 1.f;
-  if (x.coef) {
-    alpha = x.coef[3 * l];
-    beta *= x.coef[3 * l + 1];
-    gamma *= x.coef[3 * l + 2];
+  if (x.growth.coef) {
+    float fb, fa;
+    hgemm::growth_factors(x.growth, x.growth.coef + 4 * l, alpha, fb, fa);
+    beta *= fb;
+    gamma *= fa;
   }
   const int64_t stride = (int64_t)x.rest * p.bm * p.bm;
   const float* src = x.sum + (int64_t)rest * p.bm * p.bm + (int64_t)(64 * bi) * p.bm + 64 * bj;

@@ -157,10 +157,12 @@ enum { GEMM_TYPE_F32 = 2 };
  *
  * Products are on the 16-bit matrix cores, of values held in two binary16 ones (22
  * bits) at three products for one; for BF16 outputs of large matrices one value
- * is enough for all but the first three iterates.  The result differs from the
- * formula's by about 2^-19, or there by 0.12 % (beside the output's own rounding
- * of 0.17 %), in the 2-norm, for singular values of G that spread over a factor
- * of a few hundred; what is smaller than that is kept less well.  The singular values of every X
+ * is enough for all but the first three iterates.  In the 2-norm the result differs
+ * from the formula's by about 2^-19 where G's singular values are of one size, as
+ * of noise, by 2^-17 where they spread over a factor of 300 and by 2^-14 where a few
+ * are a thousand times the rest, or there (values in one) by 0.12 %, beside the
+ * output's own rounding (of 0.17 % in bf16): an F32 result is the most that can be
+ * asked for.  This holds for any eps, far above |G| too.  The singular values of every X
  * must stay below 7, as they do for coefficients that converge from [0, 1].
  *
  * steps is 1 .. 64; m, n and L go up to 2^16; others are GEMM_ERR_BAD_ARG, as is

@@ -8,8 +8,8 @@ torch = pytest.importorskip("torch")
 
 import dense_gemm_sgemm_amd as dg  # noqa: E402
 from fused_ref import DT, close, randn  # noqa: E402
-from test_tune_gpu import DEV, TYPES, gen, lora_inputs, show  # noqa: E402
-from tune_ref import lora_bwd_ref, lora_ref, lora_result  # noqa: E402
+from test_tune_gpu import ALL, DEV, TYPES, gen, lora_inputs, ortho_input, show  # noqa: E402
+from tune_ref import MUON, lora_bwd_ref, lora_ref, lora_result, ortho_ref  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -149,3 +149,83 @@ def test_a_million_adapters(M, S):
     close(dA[:, 0], wantA, 2.0 ** -8 * wantA.abs() + 2.0 ** -14 * (sizeA + most * each(x.abs() * have)),
           "dA")
     close(dB[:, :, 0], wantB, 2.0 ** -8 * wantB.abs() + 2.0 ** -14 * each(d.abs()), "dB")
+
+
+# ---------------------------------------------------------------- updates
+
+# each form: one launch a step, short tiles, the tile kernel (its ranges of K, a tall one)
+FORMS = [(2, 24, 500), (2, 500, 40), (3, 140, 200), (2, 500, 150), (1, 1100, 1160), (2, 1300, 1100),
+         (1, 1030, 5000)]
+# the documented distance from the formula in the 2-norm, with a factor of 2 for
+# "about", and half a step of the output's type, root of its squares' sum: an error of
+# rounding is anywhere within it, so over many values half a step / sqrt(3) and more
+# only where they crowd at one end of a power of two
+FINE, BF16 = 2.0 ** -18, 2 * 0.0012
+
+
+def bound(dtype, L, m, n):
+    low, size = min(m, n), L * m * n
+    two = low <= 64 or (low <= 1024 and (1.5 if low > 512 else 1) * size <= 2.5 * 2 ** 20)
+    return (FINE if two or dtype != torch.bfloat16 else BF16) + torch.finfo(dtype).eps / 2
+
+
+def ortho_off(O, ref):
+    """Matrix by matrix, what is under binary16's normal range aside."""
+    least = 2.0 ** -25 * ref[0].numel() ** 0.5 if O.dtype == torch.float16 else 0.0
+    return ((O.double() - ref).flatten(1).norm(dim=1) - least) / ref.flatten(1).norm(dim=1)
+
+
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("L,m,n", FORMS)
+def test_ortho_far_below_eps(L, m, n, out):
+    """A norm far below eps: the update is in proportion to it, and as near to the
+    formula as any other."""
+    G = ortho_input(L, m, n, "f32", 90)
+    O = torch.empty(G.shape, dtype=ALL[out], device=DEV)
+    norm = float(G.double().flatten(1).norm(dim=1).max())
+    for ratio in (0.7, 0.1, 1e-2, 1e-4, 1e-6, 1e-9, 1e-20, 1e-30):
+        eps = 1e-7 if ratio > 1e-9 else 1e3
+        H = G * (ratio * eps / norm)
+        for steps, coeffs in ((5, MUON), (1, MUON), (9, (1.5, -0.5, 0.0)), (3, (0.75, 0.5, 0.25))):
+            show("below eps", L, m, n, out, ratio, steps)
+            dg.gemm_ortho(H, O, steps=steps, coeffs=coeffs, eps=eps)
+            off = ortho_off(O, ortho_ref(H, steps, coeffs, eps))
+            assert float(off.max()) <= bound(ALL[out], L, m, n), (ratio, steps, off.tolist())
+
+
+@pytest.mark.parametrize("out", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("L,m,n", FORMS + [(1, 2048, 2048)])
+def test_ortho_as_documented(L, m, n, out):
+    """The documented distances from the formula: for noise, and, less well, for singular
+    values spread evenly over a factor of 300 and for a few directions a hundred times
+    the rest in the Frobenius norm, whose singular values are a thousand times the
+    rest's.  A value held in two is off by 2^-23 of its size, so an iterate of norm 1 by
+    2^-23 in the norm; what the step then adds to that by rounding C (a = 3.4 on its
+    diagonal, and a gain of 3.4 for what is small: as much again), A (b / a = 1.4) and
+    A^2 (c A / a, 1.2 at most) makes 4.6 of it.  The rest, of norm 0.01, gains as much
+    as that error, and 3.4 a step, so that the iterates' errors add up to 1.42 of the
+    first one's: 100 * 4.6 * 1.42 * 2^-23 = 7.8e-5 of the result, under 100 * 2^-20.
+    Singular values spread evenly: the error of the norm 2^-23 gains as the directions
+    do, in the root of their gains' mean square, which over the result's norm is
+    158 / 4.6 for 24 of them and 323 / 37 for 2048."""
+    O = torch.empty((L, m, n), dtype=ALL[out], device=DEV)
+    g = gen(91)
+    k = min(m, n)
+    q, r = (torch.linalg.qr(torch.randn((L, v, k), generator=g).double().to(DEV))[0] for v in (m, n))
+    values = torch.logspace(0, -2.477, k, dtype=torch.float64)
+    first = last = values / values.norm()
+    for _ in range(5):
+        last = MUON[0] * last + MUON[1] * last ** 3 + MUON[2] * last ** 5
+    gain = float((last / first).square().mean().sqrt() / last.norm())
+    more = {"noise": 0.0, "strong": 100 * 2.0 ** -20, "spread": 4.6 * 1.42 * 2.0 ** -23 * gain}
+    spread = (q * torch.logspace(0, -2.477, k, dtype=torch.float64, device=DEV)) @ r.mT.contiguous()
+    for source in ("f32", "bf16"):
+        for name, G in (("noise", ortho_input(L, m, n, source, 92)),
+                        ("strong", ortho_input(L, m, n, source, 93, 100.0 / min(4, k) ** 0.5)),
+                        ("spread", spread.to(ALL[source]))):
+            show("as documented", L, m, n, source, out, name)
+            dg.gemm_ortho(G, O)
+            off = ortho_off(O, ortho_ref(G))
+            show("  off", [("%.2e" % v) for v in off.tolist()])
+            most = bound(ALL[out], L, m, n) + more[name]
+            assert float(off.max()) <= most, (name, source, off.tolist())
