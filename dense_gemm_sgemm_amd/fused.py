@@ -65,9 +65,9 @@ def load_library() -> ctypes.CDLL:
 _Tensor = None   # torch.Tensor, once a call has needed it
 
 
-def _first(t):
+def _first(t, name="X"):
     """(dtype, GEMM_TYPE_*, GPU index, rows, columns, pointer, leading dimension)
-    of the call's X; the other operands are held to its type and GPU."""
+    of the call's X (or ``name``); the other operands are held to its type and GPU."""
     global _Tensor
     torch = _torch_module()
     _Tensor = torch.Tensor
@@ -77,8 +77,8 @@ def _first(t):
     elif dtype is torch.float16:
         typ = 0
     else:
-        raise TypeError("X must be a float16 or bfloat16 tensor")
-    rows, cols, ld, ptr = _matrix(t, "X", dtype)
+        raise TypeError("%s must be a float16 or bfloat16 tensor" % name)
+    rows, cols, ld, ptr = _matrix(t, name, dtype)
     return dtype, typ, t.get_device(), rows, cols, ptr, ld
 
 

@@ -173,26 +173,61 @@ def lora_workspace_bytes(X, W, A, B) -> int:
                                               *_shaped(W, "W", dtype, at, N, K), ldb)
 
 
+def _none_or(t, name, *needed):
+    """Whether ``t`` is missing; raises if one of ``needed`` (name, wanted) reads it."""
+    if t is not None:
+        return False
+    for what, wanted in needed:
+        if wanted is not None:
+            raise ValueError("%s is needed for %s" % (name, what))
+    return True
+
+
+def _last(*tensors):
+    """The length of the rows of the first tensor that there is."""
+    torch = _torch_module()
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.dim():
+            return t.shape[-1]
+    raise ValueError("one of X, W and A must be given")
+
+
 def gemm_lora_bwd(X, W, A, B, ids, T, dC, dX=None, dA=None, dB=None, scales=None, workspace=None,
                   stream=None):
     """The gradients of ``gemm_lora`` (act "none", W frozen) for the gradient dC
     [M,N] of its result and the T it stored: ``dX`` [M,K], ``dA`` [S,R,K] and
     ``dB`` [S,N,R], each computed if given; adapters that no row names get zeros.
-    ``workspace``: ``lora_bwd_workspace_bytes`` bytes, or None.  Returns
+    What the gradients asked for do not read may be None: X is read for dA, T for
+    dB, W and A for dX, B for dX and dA (one of X, W and A is needed for its
+    sizes).  ``workspace``: ``lora_bwd_workspace_bytes`` bytes, or None.  Returns
     (dX, dA, dB)."""
     torch = _torch_module()
-    dtype, typ, at, M, K, px, ldx = _first(X)
-    N = _rows(W, "W")
-    pw, ldw = _shaped(W, "W", dtype, at, N, K)
-    S, R, pa, lda, sa = _adapters(A, "A", dtype, at, None, K)
-    _, _, pb, ldb, sb = _adapters(B, "B", dtype, at, N, R, S)
+    if _none_or(X, "X", ("dA", dA)):
+        dtype, typ, at, M, N, pc, ldc = _first(dC, "dC")
+        K, px, ldx = _last(W, A, dX), None, 0
+    else:
+        dtype, typ, at, M, K, px, ldx = _first(X)
+        N = _rows(W, "W") if W is not None else _last(dC)
+        pc, ldc = _shaped(dC, "dC", dtype, at, M, N)
+    pw, ldw = (None, 0) if _none_or(W, "W", ("dX", dX)) else _shaped(W, "W", dtype, at, N, K)
+    pa, lda, sa = pb, ldb, sb = pda, ldda, sda = pdb, lddb, sdb = None, 0, 0
+    S = R = None
+    if not _none_or(A, "A", ("dX", dX)):
+        S, R, pa, lda, sa = _adapters(A, "A", dtype, at, R, K, S)
+    if dA is not None:
+        S, R, pda, ldda, sda = _adapters(dA, "dA", dtype, at, R, K, S)
+    if dB is not None:
+        R = _last(dB) if R is None else R
+        S, _, pdb, lddb, sdb = _adapters(dB, "dB", dtype, at, N, R, S)
+    if S is None:
+        return dX, dA, dB
+    if not _none_or(B, "B", ("dX", dX), ("dA", dA)):
+        pb, ldb, sb = _adapters(B, "B", dtype, at, N, R, S)[2:]
     pi = _vector(ids, "ids", torch.int64, at, M)
     ps = _scales(scales, at, S)
-    pt, ldt = _shaped(T, "T", torch.float32, at, M, R)
-    pc, ldc = _shaped(dC, "dC", dtype, at, M, N)
+    pt, ldt = (None, 0) if _none_or(T, "T", ("dB", dB)) else \
+        _shaped(T, "T", torch.float32, at, M, R)
     pdx, lddx = _optional(dX, "dX", dtype, at, M, K)
-    pda, ldda, sda = (None, 0, 0) if dA is None else _adapters(dA, "dA", dtype, at, R, K, S)[2:]
-    pdb, lddb, sdb = (None, 0, 0) if dB is None else _adapters(dB, "dB", dtype, at, N, R, S)[2:]
     lib = _lib or load_library()
     _run(at, stream, lib.gemm_lora_bwd,
          (typ, M, N, K, R, S, px, ldx, pw, ldw, pa, lda, sa, pb, ldb, sb, pi, ps, pt, ldt, pc, ldc,
@@ -204,13 +239,17 @@ def gemm_lora_bwd(X, W, A, B, ids, T, dC, dX=None, dA=None, dB=None, scales=None
 
 def lora_bwd_workspace_bytes(X, W, A, dC, want_dx: bool = True, want_da: bool = True,
                              want_db: bool = True) -> int:
-    """Workspace bytes ``gemm_lora_bwd`` needs for these tensors and gradients."""
-    dtype, typ, at, M, K, _, _ = _first(X)
-    N = _rows(W, "W")
-    S, R = _adapters(A, "A", dtype, at, None, K)[:2]
-    return load_library().gemm_lora_bwd_workspace(
-        typ, M, N, K, R, S, *_shaped(dC, "dC", dtype, at, M, N),
-        *_shaped(W, "W", dtype, at, N, K), bool(want_dx), bool(want_da), bool(want_db))
+    """Workspace bytes ``gemm_lora_bwd`` needs for these tensors and gradients (X may
+    be None, and W where dX is not wanted)."""
+    dtype, typ, at, M, N, pc, ldc = _first(dC, "dC")
+    S, R = _adapters(A, "A", dtype, at, None, None)[:2]
+    K = _last(A)
+    if X is not None:
+        _shaped(X, "X", dtype, at, M, K)
+    pw, ldw = (None, 0) if _none_or(W, "W", ("dX", want_dx or None)) else \
+        _shaped(W, "W", dtype, at, N, K)
+    return load_library().gemm_lora_bwd_workspace(typ, M, N, K, R, S, pc, ldc, pw, ldw,
+                                                  bool(want_dx), bool(want_da), bool(want_db))
 
 
 MUON = (3.4445, -4.7750, 2.0315)

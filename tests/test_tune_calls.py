@@ -132,3 +132,46 @@ def test_rows_times_adapters(lib):
         assert bwd_bytes(lib, big + 1, 8, 8, 1, big, 0, da, db) == 0
     assert call(1 << 22, 1 << 22, 1, 0, 0) == -7 and bwd_bytes(lib, 1 << 22, 8, 8, 1, 1 << 22, 1) > 0
     assert call(4, 1 << 27, 0, 1, 1) == -7                       # few rows, any adapters
+
+
+@pytest.mark.filterwarnings("ignore:Accessing the data pointer")
+def test_gradients_without_what_they_do_not_read(lib, monkeypatch):
+    """X is read for dA alone, T for dB, W and A for dX, B for dX and dA: None will do
+    elsewhere, and nothing of it reaches the library."""
+    x, w, dc = fake_gpu((2, 64), (64, 1)), fake_gpu((3, 64), (64, 1)), fake_gpu((2, 3), (3, 1))
+    a, b = fake_gpu((5, 4, 64), (256, 64, 1)), fake_gpu((5, 3, 4), (12, 4, 1))
+    ids, t = fake_gpu((2,), (1,), dtype="int64"), fake_gpu((2, 4), (4, 1), dtype="float32")
+    seen = []
+    monkeypatch.setattr(tune, "_run", lambda at, stream, fn, args, need=None, ws=None: seen.append(args))
+
+    def call(X=x, W=w, A=a, B=b, T=t, **out):
+        assert dg.gemm_lora_bwd(X, W, A, B, ids, T, dc, **out) == (
+            out.get("dX"), out.get("dA"), out.get("dB"))
+        return seen.pop()
+
+    # (type and sizes; leading dimensions of X, W, A, B, T)
+    sizes, lds = slice(0, 6), lambda s: [s[i] for i in (7, 9, 11, 14, 19)]
+    every = call(dX=x, dA=a, dB=b)
+    assert every[sizes] == (0, 2, 3, 64, 4, 5) and lds(every) == [64, 64, 64, 4, 4]
+    got = call(X=None, T=None, dX=x)
+    assert got[sizes] == every[sizes] and lds(got) == [0, 64, 64, 4, 0]
+    got = call(W=None, A=None, T=None, dA=a)
+    assert got[sizes] == every[sizes] and lds(got) == [64, 0, 0, 4, 0]
+    for keep in (dict(X=x), dict(W=w), dict(A=a)):      # one of them says how long rows are
+        got = call(**{**dict(X=None, W=None, A=None, B=None), **keep}, dB=b)
+        assert got[sizes] == every[sizes], list(keep)
+    got = call(T=None, W=None, dA=a)
+    assert got[sizes] == every[sizes]
+    for kw in (dict(W=None, dX=x), dict(A=None, dX=x), dict(B=None, dX=x), dict(X=None, dA=a),
+               dict(B=None, dA=a), dict(T=None, dB=b), dict(X=None, W=None, A=None, B=None, dB=b),
+               dict(X=None, dA=a, dX=x), dict(W=fake_gpu((3, 63), (63, 1)), X=None, dB=b),
+               dict(X=None, W=None, A=fake_gpu((5, 3, 64), (192, 64, 1)), dB=b),
+               dict(X=fake_gpu((3, 64), (64, 1)), dB=b), dict(X=None, W=w, A=None, dB=w)):
+        with pytest.raises((ValueError, TypeError)):
+            call(**kw)
+            pytest.fail(str(list(kw)))
+    need = dg.lora_bwd_workspace_bytes(x, w, a, dc, False, True, True)
+    assert need == dg.lora_bwd_workspace_bytes(None, None, a, dc, False, True, True) > 0
+    assert dg.lora_bwd_workspace_bytes(None, w, a, dc) == dg.lora_bwd_workspace_bytes(x, w, a, dc)
+    with pytest.raises(ValueError):
+        dg.lora_bwd_workspace_bytes(None, None, a, dc)

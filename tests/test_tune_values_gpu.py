@@ -151,6 +151,22 @@ def test_a_million_adapters(M, S):
     close(dB[:, :, 0], wantB, 2.0 ** -8 * wantB.abs() + 2.0 ** -14 * each(d.abs()), "dB")
 
 
+@pytest.mark.parametrize("typ", TYPES)
+@pytest.mark.parametrize("M,N,K,R,S", [(33, 100, 264, 12, 4), (900, 520, 200, 16, 3)])
+def test_gradients_without_what_they_do_not_read(M, N, K, R, S, typ):
+    dt = DT[typ]
+    X, W, A, B, ids, scales = lora_inputs(M, N, K, R, S, dt, 18)
+    dC, T = randn((M, N), 0.1, dt, gen(19)).to(DEV), lora_ref(X, W, A, B, ids)[1].float()
+    dX, dA, dB = (torch.empty_like(v) for v in (X, A, B))
+    eX, eA, eB = (torch.full_like(v, 9.0) for v in (X, A, B))
+    dg.gemm_lora_bwd(X, W, A, B, ids, T, dC, dX, dA, dB, scales=scales)
+    show("gradients alone", M, N, K, R, S, typ)
+    dg.gemm_lora_bwd(None, W, A, B, ids, None, dC, dX=eX, scales=scales)
+    dg.gemm_lora_bwd(X, None, None, B, ids, None, dC, dA=eA, scales=scales)
+    dg.gemm_lora_bwd(None, None, A, None, ids, T, dC, dB=eB, scales=scales)
+    assert torch.equal(dX, eX) and torch.equal(dA, eA) and torch.equal(dB, eB)
+
+
 # ---------------------------------------------------------------- updates
 
 # each form: one launch a step, short tiles, the tile kernel (its ranges of K, a tall one)
