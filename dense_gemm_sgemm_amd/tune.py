@@ -295,8 +295,11 @@ def gemm_ortho(G, O, steps: int = 5, coeffs=MUON, eps: float = 1e-7, workspace=N
     """``O = G`` orthogonalised by Newton-Schulz products: ``X = G / (|G| + eps)``,
     then ``steps`` times ``X = a X + b (X X^T) X + c (X X^T)^2 X``.  G and O: one
     matrix [m,n] or a stack [L,m,n] of them, float32, float16 or bfloat16 each
-    (bfloat16 results take a third of the products).  ``coeffs``: (a, b, c), or
-    one such triple a step.  ``workspace``: ``ortho_workspace_bytes`` bytes, or
+    (bfloat16 results of large matrices take a third of the products, float32 ones
+    are the nearest to the formula).  ``coeffs``: (a, b, c), or one such triple a
+    step; the singular values of every X must stay below 7, as they do for
+    coefficients that converge from [0, 1]: iterates are held in 16-bit values, and
+    larger ones become infinities.  ``workspace``: ``ortho_workspace_bytes`` bytes, or
     None.  Returns O."""
     tg, to = _type_code(G, "G"), _type_code(O, "O")
     L, m, n, ldg, stride_g, pg = _stack(G, "G")

@@ -175,3 +175,9 @@ def test_gradients_without_what_they_do_not_read(lib, monkeypatch):
     assert dg.lora_bwd_workspace_bytes(None, w, a, dc) == dg.lora_bwd_workspace_bytes(x, w, a, dc)
     with pytest.raises(ValueError):
         dg.lora_bwd_workspace_bytes(None, None, a, dc)
+
+
+def test_singular_values_are_in_the_documentation():
+    """What gemm_ortho's matrices must keep to is where a caller from Python reads it."""
+    text = " ".join(dg.gemm_ortho.__doc__.split())
+    assert "singular values" in text and "below 7" in text
