@@ -360,7 +360,7 @@ hipError_t launch_mid(const StartArgs& st, const MidPlan& p, int steps, const fl
     m.stride_a = stride_a;
     m.stride_b = stride_x;
     m.slabs = m.per = rows;
-      m.cols = cols;
+    m.cols = cols;
     m.tiles = rows * cols;
     m.splits = 1;
     m.to = x[1 - i];

@@ -58,8 +58,9 @@ extern "C" {
  *   T       : float [M][ldt], ldt >= R, or NULL: t, as gemm_lora_bwd takes it;
  *             0 for rows without an adapter, NaN for unknown ones   (written)
  *
- * t is an operand of the second product in two 16-bit values of the type (16
- * bits in bf16, 22 in fp16, of the largest of 16 ranks), so C is rounded once.
+ * t is an operand of the second product in two 16-bit values of the type, off by
+ * 2^-15 (bf16) or 2^-21 (fp16) of itself, in fp16 at least by 2^-37 of the largest of
+ * its 16 ranks, so C is rounded once.
  * An adapter of fewer ranks than R has zeros in the others.  What one row's
  * adapter holds, infinities and NaN too, reaches no other row.
  *
@@ -101,7 +102,8 @@ MI355TUNE_API unsigned long long gemm_lora_workspace(int type, int M, int N, int
  *   dA, dB  : laid out like A and B, or NULL each; adapters must not
  *             overlap                                               (written)
  *
- * dt and T are operands in two 16-bit values, as t above; sums over rows, K and
+ * dt and T are operands in two 16-bit values, as t above; in dA and dB the largest is
+ * that of all ranks of 32 of an adapter's rows.  Sums over rows, K and
  * N are fp32.  Rows without an adapter (any id below 0, or S and more) reach
  * no adapter's gradient, whatever they hold; an id of S and more makes the row
  * of dX NaN.  An adapter without rows has gradients of zero.
