@@ -264,25 +264,28 @@ struct FusedTileArgs {
 //
 // The matrices' own factors.  A matrix far below eps is kept as it would be with a
 // norm of one: iterate k is r_k times what is stored, r_0 = 2^e / (|G| + eps) for a
-// matrix stored times 2^-e, and r_k = min(1, r_0 a_0 .. a_k-1) after that, as it
-// grows while it is small (1 at once for r_0 >= 1, which is what there is if eps does
-// not count).  With A of what is stored,
+// matrix stored times 2^-e.  While r_k is under kSmall, so are the singular values;
+// they grow by g_k = |a_k| + |b_k| kSmall^2 + |c_k| kSmall^4 at most, and r_k+1 is
+// g_k r_k.  Once that would reach kSmall, and from the start if r_0 does (which it
+// does unless eps counts), r is 1.  With A of what is stored,
 //     stored_k+1 = (r_k / r_k+1) (a + b r_k^2 A + c r_k^4 A^2) stored_k.
+constexpr float kSmall = 0.125f;
 struct Growth {
   const float* coef = nullptr;   // [matrix][4]: step 0's factors of c, b and a, then
                                  // 2^64 r_0 or an infinity (r_k = 1 for k > 0)
   int first = 0;                 // step 0
-  float now = 0.f, next = 0.f;   // 2^-64 a_0 .. a_k-1, and with a_k
-  float inverse = 0.f;           // 1 / a_k
+  float now = 0.f, most = 0.f;   // 2^-64 g_0 .. g_k-1, and the largest one up to k
+  float next = 0.f, next_most = 0.f;   // the same with g_k
+  float inverse = 0.f;           // 1 / g_k
 };
-// r of a matrix whose a_0 .. a_k-1 make `grown`; own: the matrix's of coef.
-__device__ __forceinline__ float growth_rate(const float* own, float grown) {
-  return fminf(own[3] * grown, 1.f);
+// r_k of a matrix whose values of coef are `own`.
+__device__ __forceinline__ float growth_rate(const float* own, float now, float most) {
+  return own[3] * most < kSmall ? own[3] * now : 1.f;
 }
 __device__ __forceinline__ void growth_factors(const Growth& g, const float* own, float& fc,
                                                float& fb, float& fa) {
-  const float c = own[0], b = own[1], a = own[2], r = growth_rate(own, g.now);
-  const float f = growth_rate(own, g.next) < 1.f ? g.inverse : r;
+  const float c = own[0], b = own[1], a = own[2], r = growth_rate(own, g.now, g.most);
+  const float f = growth_rate(own, g.next, g.next_most) < 1.f ? g.inverse : r;
   fc = g.first ? c : f * r * r * r * r;
   fb = g.first ? b : f * r * r;
   fa = g.first ? a : f;
@@ -302,7 +305,7 @@ struct OrthoExtra {
   const half_t* q_hi = nullptr;         // laid out as hi
   const half_t* q_lo = nullptr;
   float alpha = 1.f, beta = 0.f, gamma = 0.f;
-  Growth growth;                        // (kMul: coef and now alone)
+  Growth growth;                        // (kMul: coef, now and most alone)
   void* out = nullptr;
   int out_type = 0;                     // GEMM_TYPE_F16, GEMM_TYPE_BF16 or -1 for fp32
   int64_t ldo = 0, stride_o = 0;
@@ -1179,8 +1182,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       const auto& p = args->p;
       float alpha = x.alpha, beta = x.beta, gamma = x.gamma;
       if (x.growth.coef) {
-        const Growth own = {x.growth.coef, x.growth.first, x.growth.now, x.growth.next,
-                            x.growth.inverse};
+        const Growth own = {x.growth.coef, x.growth.first, x.growth.now, x.growth.most,
+                            x.growth.next, x.growth.next_most, x.growth.inverse};
         float fc, fb, fa;
         growth_factors(own, own.coef + 4 * part, fc, fb, fa);
         alpha *= fc;
@@ -1261,7 +1264,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       const auto& x = args->x;
       const auto& p = args->p;
       float alpha = x.alpha;
-      if (x.growth.coef) alpha *= growth_rate(x.growth.coef + 4 * part, x.growth.now);
+      if (x.growth.coef) alpha *= growth_rate(x.growth.coef + 4 * part, x.growth.now, x.growth.most);
 #pragma unroll
       for (int i = 0; i < C::kBlocksM; ++i) {
         const int m = m0 + wm + 16 * i;

@@ -255,8 +255,10 @@ MI355TUNE_API int gemm_ortho(int type_g, int type_o, int L, int m, int n, const 
   hipStream_t s = static_cast<hipStream_t>(stream);
 
   char* ws = static_cast<char*>(workspace);
+  const hgemm::Growth start = growth_of(nullptr, coeffs, 0, steps);
   StartArgs st{G, ldg, stride_g, tg, m, n, L, p.blocks, reinterpret_cast<double*>(ws),
-               reinterpret_cast<float*>(ws + p.sums), (double)eps, grown(coeffs[0]), nullptr, nullptr,
+               reinterpret_cast<float*>(ws + p.sums), (double)eps, start.next, start.next_most,
+               nullptr, nullptr,
                (int64_t)p.sp * p.tp, (int64_t)(p.sp / 64) * (p.tp / 64), p.sp, p.tp};
   ws += p.sums + p.coef;
   hipError_t e = launch_tiles((const void*)norm_kernel, st, (int64_t)L * p.blocks, kThreads, 0, s);

@@ -47,7 +47,7 @@ struct StartArgs {
   double* sums;                // [L][blocks]
   float* coef;                 // [L][4] (Growth)
   double eps;
-  double grows;                // a_0 as grown() has it
+  float next, next_most;       // of Growth at step 0
   half_t *hi, *lo;             // [L][sp][tp]
   int64_t stride_x, tiles;     // tiles: 64 x 64 ones of a matrix (transposed start)
   int sp, tp;
@@ -70,29 +70,42 @@ __device__ __forceinline__ void start_of(const StartArgs& p, int64_t l, double& 
 }
 
 __device__ __forceinline__ void put_coef(const StartArgs& p, int64_t l, double rho) {
-  // step 0 sees X0, which is the normalised matrix / rho
-  const bool below = rho > 0. && rho < 1.;
-  const double back = below ? fmax(1., 1. / (rho * p.grows)) : 1.;   // 1 / r_1
-  p.coef[4 * l] = (float)(rho * rho * rho * rho * rho * back);
-  p.coef[4 * l + 1] = (float)(rho * rho * rho * back);
-  p.coef[4 * l + 2] = (float)(rho * back);
-  // (under 2^-190 the result is zero in any type)
-  p.coef[4 * l + 3] = below ? (float)fmax(rho * 0x1p64, 0x1p-126) : __builtin_inff();
+  // step 0 sees X0, which is the normalised matrix / rho (under 2^-190 the result is
+  // zero in any type)
+  float* own = p.coef + 4 * l;
+  const float small = rho > 0. && rho < hgemm::kSmall ? (float)fmax(rho * 0x1p64, 0x1p-126)
+                                                      : __builtin_inff();
+  const float given[4] = {0.f, 0.f, 0.f, small};
+  const double back = 1. / hgemm::growth_rate(given, p.next, p.next_most);
+  own[0] = (float)(rho * rho * rho * rho * rho * back);
+  own[1] = (float)(rho * rho * rho * back);
+  own[2] = (float)(rho * back);
+  own[3] = small;
 }
-// What a small singular value grows by in a step (a coefficient of next to nothing:
-// by something, so that it can be divided by).
-inline double grown(float a) { return fmax(fabs((double)a), 0x1p-10); }
 // The factors of step k, and of the result (k = steps).
 inline hgemm::Growth growth_of(const float* coef, const float* coeffs, int k, int steps) {
-  double now = 0x1p-64;
-  for (int i = 0; i < k; ++i) now *= grown(coeffs[3 * i]);
   hgemm::Growth g;
   g.coef = coef;
   g.first = k == 0;
-  g.now = (float)now;
-  if (k < steps) {
-    g.next = (float)(now * grown(coeffs[3 * k]));
-    g.inverse = (float)(1. / grown(coeffs[3 * k]));
+  double now = 0x1p-64, most = now;
+  for (int i = 0; i <= k; ++i) {
+    if (i == k) {
+      g.now = (float)now;
+      g.most = (float)most;
+      if (k == steps) break;
+    }
+    constexpr double s2 = (double)hgemm::kSmall * hgemm::kSmall;
+    const float* f = coeffs + 3 * i;
+    // (coefficients of next to nothing: by something, so that it can be divided by)
+    const double grows =
+        fmax(fabs((double)f[0]) + fabs((double)f[1]) * s2 + fabs((double)f[2]) * s2 * s2, 0x1p-10);
+    now *= grows;
+    most = fmax(most, now);
+    if (i == k) {
+      g.next = (float)now;
+      g.next_most = (float)most;
+      g.inverse = (float)(1. / grows);
+    }
   }
   return g;
 }

@@ -74,7 +74,7 @@ __device__ __forceinline__ void finish_tile(const MidArgs& p, float* t, int64_t 
   const int m0 = tm * BT, n0 = tn * BT;
   float alpha = p.alpha, beta = p.beta, gamma = p.gamma;
   if (p.last) {
-    alpha *= hgemm::growth_rate(p.growth.coef + 4 * l, p.growth.now);
+    alpha *= hgemm::growth_rate(p.growth.coef + 4 * l, p.growth.now, p.growth.most);
   } else if (p.growth.coef) {
     float fc, fb, fa;
     hgemm::growth_factors(p.growth, p.growth.coef + 4 * l, fc, fb, fa);

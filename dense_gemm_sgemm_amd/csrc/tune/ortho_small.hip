@@ -273,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void small_step_kernel(SmallArgs p, int64
   };
   const float down = ldexpf(1.f, -kScaleA);
   const float end = ldexpf(1.f, -kScaleA - kScaleX) *
-                    (p.last ? hgemm::growth_rate(values, p.growth.next) : 1.f);
+                    (p.last ? hgemm::growth_rate(values, p.growth.next, p.growth.next_most) : 1.f);
   for (int c = wave * kCols; c < p.slab; c += kWaves * kCols) {
     const int n0 = slab * p.slab + c;
     h8 xh[2][KS], xl[2][KS];

@@ -245,3 +245,31 @@ def test_ortho_as_documented(L, m, n, out):
             show("  off", [("%.2e" % v) for v in off.tolist()])
             most = bound(ALL[out], L, m, n) + more[name]
             assert float(off.max()) <= most, (name, source, off.tolist())
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("L,m,n", FORMS)
+def test_ortho_below_eps_and_growing(L, m, n, out):
+    """One direction, smaller than 1 by eps, and coefficients by which it grows faster
+    than small values do, or keeps its size while they shrink: 1 + 3 x^2 takes 0.3 to
+    4.3 in four steps, 1 + 30 x^2 takes 0.05 to 3.24 in ten, 0.75 + 0.5 x^2 + 0.25 x^4 is
+    1 at 0.6436.  An error grows with it, by 14 and 47 (relative to it), and by 1.58 a
+    step, 61 in nine."""
+    g = gen(94)
+    u, v = (torch.randn((L, s, 1), generator=g).double().to(DEV) for s in (m, n))
+    G = ((u / u.norm(dim=1, keepdim=True)) @ (v / v.norm(dim=1, keepdim=True)).mT).float()
+    G *= 0.99                                  # (so that it is stored as it is)
+    O = torch.empty(G.shape, dtype=ALL[out], device=DEV)
+    for size, steps, coeffs, more in ((0.3, 4, (1.0, 3.0, 0.0), 14), (0.1, 6, (1.0, 3.0, 0.0), 2),
+                                      (0.6436, 9, (0.75, 0.5, 0.25), 61), (0.05, 30, (1.0, 0.9, 0.0), 2),
+                                      (0.05, 11, ((1.0, 30.0, 0.0),) * 10 + ((0.5, 0.0, 0.0),), 47),
+                                      (0.03, 3, (0.0, 4.0, 0.0), 0)):
+        eps = 0.99 / size - 0.99
+        show("growing", L, m, n, out, size, steps)
+        dg.gemm_ortho(G, O, steps=steps, coeffs=coeffs, eps=eps)
+        ref = ortho_ref(G, steps, coeffs, eps)
+        off = ortho_off(O, ref)
+        assert bool(torch.isfinite(O).all()) and float(ref.abs().max()) > 0
+        if more:
+            most = more * (bound(ALL[out], L, m, n) - torch.finfo(O.dtype).eps / 2)
+            assert float(off.max()) <= most + torch.finfo(O.dtype).eps / 2, (size, off.tolist())
