@@ -44,7 +44,8 @@ bool by_rows(int M, int N, Mat x, Mat w) {
 // 192: 42 us against 45, 256: 40 against 44 (64 ranks: 61 against 52), 320: 47 against
 // 45; N 6000, K 768, M = 1000: 46 against 75; N 8192, K 2048, M = 640: 62 against 78; N
 // 8000, K 512, M = 3000: 89 against 78; N 3000, K 768, M = 1500: 47 against 46; N 1024,
-// K 4096, M = 96: 20 against 18; N 2305, K 769, M = 448: 39 against 41.
+// K 4096, M = 96: 20 against 18; N 2305, K 769, M = 448: 39 against 41.  (It does not
+// look at the ranks: with 64 of them the tiles are the faster ones from 256 rows on.)
 bool dx_by_rows(int M, int N, int K) {
   return M <= 64 || row_work(M, K) <= std::min<int64_t>(4 * (int64_t)N - 2000, 24000);
 }

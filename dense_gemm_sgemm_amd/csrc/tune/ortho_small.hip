@@ -9,7 +9,7 @@
 // either operand is 16 bytes in a row; A and C are symmetric.  Everything is in
 // two binary16 values, hi + lo, with the powers of two of ortho.hip, and each
 // product is hi hi + hi lo + lo hi: the matrix cores are idle anyway.  Sixteen
-// 16 x 4096: 8.6 us a step (its launch, one latency for X and one for the parts of
+// 16 x 4096: 8.9 us a step (its launch, one latency for X and one for the parts of
 // A), 12 for the first iterate.
 //
 // The slab is multiplied both ways round.  X^T C leaves a lane four columns of
