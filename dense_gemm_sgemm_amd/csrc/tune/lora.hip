@@ -218,7 +218,7 @@ MI355TUNE_API unsigned long long gemm_lora_bwd_workspace(int type, int M, int N,
                                                          int want_da, int want_db) {
   if (check(type, M, N, K, R, S) != GEMM_OK || bad_ld(lddc, N) ||
       (want_dx && M > 0 && K > 0 && bad_ld(ldw, K)) ||
-      ((want_da || want_db) && !can_list(M, S)))
+      (((want_da && K > 0) || (want_db && N > 0)) && !can_list(M, S)))
     return 0;
   return plan_bwd(M, N, K, R, S, Mat{in16(dC), lddc}, Mat{in16(W), ldw}, want_dx, want_da, want_db)
       .total();

@@ -12,8 +12,8 @@
  * of mi355gemm.h names them), nothing enqueued on an error.
  *
  * Sums are in fp32 or more; an output is rounded once (nearest, ties to even).
- * Results repeat bit for bit: nothing is summed in an order that changes.  No output may overlap an
- * input or another output, except where a call says so.
+ * Results repeat bit for bit: nothing is summed in an order that changes.  No
+ * output may overlap an input or another output, except where a call says so.
  *
  * Workspaces: a call that takes one needs at least the bytes its size query
  * reports for the same arguments, at a 16-byte aligned device address, or NULL
@@ -58,11 +58,10 @@ extern "C" {
  *   T       : float [M][ldt], ldt >= R, or NULL: t, as gemm_lora_bwd takes it;
  *             0 for rows without an adapter, NaN for unknown ones   (written)
  *
- * t is an operand of the second product in two 16-bit values of the type, off by
- * 2^-15 (bf16) or 2^-21 (fp16) of itself, in fp16 at least by 2^-37 of the largest of
- * its 16 ranks, so C is rounded once.
- * An adapter of fewer ranks than R has zeros in the others.  What one row's
- * adapter holds, infinities and NaN too, reaches no other row.
+ * t is an operand of the second product in two 16-bit values of the type, within
+ * 2^-15 (bf16) or 2^-21 (fp16, and 2^-37 of the largest of its 16 ranks) of itself,
+ * so C is rounded once.  An adapter of fewer ranks than R has zeros in the others.
+ * What one row's adapter holds, infinities and NaN too, reaches no other row.
  *
  * Rows whose neighbours have the same adapter share its reads; in any other
  * order each block of 16 rows reads every adapter that it names.
@@ -102,11 +101,11 @@ MI355TUNE_API unsigned long long gemm_lora_workspace(int type, int M, int N, int
  *   dA, dB  : laid out like A and B, or NULL each; adapters must not
  *             overlap                                               (written)
  *
- * dt and T are operands in two 16-bit values, as t above; in dA and dB the largest is
- * that of all ranks of 32 of an adapter's rows.  Sums over rows, K and
- * N are fp32.  Rows without an adapter (any id below 0, or S and more) reach
- * no adapter's gradient, whatever they hold; an id of S and more makes the row
- * of dX NaN.  An adapter without rows has gradients of zero.
+ * dt and T are operands in two 16-bit values, as t above; in dA and dB the largest
+ * is that of all ranks of 32 of an adapter's rows.  Sums over rows, K and N are
+ * fp32.  Rows without an adapter (any id below 0, or S and more) reach no adapter's
+ * gradient, whatever they hold; an id of S and more makes the row of dX NaN.  An
+ * adapter without rows has gradients of zero.
  *
  * For dA and dB, M * min(M, S) goes up to 2^40 (rows are looked for adapter by
  * adapter); more is GEMM_ERR_BAD_ARG.
@@ -164,8 +163,8 @@ enum { GEMM_TYPE_F32 = 2 };
  * of noise, by 2^-17 where they spread over a factor of 300 and by 2^-14 where a few
  * are a thousand times the rest, or there (values in one) by 0.12 %, beside the
  * output's own rounding (of 0.17 % in bf16): an F32 result is the most that can be
- * asked for.  This holds for any eps, far above |G| too.  The singular values of every X
- * must stay below 7, as they do for coefficients that converge from [0, 1].
+ * asked for.  This holds for any eps, far above |G| too.  The singular values of
+ * every X must stay below 7, as they do for coefficients that converge from [0, 1].
  *
  * steps is 1 .. 64; m, n and L go up to 2^16; others are GEMM_ERR_BAD_ARG, as is
  * a negative or NaN eps.  L == 0, m == 0 or n == 0 is a no-op.
