@@ -586,7 +586,10 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   struct CopyBaseX : CopyBase {   // kGradX
     int64_t sa;        // bytes between A's copies
   };
-  constexpr bool kTailA = MODE == kLora && LAY == 1;   // A's last slab from a copy, as kGradX's
+  // kLora with B K-major: OPT bit 2 says that K is whole slabs, else A's last slab
+  // comes from a copy, as kGradX's
+  constexpr bool kWholeK = MODE == kLora && LAY == 1 && (OPT & 4) != 0;
+  constexpr bool kTailA = MODE == kLora && LAY == 1 && !kWholeK;
   typedef std::conditional_t<MODE == kGradX || kTailA, CopyBaseX, CopyBase> CopyBaseT;
   // kGradX: this lane's offset in x.tail; slabs of each part of K
   uint32_t offA_x = 0;
@@ -1584,11 +1587,11 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       len = left < part_left ? left : part_left;
     } else {
       // (LAY 1 with a K tail: the last slab from K - 64)
-      run_tail = kv < BK && t == nk - 1;
+      run_tail = !kWholeK && kv < BK && t == nk - 1;
       k0 = LAY != 0 && run_tail ? (int64_t)p.K - BK : (int64_t)t * BK;
       a = p.A;
       b = p.B;
-      if (kv < BK && !run_tail) len = left - 1;
+      if (!kWholeK && kv < BK && !run_tail) len = left - 1;
     }
     run_a = kAT ? (const char*)(a + k0 * p.lda + m0) + firstTA
                 : (const char*)(a + (int64_t)m0 * p.lda + k0) + firstA;
@@ -1658,8 +1661,8 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
   // kTailA: A's side of the last slab has zeros in memory where B's rows repeat the
   // slab before, and the copying waves zero those rows here, since an infinity in
   // them times zero would be NaN.  In the last slab but one, which has code of its own
-  // for it: a branch for it in the slab loop costs spills there (4096^3, whether or not
-  // there is such a slab: 122 -> 154 us).
+  // for it: a branch for it in the slab loop costs spills there (4096 x 4104 x 4096: 139
+  // -> 170 us, and with code of its own 141).
   auto wait_tail_b_sync = [&](int stage) __attribute__((always_inline)) {
     __builtin_amdgcn_s_waitcnt(kWaitVmLgkm0);
     const int ks = (BK - fresh_args()->p.K % BK) % BK;   // 8 .. 56, or 0: whole slabs
@@ -1686,7 +1689,7 @@ void hgemm_nt_kernel(TileArgsOf<MODE> ta) {
       // kGradX needs no zeros in LDS: its A side of a tail slab has them in memory
       // (and kSym's and kMul's K is whole slabs); kLora with B K-major zeroes B alone
       if constexpr (decltype(tail_next)::value) wait_tail_b_sync((gs + 1) & 1);
-      else if constexpr (kTailA) wait_and_sync();
+      else if constexpr (kTailA || kWholeK) wait_and_sync();
       else if constexpr (RAG && MODE != kGradX && !is_ortho(MODE)) wait_zero_sync(zero_next, (gs + 1) & 1);
       else wait_and_sync();
     };
@@ -1920,7 +1923,8 @@ hipError_t launch_lora(const Args16& a, const LoraExtra& x, int slots, hipStream
   static_assert(C::WM <= 64, "a lane for each of a wave's rows");
   const int64_t tiles = (int64_t)((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN);
   // (xcd_order32; two slabs a tile, see the copies' runs in the kernel)
-  if (tiles >= (int64_t(1) << 31) || a.K <= BK) return hipErrorInvalidValue;
+  if (tiles >= (int64_t(1) << 31) || a.K <= BK || ((OPT & 4) && a.K % BK != 0))
+    return hipErrorInvalidValue;
   LoraTileArgs ta{a, tiles, x};
   void* args[] = {&ta};
   return hipLaunchKernel((const void*)hgemm_nt_kernel<BM, BN, BK, WAVES_M, WAVES_N, GM, COPY_SEL,

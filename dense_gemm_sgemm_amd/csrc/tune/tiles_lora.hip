@@ -19,15 +19,16 @@ constexpr fused::Shape kShapes[] = {
     {192, 256, 1, 192 * 256 * 11 / 10, 192 * 256 * 11 / 10},
 };
 
-template <int FMT, int LAY>
+// (W: K-major, over whole slabs of 64: no code for a last one that is none)
+template <int FMT, int LAY, int W>
 hipError_t launch(const Args16& a, const LoraExtra& x, int cus, hipStream_t stream) {
   switch (fused::choose_shape(kShapes, 3, a.M, a.N, 1, cus)) {
     case 0:
-      return hgemm::launch_lora<256, 256, BK, 4, 2, GM, 1, 2, FMT, LAY>(a, x, cus, stream);
+      return hgemm::launch_lora<256, 256, BK, 4, 2, GM, 1, 2 + W, FMT, LAY>(a, x, cus, stream);
     case 1:
-      return hgemm::launch_lora<128, 128, BK, 2, 2, GM, 0, 0, FMT, LAY>(a, x, 2 * cus, stream);
+      return hgemm::launch_lora<128, 128, BK, 2, 2, GM, 0, W, FMT, LAY>(a, x, 2 * cus, stream);
     case 2:
-      return hgemm::launch_lora<192, 256, BK, 4, 2, GM, 1, 2, FMT, LAY>(a, x, cus, stream);
+      return hgemm::launch_lora<192, 256, BK, 4, 2, GM, 1, 2 + W, FMT, LAY>(a, x, cus, stream);
     default:
       return hipErrorInvalidValue;
   }
@@ -37,9 +38,14 @@ hipError_t launch(const Args16& a, const LoraExtra& x, int cus, hipStream_t stre
 
 hipError_t launch_lora_tiles(const Args16& a, const LoraExtra& x, bool kmajor, int cus,
                              hipStream_t stream) {
-  if (a.fmt == kFmtBF16)
-    return kmajor ? launch<kFmtBF16, 1>(a, x, cus, stream) : launch<kFmtBF16, 0>(a, x, cus, stream);
-  return kmajor ? launch<kFmtF16, 1>(a, x, cus, stream) : launch<kFmtF16, 0>(a, x, cus, stream);
+  if (!kmajor)
+    return a.fmt == kFmtBF16 ? launch<kFmtBF16, 0, 0>(a, x, cus, stream)
+                             : launch<kFmtF16, 0, 0>(a, x, cus, stream);
+  if (a.K % BK == 0)
+    return a.fmt == kFmtBF16 ? launch<kFmtBF16, 1, 4>(a, x, cus, stream)
+                             : launch<kFmtF16, 1, 4>(a, x, cus, stream);
+  return a.fmt == kFmtBF16 ? launch<kFmtBF16, 1, 0>(a, x, cus, stream)
+                           : launch<kFmtF16, 1, 0>(a, x, cus, stream);
 }
 
 }  // namespace tune
